@@ -75,8 +75,18 @@ enum {
  * scale their fp32 sums by a and the weights' global scale, which is what a
  * block-scaled FP4 MMA computes, up to summation order.  It needs the view's
  * input_scale13 / input_scale2 (positive; a non-positive maximum sets
- * OES_DEV_BAD_ID and uses 1). */
-enum { OES_WFMT_BF16 = 0, OES_WFMT_NVFP4 = 1, OES_WFMT_NVFP4_W4A4 = 2 };
+ * OES_DEV_BAD_ID and uses 1).
+ * FP8 weights are e4m3 with one fp32 scale for each 128 x 128 block, and the
+ * activations are quantised the way moe_fp8_quantize does it: x for each 128
+ * values along H, the SwiGLU output h (fp32, unrounded) for each 128 along I.
+ * The products of codes are summed in fp32 over each 128 of K, scaled by both
+ * scales, and added up in fp32. */
+enum {
+  OES_WFMT_BF16 = 0,
+  OES_WFMT_NVFP4 = 1,
+  OES_WFMT_NVFP4_W4A4 = 2,
+  OES_WFMT_FP8 = 3
+};
 
 /* Eviction policies of the slot cache.  LRU is the pages' (FreeToken PR #676,
  * the author's reply: the cache is LRU only).  LRFU is the scored policy the
@@ -95,6 +105,9 @@ enum { OES_POLICY_LRU = 0, OES_POLICY_LRFU = 1 };
 #define OES_MAX_TOPK 32
 #define OES_MAX_EXPERTS 4096
 #define OES_MAX_SLOTS 8192
+
+/* Element types of the calls that take more than one. */
+enum { OES_F32 = 0, OES_BF16 = 1 };
 
 /* Capacity of moe_align_block_size's sorted_ids for R routes, E experts and
  * block size B: R + min(E, R) * (B - 1), rounded up to a multiple of B.  No
@@ -338,13 +351,17 @@ int moe_align_block_size_noalloc(const int32_t *ids, int R, int E, int B, int ig
  *   nvfp4: w13 values [2I, H/2] u8 (e2m1 pairs, element 2i in the low
  *          nibble), w13 scales [H/64, 2I, 4] e4m3 (K-chunk-major), w2 values
  *          [H, I/2], w2 scales [I/64, H, 4], then fp32 gs13, gs2, in13, in2
- *          (global scales and input scales), each section 16-byte aligned.
- * Weights decode as e2m1 * e4m3 * gs. */
+ *          (global scales and input scales), each section 16-byte aligned;
+ *   fp8:   w13 [2I, H] e4m3 (gate rows, then up rows), w2 [H, I] e4m3, then
+ *          fp32 block scales: of w13 [2 ceil(I/128), ceil(H/128)] (the gate's
+ *          rows of blocks, then the up's; each half starts its own blocks),
+ *          of w2 [ceil(H/128), ceil(I/128)], each section 16-byte aligned.
+ * NVFP4 weights decode as e2m1 * e4m3 * gs, FP8 as e4m3 * block scale. */
 typedef struct {
   int layer;                  /* the layer, for the record */
   int E;                      /* the layer's expert count (sizes the tiles) */
   const int32_t *e2s;         /* device [E]: slot of each expert, -1 = not resident */
-  int wfmt;                   /* OES_WFMT_BF16 or OES_WFMT_NVFP4 */
+  int wfmt;                   /* OES_WFMT_* */
   const void *pool;           /* device base of the slot pool [S, row_bytes] */
   int64_t row_bytes;          /* bytes per slot row */
   int S;                      /* slots in the pool */
@@ -400,6 +417,86 @@ int moe_grouped_gemm_slots(const oes_routed_experts *view, const uint16_t *x, in
                            const int32_t *block_expert, const int32_t *n_post_pad, int B,
                            void *workspace, size_t workspace_bytes, uint16_t *out,
                            int32_t *status, oes_stream_t stream);
+
+/* ------------------------------------------ 8-bit rows and the block norms */
+
+/* Activations of moe_fp8_quantize. */
+enum { OES_ACT_NONE = 0, OES_ACT_SWIGLU = 1 };
+
+/* Rows to e4m3 codes with one fp32 scale for each group of 128 values.  For
+ * each row t and group b (the last group may be short), over the group's
+ * values v:  amax = max(|v|, 2^-100), scale[t, b] = amax / 448, and
+ * q[t, i] = e4m3(448 v / amax), the quotient rounded to fp32, then to the
+ * nearest code, ties to even.  NaN values take no part in amax and get a NaN
+ * code; an infinity makes the group's scale infinite (the group reads as
+ * NaN).  act = OES_ACT_NONE: v = x[t, i], i < K.  OES_ACT_SWIGLU: rows of x
+ * are [gate (K), up (K)] and v = silu(gate) * up in fp32, unrounded.
+ * x: device, dtype OES_BF16 or OES_F32, row stride x_ld values (at least K,
+ * or 2 K); q: device bytes, row stride q_ld >= K; scale: device
+ * [T, ceil(K/128)] fp32.  T >= 0, 1 <= K <= 2^28.  Rows are read and written
+ * 8 values at a time when K, strides and addresses allow it (K a multiple of
+ * 8; x and its rows 16-byte, q and its rows 8-byte aligned). */
+int moe_fp8_quantize(const void *x, int dtype, int64_t x_ld, int T, int K, int act, uint8_t *q,
+                     int64_t q_ld, float *scale, oes_stream_t stream);
+
+/* The matrix product of 8-bit rows, as a shared expert or a projection beside
+ * the routed experts uses it:
+ *   out[t, n] = sum_b xs[t, b] * ws[n / 128, b] * sum_{k in block b} x[t, k] * w[n, k]
+ * with fp32 sums over each 128 of K (block b) and an fp32 sum over b in a
+ * fixed order; the result is rounded once.
+ * xq: device e4m3 [T, K], row stride xq_ld bytes, xs: device [T, ceil(K/128)]
+ * fp32 (moe_fp8_quantize); wq: device e4m3 [N, K], row stride wq_ld bytes,
+ * ws: device [ceil(N/128), ceil(K/128)] fp32; out: device [T, N] of dtype
+ * OES_BF16 or OES_F32, row stride out_ld values.  xq and wq are 16-byte
+ * aligned and their row strides multiples of 16 (bytes past K in a row are
+ * not used).  T >= 0, 1 <= N, K <= 2^24.  status: device word or NULL. */
+int moe_fp8_gemm(const uint8_t *xq, int64_t xq_ld, const float *xs, int T, int K, const uint8_t *wq,
+                 int64_t wq_ld, const float *ws, int N, void *out, int dtype, int64_t out_ld,
+                 int32_t *status, oes_stream_t stream);
+
+/* Gates of moe_block_norm: none; one fp32 value a token (gate[t * gate_ld]:
+ * a column of moe_gate_logits' output does); one bf16 value a channel,
+ * gate[h]; one bf16 value each, gate[t * gate_ld + h]. */
+enum { OES_GATE_NONE = 0, OES_GATE_TOKEN = 1, OES_GATE_CHANNEL = 2, OES_GATE_ELEMENT = 3 };
+
+/* The residual update after a block and the norm before the next, for each
+ * row t over its H values, in fp32:
+ *   v  = y * rsqrt(mean(y^2) + eps) * (weight_offset + post_weight)
+ *   r' = residual + residual_scale * g * v
+ *   u  = r' * rsqrt(mean(r'^2) + eps) * (weight_offset + pre_weight)
+ * g = gate, or 1 / (1 + exp(-gate)) with gate_sigmoid.  post_weight NULL:
+ * v = y.  pre_weight NULL: u = r'.  y NULL (then no post_weight and no gate):
+ * r' = residual.  r' goes into u unrounded.  Outputs, each NULL if unwanted
+ * but not all: out_residual gets r' (may be residual itself with its stride),
+ * out gets u in bf16 (may be y itself with its stride), out_q and out_scale
+ * get the unrounded u as moe_fp8_quantize's codes and scales
+ * ([T, ceil(H/128)]).  Other overlaps of buffers are not allowed.
+ * residual and out_residual are of type dtype (OES_BF16 or OES_F32); strides
+ * (*_ld) are in values.  T >= 0, 1 <= H <= 16384, eps >= 0.  Rows are read
+ * and written 8 values at a time when H is a multiple of 8 and every row and
+ * weight is 16-byte aligned (codes 8-byte). */
+typedef struct {
+  int T, H;
+  int dtype;
+  int gate_kind, gate_sigmoid;
+  float residual_scale, weight_offset, eps;
+  const void *residual;
+  int64_t residual_ld;
+  const uint16_t *y;
+  int64_t y_ld;
+  const uint16_t *post_weight; /* [H] bf16 */
+  const uint16_t *pre_weight;  /* [H] bf16 */
+  const void *gate;
+  int64_t gate_ld;
+  void *out_residual;
+  int64_t out_residual_ld;
+  uint16_t *out;
+  int64_t out_ld;
+  uint8_t *out_q;
+  int64_t out_q_ld;
+  float *out_scale;
+} oes_block_norm;
+int moe_block_norm(const oes_block_norm *args, oes_stream_t stream);
 
 /* --------------------------------------------------------- whole layer */
 

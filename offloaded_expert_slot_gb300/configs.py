@@ -23,7 +23,7 @@ class LayerConfig:
     E: int                 # the layer's expert count
     H: int                 # hidden size
     I: int                 # expert intermediate size
-    wfmt: str              # "bf16" or "nvfp4"
+    wfmt: str              # "bf16", "nvfp4" or "fp8"
     S: int                 # slots in the pool
     L: int                 # layers whose experts share the pool
     prefill: int           # slots pre-filled with seeded (layer, expert) pairs
@@ -61,13 +61,29 @@ def expert_row_bytes(wfmt: str, H: int, I: int) -> int:
     w2 values [H, I/2] u8, w2 scales [I/64, H, 4] e4m3, then four fp32
     scalars: global scale of w13, global scale of w2, input scale of w13,
     input scale of w2.  Every section starts on a 16-byte boundary.
+    fp8 row: see fp8_offsets.
     """
     if wfmt == "bf16":
         return 2 * I * H * 2 + H * I * 2
     if wfmt == "nvfp4":
         assert H % 64 == 0 and I % 64 == 0
         return (2 * I * H // 2) + (2 * I * H // 16) + (H * I // 2) + (H * I // 16) + 16
+    if wfmt == "fp8":
+        return fp8_offsets(H, I)["end"]
     raise ValueError(wfmt)
+
+
+def fp8_offsets(H: int, I: int) -> dict:
+    """Byte offsets of the sections of an FP8 expert row: w13 [2I, H] and w2
+    [H, I] e4m3, then fp32 scales of 128 x 128 blocks: w13's [2 ceil(I/128),
+    ceil(H/128)] (the gate's rows of blocks, then the up's), w2's
+    [ceil(H/128), ceil(I/128)].  Every section starts on a 16-byte boundary."""
+    hb, ib = -(-H // 128), -(-I // 128)
+    o = {"w13q": 0, "w2q": 2 * I * H}
+    o["w13s"] = o["w2q"] + H * I
+    o["w2s"] = o["w13s"] + (8 * ib * hb + 15) // 16 * 16
+    o["end"] = o["w2s"] + (4 * ib * hb + 15) // 16 * 16
+    return o
 
 
 def nvfp4_offsets(H: int, I: int) -> dict:

@@ -42,6 +42,7 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "fp8_dev.cuh"
 #include "gemm_types.h"
 #include "internal.h"
 
@@ -1309,6 +1310,7 @@ Sections sections(int wfmt, int H, int I) {
 
 int64_t expected_row_bytes(int wfmt, int H, int I) {
   if (wfmt == OES_WFMT_BF16) return (int64_t)6 * H * I;
+  if (wfmt == OES_WFMT_FP8) return fp8_row(H, I).end;
   return sections(wfmt, H, I).scal + 16;
 }
 
@@ -1319,6 +1321,8 @@ struct Ws {
   float* act;        // W4A4: the layer's two activation scales
   float* part;       // GEMM1 K split: fp32 sums of each tile's halves
   int32_t* tcount;   // GEMM1 K split: halves finished per tile and epilogue warp
+  float* hs;         // FP8: scales of h
+  float* xs;         // FP8: scales of x
   size_t bytes;
 };
 
@@ -1339,15 +1343,20 @@ Ws carve(void* base, int T, int k, int E, int H, int I, int B, int wfmt) {
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   size_t off = 0;
   uint8_t* p = static_cast<uint8_t*>(base);
+  const bool fp8 = wfmt == OES_WFMT_FP8;
   w.h = reinterpret_cast<uint16_t*>(p + off);
-  off += up((size_t)cap * I * 2);
+  off += up((size_t)cap * I * (fp8 ? 1 : 2));
+  w.hs = reinterpret_cast<float*>(p + off);
+  if (fp8) off += up((size_t)cap * ceil_div(I, kQuantGroup) * 4);
   w.y = reinterpret_cast<uint16_t*>(p + off);
   off += up((size_t)R * H * 2);
   w.x16 = reinterpret_cast<uint16_t*>(p + off);
-  if (wfmt != OES_WFMT_BF16) off += up((size_t)T * H * 2);
+  if (wfmt != OES_WFMT_BF16) off += up((size_t)T * H * (fp8 ? 1 : 2));
+  w.xs = reinterpret_cast<float*>(p + off);
+  if (fp8) off += up((size_t)T * ceil_div(H, kQuantGroup) * 4);
   w.act = reinterpret_cast<float*>(p + off);
   if (wfmt == OES_WFMT_NVFP4_W4A4) off += 256;
-  const int64_t st = split_tiles(R, E, I, B);
+  const int64_t st = fp8 ? 0 : split_tiles(R, E, I, B);
   w.part = reinterpret_cast<float*>(p + off);
   off += up((size_t)st * 2 * 2 * B * kTileM * 4);
   w.tcount = reinterpret_cast<int32_t*>(p + off);
@@ -1477,7 +1486,7 @@ int gemm_prepare(const oes_routed_experts* v, const uint16_t* x, int T, int k,
   OES_REQUIRE(H >= 64 && I >= 64 && H % 64 == 0 && I % 64 == 0 && H <= 16384 && I <= 16384,
               "moe_grouped_gemm_slots: H=%d I=%d must be multiples of 64 in [64, 16384]", H, I);
   OES_REQUIRE(v->wfmt == OES_WFMT_BF16 || v->wfmt == OES_WFMT_NVFP4 ||
-                  v->wfmt == OES_WFMT_NVFP4_W4A4,
+                  v->wfmt == OES_WFMT_NVFP4_W4A4 || v->wfmt == OES_WFMT_FP8,
               "moe_grouped_gemm_slots: bad wfmt");
   OES_REQUIRE(v->wfmt != OES_WFMT_NVFP4_W4A4 || (v->input_scale13 && v->input_scale2),
               "moe_grouped_gemm_slots: W4A4 needs the layer's input scales in the view");
@@ -1502,6 +1511,7 @@ int gemm_prepare(const oes_routed_experts* v, const uint16_t* x, int T, int k,
   const int64_t cap = OES_ALIGN_CAPACITY(R, E, B);
   const Sections sec = sections(v->wfmt, H, I);
   const uint8_t* pool = static_cast<const uint8_t*>(v->pool);
+  g->fp8 = v->wfmt == OES_WFMT_FP8;
   const int wf = v->wfmt != OES_WFMT_BF16;
   const int a4 = v->wfmt == OES_WFMT_NVFP4_W4A4;
   g->wf = wf;
@@ -1523,15 +1533,36 @@ int gemm_prepare(const oes_routed_experts* v, const uint16_t* x, int T, int k,
   g->in2 = v->input_scale2;
   g->status = status;
   if (wf) xb = ws.x16;
-  const CUtensorMapDataType t16 = wf ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  {
-    const uint64_t dims[2] = {(uint64_t)I, (uint64_t)cap};
-    const uint64_t str[1] = {(uint64_t)I * 2};
-    const uint32_t box[2] = {64, (uint32_t)B};
-    if ((rc = encode_tiled(&m2.b, t16, 2, ws.h, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))) return rc;
-  }
   const uint64_t rb = (uint64_t)v->row_bytes;
-  if (!wf) {
+  if (!g->fp8) {
+    const CUtensorMapDataType t16 = wf ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+    {
+      const uint64_t dims[2] = {(uint64_t)I, (uint64_t)cap};
+      const uint64_t str[1] = {(uint64_t)I * 2};
+      const uint32_t box[2] = {64, (uint32_t)B};
+      if ((rc = encode_tiled(&m2.b, t16, 2, ws.h, dims, str, box, CU_TENSOR_MAP_SWIZZLE_128B))) return rc;
+    }
+  }
+  if (g->fp8) {
+    // weights and h in chunks of 128 codes (128 bytes) along K
+    const Fp8Row row = fp8_row(H, I);
+    const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    const uint32_t box[3] = {128, 128, 1}, hbox[2] = {128, (uint32_t)B};
+    const uint64_t d1[3] = {(uint64_t)H, (uint64_t)2 * I, (uint64_t)S}, s1[2] = {(uint64_t)H, rb};
+    if ((rc = encode_tiled(&m1.a, u8, 3, pool, d1, s1, box, CU_TENSOR_MAP_SWIZZLE_128B))) return rc;
+    const uint64_t d2[3] = {(uint64_t)I, (uint64_t)H, (uint64_t)S}, s2[2] = {(uint64_t)I, rb};
+    if ((rc = encode_tiled(&m2.a, u8, 3, pool + row.w2, d2, s2, box, CU_TENSOR_MAP_SWIZZLE_128B)))
+      return rc;
+    const uint64_t dh[2] = {(uint64_t)I, (uint64_t)cap}, sh[1] = {(uint64_t)I};
+    if ((rc = encode_tiled(&m2.b, u8, 2, ws.h, dh, sh, hbox, CU_TENSOR_MAP_SWIZZLE_128B))) return rc;
+    g->f8.xq = reinterpret_cast<const uint8_t*>(ws.x16);
+    g->f8.xs = ws.xs;
+    g->f8.hq = reinterpret_cast<uint8_t*>(ws.h);
+    g->f8.hs = ws.hs;
+    g->f8.w2_off = row.w2;
+    g->f8.s13_off = row.s13;
+    g->f8.s2_off = row.s2;
+  } else if (!wf) {
     const uint32_t box[3] = {64, 128, 1};
     const uint64_t d1[3] = {(uint64_t)H, (uint64_t)2 * I, (uint64_t)S}, s1[2] = {(uint64_t)H * 2, rb};
     if ((rc = encode_tiled(&m1.a, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, pool + sec.w13, d1, s1, box,
@@ -1591,15 +1622,15 @@ int gemm_prepare(const oes_routed_experts* v, const uint16_t* x, int T, int k,
   g->m2 = m2;
   g->p1 = p;
   g->p1.n_mtiles = ceil_div(I, kTileM);
-  g->p1.n_kc = H / kChunkK;
+  g->p1.n_kc = g->fp8 ? ceil_div(H, kQuantGroup) : H / kChunkK;
   g->p2 = p;
   g->p2.n_mtiles = g->tm ? ceil_div(H, 256) : ceil_div(H, kTileM);
-  g->p2.n_kc = I / kChunkK;
+  g->p2.n_kc = g->fp8 ? ceil_div(I, kQuantGroup) : I / kChunkK;
   // GEMM1's K split: when the tiles of the largest routing this chunk can
   // have fill at most half the SMs (a one-token decode), each tile's K range
   // is shared by two CTAs.  Decided from the plan alone, so every launch of
   // a call, and the slot and streamed paths, split alike.
-  const int64_t st = split_tiles(R, E, I, B);
+  const int64_t st = g->fp8 ? 0 : split_tiles(R, E, I, B);
   g->split_tiles = 0;
   if (!g->tm && st > 0 && st * 2 <= num_sms() && g->p1.n_kc >= 2) {
     g->split_tiles = (int)st;
@@ -1612,10 +1643,14 @@ int gemm_prepare(const oes_routed_experts* v, const uint16_t* x, int T, int k,
   return OES_OK;
 }
 
-// The x kernels of a prepared GEMM: the f16 copy of x (NVFP4 weights), or for
-// W4A4 the layer's activation scales and the quantised x.
+// The x kernels of a prepared GEMM: the f16 copy of x (NVFP4 weights), for
+// W4A4 the layer's activation scales and the quantised x, for FP8 the codes
+// and scales of x.
 int gemm_prepare_x(const GemmPlan& g, cudaStream_t stream) {
   if (g.empty || !g.wf) return OES_OK;
+  if (g.fp8)
+    return fp8_quantize(g.x, OES_BF16, g.H, g.T, g.H, OES_ACT_NONE, const_cast<uint8_t*>(g.f8.xq), g.H,
+                        const_cast<float*>(g.f8.xs), stream);
   const int64_t n = (int64_t)g.T * g.H;
   if (g.a4) {
     launch_kernel(act_scale_kernel, 1, 256, 0, stream, g.in13, g.in2, g.E, g.act, g.status);
@@ -1641,6 +1676,7 @@ int gemm_run(const GemmPlan& g, int filter, const uint8_t* flags, const int32_t*
   p1.filter = p2.filter = filter;
   p1.flags = p2.flags = flags;
   p1.gcount = p2.gcount = gcount;
+  if (g.fp8) return fp8_gemm_run(g, p1, p2, stream);
   const int B = p1.BN;
   int rc;
   if (g.tm) rc = g.wf ? launch_gemm_tm<1, 1>(g.m1, p1, stream) : launch_gemm_tm<1, 0>(g.m1, p1, stream);

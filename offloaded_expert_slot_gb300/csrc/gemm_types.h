@@ -43,6 +43,16 @@ struct GemmParams {
   int32_t* status;
 };
 
+// The FP8 format's grouped GEMMs (gemm_fp8.cu): what they need beside
+// GemmParams.  h of the GemmParams holds codes, one byte a value.
+struct Fp8Group {
+  const uint8_t* xq;  // [T, H] codes of x
+  const float* xs;    // [T, ceil(H/128)]
+  uint8_t* hq;        // [cap, I] codes of h
+  float* hs;          // [cap, ceil(I/128)]
+  int64_t w2_off, s13_off, s2_off;  // sections of an expert row
+};
+
 // Everything needed to launch GEMM1 / GEMM2 / combine of one call.
 struct GemmPlan {
   GemmMaps m1, m2;
@@ -52,6 +62,8 @@ struct GemmPlan {
   int32_t* counters;  // GEMM1's split counts
   int n_counters;
   int wf, a4, T, k, H, E;
+  bool fp8;      // OES_WFMT_FP8: gemm_fp8.cu runs the GEMMs
+  Fp8Group f8;
   uint16_t* y;
   const uint16_t* x;        // the chunk's x (bf16)
   uint16_t* x16;            // its 16-bit copy for NVFP4 weights (workspace)
@@ -81,6 +93,16 @@ inline GemmCounters gemm_counters(const GemmPlan& plan) {
 int gemm_run(const GemmPlan& plan, int filter, const uint8_t* flags, const int32_t* gcount,
              cudaStream_t stream);
 int gemm_combine(const GemmPlan& plan, const int32_t* ids, const float* weights, uint16_t* out,
+                 cudaStream_t stream);
+
+
+// Byte offsets of an FP8 expert row's sections and the row's size.
+struct Fp8Row {
+  int64_t w2, s13, s2, end;
+};
+Fp8Row fp8_row(int H, int I);
+// GEMM1 then GEMM2 of a prepared FP8 plan; filter as for gemm_run
+int fp8_gemm_run(const GemmPlan& plan, const GemmParams& p1, const GemmParams& p2,
                  cudaStream_t stream);
 
 }  // namespace oes

@@ -44,6 +44,10 @@ struct oes_expert_source {
 
 namespace oes {
 int tile_plan(int R, int E);
+// moe_fp8_quantize's launch, its arguments checked by the caller.
+int fp8_quantize(const void* x, int dtype, int64_t x_ld, int T, int K, int act, uint8_t* q,
+                 int64_t q_ld, float* scale, cudaStream_t stream);
+
 // moe_align_block_size, which also zeroes nzero int32 words at `zero` (device)
 // in one of its kernels: a composite call clears the GEMM's K-split counters
 // there instead of in a memset of its own.

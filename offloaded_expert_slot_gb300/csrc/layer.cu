@@ -341,7 +341,7 @@ extern "C" int moe_layer_forward_slots(oes_slot_cache* cache, const oes_expert_s
     // over the hits right behind it on the caller's stream; the query's
     // copies on the side stream and each part's copied experts on the gemm
     // stream, as below.
-    if (g.a4 && (rc = gemm_prepare_x(g, stream))) return rc;
+    if ((g.a4 || g.fp8) && (rc = gemm_prepare_x(g, stream))) return rc;
     const float* logits = c->logits;
     if (!logits) {
       if ((rc = moe_gate_logits(c->x, c->gate, T, d->H, E, w.logits, stream))) return rc;
@@ -374,7 +374,7 @@ extern "C" int moe_layer_forward_slots(oes_slot_cache* cache, const oes_expert_s
     a.nzero = sc.n;
     a.status = c->status;
     a.x = c->x;
-    a.x16 = (g.wf && !g.a4) ? g.x16 : nullptr;
+    a.x16 = (g.wf && !g.a4 && !g.fp8) ? g.x16 : nullptr;
     int spad = 2;
     while (spad < cache->S) spad <<= 1;
     const size_t smem =

@@ -1,0 +1,248 @@
+// moe_block_norm: the residual update after a block and the norm before the
+// next one, in one pass over the rows.
+//
+//   v  = y * rsqrt(mean(y^2) + eps) * (offset + w_post)       (or v = y)
+//   r' = residual + residual_scale * gate * v
+//   u  = r' * rsqrt(mean(r'^2) + eps) * (offset + w_pre)      (or u = r')
+//
+// Every sum and product is fp32; r' goes into the second norm unrounded, and
+// the codes are taken from the unrounded u, so each output is rounded once.
+// What bounds it is memory traffic: 8 bytes a value in bf16 (9 with codes)
+// against about a dozen operations.  So a row is read once, kept in registers
+// across both reductions, and written once.
+#include <algorithm>
+
+#include "common.cuh"
+#include "fp8_dev.cuh"
+#include "internal.h"
+
+namespace oes {
+namespace {
+
+constexpr int kMaxH = 16384;
+
+// RT: uint16_t (bf16) or float residual.  Value e of chunk j of a row belongs
+// to thread (j * threads + tid) as value VEC * that + e.  WARP: a warp a row,
+// else a CTA a row.
+template <int VEC, int NV, bool WARP, typename RT>
+__global__ void __launch_bounds__(WARP ? 128 : 1024) block_norm_kernel(const oes_block_norm p) {
+  pdl_begin();
+  __shared__ float red[2][32];
+  __shared__ float gmax[VEC == 1 ? NV : 1][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int nthr = WARP ? 32 : blockDim.x;
+  const int tid = WARP ? lane : threadIdx.x;
+  const int nw = blockDim.x >> 5;
+  const int64_t step = (int64_t)gridDim.x * (WARP ? nw : 1);
+  const float inv_h = 1.0f / (float)p.H;
+  auto row_sum = [&](float s, int which) {
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (WARP) return s;
+    if (lane == 0) red[which][warp] = s;
+    __syncthreads();
+    s = lane < nw ? red[which][lane] : 0.0f;
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s;
+  };
+  for (int64_t row = WARP ? (int64_t)blockIdx.x * nw + warp : blockIdx.x; row < p.T; row += step) {
+    float r[NV][VEC];
+    float v[NV][VEC];
+    const RT* rp = static_cast<const RT*>(p.residual) + row * p.residual_ld;
+    const uint16_t* yp = p.y ? p.y + row * p.y_ld : nullptr;
+    float s = 0.0f;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      const int c = (j * nthr + tid) * VEC;
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) r[j][e] = v[j][e] = 0.0f;
+      if (c < p.H) {
+        load_vals<VEC>(rp + c, r[j]);
+        if (yp) load_vals<VEC>(yp + c, v[j]);
+      }
+    }
+    if (yp) {
+      float k = p.residual_scale;
+      if (p.gate_kind == OES_GATE_TOKEN) {
+        const float g = static_cast<const float*>(p.gate)[row * p.gate_ld];
+        k *= p.gate_sigmoid ? sigmoid_f32(g) : g;
+      }
+      float inv = 1.0f;
+      if (p.post_weight) {
+#pragma unroll
+        for (int j = 0; j < NV; ++j)
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) s = fmaf(v[j][e], v[j][e], s);
+        inv = rsqrtf(row_sum(s, 0) * inv_h + p.eps);
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * nthr + tid) * VEC;
+        if (c >= p.H) continue;
+        if (p.post_weight) {
+          float w[VEC];
+          load_vals<VEC>(p.post_weight + c, w);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) v[j][e] = v[j][e] * inv * (p.weight_offset + w[e]);
+        }
+        if (p.gate_kind == OES_GATE_CHANNEL || p.gate_kind == OES_GATE_ELEMENT) {
+          float g[VEC];
+          load_vals<VEC>(static_cast<const uint16_t*>(p.gate) +
+                             (p.gate_kind == OES_GATE_ELEMENT ? row * p.gate_ld : 0) + c,
+                         g);
+#pragma unroll
+          for (int e = 0; e < VEC; ++e) v[j][e] *= p.gate_sigmoid ? sigmoid_f32(g[e]) : g[e];
+        }
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) r[j][e] = fmaf(k, v[j][e], r[j][e]);
+      }
+    }
+    if (p.out_residual) {
+      RT* op = static_cast<RT*>(p.out_residual) + row * p.out_residual_ld;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * nthr + tid) * VEC;
+        if (c < p.H) store_vals<VEC>(op + c, r[j]);
+      }
+    }
+    if (!p.out && !p.out_q) continue;
+    if (p.pre_weight) {
+      s = 0.0f;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) s = fmaf(r[j][e], r[j][e], s);
+      const float inv = rsqrtf(row_sum(s, 1) * inv_h + p.eps);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * nthr + tid) * VEC;
+        if (c >= p.H) continue;
+        float w[VEC];
+        load_vals<VEC>(p.pre_weight + c, w);
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) r[j][e] = r[j][e] * inv * (p.weight_offset + w[e]);
+      }
+    }
+    if (p.out) {
+      uint16_t* op = p.out + row * p.out_ld;
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * nthr + tid) * VEC;
+        if (c < p.H) store_vals<VEC>(op + c, r[j]);
+      }
+    }
+    if (p.out_q) {
+      uint8_t* qp = p.out_q + row * p.out_q_ld;
+      float* sp = p.out_scale + row * ((p.H + kQuantGroup - 1) / kQuantGroup);
+      float a[NV];
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        a[j] = 0.0f;  // values past H are 0
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) a[j] = fmaxf(a[j], fabsf(r[j][e]));
+        // a group is 16 neighbouring lanes of 8 values, or four warps of one
+#pragma unroll
+        for (int o = VEC == 8 ? 8 : 16; o >= 1; o >>= 1)
+          a[j] = fmaxf(a[j], __shfl_xor_sync(0xffffffffu, a[j], o));
+        if (VEC == 1 && lane == 0) gmax[j][warp] = a[j];
+      }
+      if (VEC == 1) {
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < NV; ++j) {
+          const float* g = gmax[j] + (warp & ~3);
+          a[j] = fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3]));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < NV; ++j) {
+        const int c = (j * nthr + tid) * VEC;
+        if (c >= p.H) continue;
+        const QuantScale qs = quant_scale(a[j]);
+        if constexpr (VEC == 8) {
+          *reinterpret_cast<uint2*>(qp + c) =
+              make_uint2(quant4(r[j][0], r[j][1], r[j][2], r[j][3], qs),
+                         quant4(r[j][4], r[j][5], r[j][6], r[j][7], qs));
+        } else {
+          qp[c] = quant1(r[j][0], qs);
+        }
+        if (c % kQuantGroup == 0) sp[c / kQuantGroup] = qs.s;
+      }
+      if (VEC == 1) __syncthreads();  // gmax is read before the next row's is written
+    }
+  }
+}
+
+template <int VEC, int NV, bool WARP>
+int launch_norm(const oes_block_norm& p, int threads, cudaStream_t stream) {
+  const int rows = WARP ? threads / 32 : 1;
+  const int64_t want = ceil_div64(p.T, rows);
+  // CTAs that can be resident at once, so that each loops over its rows
+  const int grid = (int)std::min<int64_t>(want, (int64_t)num_sms() * std::max(1, 2048 / threads));
+  if (p.dtype == OES_BF16)
+    launch_kernel(block_norm_kernel<VEC, NV, WARP, uint16_t>, grid, threads, 0, stream, p);
+  else
+    launch_kernel(block_norm_kernel<VEC, NV, WARP, float>, grid, threads, 0, stream, p);
+  OES_CHECK_LAUNCH("block_norm_kernel");
+  return OES_OK;
+}
+
+}  // namespace
+}  // namespace oes
+
+using namespace oes;
+
+extern "C" int moe_block_norm(const oes_block_norm* a, oes_stream_t stream) {
+  OES_REQUIRE(a, "moe_block_norm: null arguments");
+  const oes_block_norm& p = *a;
+  OES_REQUIRE(p.T >= 0 && p.H >= 1, "moe_block_norm: bad T=%d H=%d", p.T, p.H);
+  if (p.H > kMaxH) {
+    set_error("moe_block_norm: H=%d is over %d", p.H, kMaxH);
+    return OES_ERR_UNSUPPORTED;
+  }
+  OES_REQUIRE(p.dtype == OES_BF16 || p.dtype == OES_F32, "moe_block_norm: bad dtype %d", p.dtype);
+  OES_REQUIRE(p.gate_kind >= OES_GATE_NONE && p.gate_kind <= OES_GATE_ELEMENT,
+              "moe_block_norm: bad gate_kind %d", p.gate_kind);
+  OES_REQUIRE(p.eps >= 0.0f, "moe_block_norm: eps must not be negative");
+  OES_REQUIRE(p.out_residual || p.out || p.out_q, "moe_block_norm: no output");
+  OES_REQUIRE((p.out_q == nullptr) == (p.out_scale == nullptr),
+              "moe_block_norm: out_q and out_scale go together");
+  OES_REQUIRE(p.y || (!p.post_weight && p.gate_kind == OES_GATE_NONE),
+              "moe_block_norm: post_weight and gate need y");
+  OES_REQUIRE((p.gate != nullptr) == (p.gate_kind != OES_GATE_NONE),
+              "moe_block_norm: gate and gate_kind disagree");
+  if (p.T == 0) return OES_OK;
+  OES_REQUIRE(p.residual, "moe_block_norm: null residual");
+  const bool elem = p.gate_kind == OES_GATE_ELEMENT;
+  OES_REQUIRE(p.residual_ld >= p.H && (!p.y || p.y_ld >= p.H) && (!elem || p.gate_ld >= p.H) &&
+                  (p.gate_kind != OES_GATE_TOKEN || p.gate_ld >= 1) &&
+                  (!p.out_residual || p.out_residual_ld >= p.H) && (!p.out || p.out_ld >= p.H) &&
+                  (!p.out_q || p.out_q_ld >= p.H),
+              "moe_block_norm: a row stride is smaller than its row");
+  const uintptr_t ra = p.dtype == OES_BF16 ? 2 : 4;
+  auto at = [](const void* q, uintptr_t n) { return ((uintptr_t)q & (n - 1)) == 0; };
+  OES_REQUIRE(at(p.residual, ra) && at(p.out_residual, ra) && at(p.y, 2) && at(p.post_weight, 2) &&
+                  at(p.pre_weight, 2) && at(p.gate, p.gate_kind == OES_GATE_TOKEN ? 4 : 2) &&
+                  at(p.out, 2) && at(p.out_scale, 4),
+              "moe_block_norm: a pointer is not aligned to its type");
+  // rows of 8 values a load when every row and weight is aligned for it
+  const int64_t rm = 16 / (int64_t)ra;
+  const bool vec = p.H % 8 == 0 && at(p.residual, 16) && p.residual_ld % rm == 0 &&
+                   (!p.y || (at(p.y, 16) && p.y_ld % 8 == 0)) && at(p.post_weight, 16) &&
+                   at(p.pre_weight, 16) && (p.gate_kind < OES_GATE_CHANNEL || at(p.gate, 16)) &&
+                   (!elem || p.gate_ld % 8 == 0) &&
+                   (!p.out_residual || (at(p.out_residual, 16) && p.out_residual_ld % rm == 0)) &&
+                   (!p.out || (at(p.out, 16) && p.out_ld % 8 == 0)) &&
+                   (!p.out_q || (at(p.out_q, 8) && p.out_q_ld % 8 == 0));
+  auto up = [](int n, int m) { return (n + m - 1) / m * m; };
+  if (vec) {
+    const int c = p.H / 8;
+    if (c <= 32) return launch_norm<8, 1, true>(p, 128, stream);
+    if (c <= 64) return launch_norm<8, 2, true>(p, 128, stream);
+    if (c <= 1024) return launch_norm<8, 1, false>(p, up(c, 32), stream);
+    return launch_norm<8, 2, false>(p, up(ceil_div(c, 2), 32), stream);
+  }
+  if (p.H <= 4096) return launch_norm<1, 4, false>(p, up(ceil_div(p.H, 4), 128), stream);
+  return launch_norm<1, 16, false>(p, up(ceil_div(p.H, 16), 128), stream);
+}

@@ -28,7 +28,7 @@ import math
 import numpy as np
 import torch
 
-from .configs import LayerConfig, expert_row_bytes, nvfp4_offsets
+from .configs import LayerConfig, expert_row_bytes, fp8_offsets, nvfp4_offsets
 
 WEIGHT_STD = 0.02
 
@@ -143,6 +143,24 @@ def quantize_nvfp4(w: torch.Tensor):
     return packed.contiguous(), sc_bytes, gs.to(torch.float32)
 
 
+# ---------------------------------------------------------------- FP8 encoder
+def quantize_fp8_blocks(w: torch.Tensor):
+    """Encode w [..., N, K] fp32 as e4m3 with one fp32 scale for each 128 x 128
+    block (amax / 448; 1 for an all-zero block; short blocks at the ends).
+
+    Returns (codes [..., N, K] u8, scales [..., ceil(N/128), ceil(K/128)] fp32).
+    """
+    N, K = w.shape[-2:]
+    nb, kb = -(-N // 128), -(-K // 128)
+    p = torch.nn.functional.pad(w, (0, kb * 128 - K, 0, nb * 128 - N))
+    p = p.reshape(*w.shape[:-2], nb, 128, kb, 128)
+    s = p.abs().amax(dim=(-3, -1)) / 448.0
+    s = torch.where(s > 0, s, torch.ones_like(s))
+    q = (p / s[..., :, None, :, None]).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    q = q.view(torch.uint8).reshape(*w.shape[:-2], nb * 128, kb * 128)[..., :N, :K]
+    return q.contiguous(), s.contiguous()
+
+
 # ---------------------------------------------------------------- expert source
 def _expert_generator(cfg: LayerConfig, layer: int, e: int, device) -> torch.Generator:
     g = torch.Generator(device=device)
@@ -156,7 +174,8 @@ def expert_rows(cfg: LayerConfig, layer: int, experts, device="cpu") -> torch.Te
     seeded generator, so any subset can be regenerated on its own.
 
     Weights ~ N(0, 0.02) drawn as fp32 and rounded to bf16; NVFP4 rows encode
-    those bf16 values (see module docstring).
+    those bf16 values (see module docstring), FP8 rows too (one scale for each
+    128 x 128 block).
     """
     E, H, I = cfg.E, cfg.H, cfg.I
     rb = expert_row_bytes(cfg.wfmt, H, I)
@@ -172,6 +191,14 @@ def expert_rows(cfg: LayerConfig, layer: int, experts, device="cpu") -> torch.Te
     if cfg.wfmt == "bf16":
         rows[:, : 2 * I * H * 2] = w13.reshape(n, -1).view(torch.uint8)
         rows[:, 2 * I * H * 2:] = w2.reshape(n, -1).view(torch.uint8)
+    elif cfg.wfmt == "fp8":
+        o = fp8_offsets(H, I)
+        rows.zero_()
+        q13, s13 = quantize_fp8_blocks(w13.to(torch.float32).reshape(n, 2, I, H))
+        q2, s2 = quantize_fp8_blocks(w2.to(torch.float32))
+        for name, part in (("w13q", q13), ("w2q", q2), ("w13s", s13), ("w2s", s2)):
+            part = part.reshape(n, -1).view(torch.uint8)
+            rows[:, o[name]:o[name] + part.shape[1]] = part
     else:
         scale_in = 0.0
         if cfg.layer_input_scales:

@@ -22,7 +22,10 @@ from . import build as _build
 
 OES_OK, OES_ERR_INVALID_ARG, OES_ERR_UNSUPPORTED, OES_ERR_CUDA, OES_ERR_CAPACITY = range(5)
 OES_DEV_CAPACITY, OES_DEV_BAD_ID, OES_DEV_TIMEOUT = 1, 2, 4
-OES_WFMT_BF16, OES_WFMT_NVFP4, OES_WFMT_NVFP4_W4A4 = 0, 1, 2
+OES_WFMT_BF16, OES_WFMT_NVFP4, OES_WFMT_NVFP4_W4A4, OES_WFMT_FP8 = 0, 1, 2, 3
+OES_F32, OES_BF16 = 0, 1
+OES_ACT_NONE, OES_ACT_SWIGLU = 0, 1
+OES_GATE_NONE, OES_GATE_TOKEN, OES_GATE_CHANNEL, OES_GATE_ELEMENT = 0, 1, 2, 3
 OES_LOGITS_F32, OES_LOGITS_BF16 = 0, 1
 OES_POLICY_LRU, OES_POLICY_LRFU = 0, 1
 OES_LRFU_MAX_K = 18
@@ -62,6 +65,17 @@ class Chunk(C.Structure):
 class LayerDesc(C.Structure):
     _fields_ = [("E", C.c_int), ("H", C.c_int), ("I", C.c_int), ("wfmt", C.c_int),
                 ("input_scale13", C.c_void_p), ("input_scale2", C.c_void_p)]
+
+
+class BlockNorm(C.Structure):
+    _fields_ = [("T", C.c_int), ("H", C.c_int), ("dtype", C.c_int), ("gate_kind", C.c_int),
+                ("gate_sigmoid", C.c_int), ("residual_scale", C.c_float),
+                ("weight_offset", C.c_float), ("eps", C.c_float), ("residual", C.c_void_p),
+                ("residual_ld", C.c_int64), ("y", C.c_void_p), ("y_ld", C.c_int64),
+                ("post_weight", C.c_void_p), ("pre_weight", C.c_void_p), ("gate", C.c_void_p),
+                ("gate_ld", C.c_int64), ("out_residual", C.c_void_p),
+                ("out_residual_ld", C.c_int64), ("out", C.c_void_p), ("out_ld", C.c_int64),
+                ("out_q", C.c_void_p), ("out_q_ld", C.c_int64), ("out_scale", C.c_void_p)]
 
 
 _lib = None
@@ -109,6 +123,9 @@ _SIGS = {
     "oes_stage_plan_layer": (_i, [_vp, _i, C.POINTER(_i), _vp, C.POINTER(_i)]),
     "moe_layers_forward_staged": (_i, [_vp, _vp, _vp, C.POINTER(LayerDesc), C.POINTER(Chunk), _vp,
                                        _vp]),
+    "moe_fp8_quantize": (_i, [_vp, _i, _i64, _i, _i, _i, _vp, _i64, _vp, _vp]),
+    "moe_fp8_gemm": (_i, [_vp, _i64, _vp, _i, _i, _vp, _i64, _vp, _i, _vp, _i, _i64, _vp, _vp]),
+    "moe_block_norm": (_i, [C.POINTER(BlockNorm), _vp]),
     "moe_layer_forward": (_i, [_vp, _vp, _vp, _vp, _i, C.POINTER(LayerDesc), C.POINTER(Chunk), _i,
                                _i, _vp, _vp, C.POINTER(_i)]),
 }
@@ -318,6 +335,51 @@ def moe_grouped_gemm_slots(view: RoutedExperts, x, T, k, ids, weights, sorted_id
     _call("moe_grouped_gemm_slots", C.byref(view), _ptr(x), T, k, _ptr(ids), _ptr(weights),
           _ptr(sorted_ids), _ptr(block_expert), _ptr(n_post_pad), B, _ptr(workspace),
           workspace_bytes, _ptr(out), _ptr(status), _stream(stream))
+
+
+# --------------------------------------------- 8-bit rows and block norms
+def _elem_type(a, func, dtype):
+    """OES_F32 / OES_BF16 of an array (bf16 or 16-bit bit patterns), unless dtype says which."""
+    if dtype is not None:
+        return dtype
+    name = str(getattr(a, "dtype", "")).replace("torch.", "")
+    if name == "float32":
+        return OES_F32
+    if name in ("bfloat16", "int16", "uint16"):
+        return OES_BF16
+    raise TypeError(f"{func}: expected fp32 or bf16 (bit patterns), or dtype=; got {name or type(a)!r}")
+
+
+def moe_fp8_quantize(x, x_ld, T, K, act, q, q_ld, scale, stream=None, dtype=None):
+    """dtype: OES_F32 or OES_BF16 of x, or None to take it from the array."""
+    _call("moe_fp8_quantize", _ptr(x), _elem_type(x, "moe_fp8_quantize", dtype), x_ld, T, K, act,
+          _ptr(q), q_ld, _ptr(scale), _stream(stream))
+
+
+def moe_fp8_gemm(xq, xq_ld, xs, T, K, wq, wq_ld, ws, N, out, out_ld, status=None, stream=None,
+                 dtype=None):
+    """dtype: OES_F32 or OES_BF16 of out, or None to take it from the array."""
+    _call("moe_fp8_gemm", _ptr(xq), xq_ld, _ptr(xs), T, K, _ptr(wq), wq_ld, _ptr(ws), N, _ptr(out),
+          _elem_type(out, "moe_fp8_gemm", dtype), out_ld, _ptr(status), _stream(stream))
+
+
+def block_norm(T, H, residual, residual_ld=None, y=None, y_ld=None, post_weight=None,
+               pre_weight=None, gate=None, gate_kind=OES_GATE_NONE, gate_ld=0, gate_sigmoid=False,
+               residual_scale=1.0, weight_offset=0.0, eps=1e-6, out_residual=None,
+               out_residual_ld=None, out=None, out_ld=None, out_q=None, out_q_ld=None,
+               out_scale=None, dtype=None) -> BlockNorm:
+    """Arguments of moe_block_norm; strides default to H.  The structure holds
+    addresses only: keep the tensors alive while it is used."""
+    ld = lambda v: H if v is None else int(v)  # noqa: E731
+    return BlockNorm(T, H, _elem_type(residual, "block_norm", dtype), gate_kind,
+                     int(bool(gate_sigmoid)), residual_scale, weight_offset, eps, _ptr(residual),
+                     ld(residual_ld), _ptr(y), ld(y_ld), _ptr(post_weight), _ptr(pre_weight),
+                     _ptr(gate), int(gate_ld), _ptr(out_residual), ld(out_residual_ld), _ptr(out),
+                     ld(out_ld), _ptr(out_q), ld(out_q_ld), _ptr(out_scale))
+
+
+def moe_block_norm(args: BlockNorm, stream=None):
+    _call("moe_block_norm", C.byref(args), _stream(stream))
 
 
 # ------------------------------------------------------------- whole layer
