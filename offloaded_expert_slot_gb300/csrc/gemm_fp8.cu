@@ -1,186 +1,854 @@
-// Matrix products of e4m3 codes with block scales: moe_fp8_gemm, and the
-// grouped SwiGLU expert GEMM of moe_grouped_gemm_slots for the FP8 format.
+// Matrix products of e4m3 codes with block scales, on tcgen05 / TMEM / TMA:
+// moe_fp8_gemm, and the grouped SwiGLU expert GEMM of moe_grouped_gemm_slots
+// for the FP8 format.
 //
 //   out[t, n] = sum_b xs[t, b] ws[n / 128, b] sum_{k in b} x[t, k] w[n, k]
 //
-// over blocks b of 128 along K: the products of codes of one block are summed
-// in fp32, scaled, and added to an fp32 accumulator, block after block.
-#include <cuda_fp16.h>
-
+// over blocks b of 128 along K.  The scales are fp32 numbers, so they cannot
+// go into the MMA: the tensor core sums the products of one block (four MMAs
+// of K = 32, fp32 in tensor memory) and the epilogue warps scale each block's
+// sums and add them to fp32 registers, block after block.  A block's sums go
+// to one of several TMEM buffers, so that the MMAs of the next blocks run
+// while the warps drain this one.
+//
+// Two kernels share this; MODE 0 is the dense product, MODE 1 the experts'
+// gate and up products with SwiGLU and h's codes, MODE 2 their down product.
+//   token-major: 128 rows x 256 weight rows a tile, for work bound by
+//     arithmetic: a block is 512 cycles of MMA, against about 270 issue slots
+//     a scheduler to drain it.
+//   weight-major: 128 weight rows x 16 or 64 rows a tile, for few rows, bound
+//     by the stream of weights.  When the tiles do not fill the GPU, the CTAs
+//     of a cluster share a tile's K range and add their sums over distributed
+//     shared memory in a fixed order.
 #include <algorithm>
 
 #include "common.cuh"
 #include "fp8_dev.cuh"
 #include "gemm_types.h"
+#include "gemm_units.cuh"
 #include "internal.h"
 
 namespace oes {
 namespace {
 
-// One launch of the product, dense or grouped.
-struct Fp8Args {
-  GemmParams g;      // grouped: the routing tables, E, S, H, I, ...
-  const uint8_t* x;  // codes of the rows (x, or h)
-  int64_t x_ld;
-  const float* xs;   // [rows, nkb]
-  const uint8_t* w;  // dense: codes [N, K]; grouped: section of the expert row 0
-  int64_t w_ld;
-  const float* ws;   // dense: [ceil(N/128), nkb]; grouped: section of expert row 0
-  int T, N, K, nkb;  // T: dense rows
-  void* out;         // MODE 0: [T, N]; MODE 1: codes of h; MODE 2: y
-  int64_t out_ld;
-  int out_f32;
-  float* hs;  // MODE 1: scales of h
+constexpr int kBlkK = 128;                 // codes (bytes) of K a pipeline stage holds
+constexpr int kTileBytes = kTileM * kBlkK;  // 128 rows of one stage
+constexpr int kEpiW0 = 4;                  // first epilogue warp
+
+struct Fp8Maps {
+  CUtensorMap w;  // weights [slots][rows][K], box 128 x 128
+  CUtensorMap x;  // MODE 0: x [T][K]; MODE 2: h [cap][I]
 };
 
-__device__ __forceinline__ void e4m3x4_f32(uint32_t w, float (&f)[4]) {
-  uint32_t lo, hi;
-  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
-      : "=r"(lo), "=r"(hi)
-      : "r"(w));
-  const float2 a = __half22float2(*reinterpret_cast<__half2*>(&lo));
-  const float2 b = __half22float2(*reinterpret_cast<__half2*>(&hi));
-  f[0] = a.x; f[1] = a.y; f[2] = b.x; f[3] = b.y;
+struct Fp8Params {
+  GemmParams g;      // grouped: routing tables and sizes; dense: status
+  const uint8_t* x;  // MODE 1: codes of x, gathered
+  const float* xs;   // scales of the rows of x (MODE 2: of h) [rows, nkb]
+  const float* ws;   // dense: block scales of w; grouped: those of the pool's row 0
+  int T, N, K, nkb;  // dense rows; weight rows (MODE 1: of gate, = I); K; blocks of K
+  int mt, nt;        // dense: row tiles, weight tiles
+  void* out;         // MODE 0 out, MODE 1 codes of h, MODE 2 y
+  int64_t out_ld;
+  int out_f32, vec;  // dense: type of out; its rows take 16-byte stores
+  float* hs;         // MODE 1: scales of h
+  int ks, ns;        // CTAs that share a tile's K range; pipeline stages
+};
+
+// One unit of work: tile m of the weights against rows block b.
+template <int MODE>
+__device__ __forceinline__ Unit unit_of(const Fp8Params& p, const UnitRec* tab, int idx, int u, int nb,
+                                        int rows) {
+  if (MODE == 0) {
+    // row tiles fastest: the CTAs of a wave share a few weight tiles and
+    // read x from L2
+    Unit t;
+    t.b = u % p.mt;
+    t.m = u / p.mt;
+    t.h = 0;
+    t.slot = 0;
+    t.nvalid = min(rows, p.T - t.b * rows);
+    t.skip = false;
+    return t;
+  }
+  return my_unit<MODE == 2>(p.g, tab, idx, u, nb);
 }
 
-// The plain kernel: a CTA computes 16 rows x 128 columns on the FP32 units,
-// one 128-block of K at a time through shared memory.
-// MODE 0 dense, 1 gate and up with SwiGLU and h's codes, 2 down.
-constexpr int kRows = 16;
+// Fills the CTA's unit table (grouped) and returns the number of units.
 template <int MODE>
-__global__ void __launch_bounds__(256) fp8_simple_kernel(const Fp8Args a) {
+__device__ __forceinline__ int unit_table(const Fp8Params& p, UnitRec* utab, int* s_scan, int worker,
+                                          int nworkers, int* nb_out) {
+  if (MODE == 0) return p.mt * p.nt;
+  const GemmParams& g = p.g;
+  const int nb = ld_tab<MODE == 2>(g.n_post_pad) / g.BN;
+  *nb_out = nb;
+  if (g.filter) {
+    const int dense = fill_filtered_units<MODE == 2>(g, nb, utab, s_scan, worker, nworkers);
+    if (dense >= 0) return dense;
+  }
+  const int total = nb * g.n_mtiles;
+  for (int i = threadIdx.x; i < kMaxUnitsPerCta; i += blockDim.x) {
+    const int u = worker + i * nworkers;
+    if (u >= total) break;
+    const Unit t = unit_info<MODE == 2>(g, u, nb);
+    utab[i] = UnitRec{t.b, t.m, t.slot, t.nvalid};
+  }
+  return total;
+}
+
+__device__ __forceinline__ const float* scales_of(const Fp8Params& p, int slot) {
+  return reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(p.ws) + (int64_t)slot * p.g.row_bytes);
+}
+
+// D[tmem] (+)= A[smem] * B[smem]^T, kind::f8f6f4 (e4m3 inputs, fp32 sums)
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
+                                          uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, "
+      "p; }" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// e4m3 x e4m3 -> fp32, both K-major, shape M x N
+__device__ __forceinline__ uint32_t idesc_f8(uint32_t M, uint32_t N) {
+  return (1u << 4) | ((N >> 3) << 17) | ((M >> 4) << 24);
+}
+// 32 lanes x 32 columns
+__device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+      "%12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, "
+      "%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+        "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+        "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]),
+        "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+        "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(taddr)
+      : "memory");
+}
+// 16 bytes global -> shared, or 16 zero bytes
+__device__ __forceinline__ void cp_async16_or_zero(uint32_t dst_smem, const void* src, bool take) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "r"(take ? 16 : 0)
+               : "memory");
+}
+__device__ __forceinline__ void named_bar(int id, int threads) {
+  asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
+// ----- clusters: a shared address of another CTA, and its barriers
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
+  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, int32_t* status) {
+  for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 "
+        "%0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (i > 64) __nanosleep(32);
+  }
+  set_status(status, OES_DEV_TIMEOUT);
+  return false;
+}
+__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+
+// ============================================================ token-major
+constexpr int kTmN = 256;  // weight rows a tile (MODE 1: 128 gate + 128 up)
+constexpr int kTmStage = (kTmN + kTileM) * kBlkK;
+constexpr int kTmEpi = 8;     // epilogue warps: two a TMEM lane quarter, 128 columns each
+constexpr int kTmGatherW0 = kEpiW0 + kTmEpi;
+__host__ __device__ constexpr int tm_threads(int mode) { return mode == 1 ? 512 : 384; }
+
+// Registers: the launch gives every thread 65536 / threads; the epilogue
+// warps (128 sums each) take what the other warpgroups give back.
+// MODE 1: 512 x 128 = 128 (56 + 2 x 200 + 56).  Else 384 x 168 = 128 (72 + 2 x 216).
+template <int MODE>
+__global__ void __launch_bounds__(tm_threads(MODE), 1)
+    fp8_tm_kernel(const __grid_constant__ Fp8Maps maps, const Fp8Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint64_t* full = reinterpret_cast<uint64_t*>(stages + p.ns * kTmStage);
+  uint64_t* empty = full + p.ns;
+  uint64_t* tfull = empty + p.ns;
+  uint64_t* tempty = tfull + 2;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tempty + 2);
+  UnitRec* utab = reinterpret_cast<UnitRec*>(tmem_holder + 4);
+  __shared__ int s_scan[33];
+  __shared__ float s_amax[2][2][kTileM];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int32_t* status = p.g.status;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.ns; ++s) {
+      // the weights' TMA, and the rows' TMA or gather threads
+      mbar_init(&full[s], 1 + (MODE == 1 ? 128 : 1));
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], kTmEpi);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.w);
+    if (MODE != 1) tma_prefetch_desc(&maps.x);
+  }
   pdl_wait();
-  constexpr int kW = MODE == 1 ? 2 : 1;
-  __shared__ uint32_t sx[kRows][33];
-  __shared__ uint32_t sw[kW][32][129];  // [k / 4][column]
-  __shared__ int s_row[kRows];          // row of x, or -1
-  __shared__ int s_out[kRows];          // row of the output
-  const int ntiles = (a.N + 127) / 128;
-  const int tile = blockIdx.x % ntiles, piece = blockIdx.x / ntiles;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint8_t* w = a.w;
-  const float* ws = a.ws;
-  if (MODE == 0) {
-    if (tid < kRows) {
-      const int t = piece * kRows + tid;
-      s_row[tid] = s_out[tid] = t < a.T ? t : -1;
-    }
-  } else {
-    const GemmParams& g = a.g;
-    const int b = piece / (g.BN / kRows), off = piece % (g.BN / kRows) * kRows;
-    if (b >= *g.n_post_pad / g.BN) return;
-    const int e = g.block_expert[b];
-    if (e < 0 || e >= g.E) return;
-    if (g.filter && g.flags[e] != g.filter) return;
-    const int slot = g.e2s[e];
-    const bool bad = slot < 0 || slot >= g.S;
-    if (tid < kRows) {
-      const int64_t i = (int64_t)b * g.BN + off + tid;
-      const int r = g.sorted_ids[i];
-      s_row[tid] = r < g.R ? (MODE == 1 ? r / g.k : (int)i) : -1;
-      s_out[tid] = r < g.R ? (MODE == 1 ? (int)i : r) : -1;
-    }
-    if (bad) {
-      __syncthreads();
-      if (MODE == 2) {
-        for (int i = tid; i < kRows * 128; i += 256) {
-          const int n = tile * 128 + (i & 127);
-          if (s_out[i >> 7] >= 0 && n < a.N)
-            static_cast<uint16_t*>(a.out)[(int64_t)s_out[i >> 7] * a.out_ld + n] = 0;
-        }
-        if (tid == 0 && s_out[0] >= 0) set_status(g.status, OES_DEV_BAD_ID);
-      }
-      return;
-    }
-    w += (int64_t)slot * g.row_bytes;
-    ws = reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(ws) + (int64_t)slot * g.row_bytes);
+  if (MODE != 0 && p.g.filter && p.g.gcount && p.g.gcount[p.g.filter] == 0) return;
+  int nb = 0;
+  const int total = unit_table<MODE>(p, utab, s_scan, blockIdx.x, gridDim.x, &nb);
+  __syncthreads();
+  if ((int)blockIdx.x >= total) return;
+  if (warp == 2) {
+    tmem_alloc(tmem_holder, 512);
+    tmem_relinquish();
+    tc_fence_before();
   }
   __syncthreads();
-  float acc[kW][2][4] = {};
-  for (int kb = 0; kb < a.nkb; ++kb) {
-    // K is read four codes a load where that stays inside a row (strides are
-    // multiples of 16), the rest of a block is zero
-    auto word = [&](const uint8_t* row, int k) {
-      uint32_t v = 0;
-      if (k + 4 <= a.K) v = *reinterpret_cast<const uint32_t*>(row + k);
-      else
-        for (int i = 0; i < 4; ++i)
-          if (k + i < a.K) v |= (uint32_t)row[k + i] << (8 * i);
-      return v;
-    };
-    for (int i = tid; i < kRows * 32; i += 256) {
-      const int r = s_row[i >> 5];
-      sx[i >> 5][i & 31] = r >= 0 ? word(a.x + r * a.x_ld, kb * 128 + (i & 31) * 4) : 0u;
-    }
-    for (int i = tid; i < kW * 128 * 32; i += 256) {
-      const int q = i >> 12, c = (i >> 5) & 127, n = tile * 128 + c;
-      sw[q][i & 31][c] = n < a.N ? word(w + ((int64_t)q * a.N + n) * a.w_ld, kb * 128 + (i & 31) * 4) : 0u;
-    }
-    __syncthreads();
-    float part[kW][2][4] = {};
-    for (int k4 = 0; k4 < 32; ++k4) {
-      float xv[2][4];
-      e4m3x4_f32(sx[2 * warp][k4], xv[0]);
-      e4m3x4_f32(sx[2 * warp + 1][k4], xv[1]);
-#pragma unroll
-      for (int q = 0; q < kW; ++q)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          float wv[4];
-          e4m3x4_f32(sw[q][k4][lane + 32 * j], wv);
-#pragma unroll
-          for (int t = 0; t < 2; ++t)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) part[q][t][j] = fmaf(xv[t][i], wv[i], part[q][t][j]);
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+
+  if (warp < kEpiW0) {
+    regs_dec<MODE == 1 ? 56 : 72>();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------- weight producer
+      int s = 0, ph = 0;
+      bool ok = true;
+      for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
+        const Unit t = unit_of<MODE>(p, utab, ui, u, nb, kTileM);
+        if (t.skip) continue;
+        const int ra = t.m * (MODE == 1 ? kTileM : kTmN);
+        const int rb = MODE == 1 ? p.N + ra : ra + kTileM;
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          ok = mbar_wait(&empty[s], ph ^ 1, status);
+          if (!ok) break;
+          uint8_t* W = stages + s * kTmStage;
+          mbar_arrive_expect_tx(&full[s], 2 * kTileBytes);
+          tma_load_3d(W, &maps.w, &full[s], kb * kBlkK, ra, t.slot);
+          tma_load_3d(W + kTileBytes, &maps.w, &full[s], kb * kBlkK, rb, t.slot);
+          if (++s == p.ns) { s = 0; ph ^= 1; }
         }
-    }
+      }
+    } else if (warp == 1 && lane == 0) {
+      // -------------------------------------------------------- MMA issuer
+      int s = 0, ph = 0;
+      uint32_t it = 0;
+      bool ok = true;
+      const uint32_t idesc = idesc_f8(kTileM, kTmN);
+      for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
+        const Unit t = unit_of<MODE>(p, utab, ui, u, nb, kTileM);
+        if (t.skip) continue;
+        for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+          const uint32_t a = it & 1;
+          ok = mbar_wait(&tempty[a], ((it >> 1) & 1) ^ 1, status) && mbar_wait(&full[s], ph, status);
+          if (!ok) break;
+          tc_fence_after();
+          if (MODE == 1) fence_proxy_async_smem();  // cp.async-written rows -> tensor core
+          const uint32_t W = smem_u32(stages + s * kTmStage);
+          const uint64_t wd = smem_desc_sw128(W), xd = smem_desc_sw128(W + 2 * kTileBytes);
 #pragma unroll
-    for (int q = 0; q < kW; ++q) {
-      const float sb = ws[((int64_t)q * ntiles + tile) * a.nkb + kb];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int r = s_row[2 * warp + t];
-        const float sc = r >= 0 ? a.xs[(int64_t)r * a.nkb + kb] * sb : 0.0f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[q][t][j] = fmaf(part[q][t][j], sc, acc[q][t][j]);
+          for (int kk = 0; kk < kBlkK / 32; ++kk)
+            tc_mma_f8(tmem_base + a * kTmN, xd + 2 * kk, wd + 2 * kk, idesc, kk ? 1u : 0u);
+          tc_commit(&empty[s]);
+          tc_commit(&tfull[a]);
+          if (++s == p.ns) { s = 0; ph ^= 1; }
+        }
+      }
+    } else if (MODE != 1 && warp == 3 && lane == 0) {
+      // ------------------------------------------------------ rows producer
+      int s = 0, ph = 0;
+      bool ok = true;
+      for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
+        const Unit t = unit_of<MODE>(p, utab, ui, u, nb, kTileM);
+        if (t.skip) continue;
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          ok = mbar_wait(&empty[s], ph ^ 1, status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&full[s], kTileBytes);
+          tma_load_2d(stages + s * kTmStage + 2 * kTileBytes, &maps.x, &full[s], kb * kBlkK, t.b * kTileM);
+          if (++s == p.ns) { s = 0; ph ^= 1; }
+        }
       }
     }
-    __syncthreads();
+  } else if (warp < kTmGatherW0) {
+    regs_inc<MODE == 1 ? 200 : 216>();
+    // ---------------------------------------------------------- epilogue
+    const int q = warp & 3, half = (warp - kEpiW0) >> 2;
+    const int row = q * 32 + lane;  // TMEM lane = row of the tile
+    const int nwb = (p.N + 127) / 128;  // blocks of weight rows
+    uint32_t it = 0;
+    int par = 0;
+    bool ok = true;
+    for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
+      const Unit t = unit_of<MODE>(p, utab, ui, u, nb, kTileM);
+      const bool live = row < t.nvalid;
+      const int col0 = t.m * kTmN + half * kTileM;  // MODE 0, 2: first column of this warp
+      int r = 0;                                    // row of out (MODE 2: the route)
+      if (MODE == 2 && live) r = p.g.sorted_ids[(int64_t)t.b * p.g.BN + row];
+      if (t.skip) {
+        if (MODE == 2 && live && t.slot != kFiltered) {
+          // an expert without a slot: its routes get zeros (and a status bit)
+          uint16_t* y = static_cast<uint16_t*>(p.out) + (int64_t)r * p.out_ld;
+          for (int c = col0; c < min(col0 + kTileM, p.N); c += 8)
+            *reinterpret_cast<uint4*>(y + c) = make_uint4(0, 0, 0, 0);
+          if (row == 0) set_status(status, OES_DEV_BAD_ID);
+        }
+        continue;
+      }
+      const float* xs = p.xs;
+      if (MODE == 1) {
+        if (live) xs += (int64_t)(p.g.sorted_ids[(int64_t)t.b * p.g.BN + row] / p.g.k) * p.nkb;
+      } else if (live) {
+        xs += ((int64_t)t.b * kTileM + row) * p.nkb;
+      }
+      const float* ws = MODE == 0 ? p.ws : scales_of(p, t.slot);
+      // MODE 1: 64 gate columns and the same 64 up columns, so that a thread
+      // has both factors of its values of h
+      const float* ws0 = ws + (int64_t)(MODE == 1 ? t.m : col0 / 128) * p.nkb;
+      const float* ws1 = ws0 + (int64_t)nwb * p.nkb;
+      const bool on = q * 32 < t.nvalid && (MODE == 1 ? t.m * kTileM + half * 64 : col0) < p.N;
+      float acc[128];
+#pragma unroll
+      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+      float xn = xs[0], wn0 = on ? ws0[0] : 0.0f, wn1 = (MODE == 1 && on) ? ws1[0] : 0.0f;
+      for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+        const uint32_t a = it & 1;
+        const float s0 = xn * wn0, s1 = MODE == 1 ? xn * wn1 : s0;
+        if (kb + 1 < p.nkb && on) {  // the next block's scales
+          xn = xs[kb + 1];
+          wn0 = ws0[kb + 1];
+          if (MODE == 1) wn1 = ws1[kb + 1];
+        }
+        ok = mbar_wait(&tfull[a], (it >> 1) & 1, status);
+        if (!ok) break;
+        tc_fence_after();
+        if (on) {
+          const uint32_t tl = tmem_base + ((uint32_t)(q * 32) << 16) + a * kTmN;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            uint32_t d[32];
+            tmem_ld_32(tl + (MODE == 1 ? (c >> 1) * kTileM + half * 64 + (c & 1) * 32 : half * kTileM + c * 32), d);
+            tc_wait_ld();
+            if (c == 3) {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&tempty[a]);
+            }
+            const float s = c >= 2 ? s1 : s0;
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[c * 32 + j] = fmaf(__uint_as_float(d[j]), s, acc[c * 32 + j]);
+          }
+        } else {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[a]);
+        }
+      }
+      if (!ok) break;
+      if (MODE == 1) {
+        if (q * 32 >= t.nvalid) continue;  // both warps of the quarter
+        // h, the amax of its 128 columns with the other half's warp, codes
+        float m = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 64; ++j) {
+          acc[j] = on ? silu_f32(acc[j]) * acc[64 + j] : 0.0f;
+          m = fmaxf(m, fabsf(acc[j]));
+        }
+        s_amax[par][half][row] = m;
+        named_bar(1 + q, 64);
+        const QuantScale qs = quant_scale(fmaxf(m, s_amax[par][half ^ 1][row]));
+        par ^= 1;
+        if (live) {
+          const int64_t hr = (int64_t)t.b * p.g.BN + row;
+          if (on) {
+            uint8_t* h = static_cast<uint8_t*>(p.out) + hr * p.out_ld + t.m * kTileM + half * 64;
+#pragma unroll
+            for (int j = 0; j < 64; j += 16) {
+              uint32_t w[4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                w[i] = quant4(acc[j + 4 * i], acc[j + 4 * i + 1], acc[j + 4 * i + 2], acc[j + 4 * i + 3], qs);
+              *reinterpret_cast<uint4*>(h + j) = make_uint4(w[0], w[1], w[2], w[3]);
+            }
+          }
+          if (half == 0) p.hs[hr * nwb + t.m] = qs.s;
+        }
+      } else if (live && on) {
+        if (MODE == 0) r = t.b * kTileM + row;
+        if (MODE == 2 || !p.out_f32) {
+          uint16_t* o = static_cast<uint16_t*>(p.out) + (int64_t)r * p.out_ld + col0;
+#pragma unroll
+          for (int j = 0; j < 128; j += 8) {
+            if (col0 + j >= p.N) break;
+            if (MODE == 2 || (p.vec && col0 + j + 8 <= p.N)) {
+              float v[8];
+#pragma unroll
+              for (int i = 0; i < 8; ++i) v[i] = acc[j + i];
+              store_vals<8>(o + j, v);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i)
+                if (col0 + j + i < p.N) o[j + i] = (uint16_t)f32_bf16(acc[j + i]);
+            }
+          }
+        } else {
+          float* o = static_cast<float*>(p.out) + (int64_t)r * p.out_ld + col0;
+#pragma unroll
+          for (int j = 0; j < 128; j += 4) {
+            if (col0 + j >= p.N) break;
+            if (p.vec && col0 + j + 4 <= p.N) {
+              *reinterpret_cast<float4*>(o + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                if (col0 + j + i < p.N) o[j + i] = acc[j + i];
+            }
+          }
+        }
+      }
+    }
+  } else if (MODE == 1) {
+    regs_dec<56>();
+    // ------------------------------------------------------- token gather
+    // thread g copies 16-byte chunk g % 8 of rows g / 8 + 16 j; its copies
+    // arrive on the stage's barrier when they complete.  Bytes past H (its
+    // last block may be half of one) are zeros: a weight's zero there would
+    // not silence a NaN code.
+    const int g = threadIdx.x - kTmGatherW0 * 32;
+    const int c = g & 7, r0 = g >> 3;
+    int s = 0, ph = 0;
+    bool ok = true;
+    for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
+      const Unit t = unit_of<MODE>(p, utab, ui, u, nb, kTileM);
+      if (t.skip) continue;
+      const int n16 = round16(t.nvalid);
+      const uint8_t* src[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int n = r0 + 16 * j;
+        const int tk = n < t.nvalid ? p.g.sorted_ids[(int64_t)t.b * p.g.BN + n] / p.g.k : 0;
+        src[j] = p.x + (int64_t)tk * p.K + c * 16;
+      }
+      for (int kb = 0; kb < p.nkb; ++kb) {
+        if (lane == 0) ok = mbar_wait(&empty[s], ph ^ 1, status);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        const uint32_t X = smem_u32(stages + s * kTmStage + 2 * kTileBytes);
+        const bool in = kb * kBlkK + c * 16 < p.K;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int n = r0 + 16 * j;
+          if (n < n16) cp_async16_or_zero(X + n * kBlkK + ((c ^ (n & 7)) << 4), in ? src[j] + kb * kBlkK : src[j], in);
+        }
+        cp_async_mbar_arrive(&full[s]);
+        if (++s == p.ns) { s = 0; ph ^= 1; }
+      }
+    }
+    cp_async_wait_all();
   }
-#pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int r = s_out[2 * warp + t];
-    if (r < 0) continue;  // the whole warp
-    float h[4], m = 0.0f;
-    if (MODE == 1) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        h[j] = tile * 128 + lane + 32 * j < a.N ? silu_f32(acc[0][t][j]) * acc[kW - 1][t][j] : 0.0f;
-        m = fmaxf(m, fabsf(h[j]));
-      }
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    }
-    const QuantScale qs = quant_scale(m);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = tile * 128 + lane + 32 * j;
-      if (n >= a.N) continue;
-      const int64_t o = (int64_t)r * a.out_ld + n;
-      if (MODE == 1) static_cast<uint8_t*>(a.out)[o] = quant1(h[j], qs);
-      else if (MODE == 0 && a.out_f32) static_cast<float*>(a.out)[o] = acc[0][t][j];
-      else static_cast<uint16_t*>(a.out)[o] = (uint16_t)f32_bf16(acc[0][t][j]);
-    }
-    if (MODE == 1 && lane == 0) a.hs[(int64_t)r * ntiles + tile] = qs.s;
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
   }
 }
 
+// =========================================================== weight-major
+// BN rows a tile (16, or 64 for the dense product).  Warps: 0 weights, 1 MMA,
+// 2 TMEM, 3 rows (TMA), 4-7 epilogue, 8-11 token gather (MODE 1).
+constexpr int kWmAcc = 4;  // TMEM buffers
+__host__ __device__ constexpr int wm_threads(int mode) { return mode == 1 ? 384 : 256; }
+__host__ __device__ constexpr int wm_stage(int mode, int BN) {
+  return (mode == 1 ? 2 : 1) * kTileBytes + BN * kBlkK;
+}
+
+template <int MODE, int BN>
+__global__ void __launch_bounds__(wm_threads(MODE), 1)
+    fp8_wm_kernel(const __grid_constant__ Fp8Maps maps, const Fp8Params p) {
+  constexpr int kA = MODE == 1 ? 2 : 1;  // weight tiles a stage (gate and up)
+  constexpr int kStage = wm_stage(MODE, BN);
+  constexpr uint32_t kCols = kWmAcc * kA * BN;  // TMEM columns: 64, 128 or 256
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages =
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  float* red = reinterpret_cast<float*>(stages + p.ns * kStage);  // ks > 1: [kA][ks][BN / ks][128]
+  uint64_t* full = reinterpret_cast<uint64_t*>(red + (p.ks > 1 ? kA * BN * kTileM : 0));
+  uint64_t* empty = full + p.ns;
+  uint64_t* tfull = empty + p.ns;
+  uint64_t* tempty = tfull + kWmAcc;
+  uint64_t* rfull = tempty + kWmAcc;  // [4]: a warp's sums of every CTA of the cluster are in
+  uint64_t* rempty = rfull + 4;       // [4]: every CTA has read what this warp sent
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(rempty + 4);
+  UnitRec* utab = reinterpret_cast<UnitRec*>(tmem_holder + 4);
+  __shared__ int s_scan[33];
+  __shared__ float s_amax[2][4][BN];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  int32_t* status = p.g.status;
+  // the CTAs of a cluster have neighbouring block indices
+  const int ks = p.ks, rank = (int)blockIdx.x % ks;
+  const int worker = (int)blockIdx.x / ks, nworkers = (int)gridDim.x / ks;
+  const int k_lo = rank * p.nkb / ks, k_hi = (rank + 1) * p.nkb / ks;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < p.ns; ++s) {
+      mbar_init(&full[s], 1 + (MODE == 1 ? 128 : 1));
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < kWmAcc; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 4);
+    }
+    for (int w = 0; w < 4; ++w) {
+      mbar_init(&rfull[w], ks);
+      mbar_init(&rempty[w], ks);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.w);
+    if (MODE != 1) tma_prefetch_desc(&maps.x);
+  }
+  // The down product is launched while the gate and up product runs (which
+  // releases it after its set-up): all it reads but h was complete before
+  // that kernel passed this wait, so it builds its unit table and streams its
+  // first weights now, and only what reads h waits (below).
+  if (MODE != 2) pdl_wait();
+  if (MODE != 0 && p.g.filter && p.g.gcount && ld_tab<MODE == 2>(p.g.gcount + p.g.filter) == 0) return;
+  int nb = 0;
+  const int total = unit_table<MODE>(p, utab, s_scan, worker, nworkers, &nb);
+  __syncthreads();
+  if (worker >= total) return;  // the whole cluster
+  if (warp == 2) {
+    tmem_alloc(tmem_holder, kCols);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  if (ks > 1) cluster_barrier();  // every CTA's barriers are initialised
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_holder;
+  if (MODE == 1 && total <= 2 * nworkers) pdl_trigger();
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------------------------------------------- weight producer
+      int s = 0, ph = 0;
+      bool ok = true;
+      for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
+        const Unit t = unit_of<MODE>(p, utab, ui, u, nb, BN);
+        if (t.skip) continue;
+        for (int kb = k_lo; kb < k_hi; ++kb) {
+          ok = mbar_wait(&empty[s], ph ^ 1, status);
+          if (!ok) break;
+          uint8_t* W = stages + s * kStage;
+          mbar_arrive_expect_tx(&full[s], kA * kTileBytes);
+          tma_load_3d(W, &maps.w, &full[s], kb * kBlkK, t.m * kTileM, t.slot);
+          if (MODE == 1)
+            tma_load_3d(W + kTileBytes, &maps.w, &full[s], kb * kBlkK, p.N + t.m * kTileM, t.slot);
+          if (++s == p.ns) { s = 0; ph ^= 1; }
+        }
+      }
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      // -------------------------------------------------------- MMA issuer
+      int s = 0, ph = 0;
+      uint32_t it = 0;
+      bool ok = true;
+      for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
+        const Unit t = unit_of<MODE>(p, utab, ui, u, nb, BN);
+        if (t.skip) continue;
+        const uint32_t idesc = idesc_f8(kTileM, round16(t.nvalid));
+        for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
+          const uint32_t a = it % kWmAcc;
+          ok = mbar_wait(&tempty[a], ((it / kWmAcc) & 1) ^ 1, status) && mbar_wait(&full[s], ph, status);
+          if (!ok) break;
+          tc_fence_after();
+          if (MODE == 1) fence_proxy_async_smem();
+          const uint32_t W = smem_u32(stages + s * kStage);
+          const uint64_t wd = smem_desc_sw128(W), xd = smem_desc_sw128(W + kA * kTileBytes);
+          const uint32_t d = tmem_base + a * kA * BN;
+#pragma unroll
+          for (int kk = 0; kk < kBlkK / 32; ++kk) {
+            tc_mma_f8(d, wd + 2 * kk, xd + 2 * kk, idesc, kk ? 1u : 0u);
+            if (MODE == 1)
+              tc_mma_f8(d + BN, wd + (kTileBytes >> 4) + 2 * kk, xd + 2 * kk, idesc, kk ? 1u : 0u);
+          }
+          tc_commit(&empty[s]);
+          tc_commit(&tfull[a]);
+          if (++s == p.ns) { s = 0; ph ^= 1; }
+        }
+      }
+    }
+  } else if (warp == 3) {
+    if (MODE != 1 && lane == 0) {
+      // ------------------------------------------------------ rows producer
+      if (MODE == 2) pdl_wait();  // h is the kernel before's output
+      int s = 0, ph = 0;
+      bool ok = true;
+      for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
+        const Unit t = unit_of<MODE>(p, utab, ui, u, nb, BN);
+        if (t.skip) continue;
+        for (int kb = k_lo; kb < k_hi; ++kb) {
+          ok = mbar_wait(&empty[s], ph ^ 1, status);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&full[s], BN * kBlkK);
+          tma_load_2d(stages + s * kStage + kA * kTileBytes, &maps.x, &full[s], kb * kBlkK, t.b * BN);
+          if (++s == p.ns) { s = 0; ph ^= 1; }
+        }
+      }
+    }
+  } else if (warp >= kEpiW0 && warp < kEpiW0 + 4) {
+    // ---------------------------------------------------------- epilogue
+    if (MODE == 2) pdl_wait();  // h's scales
+    const int q = warp & 3;
+    const int row = q * 32 + lane;  // TMEM lane = weight row of the tile
+    const int nwb = (p.N + 127) / 128;
+    const int own = BN / ks;        // columns this CTA finishes, from rank * own
+    uint32_t it = 0, un = 0;
+    bool ok = true;
+    for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
+      const Unit t = unit_of<MODE>(p, utab, ui, u, nb, BN);
+      const int wrow = t.m * kTileM + row;
+      if (t.skip) {
+        if (MODE == 2 && t.nvalid > 0 && t.slot != kFiltered && rank == 0) {
+          // an expert without a slot: its routes get zeros (and a status bit)
+          if (wrow < p.N)
+            for (int n = 0; n < t.nvalid; ++n)
+              static_cast<uint16_t*>(p.out)[(int64_t)p.g.sorted_ids[(int64_t)t.b * p.g.BN + n] * p.out_ld + wrow] = 0;
+          if (row == 0) set_status(status, OES_DEV_BAD_ID);
+        }
+        continue;
+      }
+      // MODE 1, 2: the block's routes, one a lane
+      int sid = 0;
+      if (MODE != 0 && lane < t.nvalid) sid = p.g.sorted_ids[(int64_t)t.b * p.g.BN + lane];
+      const float* ws = MODE == 0 ? p.ws : scales_of(p, t.slot);
+      const float* ws0 = ws + (int64_t)t.m * p.nkb;
+      const float* ws1 = ws0 + (int64_t)nwb * p.nkb;
+      float acc[kA][BN];
+#pragma unroll
+      for (int i = 0; i < kA; ++i)
+#pragma unroll
+        for (int n = 0; n < BN; ++n) acc[i][n] = 0.0f;
+      for (int k0 = k_lo; k0 < k_hi && ok; k0 += 32) {
+        // lane l holds the scales of block k0 + l: of each row, times the weights'
+        const int k = k0 + lane;
+        const bool kin = k < k_hi;
+        const float w0 = kin ? ws0[k] : 0.0f, w1 = (MODE == 1 && kin) ? ws1[k] : 0.0f;
+        float sc[kA][BN];
+#pragma unroll
+        for (int n = 0; n < BN; ++n) {
+          const int tk = MODE == 1 ? __shfl_sync(0xffffffffu, sid, n & 31) / p.g.k : t.b * BN + n;
+          const float x = (n < t.nvalid && kin) ? p.xs[(int64_t)tk * p.nkb + k] : 0.0f;
+          sc[0][n] = x * w0;
+          if (MODE == 1) sc[kA - 1][n] = x * w1;
+        }
+        const int k1 = min(k_hi, k0 + 32);
+        for (int kb = k0; kb < k1; ++kb, ++it) {
+          const uint32_t a = it % kWmAcc;
+          ok = mbar_wait(&tfull[a], (it / kWmAcc) & 1, status);
+          if (!ok) break;
+          tc_fence_after();
+          const uint32_t tl = tmem_base + ((uint32_t)(q * 32) << 16) + a * kA * BN;
+#pragma unroll
+          for (int i = 0; i < kA; ++i)
+#pragma unroll
+            for (int c = 0; c < BN; c += 16) {
+              if (c >= t.nvalid) continue;
+              uint32_t d[16];
+              tmem_ld_16(tl + i * BN + c, d);
+              tc_wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j)
+                acc[i][c + j] = fmaf(__uint_as_float(d[j]), __shfl_sync(0xffffffffu, sc[i][c + j], kb - k0),
+                                     acc[i][c + j]);
+            }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[a]);
+        }
+      }
+      if (!ok) break;
+      if (ks > 1) {
+        // each CTA of the cluster finishes `own` columns: send the others
+        // theirs, then add up this CTA's in rank order
+        ok = mbar_wait_cluster(&rempty[q], (un & 1) ^ 1, status);
+        if (!ok) break;
+        const uint32_t base = smem_u32(red) + row * 4;
+#pragma unroll
+        for (int n = 0; n < BN; ++n) {
+          const int d = n / own, j = n % own;
+#pragma unroll
+          for (int i = 0; i < kA; ++i)
+            if (n < t.nvalid)
+              st_cluster(map_rank(base + (((i * ks + rank) * own + j) * kTileM) * 4, d), acc[i][n]);
+        }
+        fence_cluster();
+        __syncwarp();
+        if (lane < ks) mbar_arrive_cluster(map_rank(smem_u32(&rfull[q]), lane));
+        ok = mbar_wait_cluster(&rfull[q], un & 1, status);
+        if (!ok) break;
+#pragma unroll
+        for (int i = 0; i < kA; ++i)
+#pragma unroll
+          for (int j = 0; j < BN; ++j) {
+            float v = 0.0f;
+            if (j < own && rank * own + j < t.nvalid)
+              for (int r = 0; r < ks; ++r) v += red[((i * ks + r) * own + j) * kTileM + row];
+            acc[i][j] = v;
+          }
+        __syncwarp();
+        if (lane < ks) mbar_arrive_cluster(map_rank(smem_u32(&rempty[q]), lane));
+      }
+      // columns n0 .. n0 + own - 1 of the tile are in acc[..][0 .. own - 1]
+      const int n0 = rank * own;
+      if (MODE == 1) {
+        const bool in = wrow < p.N;
+#pragma unroll
+        for (int j = 0; j < BN; ++j) {
+          if (j >= own) continue;
+          const float h = in && n0 + j < t.nvalid ? silu_f32(acc[0][j]) * acc[kA - 1][j] : 0.0f;
+          acc[0][j] = h;
+          // positive fp32 numbers order like their bits; a NaN takes no part
+          const uint32_t bits = h == h ? __float_as_uint(fabsf(h)) : 0u;
+          const uint32_t m = __reduce_max_sync(0xffffffffu, bits);
+          if (lane == 0) s_amax[un & 1][q][j] = __uint_as_float(m);
+        }
+        named_bar(1, 128);
+#pragma unroll
+        for (int j = 0; j < BN; ++j) {
+          if (j >= own || n0 + j >= t.nvalid) continue;
+          const float(*am)[BN] = s_amax[un & 1];
+          const QuantScale qs = quant_scale(fmaxf(fmaxf(am[0][j], am[1][j]), fmaxf(am[2][j], am[3][j])));
+          const int64_t hr = (int64_t)t.b * p.g.BN + n0 + j;
+          if (in) static_cast<uint8_t*>(p.out)[hr * p.out_ld + wrow] = quant1(acc[0][j], qs);
+          if (row == 0) p.hs[hr * nwb + t.m] = qs.s;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < BN; ++j) {
+          if (j >= own) continue;
+          const int n = n0 + j;
+          const int r = MODE == 2 ? __shfl_sync(0xffffffffu, sid, n & 31) : t.b * BN + n;
+          if (n >= t.nvalid || wrow >= p.N) continue;
+          const int64_t o = (int64_t)r * p.out_ld + wrow;
+          if (MODE == 0 && p.out_f32) static_cast<float*>(p.out)[o] = acc[0][j];
+          else static_cast<uint16_t*>(p.out)[o] = (uint16_t)f32_bf16(acc[0][j]);
+        }
+      }
+      ++un;
+    }
+  } else if (MODE == 1 && warp >= 8) {
+    // -------------------------------------------- token gather (as above)
+    const int g = threadIdx.x - 256;
+    const int c = g & 7, n = g >> 3;
+    int s = 0, ph = 0;
+    bool ok = true;
+    for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
+      const Unit t = unit_of<MODE>(p, utab, ui, u, nb, BN);
+      if (t.skip) continue;
+      const int tk = n < t.nvalid ? p.g.sorted_ids[(int64_t)t.b * p.g.BN + n] / p.g.k : 0;
+      const uint8_t* src = p.x + (int64_t)tk * p.K + c * 16;
+      for (int kb = k_lo; kb < k_hi; ++kb) {
+        if (lane == 0) ok = mbar_wait(&empty[s], ph ^ 1, status);
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        const bool in = kb * kBlkK + c * 16 < p.K;
+        cp_async16_or_zero(smem_u32(stages + s * kStage + kA * kTileBytes) + n * kBlkK + ((c ^ (n & 7)) << 4),
+                           in ? src + kb * kBlkK : src, in);
+        cp_async_mbar_arrive(&full[s]);
+        if (++s == p.ns) { s = 0; ph ^= 1; }
+      }
+    }
+    cp_async_wait_all();
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    tc_fence_after();
+    tmem_dealloc(tmem_base, kCols);
+  }
+  // no CTA leaves while another may still send to it
+  if (ks > 1) cluster_barrier();
+}
+
+// ------------------------------------------------------------------ launches
+constexpr size_t kSmemBudget = 222 * 1024;
+
 template <int MODE>
-int launch_simple(const Fp8Args& a, int64_t pieces, cudaStream_t stream) {
-  const int64_t grid = pieces * ceil_div(a.N, 128);
-  OES_REQUIRE(grid <= 0x7FFFFFFF, "FP8 product: too many tiles");
-  launch_kernel(fp8_simple_kernel<MODE>, dim3((unsigned)grid), 256, 0, stream, a);
-  OES_CHECK_LAUNCH("fp8_simple_kernel");
+int launch_tm(const Fp8Maps& maps, Fp8Params p, cudaStream_t stream) {
+  p.ks = 1;
+  p.ns = 4;
+  const size_t smem = 1024 + (size_t)p.ns * kTmStage + (2 * p.ns + 4) * 8 + 16 + kMaxUnitsPerCta * sizeof(UnitRec);
+  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(fp8_tm_kernel<MODE>), smem,
+                                "fp8_tm_kernel: shared memory limit");
+  if (rc) return rc;
+  const int64_t units = MODE == 0 ? (int64_t)p.mt * p.nt : INT64_MAX;
+  launch_kernel(fp8_tm_kernel<MODE>, (int)std::min<int64_t>(num_sms(), units), tm_threads(MODE), smem, stream, maps, p);
+  OES_CHECK_LAUNCH("fp8_tm_kernel");
+  return OES_OK;
+}
+
+// CTAs that share a tile: the largest of 8, 4, 2, 1 that keeps every tile
+// resident at once and leaves each CTA at least two blocks of K.  units: the
+// most units the launch can have, known on the host.
+int k_shares(int64_t units, int nkb) {
+  for (int ks = 8; ks > 1; ks /= 2)
+    if (units * ks <= num_sms() && nkb >= 2 * ks) return ks;
+  return 1;
+}
+
+template <int MODE, int BN>
+int launch_wm(const Fp8Maps& maps, Fp8Params p, int64_t units, cudaStream_t stream) {
+  constexpr int stage = wm_stage(MODE, BN);
+  p.ks = k_shares(units, p.nkb);
+  const size_t fixed = 1024 + (p.ks > 1 ? (MODE == 1 ? 2 : 1) * BN * kTileM * 4 : 0) + 64 * 8 + 16 +
+                       kMaxUnitsPerCta * sizeof(UnitRec);
+  p.ns = (int)std::min<size_t>(12, (kSmemBudget - fixed) / stage);
+  const size_t smem = fixed + (size_t)p.ns * stage;
+  auto kernel = fp8_wm_kernel<MODE, BN>;
+  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem, "fp8_wm_kernel: shared memory limit");
+  if (rc) return rc;
+  const int workers = (int)std::min<int64_t>(num_sms() / p.ks, std::max<int64_t>(units, 1));
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = p.ks;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(workers * p.ks);
+  cfg.blockDim = dim3(wm_threads(MODE));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = t_programmatic_launch ? attr : attr + 1;
+  cfg.numAttrs = (t_programmatic_launch ? 1 : 0) + (p.ks > 1 ? 1 : 0);
+  cudaLaunchKernelEx(&cfg, kernel, maps, p);
+  OES_CHECK_LAUNCH("fp8_wm_kernel");
   return OES_OK;
 }
 
@@ -198,36 +866,33 @@ Fp8Row fp8_row(int H, int I) {
 }
 
 int fp8_gemm_run(const GemmPlan& g, const GemmParams& p1, const GemmParams& p2, cudaStream_t stream) {
-  const int64_t cap = OES_ALIGN_CAPACITY(p1.R, p1.E, p1.BN);
-  Fp8Args a{};
-  a.g = p1;
-  a.x = g.f8.xq;
-  a.x_ld = p1.H;
-  a.xs = g.f8.xs;
-  a.w = p1.pool;
-  a.w_ld = p1.H;
-  a.ws = reinterpret_cast<const float*>(p1.pool + g.f8.s13_off);
-  a.N = p1.I;
-  a.K = p1.H;
-  a.nkb = p1.n_kc;
-  a.out = g.f8.hq;
-  a.out_ld = p1.I;
-  a.hs = g.f8.hs;
-  int rc = launch_simple<1>(a, cap / kRows, stream);
+  const int64_t blocks = OES_ALIGN_CAPACITY(p1.R, p1.E, p1.BN) / p1.BN;
+  Fp8Maps m{};
+  Fp8Params p{};
+  p.g = p1;
+  m.w = g.m1.a;
+  p.x = g.f8.xq;
+  p.xs = g.f8.xs;
+  p.ws = reinterpret_cast<const float*>(p1.pool + g.f8.s13_off);
+  p.N = p1.I;
+  p.K = p1.H;
+  p.nkb = p1.n_kc;
+  p.out = g.f8.hq;
+  p.out_ld = p1.I;
+  p.hs = g.f8.hs;
+  int rc = g.tm ? launch_tm<1>(m, p, stream) : launch_wm<1, 16>(m, p, blocks * p1.n_mtiles, stream);
   if (rc) return rc;
-  a.g = p2;
-  a.x = g.f8.hq;
-  a.x_ld = p1.I;
-  a.xs = g.f8.hs;
-  a.w = p1.pool + g.f8.w2_off;
-  a.w_ld = p1.I;
-  a.ws = reinterpret_cast<const float*>(p1.pool + g.f8.s2_off);
-  a.N = p1.H;
-  a.K = p1.I;
-  a.nkb = p2.n_kc;
-  a.out = p2.y;
-  a.out_ld = p1.H;
-  return launch_simple<2>(a, cap / kRows, stream);
+  p.g = p2;
+  m.w = g.m2.a;
+  m.x = g.m2.b;
+  p.xs = g.f8.hs;
+  p.ws = reinterpret_cast<const float*>(p1.pool + g.f8.s2_off);
+  p.N = p1.H;
+  p.K = p1.I;
+  p.nkb = p2.n_kc;
+  p.out = p2.y;
+  p.out_ld = p1.H;
+  return g.tm ? launch_tm<2>(m, p, stream) : launch_wm<2, 16>(m, p, blocks * p2.n_mtiles, stream);
 }
 
 }  // namespace oes
@@ -249,20 +914,36 @@ extern "C" int moe_fp8_gemm(const uint8_t* xq, int64_t xq_ld, const float* xs, i
   OES_REQUIRE(((uintptr_t)xs & 3) == 0 && ((uintptr_t)ws & 3) == 0 &&
                   ((uintptr_t)out & (dtype == OES_BF16 ? 1 : 3)) == 0,
               "moe_fp8_gemm: a pointer is not aligned to its type");
-  Fp8Args a{};
-  a.x = xq;
-  a.x_ld = xq_ld;
-  a.xs = xs;
-  a.w = wq;
-  a.w_ld = wq_ld;
-  a.ws = ws;
-  a.T = T;
-  a.N = N;
-  a.K = K;
-  a.nkb = ceil_div(K, kQuantGroup);
-  a.out = out;
-  a.out_ld = out_ld;
-  a.out_f32 = dtype == OES_F32;
-  a.g.status = status;
-  return launch_simple<0>(a, ceil_div(T, kRows), stream);
+  // The token-major kernel once its tiles fill most of the GPU; below that
+  // its few CTAs would each walk the whole of K.
+  const int64_t tiles = (int64_t)ceil_div(T, kTileM) * ceil_div(N, kTmN);
+  const bool tm = tiles * 4 >= (int64_t)num_sms() * 3;
+  const int bn = tm ? kTileM : T <= 16 ? 16 : 64;
+  Fp8Params p{};
+  p.g.status = status;
+  p.xs = xs;
+  p.ws = ws;
+  p.T = T;
+  p.N = N;
+  p.K = K;
+  p.nkb = ceil_div(K, kQuantGroup);
+  p.mt = ceil_div(T, bn);
+  p.nt = ceil_div(N, tm ? kTmN : kTileM);
+  OES_REQUIRE((int64_t)p.mt * p.nt <= 0x7FFFFFFF - 4096, "moe_fp8_gemm: too many tiles (T=%d N=%d)", T, N);
+  p.out = out;
+  p.out_ld = out_ld;
+  p.out_f32 = dtype == OES_F32;
+  p.vec = ((uintptr_t)out & 15) == 0 && out_ld % (p.out_f32 ? 4 : 8) == 0;
+  Fp8Maps m;
+  const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+  const uint64_t dw[3] = {(uint64_t)K, (uint64_t)N, 1}, sw[2] = {(uint64_t)wq_ld, (uint64_t)wq_ld * N};
+  const uint32_t bw[3] = {kBlkK, kTileM, 1};
+  int rc = encode_tiled(&m.w, u8, 3, wq, dw, sw, bw, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc) return rc;
+  const uint64_t dx[2] = {(uint64_t)K, (uint64_t)T}, sx[1] = {(uint64_t)xq_ld};
+  const uint32_t bx[2] = {kBlkK, (uint32_t)bn};
+  if ((rc = encode_tiled(&m.x, u8, 2, xq, dx, sx, bx, CU_TENSOR_MAP_SWIZZLE_128B))) return rc;
+  if (tm) return launch_tm<0>(m, p, stream);
+  const int64_t units = (int64_t)p.mt * p.nt;
+  return bn == 16 ? launch_wm<0, 16>(m, p, units, stream) : launch_wm<0, 64>(m, p, units, stream);
 }
