@@ -74,6 +74,13 @@ __device__ __forceinline__ float bf16_f32(uint32_t bits) { return __uint_as_floa
 __device__ __forceinline__ uint32_t f32_bf16(float v) {
   return __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
+// two values -> bf16x2, lo in the low half
+__device__ __forceinline__ uint32_t f32x2_bf16x2(float lo, float hi) {
+  uint32_t r;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+  return r;
+}
+
 template <int VEC>
 __device__ __forceinline__ void load_vals(const uint16_t* p, float (&v)[VEC]) {
   if constexpr (VEC == 8) {
@@ -105,7 +112,7 @@ __device__ __forceinline__ void store_vals(uint16_t* p, const float (&v)[VEC]) {
   if constexpr (VEC == 8) {
     uint32_t u[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) u[i] = f32_bf16(v[2 * i]) | (f32_bf16(v[2 * i + 1]) << 16);
+    for (int i = 0; i < 4; ++i) u[i] = f32x2_bf16x2(v[2 * i], v[2 * i + 1]);
     *reinterpret_cast<uint4*>(p) = make_uint4(u[0], u[1], u[2], u[3]);
   } else {
 #pragma unroll
@@ -124,6 +131,20 @@ __device__ __forceinline__ void store_vals(float* p, const float (&v)[VEC]) {
 }
 
 __device__ __forceinline__ float sigmoid_f32(float g) { return 1.0f / (1.0f + expf(-g)); }
-__device__ __forceinline__ float silu_f32(float g) { return g / (1.0f + expf(-g)); }
+
+// g / (1 + exp(-g)) for the epilogues, where it runs beside the MMAs: two
+// special-function operations and six others.  exp(-g) = 2^hi (1 + lo ln 2)
+// with hi + lo = -g log2(e), lo the rounding error of the product; within
+// 10 units of 2^-24 of g / (1 + exp(-g)).
+__device__ __forceinline__ float silu_f32(float g) {
+  constexpr float kLog2e = 1.44269504f, kLn2 = 0.693147182f;
+  const float hi = g * -kLog2e;
+  const float lo = fmaf(g, -kLog2e, -hi);
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(hi));
+  e = fmaf(lo, kLn2, 1.0f) * e;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.0f + e));
+  return g * r;
+}
 
 }  // namespace oes

@@ -51,11 +51,18 @@ struct Fp8Params {
   int64_t out_ld;
   int out_f32, vec;  // dense: type of out; its rows take 16-byte stores
   float* hs;         // MODE 1: scales of h
-  int ks, ns;        // CTAs that share a tile's K range; pipeline stages
+  int ks_log, ns;    // 2^ks_log CTAs share a tile's K range; pipeline stages
 };
 
+// A unit past the CTA's table, out of line: five roles look units up.  (The
+// token-major kernel cannot call functions: it moves registers between warps.)
+template <bool CG>
+__device__ __noinline__ Unit unit_past_table(const GemmParams& g, int u, int nb) {
+  return unit_info<CG>(g, u, nb);
+}
+
 // One unit of work: tile m of the weights against rows block b.
-template <int MODE>
+template <int MODE, bool TM>
 __device__ __forceinline__ Unit unit_of(const Fp8Params& p, const UnitRec* tab, int idx, int u, int nb,
                                         int rows) {
   if (MODE == 0) {
@@ -70,7 +77,17 @@ __device__ __forceinline__ Unit unit_of(const Fp8Params& p, const UnitRec* tab, 
     t.skip = false;
     return t;
   }
-  return my_unit<MODE == 2>(p.g, tab, idx, u, nb);
+  if (idx >= kMaxUnitsPerCta)
+    return TM ? unit_info<MODE == 2>(p.g, u, nb) : unit_past_table<MODE == 2>(p.g, u, nb);
+  const UnitRec r = tab[idx];
+  Unit t;
+  t.b = r.b;
+  t.m = r.m;
+  t.h = 0;
+  t.slot = r.slot;
+  t.nvalid = r.nvalid;
+  t.skip = t.slot < 0 || t.slot >= p.g.S || t.nvalid == 0;
+  return t;
 }
 
 // Fills the CTA's unit table (grouped) and returns the number of units.
@@ -126,10 +143,28 @@ __device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
+// Two FMAs by one scale: acc += {d0, d1} * {s, s}
+__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
+  uint64_t r;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+  return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t d0, uint32_t d1, uint64_t s) {
+  asm("{ .reg .b64 d; mov.b64 d, {%1, %2}; fma.rn.f32x2 %0, d, %3, %0; }"
+      : "+l"(acc)
+      : "r"(d0), "r"(d1), "l"(s));
+}
 // 16 bytes global -> shared, or 16 zero bytes
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst_smem, const void* src, bool take) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "r"(take ? 16 : 0)
                : "memory");
+}
+// 4 bytes global -> shared
+__device__ __forceinline__ void cp_async4(uint32_t dst_smem, const void* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst_smem), "l"(src) : "memory");
 }
 __device__ __forceinline__ void named_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
@@ -181,14 +216,25 @@ constexpr int kTmN = 256;  // weight rows a tile (MODE 1: 128 gate + 128 up)
 constexpr int kTmStage = (kTmN + kTileM) * kBlkK;
 constexpr int kTmEpi = 8;     // epilogue warps: two a TMEM lane quarter, 128 columns each
 constexpr int kTmGatherW0 = kEpiW0 + kTmEpi;
+// Scales reach the epilogue through shared memory, fetched ahead by warp 2
+// like the operands: read from global memory by the epilogue itself, one
+// block ahead, their latency set the pace (4096 x 8192 x 4096: 160 us).
+// A slot holds 8 blocks of K: [block][row] of x, [2][block] of the weights.
+constexpr int kTmScK = 8;
+constexpr int kTmScFloats = kTmScK * (kTileM + 2);
+constexpr int kScSlots = 2;
+// Each epilogue warp turns its results, a row a thread, into whole 64-byte
+// pieces of rows in 2 KB of shared memory before it stores them: 16-byte
+// stores to 32 different rows at a time cost 4 us a tile.
+constexpr int kStgBytes = 32 * 64;
 __host__ __device__ constexpr int tm_threads(int mode) { return mode == 1 ? 512 : 384; }
 
 // Registers: the launch gives every thread 65536 / threads; the epilogue
 // warps (128 sums each) take what the other warpgroups give back.
 // MODE 1: 512 x 128 = 128 (56 + 2 x 200 + 56).  Else 384 x 168 = 128 (72 + 2 x 216).
-template <int MODE>
+template <int MODE, typename OT>
 __global__ void __launch_bounds__(tm_threads(MODE), 1)
-    fp8_tm_kernel(const __grid_constant__ Fp8Maps maps, const Fp8Params p) {
+    fp8_tm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -196,8 +242,12 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
   uint64_t* empty = full + p.ns;
   uint64_t* tfull = empty + p.ns;
   uint64_t* tempty = tfull + 2;
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* sfull = tempty + 2;
+  uint64_t* sempty = sfull + kScSlots;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sempty + kScSlots);
   UnitRec* utab = reinterpret_cast<UnitRec*>(tmem_holder + 4);
+  uint8_t* stg_all = reinterpret_cast<uint8_t*>(utab + kMaxUnitsPerCta);
+  float* sc_tab = reinterpret_cast<float*>(stg_all + kTmEpi * kStgBytes);
   __shared__ int s_scan[33];
   __shared__ float s_amax[2][2][kTileM];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -211,6 +261,10 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], kTmEpi);
+    }
+    for (int a = 0; a < kScSlots; ++a) {
+      mbar_init(&sfull[a], 32);
+      mbar_init(&sempty[a], kTmEpi);
     }
     fence_mbar_init();
     tma_prefetch_desc(&maps.w);
@@ -238,10 +292,11 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
       int s = 0, ph = 0;
       bool ok = true;
       for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
-        const Unit t = unit_of<MODE>(p, utab, ui, u, nb, kTileM);
+        const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
         if (t.skip) continue;
         const int ra = t.m * (MODE == 1 ? kTileM : kTmN);
         const int rb = MODE == 1 ? p.N + ra : ra + kTileM;
+#pragma unroll 1
         for (int kb = 0; kb < p.nkb; ++kb) {
           ok = mbar_wait(&empty[s], ph ^ 1, status);
           if (!ok) break;
@@ -259,7 +314,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
       bool ok = true;
       const uint32_t idesc = idesc_f8(kTileM, kTmN);
       for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
-        const Unit t = unit_of<MODE>(p, utab, ui, u, nb, kTileM);
+        const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
         if (t.skip) continue;
         for (int kb = 0; kb < p.nkb; ++kb, ++it) {
           const uint32_t a = it & 1;
@@ -277,13 +332,54 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
           if (++s == p.ns) { s = 0; ph ^= 1; }
         }
       }
+    } else if (warp == 2) {
+      // ---------------------------------------------------- scale producer
+      // lane l: rows l + 32 i and, of the weights' 2 x 8 scales, one
+      const int nwb = (p.N + 127) / 128;  // blocks of weight rows
+      uint32_t n = 0;
+      bool ok = true;
+      for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
+        const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
+        if (t.skip) continue;
+        const float* xr[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = lane + 32 * i;
+          int64_t r = 0;  // rows past the block's last: any scale does
+          if (row < t.nvalid) {
+            const int64_t at = (int64_t)t.b * kTileM + row;
+            r = MODE == 1 ? p.g.sorted_ids[at] / p.g.k : at;
+          }
+          xr[i] = p.xs + r * p.nkb;
+        }
+        // MODE 1: the gate's and the up's row of blocks; else the two halves'
+        const int h = (lane >> 3) & 1, wb = MODE == 1 ? t.m + h * nwb : 2 * t.m + h;
+        const float* wr = (MODE == 0 ? p.ws : scales_of(p, t.slot)) +
+                          (int64_t)(MODE == 1 || wb < nwb ? wb : 2 * t.m) * p.nkb;
+        for (int k0 = 0; k0 < p.nkb; k0 += kTmScK, ++n) {
+          const int slot = n % kScSlots;
+          ok = mbar_wait(&sempty[slot], ((n / kScSlots) & 1) ^ 1, status);
+          if (!ok) break;
+          float* tab = sc_tab + slot * kTmScFloats;
+          const int kn = min(kTmScK, p.nkb - k0);
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            for (int k = 0; k < kn; ++k)
+              cp_async4(smem_u32(tab + k * kTileM + lane + 32 * i), xr[i] + k0 + k);
+          if (lane < 16 && (lane & 7) < kn)
+            cp_async4(smem_u32(tab + kTmScK * kTileM + lane), wr + k0 + (lane & 7));
+          cp_async_mbar_arrive(&sfull[slot]);
+        }
+      }
+      cp_async_wait_all();
     } else if (MODE != 1 && warp == 3 && lane == 0) {
       // ------------------------------------------------------ rows producer
       int s = 0, ph = 0;
       bool ok = true;
       for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
-        const Unit t = unit_of<MODE>(p, utab, ui, u, nb, kTileM);
+        const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
         if (t.skip) continue;
+#pragma unroll 1
         for (int kb = 0; kb < p.nkb; ++kb) {
           ok = mbar_wait(&empty[s], ph ^ 1, status);
           if (!ok) break;
@@ -299,11 +395,12 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
     const int q = warp & 3, half = (warp - kEpiW0) >> 2;
     const int row = q * 32 + lane;  // TMEM lane = row of the tile
     const int nwb = (p.N + 127) / 128;  // blocks of weight rows
-    uint32_t it = 0;
+    uint8_t* const stg = stg_all + (warp - kEpiW0) * kStgBytes;
+    uint32_t it = 0, sn = 0;
     int par = 0;
     bool ok = true;
     for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
-      const Unit t = unit_of<MODE>(p, utab, ui, u, nb, kTileM);
+      const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
       const bool live = row < t.nvalid;
       const int col0 = t.m * kTmN + half * kTileM;  // MODE 0, 2: first column of this warp
       int r = 0;                                    // row of out (MODE 2: the route)
@@ -318,35 +415,35 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
         }
         continue;
       }
-      const float* xs = p.xs;
-      if (MODE == 1) {
-        if (live) xs += (int64_t)(p.g.sorted_ids[(int64_t)t.b * p.g.BN + row] / p.g.k) * p.nkb;
-      } else if (live) {
-        xs += ((int64_t)t.b * kTileM + row) * p.nkb;
-      }
-      const float* ws = MODE == 0 ? p.ws : scales_of(p, t.slot);
-      // MODE 1: 64 gate columns and the same 64 up columns, so that a thread
-      // has both factors of its values of h
-      const float* ws0 = ws + (int64_t)(MODE == 1 ? t.m : col0 / 128) * p.nkb;
-      const float* ws1 = ws0 + (int64_t)nwb * p.nkb;
       const bool on = q * 32 < t.nvalid && (MODE == 1 ? t.m * kTileM + half * 64 : col0) < p.N;
-      float acc[128];
+      uint64_t acc[64];  // 128 fp32 sums in pairs of neighbouring columns
 #pragma unroll
-      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
-      float xn = xs[0], wn0 = on ? ws0[0] : 0.0f, wn1 = (MODE == 1 && on) ? ws1[0] : 0.0f;
+      for (int j = 0; j < 64; ++j) acc[j] = 0;
+#pragma unroll 1
       for (int kb = 0; kb < p.nkb; ++kb, ++it) {
         const uint32_t a = it & 1;
-        const float s0 = xn * wn0, s1 = MODE == 1 ? xn * wn1 : s0;
-        if (kb + 1 < p.nkb && on) {  // the next block's scales
-          xn = xs[kb + 1];
-          wn0 = ws0[kb + 1];
-          if (MODE == 1) wn1 = ws1[kb + 1];
+        const int slot = sn % kScSlots, ki = kb % kTmScK;
+        if (ki == 0) {
+          ok = mbar_wait(&sfull[slot], (sn / kScSlots) & 1, status);
+          if (!ok) break;
+        }
+        const float* tab = sc_tab + slot * kTmScFloats;
+        // MODE 1: 64 gate columns and the same 64 up columns, so that a
+        // thread has both factors of its values of h
+        const float x = tab[ki * kTileM + row];
+        const float s0 = x * tab[kTmScK * kTileM + (MODE == 1 ? 0 : half) * kTmScK + ki];
+        const float s1 = MODE == 1 ? x * tab[kTmScK * kTileM + kTmScK + ki] : s0;
+        if (ki == kTmScK - 1 || kb == p.nkb - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sempty[slot]);
+          ++sn;
         }
         ok = mbar_wait(&tfull[a], (it >> 1) & 1, status);
         if (!ok) break;
         tc_fence_after();
         if (on) {
           const uint32_t tl = tmem_base + ((uint32_t)(q * 32) << 16) + a * kTmN;
+          const uint64_t sp0 = pack2(s0, s0), sp1 = MODE == 1 ? pack2(s1, s1) : sp0;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t d[32];
@@ -357,9 +454,8 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
               __syncwarp();
               if (lane == 0) mbar_arrive(&tempty[a]);
             }
-            const float s = c >= 2 ? s1 : s0;
 #pragma unroll
-            for (int j = 0; j < 32; ++j) acc[c * 32 + j] = fmaf(__uint_as_float(d[j]), s, acc[c * 32 + j]);
+            for (int j = 0; j < 16; ++j) fma2(acc[c * 16 + j], d[2 * j], d[2 * j + 1], c >= 2 ? sp1 : sp0);
           }
         } else {
           tc_fence_before();
@@ -368,65 +464,94 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
         }
       }
       if (!ok) break;
+      // piece c (16 bytes) of a row's 64 lies at c ^ (row / 2 % 4): no two of
+      // eight lanes meet in a bank, writing rows or reading pieces
+      uint8_t* const stg_w = stg + lane * 64;
+      const int sw = (lane >> 1) & 3;
       if (MODE == 1) {
         if (q * 32 >= t.nvalid) continue;  // both warps of the quarter
         // h, the amax of its 128 columns with the other half's warp, codes
         float m = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 64; ++j) {
-          acc[j] = on ? silu_f32(acc[j]) * acc[64 + j] : 0.0f;
-          m = fmaxf(m, fabsf(acc[j]));
+        for (int j = 0; j < 32; ++j) {
+          float g0, g1, u0, u1;
+          unpack2(acc[j], g0, g1);
+          unpack2(acc[32 + j], u0, u1);
+          g0 = silu_f32(g0) * u0;
+          g1 = silu_f32(g1) * u1;
+          m = fmaxf(m, fmaxf(fabsf(g0), fabsf(g1)));
+          acc[j] = pack2(g0, g1);
         }
+        if (!on) m = 0.0f;
         s_amax[par][half][row] = m;
         named_bar(1 + q, 64);
         const QuantScale qs = quant_scale(fmaxf(m, s_amax[par][half ^ 1][row]));
         par ^= 1;
-        if (live) {
-          const int64_t hr = (int64_t)t.b * p.g.BN + row;
-          if (on) {
-            uint8_t* h = static_cast<uint8_t*>(p.out) + hr * p.out_ld + t.m * kTileM + half * 64;
+        const int64_t hr0 = (int64_t)t.b * p.g.BN + q * 32;
+        if (on) {
 #pragma unroll
-            for (int j = 0; j < 64; j += 16) {
-              uint32_t w[4];
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = quant4(acc[j + 4 * i], acc[j + 4 * i + 1], acc[j + 4 * i + 2], acc[j + 4 * i + 3], qs);
-              *reinterpret_cast<uint4*>(h + j) = make_uint4(w[0], w[1], w[2], w[3]);
+            for (int i = 0; i < 4; ++i) {
+              float v0, v1, v2, v3;
+              unpack2(acc[c * 8 + 2 * i], v0, v1);
+              unpack2(acc[c * 8 + 2 * i + 1], v2, v3);
+              w[i] = quant4(v0, v1, v2, v3, qs);
             }
+            *reinterpret_cast<uint4*>(stg_w + ((c ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
-          if (half == 0) p.hs[hr * nwb + t.m] = qs.s;
+          __syncwarp();
+          uint8_t* h = static_cast<uint8_t*>(p.out) + hr0 * p.out_ld + t.m * kTileM + half * 64;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = 8 * i + (lane >> 2), c = lane & 3;
+            const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
+            if (q * 32 + rr < t.nvalid) *reinterpret_cast<uint4*>(h + rr * p.out_ld + c * 16) = v;
+          }
+          __syncwarp();
         }
-      } else if (live && on) {
+        if (live && half == 0) p.hs[(hr0 + lane) * nwb + t.m] = qs.s;
+      } else if (on) {
+        constexpr int kPer = 64 / (int)sizeof(OT);  // columns of a piece
+        constexpr int kVec = 16 / (int)sizeof(OT);
         if (MODE == 0) r = t.b * kTileM + row;
-        if (MODE == 2 || !p.out_f32) {
-          uint16_t* o = static_cast<uint16_t*>(p.out) + (int64_t)r * p.out_ld + col0;
 #pragma unroll
-          for (int j = 0; j < 128; j += 8) {
-            if (col0 + j >= p.N) break;
-            if (MODE == 2 || (p.vec && col0 + j + 8 <= p.N)) {
-              float v[8];
+        for (int pc = 0; pc < 128 / kPer; ++pc) {
 #pragma unroll
-              for (int i = 0; i < 8; ++i) v[i] = acc[j + i];
-              store_vals<8>(o + j, v);
-            } else {
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w[4];
 #pragma unroll
-              for (int i = 0; i < 8; ++i)
-                if (col0 + j + i < p.N) o[j + i] = (uint16_t)f32_bf16(acc[j + i]);
+            for (int i = 0; i < 4; ++i) {
+              float lo, hi;
+              if constexpr (sizeof(OT) == 2) {
+                unpack2(acc[(pc * kPer + c * 8) / 2 + i], lo, hi);
+                w[i] = f32x2_bf16x2(lo, hi);
+              } else {
+                unpack2(acc[(pc * kPer + c * 4) / 2 + i / 2], lo, hi);
+                w[i] = __float_as_uint(i & 1 ? hi : lo);
+              }
+            }
+            *reinterpret_cast<uint4*>(stg_w + ((c ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int rr = 8 * i + (lane >> 2), c = lane & 3;
+            const int ro = __shfl_sync(0xffffffffu, r, rr);
+            const int col = col0 + pc * kPer + c * kVec;
+            const uint8_t* from = stg + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4);
+            if (q * 32 + rr < t.nvalid && col < p.N) {
+              OT* o = static_cast<OT*>(p.out) + (int64_t)ro * p.out_ld + col;
+              if (MODE == 2 || (p.vec && col + kVec <= p.N)) {
+                *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(from);
+              } else {
+#pragma unroll 1
+                for (int e = 0; e < min(kVec, p.N - col); ++e) o[e] = reinterpret_cast<const OT*>(from)[e];
+              }
             }
           }
-        } else {
-          float* o = static_cast<float*>(p.out) + (int64_t)r * p.out_ld + col0;
-#pragma unroll
-          for (int j = 0; j < 128; j += 4) {
-            if (col0 + j >= p.N) break;
-            if (p.vec && col0 + j + 4 <= p.N) {
-              *reinterpret_cast<float4*>(o + j) = make_float4(acc[j], acc[j + 1], acc[j + 2], acc[j + 3]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                if (col0 + j + i < p.N) o[j + i] = acc[j + i];
-            }
-          }
+          __syncwarp();
         }
       }
     }
@@ -442,7 +567,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
     int s = 0, ph = 0;
     bool ok = true;
     for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
-      const Unit t = unit_of<MODE>(p, utab, ui, u, nb, kTileM);
+      const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
       if (t.skip) continue;
       const int n16 = round16(t.nvalid);
       const uint8_t* src[8];
@@ -452,6 +577,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
         const int tk = n < t.nvalid ? p.g.sorted_ids[(int64_t)t.b * p.g.BN + n] / p.g.k : 0;
         src[j] = p.x + (int64_t)tk * p.K + c * 16;
       }
+#pragma unroll 1
       for (int kb = 0; kb < p.nkb; ++kb) {
         if (lane == 0) ok = mbar_wait(&empty[s], ph ^ 1, status);
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -482,6 +608,10 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
 // BN rows a tile (16, or 64 for the dense product).  Warps: 0 weights, 1 MMA,
 // 2 TMEM, 3 rows (TMA), 4-7 epilogue, 8-11 token gather (MODE 1).
 constexpr int kWmAcc = 4;  // TMEM buffers
+// A slot of scales (see above) holds 32 blocks of K: [block][BN] of the rows,
+// [kA][block] of the weights.
+constexpr int kWmScK = 32;
+__host__ __device__ constexpr int wm_sc_floats(int mode, int BN) { return kWmScK * (BN + (mode == 1 ? 2 : 1)); }
 __host__ __device__ constexpr int wm_threads(int mode) { return mode == 1 ? 384 : 256; }
 __host__ __device__ constexpr int wm_stage(int mode, int BN) {
   return (mode == 1 ? 2 : 1) * kTileBytes + BN * kBlkK;
@@ -489,30 +619,34 @@ __host__ __device__ constexpr int wm_stage(int mode, int BN) {
 
 template <int MODE, int BN>
 __global__ void __launch_bounds__(wm_threads(MODE), 1)
-    fp8_wm_kernel(const __grid_constant__ Fp8Maps maps, const Fp8Params p) {
+    fp8_wm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Params p) {
   constexpr int kA = MODE == 1 ? 2 : 1;  // weight tiles a stage (gate and up)
   constexpr int kStage = wm_stage(MODE, BN);
   constexpr uint32_t kCols = kWmAcc * kA * BN;  // TMEM columns: 64, 128 or 256
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  float* red = reinterpret_cast<float*>(stages + p.ns * kStage);  // ks > 1: [kA][ks][BN / ks][128]
-  uint64_t* full = reinterpret_cast<uint64_t*>(red + (p.ks > 1 ? kA * BN * kTileM : 0));
+  float* red = reinterpret_cast<float*>(stages + p.ns * kStage);  // [kA][ks][BN / ks][128]
+  uint64_t* full = reinterpret_cast<uint64_t*>(red + kA * BN * kTileM);
   uint64_t* empty = full + p.ns;
   uint64_t* tfull = empty + p.ns;
   uint64_t* tempty = tfull + kWmAcc;
   uint64_t* rfull = tempty + kWmAcc;  // [4]: a warp's sums of every CTA of the cluster are in
   uint64_t* rempty = rfull + 4;       // [4]: every CTA has read what this warp sent
-  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(rempty + 4);
+  uint64_t* sfull = rempty + 4;
+  uint64_t* sempty = sfull + kScSlots;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sempty + kScSlots);
   UnitRec* utab = reinterpret_cast<UnitRec*>(tmem_holder + 4);
+  float* sc_tab = reinterpret_cast<float*>(utab + kMaxUnitsPerCta);
+  constexpr int kScFloats = wm_sc_floats(MODE, BN);
   __shared__ int s_scan[33];
   __shared__ float s_amax[2][4][BN];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   int32_t* status = p.g.status;
   // the CTAs of a cluster have neighbouring block indices
-  const int ks = p.ks, rank = (int)blockIdx.x % ks;
-  const int worker = (int)blockIdx.x / ks, nworkers = (int)gridDim.x / ks;
-  const int k_lo = rank * p.nkb / ks, k_hi = (rank + 1) * p.nkb / ks;
+  const int ks = 1 << p.ks_log, rank = (int)blockIdx.x & (ks - 1);
+  const int worker = (int)blockIdx.x >> p.ks_log, nworkers = (int)gridDim.x >> p.ks_log;
+  const int k_lo = (rank * p.nkb) >> p.ks_log, k_hi = ((rank + 1) * p.nkb) >> p.ks_log;
   if (threadIdx.x == 0) {
     for (int s = 0; s < p.ns; ++s) {
       mbar_init(&full[s], 1 + (MODE == 1 ? 128 : 1));
@@ -525,6 +659,10 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     for (int w = 0; w < 4; ++w) {
       mbar_init(&rfull[w], ks);
       mbar_init(&rempty[w], ks);
+    }
+    for (int a = 0; a < kScSlots; ++a) {
+      mbar_init(&sfull[a], 32);
+      mbar_init(&sempty[a], 4);
     }
     fence_mbar_init();
     tma_prefetch_desc(&maps.w);
@@ -557,8 +695,9 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       int s = 0, ph = 0;
       bool ok = true;
       for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
-        const Unit t = unit_of<MODE>(p, utab, ui, u, nb, BN);
+        const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
         if (t.skip) continue;
+#pragma unroll 1
         for (int kb = k_lo; kb < k_hi; ++kb) {
           ok = mbar_wait(&empty[s], ph ^ 1, status);
           if (!ok) break;
@@ -578,7 +717,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       uint32_t it = 0;
       bool ok = true;
       for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
-        const Unit t = unit_of<MODE>(p, utab, ui, u, nb, BN);
+        const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
         if (t.skip) continue;
         const uint32_t idesc = idesc_f8(kTileM, round16(t.nvalid));
         for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
@@ -602,6 +741,35 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
         }
       }
     }
+  } else if (warp == 2) {
+    // ------------------------------------------------------ scale producer
+    if (MODE == 2) pdl_wait();  // h's scales
+    const int nwb = (p.N + 127) / 128;
+    uint32_t i = 0;
+    bool ok = true;
+    for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
+      const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
+      if (t.skip) continue;
+      int tk = 0;  // MODE 1: the rows' tokens, one a lane
+      if (MODE == 1 && lane < t.nvalid) tk = p.g.sorted_ids[(int64_t)t.b * p.g.BN + lane] / p.g.k;
+      const float* w = (MODE == 0 ? p.ws : scales_of(p, t.slot)) + (int64_t)t.m * p.nkb;
+      for (int k0 = k_lo; k0 < k_hi; k0 += kWmScK, ++i) {
+        const int slot = i % kScSlots, k = k0 + lane;
+        ok = mbar_wait(&sempty[slot], ((i / kScSlots) & 1) ^ 1, status);
+        if (!ok) break;
+        float* tab = sc_tab + slot * kScFloats;
+        for (int n = 0; n < t.nvalid; ++n) {
+          const int r = MODE == 1 ? __shfl_sync(0xffffffffu, tk, n & 31) : t.b * BN + n;
+          if (k < k_hi) cp_async4(smem_u32(tab + lane * BN + n), p.xs + (int64_t)r * p.nkb + k);
+        }
+        if (k < k_hi) {
+          cp_async4(smem_u32(tab + kWmScK * BN + lane), w + k);
+          if (MODE == 1) cp_async4(smem_u32(tab + kWmScK * (BN + 1) + lane), w + (int64_t)nwb * p.nkb + k);
+        }
+        cp_async_mbar_arrive(&sfull[slot]);
+      }
+    }
+    cp_async_wait_all();
   } else if (warp == 3) {
     if (MODE != 1 && lane == 0) {
       // ------------------------------------------------------ rows producer
@@ -609,8 +777,9 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       int s = 0, ph = 0;
       bool ok = true;
       for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
-        const Unit t = unit_of<MODE>(p, utab, ui, u, nb, BN);
+        const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
         if (t.skip) continue;
+#pragma unroll 1
         for (int kb = k_lo; kb < k_hi; ++kb) {
           ok = mbar_wait(&empty[s], ph ^ 1, status);
           if (!ok) break;
@@ -622,15 +791,15 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     }
   } else if (warp >= kEpiW0 && warp < kEpiW0 + 4) {
     // ---------------------------------------------------------- epilogue
-    if (MODE == 2) pdl_wait();  // h's scales
     const int q = warp & 3;
     const int row = q * 32 + lane;  // TMEM lane = weight row of the tile
     const int nwb = (p.N + 127) / 128;
-    const int own = BN / ks;        // columns this CTA finishes, from rank * own
-    uint32_t it = 0, un = 0;
+    // log2 of the columns this CTA finishes, from rank * own
+    const int own_log = (BN == 16 ? 4 : 6) - p.ks_log, own = 1 << own_log;
+    uint32_t it = 0, un = 0, sn = 0;
     bool ok = true;
     for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
-      const Unit t = unit_of<MODE>(p, utab, ui, u, nb, BN);
+      const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
       const int wrow = t.m * kTileM + row;
       if (t.skip) {
         if (MODE == 2 && t.nvalid > 0 && t.slot != kFiltered && rank == 0) {
@@ -645,119 +814,121 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       // MODE 1, 2: the block's routes, one a lane
       int sid = 0;
       if (MODE != 0 && lane < t.nvalid) sid = p.g.sorted_ids[(int64_t)t.b * p.g.BN + lane];
-      const float* ws = MODE == 0 ? p.ws : scales_of(p, t.slot);
-      const float* ws0 = ws + (int64_t)t.m * p.nkb;
-      const float* ws1 = ws0 + (int64_t)nwb * p.nkb;
       float acc[kA][BN];
 #pragma unroll
       for (int i = 0; i < kA; ++i)
 #pragma unroll
         for (int n = 0; n < BN; ++n) acc[i][n] = 0.0f;
-      for (int k0 = k_lo; k0 < k_hi && ok; k0 += 32) {
-        // lane l holds the scales of block k0 + l: of each row, times the weights'
-        const int k = k0 + lane;
-        const bool kin = k < k_hi;
-        const float w0 = kin ? ws0[k] : 0.0f, w1 = (MODE == 1 && kin) ? ws1[k] : 0.0f;
-        float sc[kA][BN];
-#pragma unroll
-        for (int n = 0; n < BN; ++n) {
-          const int tk = MODE == 1 ? __shfl_sync(0xffffffffu, sid, n & 31) / p.g.k : t.b * BN + n;
-          const float x = (n < t.nvalid && kin) ? p.xs[(int64_t)tk * p.nkb + k] : 0.0f;
-          sc[0][n] = x * w0;
-          if (MODE == 1) sc[kA - 1][n] = x * w1;
-        }
-        const int k1 = min(k_hi, k0 + 32);
-        for (int kb = k0; kb < k1; ++kb, ++it) {
-          const uint32_t a = it % kWmAcc;
-          ok = mbar_wait(&tfull[a], (it / kWmAcc) & 1, status);
+#pragma unroll 1
+      for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
+        const uint32_t a = it % kWmAcc;
+        const int slot = sn % kScSlots, ki = (kb - k_lo) % kWmScK;
+        if (ki == 0) {
+          ok = mbar_wait(&sfull[slot], (sn / kScSlots) & 1, status);
           if (!ok) break;
-          tc_fence_after();
-          const uint32_t tl = tmem_base + ((uint32_t)(q * 32) << 16) + a * kA * BN;
+        }
+        ok = mbar_wait(&tfull[a], (it / kWmAcc) & 1, status);
+        if (!ok) break;
+        tc_fence_after();
+        const float* tab = sc_tab + slot * kScFloats;
+        const uint32_t tl = tmem_base + ((uint32_t)(q * 32) << 16) + a * kA * BN;
 #pragma unroll
-          for (int i = 0; i < kA; ++i)
+        for (int c = 0; c < BN; c += 16) {
+          if (c >= t.nvalid) continue;
+          uint32_t d[kA][16];
 #pragma unroll
-            for (int c = 0; c < BN; c += 16) {
-              if (c >= t.nvalid) continue;
-              uint32_t d[16];
-              tmem_ld_16(tl + i * BN + c, d);
-              tc_wait_ld();
+          for (int i = 0; i < kA; ++i) tmem_ld_16(tl + i * BN + c, d[i]);
+          float x[16];
 #pragma unroll
-              for (int j = 0; j < 16; ++j)
-                acc[i][c + j] = fmaf(__uint_as_float(d[j]), __shfl_sync(0xffffffffu, sc[i][c + j], kb - k0),
-                                     acc[i][c + j]);
-            }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tempty[a]);
+          for (int j = 0; j < 16; j += 4) {
+            const float4 v = *reinterpret_cast<const float4*>(tab + ki * BN + c + j);
+            x[j] = v.x; x[j + 1] = v.y; x[j + 2] = v.z; x[j + 3] = v.w;
+          }
+          tc_wait_ld();
+#pragma unroll
+          for (int i = 0; i < kA; ++i) {
+            const float w = tab[kWmScK * (BN + i) + ki];
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[i][c + j] = fmaf(__uint_as_float(d[i][j]), x[j] * w, acc[i][c + j]);
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[a]);
+        if (ki == kWmScK - 1 || kb == k_hi - 1) {
+          if (lane == 0) mbar_arrive(&sempty[slot]);
+          ++sn;
         }
       }
       if (!ok) break;
+      // The sums go through shared memory, so that what follows is a loop
+      // over columns: unrolled over registers it was 250 KB of code, and
+      // fetching it took longer than the product.  Each CTA of a cluster
+      // finishes `own` columns: it sends the others theirs and adds up its
+      // own in rank order.
       if (ks > 1) {
-        // each CTA of the cluster finishes `own` columns: send the others
-        // theirs, then add up this CTA's in rank order
         ok = mbar_wait_cluster(&rempty[q], (un & 1) ^ 1, status);
         if (!ok) break;
+      }
+      {
         const uint32_t base = smem_u32(red) + row * 4;
 #pragma unroll
         for (int n = 0; n < BN; ++n) {
-          const int d = n / own, j = n % own;
+          if (n >= t.nvalid) continue;
+          const int d = n >> own_log, j = n & (own - 1);
+          const uint32_t to = map_rank(base + (((rank << own_log) + j) * kTileM) * 4, d);
 #pragma unroll
-          for (int i = 0; i < kA; ++i)
-            if (n < t.nvalid)
-              st_cluster(map_rank(base + (((i * ks + rank) * own + j) * kTileM) * 4, d), acc[i][n]);
+          for (int i = 0; i < kA; ++i) st_cluster(to + i * (BN * kTileM * 4), acc[i][n]);
         }
+      }
+      if (ks > 1) {
         fence_cluster();
         __syncwarp();
         if (lane < ks) mbar_arrive_cluster(map_rank(smem_u32(&rfull[q]), lane));
         ok = mbar_wait_cluster(&rfull[q], un & 1, status);
         if (!ok) break;
-#pragma unroll
-        for (int i = 0; i < kA; ++i)
-#pragma unroll
-          for (int j = 0; j < BN; ++j) {
-            float v = 0.0f;
-            if (j < own && rank * own + j < t.nvalid)
-              for (int r = 0; r < ks; ++r) v += red[((i * ks + r) * own + j) * kTileM + row];
-            acc[i][j] = v;
-          }
-        __syncwarp();
-        if (lane < ks) mbar_arrive_cluster(map_rank(smem_u32(&rempty[q]), lane));
       }
-      // columns n0 .. n0 + own - 1 of the tile are in acc[..][0 .. own - 1]
-      const int n0 = rank * own;
+      const int n0 = rank << own_log, mine = min(own, t.nvalid - n0);
+      auto sum = [&](int i, int j) {
+        const float* v = red + (i * BN + j) * kTileM + row;
+        float s = v[0];
+        for (int r = 1; r < ks; ++r) s += v[(r << own_log) * kTileM];
+        return s;
+      };
       if (MODE == 1) {
         const bool in = wrow < p.N;
-#pragma unroll
-        for (int j = 0; j < BN; ++j) {
-          if (j >= own) continue;
-          const float h = in && n0 + j < t.nvalid ? silu_f32(acc[0][j]) * acc[kA - 1][j] : 0.0f;
-          acc[0][j] = h;
+#pragma unroll 2
+        for (int j = 0; j < mine; ++j) {
+          const float h = in ? silu_f32(sum(0, j)) * sum(1, j) : 0.0f;
+          red[j * kTileM + row] = h;  // over this row's first sum, just read
           // positive fp32 numbers order like their bits; a NaN takes no part
-          const uint32_t bits = h == h ? __float_as_uint(fabsf(h)) : 0u;
-          const uint32_t m = __reduce_max_sync(0xffffffffu, bits);
+          const uint32_t m = __reduce_max_sync(0xffffffffu, h == h ? __float_as_uint(fabsf(h)) : 0u);
           if (lane == 0) s_amax[un & 1][q][j] = __uint_as_float(m);
         }
         named_bar(1, 128);
-#pragma unroll
-        for (int j = 0; j < BN; ++j) {
-          if (j >= own || n0 + j >= t.nvalid) continue;
+#pragma unroll 2
+        for (int j = 0; j < mine; ++j) {
           const float(*am)[BN] = s_amax[un & 1];
           const QuantScale qs = quant_scale(fmaxf(fmaxf(am[0][j], am[1][j]), fmaxf(am[2][j], am[3][j])));
           const int64_t hr = (int64_t)t.b * p.g.BN + n0 + j;
-          if (in) static_cast<uint8_t*>(p.out)[hr * p.out_ld + wrow] = quant1(acc[0][j], qs);
+          if (in) static_cast<uint8_t*>(p.out)[hr * p.out_ld + wrow] = quant1(red[j * kTileM + row], qs);
           if (row == 0) p.hs[hr * nwb + t.m] = qs.s;
         }
       } else {
-#pragma unroll
-        for (int j = 0; j < BN; ++j) {
-          if (j >= own) continue;
+#pragma unroll 2
+        for (int j = 0; j < mine; ++j) {
           const int n = n0 + j;
           const int r = MODE == 2 ? __shfl_sync(0xffffffffu, sid, n & 31) : t.b * BN + n;
-          if (n >= t.nvalid || wrow >= p.N) continue;
+          const float v = sum(0, j);
+          if (wrow >= p.N) continue;
           const int64_t o = (int64_t)r * p.out_ld + wrow;
-          if (MODE == 0 && p.out_f32) static_cast<float*>(p.out)[o] = acc[0][j];
-          else static_cast<uint16_t*>(p.out)[o] = (uint16_t)f32_bf16(acc[0][j]);
+          if (MODE == 0 && p.out_f32) static_cast<float*>(p.out)[o] = v;
+          else static_cast<uint16_t*>(p.out)[o] = (uint16_t)f32_bf16(v);
         }
+      }
+      if (ks > 1) {
+        __syncwarp();
+        if (lane < ks) mbar_arrive_cluster(map_rank(smem_u32(&rempty[q]), lane));
       }
       ++un;
     }
@@ -768,10 +939,11 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     int s = 0, ph = 0;
     bool ok = true;
     for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
-      const Unit t = unit_of<MODE>(p, utab, ui, u, nb, BN);
+      const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
       if (t.skip) continue;
       const int tk = n < t.nvalid ? p.g.sorted_ids[(int64_t)t.b * p.g.BN + n] / p.g.k : 0;
       const uint8_t* src = p.x + (int64_t)tk * p.K + c * 16;
+#pragma unroll 1
       for (int kb = k_lo; kb < k_hi; ++kb) {
         if (lane == 0) ok = mbar_wait(&empty[s], ph ^ 1, status);
         ok = __shfl_sync(0xffffffffu, ok, 0);
@@ -799,54 +971,56 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
 // ------------------------------------------------------------------ launches
 constexpr size_t kSmemBudget = 222 * 1024;
 
-template <int MODE>
+template <int MODE, typename OT>
 int launch_tm(const Fp8Maps& maps, Fp8Params p, cudaStream_t stream) {
-  p.ks = 1;
+  p.ks_log = 0;
   p.ns = 4;
-  const size_t smem = 1024 + (size_t)p.ns * kTmStage + (2 * p.ns + 4) * 8 + 16 + kMaxUnitsPerCta * sizeof(UnitRec);
-  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(fp8_tm_kernel<MODE>), smem,
+  const size_t smem = 1024 + (size_t)p.ns * kTmStage + (2 * p.ns + 4 + 2 * kScSlots) * 8 + 16 +
+                      kMaxUnitsPerCta * sizeof(UnitRec) + kTmEpi * kStgBytes + kScSlots * kTmScFloats * 4;
+  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(fp8_tm_kernel<MODE, OT>), smem,
                                 "fp8_tm_kernel: shared memory limit");
   if (rc) return rc;
   const int64_t units = MODE == 0 ? (int64_t)p.mt * p.nt : INT64_MAX;
-  launch_kernel(fp8_tm_kernel<MODE>, (int)std::min<int64_t>(num_sms(), units), tm_threads(MODE), smem, stream, maps, p);
+  launch_kernel(fp8_tm_kernel<MODE, OT>, (int)std::min<int64_t>(num_sms(), units), tm_threads(MODE), smem, stream, maps, p);
   OES_CHECK_LAUNCH("fp8_tm_kernel");
   return OES_OK;
 }
 
-// CTAs that share a tile: the largest of 8, 4, 2, 1 that keeps every tile
-// resident at once and leaves each CTA at least two blocks of K.  units: the
-// most units the launch can have, known on the host.
-int k_shares(int64_t units, int nkb) {
-  for (int ks = 8; ks > 1; ks /= 2)
-    if (units * ks <= num_sms() && nkb >= 2 * ks) return ks;
-  return 1;
+// log2 of the CTAs that share a tile: the largest of 8, 4, 2, 1 that keeps
+// every tile resident at once and leaves each CTA at least two blocks of K.
+// units: the most units the launch can have, known on the host.
+int k_shares_log(int64_t units, int nkb) {
+  for (int l = 3; l > 0; --l)
+    if ((units << l) <= num_sms() && nkb >= (2 << l)) return l;
+  return 0;
 }
 
 template <int MODE, int BN>
 int launch_wm(const Fp8Maps& maps, Fp8Params p, int64_t units, cudaStream_t stream) {
   constexpr int stage = wm_stage(MODE, BN);
-  p.ks = k_shares(units, p.nkb);
-  const size_t fixed = 1024 + (p.ks > 1 ? (MODE == 1 ? 2 : 1) * BN * kTileM * 4 : 0) + 64 * 8 + 16 +
-                       kMaxUnitsPerCta * sizeof(UnitRec);
+  p.ks_log = k_shares_log(units, p.nkb);
+  const int ks = 1 << p.ks_log;
+  const size_t fixed = 1024 + (size_t)(MODE == 1 ? 2 : 1) * BN * kTileM * 4 + 64 * 8 + 16 +
+                       kMaxUnitsPerCta * sizeof(UnitRec) + kScSlots * wm_sc_floats(MODE, BN) * 4;
   p.ns = (int)std::min<size_t>(12, (kSmemBudget - fixed) / stage);
   const size_t smem = fixed + (size_t)p.ns * stage;
   auto kernel = fp8_wm_kernel<MODE, BN>;
   int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kernel), smem, "fp8_wm_kernel: shared memory limit");
   if (rc) return rc;
-  const int workers = (int)std::min<int64_t>(num_sms() / p.ks, std::max<int64_t>(units, 1));
+  const int workers = (int)std::min<int64_t>(num_sms() / ks, std::max<int64_t>(units, 1));
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = p.ks;
+  attr[1].val.clusterDim.x = ks;
   attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(workers * p.ks);
+  cfg.gridDim = dim3(workers * ks);
   cfg.blockDim = dim3(wm_threads(MODE));
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
   cfg.attrs = t_programmatic_launch ? attr : attr + 1;
-  cfg.numAttrs = (t_programmatic_launch ? 1 : 0) + (p.ks > 1 ? 1 : 0);
+  cfg.numAttrs = (t_programmatic_launch ? 1 : 0) + (ks > 1 ? 1 : 0);
   cudaLaunchKernelEx(&cfg, kernel, maps, p);
   OES_CHECK_LAUNCH("fp8_wm_kernel");
   return OES_OK;
@@ -880,7 +1054,7 @@ int fp8_gemm_run(const GemmPlan& g, const GemmParams& p1, const GemmParams& p2, 
   p.out = g.f8.hq;
   p.out_ld = p1.I;
   p.hs = g.f8.hs;
-  int rc = g.tm ? launch_tm<1>(m, p, stream) : launch_wm<1, 16>(m, p, blocks * p1.n_mtiles, stream);
+  int rc = g.tm ? launch_tm<1, uint16_t>(m, p, stream) : launch_wm<1, 16>(m, p, blocks * p1.n_mtiles, stream);
   if (rc) return rc;
   p.g = p2;
   m.w = g.m2.a;
@@ -892,7 +1066,7 @@ int fp8_gemm_run(const GemmPlan& g, const GemmParams& p1, const GemmParams& p2, 
   p.nkb = p2.n_kc;
   p.out = p2.y;
   p.out_ld = p1.H;
-  return g.tm ? launch_tm<2>(m, p, stream) : launch_wm<2, 16>(m, p, blocks * p2.n_mtiles, stream);
+  return g.tm ? launch_tm<2, uint16_t>(m, p, stream) : launch_wm<2, 16>(m, p, blocks * p2.n_mtiles, stream);
 }
 
 }  // namespace oes
@@ -943,7 +1117,7 @@ extern "C" int moe_fp8_gemm(const uint8_t* xq, int64_t xq_ld, const float* xs, i
   const uint64_t dx[2] = {(uint64_t)K, (uint64_t)T}, sx[1] = {(uint64_t)xq_ld};
   const uint32_t bx[2] = {kBlkK, (uint32_t)bn};
   if ((rc = encode_tiled(&m.x, u8, 2, xq, dx, sx, bx, CU_TENSOR_MAP_SWIZZLE_128B))) return rc;
-  if (tm) return launch_tm<0>(m, p, stream);
+  if (tm) return p.out_f32 ? launch_tm<0, float>(m, p, stream) : launch_tm<0, uint16_t>(m, p, stream);
   const int64_t units = (int64_t)p.mt * p.nt;
   return bn == 16 ? launch_wm<0, 16>(m, p, units, stream) : launch_wm<0, 64>(m, p, units, stream);
 }
