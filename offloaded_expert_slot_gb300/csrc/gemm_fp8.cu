@@ -143,19 +143,10 @@ __device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
-// Two FMAs by one scale: acc += {d0, d1} * {s, s}
-__device__ __forceinline__ uint64_t pack2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-__device__ __forceinline__ void unpack2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ void fma2(uint64_t& acc, uint32_t d0, uint32_t d1, uint64_t s) {
-  asm("{ .reg .b64 d; mov.b64 d, {%1, %2}; fma.rn.f32x2 %0, d, %3, %0; }"
-      : "+l"(acc)
-      : "r"(d0), "r"(d1), "l"(s));
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
+  return r != 0;
 }
 // 16 bytes global -> shared, or 16 zero bytes
 __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst_smem, const void* src, bool take) {
@@ -307,28 +298,37 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
           if (++s == p.ns) { s = 0; ph ^= 1; }
         }
       }
-    } else if (warp == 1 && lane == 0) {
+    } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
+      // The whole warp walks the loop and one elected lane issues, so that the
+      // descriptors stay in uniform registers: issued from a one-lane branch,
+      // each hand-off took 0.09 us longer.
       int s = 0, ph = 0;
       uint32_t it = 0;
       bool ok = true;
       const uint32_t idesc = idesc_f8(kTileM, kTmN);
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(stages));
+      const bool leader = elect_one();
       for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
         const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
         if (t.skip) continue;
+#pragma unroll 1
         for (int kb = 0; kb < p.nkb; ++kb, ++it) {
           const uint32_t a = it & 1;
           ok = mbar_wait(&tempty[a], ((it >> 1) & 1) ^ 1, status) && mbar_wait(&full[s], ph, status);
+          ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           if (MODE == 1) fence_proxy_async_smem();  // cp.async-written rows -> tensor core
-          const uint32_t W = smem_u32(stages + s * kTmStage);
-          const uint64_t wd = smem_desc_sw128(W), xd = smem_desc_sw128(W + 2 * kTileBytes);
+          if (leader) {
+            const uint64_t wd = desc0 + (uint32_t)(s * (kTmStage >> 4)), xd = wd + (2 * kTileBytes >> 4);
 #pragma unroll
-          for (int kk = 0; kk < kBlkK / 32; ++kk)
-            tc_mma_f8(tmem_base + a * kTmN, xd + 2 * kk, wd + 2 * kk, idesc, kk ? 1u : 0u);
-          tc_commit(&empty[s]);
-          tc_commit(&tfull[a]);
+            for (int kk = 0; kk < kBlkK / 32; ++kk)
+              tc_mma_f8(tmem_base + a * kTmN, xd + 2 * kk, wd + 2 * kk, idesc, kk ? 1u : 0u);
+            tc_commit(&empty[s]);
+            tc_commit(&tfull[a]);
+          }
+          __syncwarp();
           if (++s == p.ns) { s = 0; ph ^= 1; }
         }
       }
@@ -416,9 +416,9 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
         continue;
       }
       const bool on = q * 32 < t.nvalid && (MODE == 1 ? t.m * kTileM + half * 64 : col0) < p.N;
-      uint64_t acc[64];  // 128 fp32 sums in pairs of neighbouring columns
+      float acc[128];
 #pragma unroll
-      for (int j = 0; j < 64; ++j) acc[j] = 0;
+      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
 #pragma unroll 1
       for (int kb = 0; kb < p.nkb; ++kb, ++it) {
         const uint32_t a = it & 1;
@@ -443,7 +443,6 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
         tc_fence_after();
         if (on) {
           const uint32_t tl = tmem_base + ((uint32_t)(q * 32) << 16) + a * kTmN;
-          const uint64_t sp0 = pack2(s0, s0), sp1 = MODE == 1 ? pack2(s1, s1) : sp0;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t d[32];
@@ -455,7 +454,8 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
               if (lane == 0) mbar_arrive(&tempty[a]);
             }
 #pragma unroll
-            for (int j = 0; j < 16; ++j) fma2(acc[c * 16 + j], d[2 * j], d[2 * j + 1], c >= 2 ? sp1 : sp0);
+            for (int j = 0; j < 32; ++j)
+              acc[c * 32 + j] = fmaf(__uint_as_float(d[j]), c >= 2 ? s1 : s0, acc[c * 32 + j]);
           }
         } else {
           tc_fence_before();
@@ -473,14 +473,9 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
         // h, the amax of its 128 columns with the other half's warp, codes
         float m = 0.0f;
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          float g0, g1, u0, u1;
-          unpack2(acc[j], g0, g1);
-          unpack2(acc[32 + j], u0, u1);
-          g0 = silu_f32(g0) * u0;
-          g1 = silu_f32(g1) * u1;
-          m = fmaxf(m, fmaxf(fabsf(g0), fabsf(g1)));
-          acc[j] = pack2(g0, g1);
+        for (int j = 0; j < 64; ++j) {
+          acc[j] = silu_f32(acc[j]) * acc[64 + j];
+          m = fmaxf(m, fabsf(acc[j]));
         }
         if (!on) m = 0.0f;
         s_amax[par][half][row] = m;
@@ -494,10 +489,8 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float v0, v1, v2, v3;
-              unpack2(acc[c * 8 + 2 * i], v0, v1);
-              unpack2(acc[c * 8 + 2 * i + 1], v2, v3);
-              w[i] = quant4(v0, v1, v2, v3, qs);
+              const float* v = acc + c * 16 + 4 * i;
+              w[i] = quant4(v[0], v[1], v[2], v[3], qs);
             }
             *reinterpret_cast<uint4*>(stg_w + ((c ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
@@ -523,14 +516,9 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
             uint32_t w[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float lo, hi;
-              if constexpr (sizeof(OT) == 2) {
-                unpack2(acc[(pc * kPer + c * 8) / 2 + i], lo, hi);
-                w[i] = f32x2_bf16x2(lo, hi);
-              } else {
-                unpack2(acc[(pc * kPer + c * 4) / 2 + i / 2], lo, hi);
-                w[i] = __float_as_uint(i & 1 ? hi : lo);
-              }
+              const float* v = acc + pc * kPer + c * kVec;
+              if constexpr (sizeof(OT) == 2) w[i] = f32x2_bf16x2(v[2 * i], v[2 * i + 1]);
+              else w[i] = __float_as_uint(v[i]);
             }
             *reinterpret_cast<uint4*>(stg_w + ((c ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
@@ -711,23 +699,26 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       }
     }
   } else if (warp == 1) {
-    if (lane == 0) {
-      // -------------------------------------------------------- MMA issuer
-      int s = 0, ph = 0;
-      uint32_t it = 0;
-      bool ok = true;
-      for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
-        const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
-        if (t.skip) continue;
-        const uint32_t idesc = idesc_f8(kTileM, round16(t.nvalid));
-        for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
-          const uint32_t a = it % kWmAcc;
-          ok = mbar_wait(&tempty[a], ((it / kWmAcc) & 1) ^ 1, status) && mbar_wait(&full[s], ph, status);
-          if (!ok) break;
-          tc_fence_after();
-          if (MODE == 1) fence_proxy_async_smem();
-          const uint32_t W = smem_u32(stages + s * kStage);
-          const uint64_t wd = smem_desc_sw128(W), xd = smem_desc_sw128(W + kA * kTileBytes);
+    // ---------------------------------------------------------- MMA issuer
+    int s = 0, ph = 0;
+    uint32_t it = 0;
+    bool ok = true;
+    const uint64_t desc0 = smem_desc_sw128(smem_u32(stages));
+    const bool leader = elect_one();
+    for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
+      const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
+      if (t.skip) continue;
+      const uint32_t idesc = idesc_f8(kTileM, round16(t.nvalid));
+#pragma unroll 1
+      for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
+        const uint32_t a = it % kWmAcc;
+        ok = mbar_wait(&tempty[a], ((it / kWmAcc) & 1) ^ 1, status) && mbar_wait(&full[s], ph, status);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        tc_fence_after();
+        if (MODE == 1) fence_proxy_async_smem();
+        if (leader) {
+          const uint64_t wd = desc0 + (uint32_t)(s * (kStage >> 4)), xd = wd + (kA * kTileBytes >> 4);
           const uint32_t d = tmem_base + a * kA * BN;
 #pragma unroll
           for (int kk = 0; kk < kBlkK / 32; ++kk) {
@@ -737,8 +728,9 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
           }
           tc_commit(&empty[s]);
           tc_commit(&tfull[a]);
-          if (++s == p.ns) { s = 0; ph ^= 1; }
         }
+        __syncwarp();
+        if (++s == p.ns) { s = 0; ph ^= 1; }
       }
     }
   } else if (warp == 2) {
