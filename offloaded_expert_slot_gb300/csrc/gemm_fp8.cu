@@ -49,7 +49,7 @@ struct Fp8Params {
   int mt, nt;        // dense: row tiles, weight tiles
   void* out;         // MODE 0 out, MODE 1 codes of h, MODE 2 y
   int64_t out_ld;
-  int out_f32, vec;  // dense: type of out; its rows take 16-byte stores
+  int out_f32, vec;  // dense: type of out; its rows and their pieces are multiples of 16 bytes
   float* hs;         // MODE 1: scales of h
   int ks_log, ns;    // 2^ks_log CTAs share a tile's K range; pipeline stages
 };
@@ -116,6 +116,25 @@ __device__ __forceinline__ const float* scales_of(const Fp8Params& p, int slot) 
   return reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(p.ws) + (int64_t)slot * p.g.row_bytes);
 }
 
+// The bounded wait of these kernels.  The loop is in the asm, so that a warp
+// that waits together stays together: written as a loop in C++, with a lane's
+// own exit, each hand-off between MMA and epilogue took 60 cycles longer.
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+  uint32_t ok;
+  asm volatile(
+      "{ .reg .pred p; .reg .u32 n; mov.u32 n, 0;\n"
+      "W%=: mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      "@p bra D%=;\n"
+      "add.u32 n, n, 1;\n"
+      "setp.lt.u32 p, n, %3;\n"
+      "@p bra W%=;\n"
+      "D%=: selp.u32 %0, 1, 0, p; }"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "n"(kWaitLimit)
+      : "memory");
+  if (!ok) set_status(status, OES_DEV_TIMEOUT);
+  return ok != 0;
+}
 // D[tmem] (+)= A[smem] * B[smem]^T, kind::f8f6f4 (e4m3 inputs, fp32 sums)
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                           uint32_t idesc, uint32_t accumulate) {
@@ -157,6 +176,19 @@ __device__ __forceinline__ void cp_async16_or_zero(uint32_t dst_smem, const void
 __device__ __forceinline__ void cp_async4(uint32_t dst_smem, const void* src) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst_smem), "l"(src) : "memory");
 }
+// Asynchronous copy of a row piece to global memory, by the thread that wrote
+// it (16-byte aligned, a multiple of 16 bytes), and the thread's waits for its
+// copies: until they have read shared memory, or until they are done.
+__device__ __forceinline__ void bulk_store(void* dst, const void* src, int bytes) {
+  fence_proxy_async_smem();
+  asm volatile(
+      "cp.async.bulk.global.shared::cta.bulk_group [%0], [%1], %2;\n"
+      "cp.async.bulk.commit_group;" ::"l"(dst),
+      "r"(smem_u32(src)), "r"(bytes)
+      : "memory");
+}
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
 __device__ __forceinline__ void named_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
 }
@@ -203,8 +235,9 @@ __device__ __forceinline__ void cluster_barrier() {
 }
 
 // ============================================================ token-major
-constexpr int kTmN = 256;  // weight rows a tile (MODE 1: 128 gate + 128 up)
-constexpr int kTmStage = (kTmN + kTileM) * kBlkK;
+// TN weight rows a tile (MODE 1: 128 gate + 128 up).  TMEM holds 512 / TN
+// blocks' sums.
+__host__ __device__ constexpr int tm_stage(int TN) { return (TN + kTileM) * kBlkK; }
 constexpr int kTmEpi = 8;     // epilogue warps: two a TMEM lane quarter, 128 columns each
 constexpr int kTmGatherW0 = kEpiW0 + kTmEpi;
 // Scales reach the epilogue through shared memory, fetched ahead by warp 2
@@ -214,31 +247,47 @@ constexpr int kTmGatherW0 = kEpiW0 + kTmEpi;
 constexpr int kTmScK = 8;
 constexpr int kTmScFloats = kTmScK * (kTileM + 2);
 constexpr int kScSlots = 2;
-// Each epilogue warp turns its results, a row a thread, into whole 64-byte
-// pieces of rows in 2 KB of shared memory before it stores them: 16-byte
-// stores to 32 different rows at a time cost 4 us a tile.
-constexpr int kStgBytes = 32 * 64;
+// Results leave through shared memory, since 16-byte stores to 32 different rows
+// at a time cost 4 us a tile.  The dense and the down product turn pieces of 64
+// bytes of 32 rows around in 2 KB a warp and store them in whole sectors.  h's
+// codes are copied out asynchronously, a thread its row's 64 bytes (rows 80
+// bytes apart, so that eight lanes never meet in a bank).
+__host__ __device__ constexpr int stg_row(int mode) {
+  return mode == 1 ? 64 + 16 : 64;
+}
 __host__ __device__ constexpr int tm_threads(int mode) { return mode == 1 ? 512 : 384; }
 
 // Registers: the launch gives every thread 65536 / threads; the epilogue
 // warps (128 sums each) take what the other warpgroups give back.
 // MODE 1: 512 x 128 = 128 (56 + 2 x 200 + 56).  Else 384 x 168 = 128 (72 + 2 x 216).
-template <int MODE, typename OT>
+// The dense kernel keeps the library's wait: it measured 135 us at 4096 x 8192 x
+// 4096 with it and 154 us with the asm loop, the experts' kernels 3 % better
+// with the loop.
+template <int MODE>
+__device__ __forceinline__ bool tm_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
+  return MODE == 0 ? mbar_wait(bar, parity, status) : bar_wait(bar, parity, status);
+}
+
+template <int MODE, typename OT, int TN>
 __global__ void __launch_bounds__(tm_threads(MODE), 1)
     fp8_tm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Params p) {
+  constexpr int kStage = tm_stage(TN);
+  constexpr int kBufs = 512 / TN;
+  constexpr int kCols = TN / 2;  // columns of an epilogue warp
+  constexpr int kStgRow = stg_row(MODE);
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-  uint64_t* full = reinterpret_cast<uint64_t*>(stages + p.ns * kTmStage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(stages + p.ns * kStage);
   uint64_t* empty = full + p.ns;
   uint64_t* tfull = empty + p.ns;
-  uint64_t* tempty = tfull + 2;
-  uint64_t* sfull = tempty + 2;
+  uint64_t* tempty = tfull + kBufs;
+  uint64_t* sfull = tempty + kBufs;
   uint64_t* sempty = sfull + kScSlots;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sempty + kScSlots);
   UnitRec* utab = reinterpret_cast<UnitRec*>(tmem_holder + 4);
-  uint8_t* stg_all = reinterpret_cast<uint8_t*>(utab + kMaxUnitsPerCta);
-  float* sc_tab = reinterpret_cast<float*>(stg_all + kTmEpi * kStgBytes);
+  uint8_t* stg_all = reinterpret_cast<uint8_t*>(utab + (MODE == 0 ? 0 : kMaxUnitsPerCta));
+  float* sc_tab = reinterpret_cast<float*>(stg_all + kTmEpi * 32 * kStgRow);
   __shared__ int s_scan[33];
   __shared__ float s_amax[2][2][kTileM];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -249,7 +298,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
       mbar_init(&full[s], 1 + (MODE == 1 ? 128 : 1));
       mbar_init(&empty[s], 1);
     }
-    for (int a = 0; a < 2; ++a) {
+    for (int a = 0; a < kBufs; ++a) {
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], kTmEpi);
     }
@@ -277,7 +326,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
   const uint32_t tmem_base = *tmem_holder;
 
   if (warp < kEpiW0) {
-    regs_dec<MODE == 1 ? 56 : 72>();
+    if (TN == 256) regs_dec<MODE == 1 ? 56 : 72>();
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- weight producer
       int s = 0, ph = 0;
@@ -285,16 +334,16 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
       for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
         const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
         if (t.skip) continue;
-        const int ra = t.m * (MODE == 1 ? kTileM : kTmN);
+        const int ra = t.m * (MODE == 1 ? kTileM : TN);
         const int rb = MODE == 1 ? p.N + ra : ra + kTileM;
 #pragma unroll 1
         for (int kb = 0; kb < p.nkb; ++kb) {
-          ok = mbar_wait(&empty[s], ph ^ 1, status);
+          ok = tm_wait<MODE>(&empty[s], ph ^ 1, status);
           if (!ok) break;
-          uint8_t* W = stages + s * kTmStage;
-          mbar_arrive_expect_tx(&full[s], 2 * kTileBytes);
+          uint8_t* W = stages + s * kStage;
+          mbar_arrive_expect_tx(&full[s], TN * kBlkK);
           tma_load_3d(W, &maps.w, &full[s], kb * kBlkK, ra, t.slot);
-          tma_load_3d(W + kTileBytes, &maps.w, &full[s], kb * kBlkK, rb, t.slot);
+          if (TN == 256) tma_load_3d(W + kTileBytes, &maps.w, &full[s], kb * kBlkK, rb, t.slot);
           if (++s == p.ns) { s = 0; ph ^= 1; }
         }
       }
@@ -306,7 +355,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
       int s = 0, ph = 0;
       uint32_t it = 0;
       bool ok = true;
-      const uint32_t idesc = idesc_f8(kTileM, kTmN);
+      const uint32_t idesc = idesc_f8(kTileM, TN);
       const uint64_t desc0 = smem_desc_sw128(smem_u32(stages));
       const bool leader = elect_one();
       for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
@@ -314,17 +363,18 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
         if (t.skip) continue;
 #pragma unroll 1
         for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-          const uint32_t a = it & 1;
-          ok = mbar_wait(&tempty[a], ((it >> 1) & 1) ^ 1, status) && mbar_wait(&full[s], ph, status);
+          const uint32_t a = it % kBufs;
+          ok = tm_wait<MODE>(&full[s], ph, status);
+          ok = tm_wait<MODE>(&tempty[a], ((it / kBufs) & 1) ^ 1, status) && ok;
           ok = __all_sync(0xffffffffu, ok);
           if (!ok) break;
           tc_fence_after();
           if (MODE == 1) fence_proxy_async_smem();  // cp.async-written rows -> tensor core
           if (leader) {
-            const uint64_t wd = desc0 + (uint32_t)(s * (kTmStage >> 4)), xd = wd + (2 * kTileBytes >> 4);
+            const uint64_t wd = desc0 + (uint32_t)(s * (kStage >> 4)), xd = wd + (TN * kBlkK >> 4);
 #pragma unroll
             for (int kk = 0; kk < kBlkK / 32; ++kk)
-              tc_mma_f8(tmem_base + a * kTmN, xd + 2 * kk, wd + 2 * kk, idesc, kk ? 1u : 0u);
+              tc_mma_f8(tmem_base + a * TN, xd + 2 * kk, wd + 2 * kk, idesc, kk ? 1u : 0u);
             tc_commit(&empty[s]);
             tc_commit(&tfull[a]);
           }
@@ -353,12 +403,12 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
           xr[i] = p.xs + r * p.nkb;
         }
         // MODE 1: the gate's and the up's row of blocks; else the two halves'
-        const int h = (lane >> 3) & 1, wb = MODE == 1 ? t.m + h * nwb : 2 * t.m + h;
+        const int h = (lane >> 3) & 1, wb = MODE == 1 ? t.m + h * nwb : TN == 256 ? 2 * t.m + h : t.m;
         const float* wr = (MODE == 0 ? p.ws : scales_of(p, t.slot)) +
-                          (int64_t)(MODE == 1 || wb < nwb ? wb : 2 * t.m) * p.nkb;
+                          (int64_t)(MODE == 1 || wb < nwb ? wb : wb - 1) * p.nkb;
         for (int k0 = 0; k0 < p.nkb; k0 += kTmScK, ++n) {
           const int slot = n % kScSlots;
-          ok = mbar_wait(&sempty[slot], ((n / kScSlots) & 1) ^ 1, status);
+          ok = tm_wait<MODE>(&sempty[slot], ((n / kScSlots) & 1) ^ 1, status);
           if (!ok) break;
           float* tab = sc_tab + slot * kTmScFloats;
           const int kn = min(kTmScK, p.nkb - k0);
@@ -381,100 +431,112 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
         if (t.skip) continue;
 #pragma unroll 1
         for (int kb = 0; kb < p.nkb; ++kb) {
-          ok = mbar_wait(&empty[s], ph ^ 1, status);
+          ok = tm_wait<MODE>(&empty[s], ph ^ 1, status);
           if (!ok) break;
           mbar_arrive_expect_tx(&full[s], kTileBytes);
-          tma_load_2d(stages + s * kTmStage + 2 * kTileBytes, &maps.x, &full[s], kb * kBlkK, t.b * kTileM);
+          tma_load_2d(stages + s * kStage + TN * kBlkK, &maps.x, &full[s], kb * kBlkK, t.b * kTileM);
           if (++s == p.ns) { s = 0; ph ^= 1; }
         }
       }
     }
   } else if (warp < kTmGatherW0) {
-    regs_inc<MODE == 1 ? 200 : 216>();
+    if (TN == 256) regs_inc<MODE == 1 ? 200 : 216>();
     // ---------------------------------------------------------- epilogue
     const int q = warp & 3, half = (warp - kEpiW0) >> 2;
     const int row = q * 32 + lane;  // TMEM lane = row of the tile
     const int nwb = (p.N + 127) / 128;  // blocks of weight rows
-    uint8_t* const stg = stg_all + (warp - kEpiW0) * kStgBytes;
+    // this warp's staged rows, and this thread's
+    uint8_t* const stg = stg_all + (warp - kEpiW0) * 32 * kStgRow;
+    uint8_t* const mine = stg + lane * kStgRow;
     uint32_t it = 0, sn = 0;
     int par = 0;
     bool ok = true;
     for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
       const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
       const bool live = row < t.nvalid;
-      const int col0 = t.m * kTmN + half * kTileM;  // MODE 0, 2: first column of this warp
+      const int col0 = t.m * TN + half * kCols;  // MODE 0, 2: first column of this warp
       int r = 0;                                    // row of out (MODE 2: the route)
       if (MODE == 2 && live) r = p.g.sorted_ids[(int64_t)t.b * p.g.BN + row];
       if (t.skip) {
         if (MODE == 2 && live && t.slot != kFiltered) {
           // an expert without a slot: its routes get zeros (and a status bit)
           uint16_t* y = static_cast<uint16_t*>(p.out) + (int64_t)r * p.out_ld;
-          for (int c = col0; c < min(col0 + kTileM, p.N); c += 8)
+          for (int c = col0; c < min(col0 + kCols, p.N); c += 8)
             *reinterpret_cast<uint4*>(y + c) = make_uint4(0, 0, 0, 0);
           if (row == 0) set_status(status, OES_DEV_BAD_ID);
         }
         continue;
       }
       const bool on = q * 32 < t.nvalid && (MODE == 1 ? t.m * kTileM + half * 64 : col0) < p.N;
-      float acc[128];
+      float acc[kCols];
 #pragma unroll
-      for (int j = 0; j < 128; ++j) acc[j] = 0.0f;
+      for (int j = 0; j < kCols; ++j) acc[j] = 0.0f;
+      // Columns of this warp's piece c of 32: MODE 1 takes 64 gate columns and
+      // the same 64 up columns, so that a thread has both factors of its h.
+      constexpr int kPieces = kCols / 32;
+      auto piece = [&](int c) {
+        return MODE == 1 ? (c >> 1) * kTileM + half * 64 + (c & 1) * 32 : half * kCols + c * 32;
+      };
 #pragma unroll 1
-      for (int kb = 0; kb < p.nkb; ++kb, ++it) {
-        const uint32_t a = it & 1;
-        const int slot = sn % kScSlots, ki = kb % kTmScK;
-        if (ki == 0) {
-          ok = mbar_wait(&sfull[slot], (sn / kScSlots) & 1, status);
-          if (!ok) break;
-        }
-        const float* tab = sc_tab + slot * kTmScFloats;
-        // MODE 1: 64 gate columns and the same 64 up columns, so that a
-        // thread has both factors of its values of h
-        const float x = tab[ki * kTileM + row];
-        const float s0 = x * tab[kTmScK * kTileM + (MODE == 1 ? 0 : half) * kTmScK + ki];
-        const float s1 = MODE == 1 ? x * tab[kTmScK * kTileM + kTmScK + ki] : s0;
-        if (ki == kTmScK - 1 || kb == p.nkb - 1) {
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sempty[slot]);
-          ++sn;
-        }
-        ok = mbar_wait(&tfull[a], (it >> 1) & 1, status);
+      for (int k0 = 0; k0 < p.nkb; k0 += kTmScK, ++sn) {
+        const int slot = sn % kScSlots;
+        ok = tm_wait<MODE>(&sfull[slot], (sn / kScSlots) & 1, status);
         if (!ok) break;
-        tc_fence_after();
-        if (on) {
-          const uint32_t tl = tmem_base + ((uint32_t)(q * 32) << 16) + a * kTmN;
+        const float* xt = sc_tab + slot * kTmScFloats + row;
+        const float* wt = sc_tab + slot * kTmScFloats + kTmScK * kTileM + (MODE == 1 || TN == 128 ? 0 : half * kTmScK);
+        float s0 = xt[0] * wt[0], s1 = MODE == 1 ? xt[0] * wt[kTmScK] : s0;
+        const int kn = min(kTmScK, p.nkb - k0);
+#pragma unroll 1
+        for (int ki = 0; ki < kn; ++ki, ++it) {
+          const uint32_t a = it % kBufs;
+          ok = tm_wait<MODE>(&tfull[a], (it / kBufs) & 1, status);
+          if (!ok) break;
+          tc_fence_after();
+          // the next block's scales come in while this one's sums do
+          xt += kTileM;
+          ++wt;
+          const bool more = ki + 1 < kn;
+          const float xn = more ? xt[0] : 0.0f, w0 = more ? wt[0] : 0.0f;
+          const float w1 = MODE == 1 && more ? wt[kTmScK] : 0.0f;
+          if (on) {
+            // the loads of one piece run under the FMAs of the one before
+            const uint32_t tl = tmem_base + ((uint32_t)(q * 32) << 16) + a * TN;
+            uint32_t d[2][32];
+            tmem_ld_32(tl + piece(0), d[0]);
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t d[32];
-            tmem_ld_32(tl + (MODE == 1 ? (c >> 1) * kTileM + half * 64 + (c & 1) * 32 : half * kTileM + c * 32), d);
-            tc_wait_ld();
-            if (c == 3) {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&tempty[a]);
+            for (int c = 0; c < kPieces; ++c) {
+              tc_wait_ld();
+              if (c + 1 < kPieces) {
+                tmem_ld_32(tl + piece(c + 1), d[(c + 1) & 1]);
+              } else {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&tempty[a]);
+              }
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                acc[c * 32 + j] = fmaf(__uint_as_float(d[c & 1][j]), c >= kPieces / 2 ? s1 : s0, acc[c * 32 + j]);
             }
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              acc[c * 32 + j] = fmaf(__uint_as_float(d[j]), c >= 2 ? s1 : s0, acc[c * 32 + j]);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&tempty[a]);
           }
-        } else {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&tempty[a]);
+          s0 = xn * w0;
+          s1 = MODE == 1 ? xn * w1 : s0;
         }
+        if (!ok) break;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sempty[slot]);
       }
       if (!ok) break;
-      // piece c (16 bytes) of a row's 64 lies at c ^ (row / 2 % 4): no two of
-      // eight lanes meet in a bank, writing rows or reading pieces
-      uint8_t* const stg_w = stg + lane * 64;
-      const int sw = (lane >> 1) & 3;
       if (MODE == 1) {
         if (q * 32 >= t.nvalid) continue;  // both warps of the quarter
         // h, the amax of its 128 columns with the other half's warp, codes
         float m = 0.0f;
 #pragma unroll
         for (int j = 0; j < 64; ++j) {
-          acc[j] = silu_f32(acc[j]) * acc[64 + j];
+          acc[j] = silu_f32(acc[j]) * acc[kCols / 2 + j];
           m = fmaxf(m, fabsf(acc[j]));
         }
         if (!on) m = 0.0f;
@@ -482,35 +544,30 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
         named_bar(1 + q, 64);
         const QuantScale qs = quant_scale(fmaxf(m, s_amax[par][half ^ 1][row]));
         par ^= 1;
-        const int64_t hr0 = (int64_t)t.b * p.g.BN + q * 32;
-        if (on) {
+        if (live) {
+          const int64_t hr = (int64_t)t.b * p.g.BN + row;
+          if (on) {
+            bulk_wait_read();  // the tile before has left this row
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w[4];
+            for (int c = 0; c < 4; ++c) {
+              uint32_t w[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float* v = acc + c * 16 + 4 * i;
-              w[i] = quant4(v[0], v[1], v[2], v[3], qs);
+              for (int i = 0; i < 4; ++i) {
+                const float* v = acc + c * 16 + 4 * i;
+                w[i] = quant4(v[0], v[1], v[2], v[3], qs);
+              }
+              *reinterpret_cast<uint4*>(mine + c * 16) = make_uint4(w[0], w[1], w[2], w[3]);
             }
-            *reinterpret_cast<uint4*>(stg_w + ((c ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            bulk_store(static_cast<uint8_t*>(p.out) + hr * p.out_ld + t.m * kTileM + half * 64, mine, 64);
           }
-          __syncwarp();
-          uint8_t* h = static_cast<uint8_t*>(p.out) + hr0 * p.out_ld + t.m * kTileM + half * 64;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = 8 * i + (lane >> 2), c = lane & 3;
-            const uint4 v = *reinterpret_cast<const uint4*>(stg + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4));
-            if (q * 32 + rr < t.nvalid) *reinterpret_cast<uint4*>(h + rr * p.out_ld + c * 16) = v;
-          }
-          __syncwarp();
+          if (half == 0) p.hs[hr * nwb + t.m] = qs.s;
         }
-        if (live && half == 0) p.hs[(hr0 + lane) * nwb + t.m] = qs.s;
       } else if (on) {
         constexpr int kPer = 64 / (int)sizeof(OT);  // columns of a piece
         constexpr int kVec = 16 / (int)sizeof(OT);
         if (MODE == 0) r = t.b * kTileM + row;
 #pragma unroll
-        for (int pc = 0; pc < 128 / kPer; ++pc) {
+        for (int pc = 0; pc < kCols / kPer; ++pc) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             uint32_t w[4];
@@ -520,7 +577,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
               if constexpr (sizeof(OT) == 2) w[i] = f32x2_bf16x2(v[2 * i], v[2 * i + 1]);
               else w[i] = __float_as_uint(v[i]);
             }
-            *reinterpret_cast<uint4*>(stg_w + ((c ^ sw) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+            *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
           }
           __syncwarp();
 #pragma unroll
@@ -543,6 +600,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
         }
       }
     }
+    if (MODE == 1) bulk_wait_all();  // the copies out of this CTA's shared memory
   } else if (MODE == 1) {
     regs_dec<56>();
     // ------------------------------------------------------- token gather
@@ -567,10 +625,10 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
       }
 #pragma unroll 1
       for (int kb = 0; kb < p.nkb; ++kb) {
-        if (lane == 0) ok = mbar_wait(&empty[s], ph ^ 1, status);
+        if (lane == 0) ok = tm_wait<MODE>(&empty[s], ph ^ 1, status);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
-        const uint32_t X = smem_u32(stages + s * kTmStage + 2 * kTileBytes);
+        const uint32_t X = smem_u32(stages + s * kStage + TN * kBlkK);
         const bool in = kb * kBlkK + c * 16 < p.K;
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
@@ -687,7 +745,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
         if (t.skip) continue;
 #pragma unroll 1
         for (int kb = k_lo; kb < k_hi; ++kb) {
-          ok = mbar_wait(&empty[s], ph ^ 1, status);
+          ok = bar_wait(&empty[s], ph ^ 1, status);
           if (!ok) break;
           uint8_t* W = stages + s * kStage;
           mbar_arrive_expect_tx(&full[s], kA * kTileBytes);
@@ -712,7 +770,8 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
 #pragma unroll 1
       for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
         const uint32_t a = it % kWmAcc;
-        ok = mbar_wait(&tempty[a], ((it / kWmAcc) & 1) ^ 1, status) && mbar_wait(&full[s], ph, status);
+        ok = bar_wait(&full[s], ph, status);
+        ok = bar_wait(&tempty[a], ((it / kWmAcc) & 1) ^ 1, status) && ok;
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         tc_fence_after();
@@ -747,7 +806,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       const float* w = (MODE == 0 ? p.ws : scales_of(p, t.slot)) + (int64_t)t.m * p.nkb;
       for (int k0 = k_lo; k0 < k_hi; k0 += kWmScK, ++i) {
         const int slot = i % kScSlots, k = k0 + lane;
-        ok = mbar_wait(&sempty[slot], ((i / kScSlots) & 1) ^ 1, status);
+        ok = bar_wait(&sempty[slot], ((i / kScSlots) & 1) ^ 1, status);
         if (!ok) break;
         float* tab = sc_tab + slot * kScFloats;
         for (int n = 0; n < t.nvalid; ++n) {
@@ -773,7 +832,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
         if (t.skip) continue;
 #pragma unroll 1
         for (int kb = k_lo; kb < k_hi; ++kb) {
-          ok = mbar_wait(&empty[s], ph ^ 1, status);
+          ok = bar_wait(&empty[s], ph ^ 1, status);
           if (!ok) break;
           mbar_arrive_expect_tx(&full[s], BN * kBlkK);
           tma_load_2d(stages + s * kStage + kA * kTileBytes, &maps.x, &full[s], kb * kBlkK, t.b * BN);
@@ -816,10 +875,10 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
         const uint32_t a = it % kWmAcc;
         const int slot = sn % kScSlots, ki = (kb - k_lo) % kWmScK;
         if (ki == 0) {
-          ok = mbar_wait(&sfull[slot], (sn / kScSlots) & 1, status);
+          ok = bar_wait(&sfull[slot], (sn / kScSlots) & 1, status);
           if (!ok) break;
         }
-        ok = mbar_wait(&tfull[a], (it / kWmAcc) & 1, status);
+        ok = bar_wait(&tfull[a], (it / kWmAcc) & 1, status);
         if (!ok) break;
         tc_fence_after();
         const float* tab = sc_tab + slot * kScFloats;
@@ -937,7 +996,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       const uint8_t* src = p.x + (int64_t)tk * p.K + c * 16;
 #pragma unroll 1
       for (int kb = k_lo; kb < k_hi; ++kb) {
-        if (lane == 0) ok = mbar_wait(&empty[s], ph ^ 1, status);
+        if (lane == 0) ok = bar_wait(&empty[s], ph ^ 1, status);
         ok = __shfl_sync(0xffffffffu, ok, 0);
         if (!ok) break;
         const bool in = kb * kBlkK + c * 16 < p.K;
@@ -961,19 +1020,21 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
 }
 
 // ------------------------------------------------------------------ launches
-constexpr size_t kSmemBudget = 222 * 1024;
+constexpr size_t kSmemBudget = 227 * 1024 - 2560;  // beside the kernels' static shared memory
+constexpr int kTmN0 = 256, kTmN2 = 128;  // weight rows a tile: dense, down
 
-template <int MODE, typename OT>
+template <int MODE, typename OT, int TN>
 int launch_tm(const Fp8Maps& maps, Fp8Params p, cudaStream_t stream) {
   p.ks_log = 0;
-  p.ns = 4;
-  const size_t smem = 1024 + (size_t)p.ns * kTmStage + (2 * p.ns + 4 + 2 * kScSlots) * 8 + 16 +
-                      kMaxUnitsPerCta * sizeof(UnitRec) + kTmEpi * kStgBytes + kScSlots * kTmScFloats * 4;
-  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(fp8_tm_kernel<MODE, OT>), smem,
+  const size_t fixed = 1024 + 64 * 8 + 16 + (MODE == 0 ? 0 : kMaxUnitsPerCta * sizeof(UnitRec)) +
+                       kTmEpi * 32 * stg_row(MODE) + kScSlots * kTmScFloats * 4;
+  p.ns = (int)std::min<size_t>(6, (kSmemBudget - fixed) / tm_stage(TN));
+  const size_t smem = fixed + (size_t)p.ns * tm_stage(TN);
+  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(fp8_tm_kernel<MODE, OT, TN>), smem,
                                 "fp8_tm_kernel: shared memory limit");
   if (rc) return rc;
   const int64_t units = MODE == 0 ? (int64_t)p.mt * p.nt : INT64_MAX;
-  launch_kernel(fp8_tm_kernel<MODE, OT>, (int)std::min<int64_t>(num_sms(), units), tm_threads(MODE), smem, stream, maps, p);
+  launch_kernel(fp8_tm_kernel<MODE, OT, TN>, (int)std::min<int64_t>(num_sms(), units), tm_threads(MODE), smem, stream, maps, p);
   OES_CHECK_LAUNCH("fp8_tm_kernel");
   return OES_OK;
 }
@@ -1046,9 +1107,10 @@ int fp8_gemm_run(const GemmPlan& g, const GemmParams& p1, const GemmParams& p2, 
   p.out = g.f8.hq;
   p.out_ld = p1.I;
   p.hs = g.f8.hs;
-  int rc = g.tm ? launch_tm<1, uint16_t>(m, p, stream) : launch_wm<1, 16>(m, p, blocks * p1.n_mtiles, stream);
+  int rc = g.tm ? launch_tm<1, uint16_t, 256>(m, p, stream) : launch_wm<1, 16>(m, p, blocks * p1.n_mtiles, stream);
   if (rc) return rc;
   p.g = p2;
+  if (g.tm) p.g.n_mtiles = ceil_div(p1.H, kTmN2);
   m.w = g.m2.a;
   m.x = g.m2.b;
   p.xs = g.f8.hs;
@@ -1058,7 +1120,7 @@ int fp8_gemm_run(const GemmPlan& g, const GemmParams& p1, const GemmParams& p2, 
   p.nkb = p2.n_kc;
   p.out = p2.y;
   p.out_ld = p1.H;
-  return g.tm ? launch_tm<2, uint16_t>(m, p, stream) : launch_wm<2, 16>(m, p, blocks * p2.n_mtiles, stream);
+  return g.tm ? launch_tm<2, uint16_t, kTmN2>(m, p, stream) : launch_wm<2, 16>(m, p, blocks * p2.n_mtiles, stream);
 }
 
 }  // namespace oes
@@ -1082,7 +1144,7 @@ extern "C" int moe_fp8_gemm(const uint8_t* xq, int64_t xq_ld, const float* xs, i
               "moe_fp8_gemm: a pointer is not aligned to its type");
   // The token-major kernel once its tiles fill most of the GPU; below that
   // its few CTAs would each walk the whole of K.
-  const int64_t tiles = (int64_t)ceil_div(T, kTileM) * ceil_div(N, kTmN);
+  const int64_t tiles = (int64_t)ceil_div(T, kTileM) * ceil_div(N, kTmN0);
   const bool tm = tiles * 4 >= (int64_t)num_sms() * 3;
   const int bn = tm ? kTileM : T <= 16 ? 16 : 64;
   Fp8Params p{};
@@ -1094,12 +1156,12 @@ extern "C" int moe_fp8_gemm(const uint8_t* xq, int64_t xq_ld, const float* xs, i
   p.K = K;
   p.nkb = ceil_div(K, kQuantGroup);
   p.mt = ceil_div(T, bn);
-  p.nt = ceil_div(N, tm ? kTmN : kTileM);
+  p.nt = ceil_div(N, tm ? kTmN0 : kTileM);
   OES_REQUIRE((int64_t)p.mt * p.nt <= 0x7FFFFFFF - 4096, "moe_fp8_gemm: too many tiles (T=%d N=%d)", T, N);
   p.out = out;
   p.out_ld = out_ld;
   p.out_f32 = dtype == OES_F32;
-  p.vec = ((uintptr_t)out & 15) == 0 && out_ld % (p.out_f32 ? 4 : 8) == 0;
+  p.vec = ((uintptr_t)out & 15) == 0 && out_ld % (p.out_f32 ? 4 : 8) == 0 && N % (p.out_f32 ? 4 : 8) == 0;
   Fp8Maps m;
   const CUtensorMapDataType u8 = CU_TENSOR_MAP_DATA_TYPE_UINT8;
   const uint64_t dw[3] = {(uint64_t)K, (uint64_t)N, 1}, sw[2] = {(uint64_t)wq_ld, (uint64_t)wq_ld * N};
@@ -1109,7 +1171,7 @@ extern "C" int moe_fp8_gemm(const uint8_t* xq, int64_t xq_ld, const float* xs, i
   const uint64_t dx[2] = {(uint64_t)K, (uint64_t)T}, sx[1] = {(uint64_t)xq_ld};
   const uint32_t bx[2] = {kBlkK, (uint32_t)bn};
   if ((rc = encode_tiled(&m.x, u8, 2, xq, dx, sx, bx, CU_TENSOR_MAP_SWIZZLE_128B))) return rc;
-  if (tm) return p.out_f32 ? launch_tm<0, float>(m, p, stream) : launch_tm<0, uint16_t>(m, p, stream);
+  if (tm) return p.out_f32 ? launch_tm<0, float, kTmN0>(m, p, stream) : launch_tm<0, uint16_t, kTmN0>(m, p, stream);
   const int64_t units = (int64_t)p.mt * p.nt;
   return bn == 16 ? launch_wm<0, 16>(m, p, units, stream) : launch_wm<0, 64>(m, p, units, stream);
 }

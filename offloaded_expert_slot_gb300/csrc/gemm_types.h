@@ -14,7 +14,7 @@ struct GemmMaps {
   CUtensorMap a;   // 16-bit weights [S][rows][K] (bf16 path)
   CUtensorMap q;   // NVFP4 values [S][rows][K/2] bytes
   CUtensorMap sc;  // NVFP4 scales [S][K/64][rows] u32
-  CUtensorMap b;   // GEMM2: h [cap][I]
+  CUtensorMap b;   // GEMM2: h [cap][I]; FP8 GEMM1: x [T][H], a row at a time
 };
 
 struct GemmParams {
