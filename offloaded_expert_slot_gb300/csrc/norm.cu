@@ -20,15 +20,43 @@ namespace oes {
 namespace {
 
 constexpr int kMaxH = 16384;
+constexpr int kNormResident = 512;  // threads an SM holds at once
+
+// CTAs an SM shall hold, 0 to leave that to the compiler: rows of single values
+// are short of loads in flight, so their threads get 64 registers at most.
+constexpr int norm_ctas(int vec, int maxt) { return vec == 1 && maxt <= 512 ? 2 : 0; }
+
+// VEC values of a row as they lie in memory.
+template <int VEC, typename T>
+struct Raw {
+  T v[VEC];
+  __device__ __forceinline__ void load(const T* p) {
+    if constexpr (VEC == 8) {
+#pragma unroll
+      for (int i = 0; i < (int)sizeof(T) / 2; ++i) reinterpret_cast<uint4*>(v)[i] = reinterpret_cast<const uint4*>(p)[i];
+    } else {
+#pragma unroll
+      for (int i = 0; i < VEC; ++i) v[i] = p[i];
+    }
+  }
+  __device__ __forceinline__ float at(int i) const {
+    if constexpr (sizeof(T) == 2) return bf16_f32(v[i]);
+    else return v[i];
+  }
+};
 
 // RT: uint16_t (bf16) or float residual.  Value e of chunk j of a row belongs
 // to thread (j * threads + tid) as value VEC * that + e.  WARP: a warp a row,
-// else a CTA a row.
-template <int VEC, int NV, bool WARP, typename RT>
-__global__ void __launch_bounds__(WARP ? 128 : 1024) block_norm_kernel(const oes_block_norm p) {
+// else a CTA a row.  GATED: the gate has a value a channel or an element.  A
+// CTA walks rows; where registers allow (kAhead) its weights stay in them and
+// the next row is on its way while this one is reduced.
+template <int VEC, int NV, bool WARP, int MAXT, bool GATED, typename RT>
+__global__ void __launch_bounds__(MAXT, norm_ctas(VEC, MAXT)) block_norm_kernel(const oes_block_norm p) {
   pdl_begin();
+  constexpr bool kAhead = VEC == 8 && MAXT <= 512;
   __shared__ float red[2][32];
   __shared__ float gmax[VEC == 1 ? NV : 1][32];
+  __shared__ QuantScale gscale[VEC == 1 ? NV : 1][8];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int nthr = WARP ? 32 : blockDim.x;
   const int tid = WARP ? lane : threadIdx.x;
@@ -43,31 +71,62 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) block_norm_kernel(const oes
     __syncthreads();
     s = lane < nw ? red[which][lane] : 0.0f;
 #pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    return s;
+    for (int o = MAXT / 64; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return __shfl_sync(0xffffffffu, s, 0);
   };
-  for (int64_t row = WARP ? (int64_t)blockIdx.x * nw + warp : blockIdx.x; row < p.T; row += step) {
-    float r[NV][VEC];
-    float v[NV][VEC];
-    const RT* rp = static_cast<const RT*>(p.residual) + row * p.residual_ld;
-    const uint16_t* yp = p.y ? p.y + row * p.y_ld : nullptr;
-    float s = 0.0f;
+  auto col = [&](int j) { return (j * nthr + tid) * VEC; };
+  using W = Raw<VEC, uint16_t>;
+  auto load_w = [&](const uint16_t* w, int j) {
+    W x = {};
+    if (w && col(j) < p.H) x.load(w + col(j));
+    return x;
+  };
+  W wpost[NV], wpre[NV];
+  if (kAhead) {
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
-      const int c = (j * nthr + tid) * VEC;
-#pragma unroll
-      for (int e = 0; e < VEC; ++e) r[j][e] = v[j][e] = 0.0f;
-      if (c < p.H) {
-        load_vals<VEC>(rp + c, r[j]);
-        if (yp) load_vals<VEC>(yp + c, v[j]);
-      }
+      wpost[j] = load_w(p.post_weight, j);
+      wpre[j] = load_w(p.pre_weight, j);
     }
-    if (yp) {
-      float k = p.residual_scale;
-      if (p.gate_kind == OES_GATE_TOKEN) {
-        const float g = static_cast<const float*>(p.gate)[row * p.gate_ld];
-        k *= p.gate_sigmoid ? sigmoid_f32(g) : g;
+  }
+  Raw<VEC, RT> rn[NV] = {};
+  W yn[NV] = {};
+  float gn = 0.0f;
+  auto fetch = [&](int64_t row) {
+    if (row >= p.T) return;
+#pragma unroll
+    for (int j = 0; j < NV; ++j) {
+      if (col(j) >= p.H) continue;
+      rn[j].load(static_cast<const RT*>(p.residual) + row * p.residual_ld + col(j));
+      if (p.y) yn[j].load(p.y + row * p.y_ld + col(j));
+    }
+    if (p.gate_kind == OES_GATE_TOKEN) gn = static_cast<const float*>(p.gate)[row * p.gate_ld];
+  };
+  int64_t row = WARP ? (int64_t)blockIdx.x * nw + warp : blockIdx.x;
+  if (kAhead) fetch(row);
+  for (; row < p.T; row += step) {
+    float r[NV][VEC];
+    float v[NV][VEC];
+    if (!kAhead) fetch(row);
+    const float gt = gn;
+    W ge[GATED ? NV : 1];
+    if (GATED) {
+      const uint16_t* g = static_cast<const uint16_t*>(p.gate) + (p.gate_kind == OES_GATE_ELEMENT ? row * p.gate_ld : 0);
+#pragma unroll
+      for (int j = 0; j < NV; ++j) ge[j] = load_w(g, j);
+    }
+#pragma unroll
+    for (int j = 0; j < NV; ++j)
+#pragma unroll
+      for (int e = 0; e < VEC; ++e) {
+        r[j][e] = col(j) < p.H ? rn[j].at(e) : 0.0f;
+        v[j][e] = p.y && col(j) < p.H ? yn[j].at(e) : 0.0f;
       }
+    if (kAhead) fetch(row + step);
+    float s = 0.0f;
+    if (p.y) {
+      float k = p.residual_scale;
+      if (p.gate_kind == OES_GATE_TOKEN) k *= p.gate_sigmoid ? sigmoid_f32(gt) : gt;
       float inv = 1.0f;
       if (p.post_weight) {
 #pragma unroll
@@ -78,33 +137,24 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) block_norm_kernel(const oes
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (j * nthr + tid) * VEC;
-        if (c >= p.H) continue;
-        if (p.post_weight) {
-          float w[VEC];
-          load_vals<VEC>(p.post_weight + c, w);
+        if (col(j) >= p.H) continue;
+        const W w = kAhead ? wpost[j] : load_w(p.post_weight, j);
 #pragma unroll
-          for (int e = 0; e < VEC; ++e) v[j][e] = v[j][e] * inv * (p.weight_offset + w[e]);
+        for (int e = 0; e < VEC; ++e) {
+          if (p.post_weight) v[j][e] = v[j][e] * inv * (p.weight_offset + w.at(e));
+          if (GATED) {
+            const float g = ge[j].at(e);
+            v[j][e] *= p.gate_sigmoid ? sigmoid_f32(g) : g;
+          }
+          r[j][e] = fmaf(k, v[j][e], r[j][e]);
         }
-        if (p.gate_kind == OES_GATE_CHANNEL || p.gate_kind == OES_GATE_ELEMENT) {
-          float g[VEC];
-          load_vals<VEC>(static_cast<const uint16_t*>(p.gate) +
-                             (p.gate_kind == OES_GATE_ELEMENT ? row * p.gate_ld : 0) + c,
-                         g);
-#pragma unroll
-          for (int e = 0; e < VEC; ++e) v[j][e] *= p.gate_sigmoid ? sigmoid_f32(g[e]) : g[e];
-        }
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) r[j][e] = fmaf(k, v[j][e], r[j][e]);
       }
     }
     if (p.out_residual) {
       RT* op = static_cast<RT*>(p.out_residual) + row * p.out_residual_ld;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (j * nthr + tid) * VEC;
-        if (c < p.H) store_vals<VEC>(op + c, r[j]);
-      }
+      for (int j = 0; j < NV; ++j)
+        if (col(j) < p.H) store_vals<VEC>(op + col(j), r[j]);
     }
     if (!p.out && !p.out_q) continue;
     if (p.pre_weight) {
@@ -116,21 +166,17 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) block_norm_kernel(const oes
       const float inv = rsqrtf(row_sum(s, 1) * inv_h + p.eps);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (j * nthr + tid) * VEC;
-        if (c >= p.H) continue;
-        float w[VEC];
-        load_vals<VEC>(p.pre_weight + c, w);
+        if (col(j) >= p.H) continue;
+        const W w = kAhead ? wpre[j] : load_w(p.pre_weight, j);
 #pragma unroll
-        for (int e = 0; e < VEC; ++e) r[j][e] = r[j][e] * inv * (p.weight_offset + w[e]);
+        for (int e = 0; e < VEC; ++e) r[j][e] = r[j][e] * inv * (p.weight_offset + w.at(e));
       }
     }
     if (p.out) {
       uint16_t* op = p.out + row * p.out_ld;
 #pragma unroll
-      for (int j = 0; j < NV; ++j) {
-        const int c = (j * nthr + tid) * VEC;
-        if (c < p.H) store_vals<VEC>(op + c, r[j]);
-      }
+      for (int j = 0; j < NV; ++j)
+        if (col(j) < p.H) store_vals<VEC>(op + col(j), r[j]);
     }
     if (p.out_q) {
       uint8_t* qp = p.out_q + row * p.out_q_ld;
@@ -148,18 +194,19 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) block_norm_kernel(const oes
         if (VEC == 1 && lane == 0) gmax[j][warp] = a[j];
       }
       if (VEC == 1) {
+        // a group's scale is worked out once, by one of its four warps
         __syncthreads();
-#pragma unroll
-        for (int j = 0; j < NV; ++j) {
-          const float* g = gmax[j] + (warp & ~3);
-          a[j] = fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3]));
+        if ((warp & 3) == 0 && lane < NV) {
+          const float* g = gmax[lane] + warp;
+          gscale[lane][warp >> 2] = quant_scale(fmaxf(fmaxf(g[0], g[1]), fmaxf(g[2], g[3])));
         }
+        __syncthreads();
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
-        const int c = (j * nthr + tid) * VEC;
+        const int c = col(j);
         if (c >= p.H) continue;
-        const QuantScale qs = quant_scale(a[j]);
+        const QuantScale qs = VEC == 8 ? quant_scale(a[j]) : gscale[VEC == 8 ? 0 : j][warp >> 2];
         if constexpr (VEC == 8) {
           *reinterpret_cast<uint2*>(qp + c) =
               make_uint2(quant4(r[j][0], r[j][1], r[j][2], r[j][3], qs),
@@ -174,16 +221,22 @@ __global__ void __launch_bounds__(WARP ? 128 : 1024) block_norm_kernel(const oes
   }
 }
 
-template <int VEC, int NV, bool WARP>
+template <int VEC, int NV, bool WARP, int MAXT>
 int launch_norm(const oes_block_norm& p, int threads, cudaStream_t stream) {
   const int rows = WARP ? threads / 32 : 1;
   const int64_t want = ceil_div64(p.T, rows);
-  // CTAs that can be resident at once, so that each loops over its rows
-  const int grid = (int)std::min<int64_t>(want, (int64_t)num_sms() * std::max(1, 2048 / threads));
-  if (p.dtype == OES_BF16)
-    launch_kernel(block_norm_kernel<VEC, NV, WARP, uint16_t>, grid, threads, 0, stream, p);
-  else
-    launch_kernel(block_norm_kernel<VEC, NV, WARP, float>, grid, threads, 0, stream, p);
+  // about the CTAs that are resident at once, so that each walks its rows
+  const int grid =
+      (int)std::min<int64_t>(want, (int64_t)num_sms() * std::max(1, (VEC == 8 ? kNormResident : 2048) / threads));
+  auto go = [&](auto kernel) { launch_kernel(kernel, grid, threads, 0, stream, p); };
+  const bool gated = p.gate_kind >= OES_GATE_CHANNEL;
+  if (p.dtype == OES_BF16) {
+    if (gated) go(block_norm_kernel<VEC, NV, WARP, MAXT, true, uint16_t>);
+    else go(block_norm_kernel<VEC, NV, WARP, MAXT, false, uint16_t>);
+  } else {
+    if (gated) go(block_norm_kernel<VEC, NV, WARP, MAXT, true, float>);
+    else go(block_norm_kernel<VEC, NV, WARP, MAXT, false, float>);
+  }
   OES_CHECK_LAUNCH("block_norm_kernel");
   return OES_OK;
 }
@@ -237,12 +290,14 @@ extern "C" int moe_block_norm(const oes_block_norm* a, oes_stream_t stream) {
                    (!p.out_q || (at(p.out_q, 8) && p.out_q_ld % 8 == 0));
   auto up = [](int n, int m) { return (n + m - 1) / m * m; };
   if (vec) {
-    const int c = p.H / 8;
-    if (c <= 32) return launch_norm<8, 1, true>(p, 128, stream);
-    if (c <= 64) return launch_norm<8, 2, true>(p, 128, stream);
-    if (c <= 1024) return launch_norm<8, 1, false>(p, up(c, 32), stream);
-    return launch_norm<8, 2, false>(p, up(ceil_div(c, 2), 32), stream);
+    const int c = p.H / 8, half = up(ceil_div(c, 2), 32);  // 16 values a thread
+    if (c <= 64) return launch_norm<8, 2, true, 128>(p, 128, stream);
+    if (half <= 128) return launch_norm<8, 2, false, 128>(p, half, stream);
+    if (half <= 256) return launch_norm<8, 2, false, 256>(p, half, stream);
+    if (half <= 512) return launch_norm<8, 2, false, 512>(p, half, stream);
+    return launch_norm<8, 2, false, 1024>(p, half, stream);
   }
-  if (p.H <= 4096) return launch_norm<1, 4, false>(p, up(ceil_div(p.H, 4), 128), stream);
-  return launch_norm<1, 16, false>(p, up(ceil_div(p.H, 16), 128), stream);
+  if (p.H <= 2048) return launch_norm<1, 4, false, 512>(p, up(ceil_div(p.H, 4), 128), stream);
+  if (p.H <= 4096) return launch_norm<1, 4, false, 1024>(p, up(ceil_div(p.H, 4), 128), stream);
+  return launch_norm<1, 16, false, 1024>(p, up(ceil_div(p.H, 16), 128), stream);
 }
