@@ -155,9 +155,7 @@ def load(build_if_missing: bool = False):
 
 
 def _ptr(x):
-    if x is None:
-        return None
-    if isinstance(x, int):
+    if x is None or isinstance(x, int):
         return x
     if hasattr(x, "data_ptr"):
         return x.data_ptr()
@@ -166,10 +164,28 @@ def _ptr(x):
     raise TypeError(f"cannot take the address of {type(x)}")
 
 
+_current_stream = None
+
+
+def _torch_stream() -> int:
+    """torch's current stream as a raw handle; the raw getter where this torch
+    has one (a Stream object costs several microseconds a call)."""
+    global _current_stream
+    if _current_stream is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        dev = getattr(torch._C, "_cuda_getDevice", None)
+        if raw is None or dev is None:
+            _current_stream = lambda: torch.cuda.current_stream().cuda_stream  # noqa: E731
+        else:
+            torch.cuda.current_stream()      # initialises CUDA
+            _current_stream = lambda: raw(dev())  # noqa: E731
+    return _current_stream()
+
+
 def _stream(s):
     if s is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        return _torch_stream()
     if isinstance(s, int):
         return s
     return s.cuda_stream
@@ -180,9 +196,16 @@ def _check(rc: int, func: str):
         raise OesError(rc, func, (load().oes_last_error() or b"").decode())
 
 
+_funcs: dict = {}
+
+
 def _call(name, *args):
-    rc = getattr(load(), name)(*args)
-    _check(rc, name)
+    f = _funcs.get(name)
+    if f is None:
+        f = _funcs[name] = getattr(load(), name)
+    rc = f(*args)
+    if rc != OES_OK:
+        _check(rc, name)
 
 
 # ------------------------------------------------------------------- route
@@ -338,15 +361,22 @@ def moe_grouped_gemm_slots(view: RoutedExperts, x, T, k, ids, weights, sorted_id
 
 
 # --------------------------------------------- 8-bit rows and block norms
+_elem_types: dict = {}      # dtype object -> OES_F32 / OES_BF16
+
+
 def _elem_type(a, func, dtype):
     """OES_F32 / OES_BF16 of an array (bf16 or 16-bit bit patterns), unless dtype says which."""
     if dtype is not None:
         return dtype
-    name = str(getattr(a, "dtype", "")).replace("torch.", "")
+    t = getattr(a, "dtype", None)
+    known = _elem_types.get(t)
+    if known is not None:
+        return known
+    name = str(t).replace("torch.", "")
     if name == "float32":
-        return OES_F32
+        return _elem_types.setdefault(t, OES_F32)
     if name in ("bfloat16", "int16", "uint16"):
-        return OES_BF16
+        return _elem_types.setdefault(t, OES_BF16)
     raise TypeError(f"{func}: expected fp32 or bf16 (bit patterns), or dtype=; got {name or type(a)!r}")
 
 
