@@ -16,7 +16,7 @@
 //   token-major: 128 rows x 256 weight rows a tile, for work bound by
 //     arithmetic: a block is 512 cycles of MMA, against about 270 issue slots
 //     a scheduler to drain it.
-//   weight-major: 128 weight rows x 16, 32 or 64 rows a tile, for few rows, bound
+//   weight-major: 128 weight rows x 16 or 32 rows a tile, for few rows, bound
 //     by the stream of weights.  When the tiles do not fill the GPU, the CTAs
 //     of a cluster share a tile's K range and add their sums over distributed
 //     shared memory in a fixed order.
@@ -651,7 +651,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
 }
 
 // =========================================================== weight-major
-// BN rows a tile (16; the dense product 32 or 64 too).  Warps: 0 weights, 1 MMA,
+// BN rows a tile (16; the dense product 32 too).  Warps: 0 weights, 1 MMA,
 // 2 TMEM, 3 rows (TMA), 4-7 epilogue, 8-11 token gather (MODE 1).
 constexpr int kWmAcc = 4;  // TMEM buffers
 // A slot of scales (see above) holds 32 blocks of K: [block][BN] of the rows,
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     fp8_wm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Params p) {
   constexpr int kA = MODE == 1 ? 2 : 1;  // weight tiles a stage (gate and up)
   constexpr int kStage = wm_stage(MODE, BN);
-  constexpr uint32_t kCols = kWmAcc * kA * BN;  // TMEM columns: 64, 128 or 256
+  constexpr uint32_t kCols = kWmAcc * kA * BN;  // TMEM columns: 64 or 128
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages =
       reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -717,7 +717,8 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
   // The down product is launched while the gate and up product runs (which
   // releases it after its set-up): all it reads but h was complete before
   // that kernel passed this wait, so it builds its unit table and streams its
-  // first weights now, and only what reads h waits (below).
+  // first weights now, and only what reads h waits (below).  Tables it reads
+  // without waiting are read through L2.
   if (MODE != 2) pdl_wait();
   if (MODE != 0 && p.g.filter && p.g.gcount && ld_tab<MODE == 2>(p.g.gcount + p.g.filter) == 0) return;
   int nb = 0;
@@ -846,7 +847,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     const int row = q * 32 + lane;  // TMEM lane = weight row of the tile
     const int nwb = (p.N + 127) / 128;
     // log2 of the columns this CTA finishes, from rank * own
-    const int own_log = (BN == 16 ? 4 : BN == 32 ? 5 : 6) - p.ks_log, own = 1 << own_log;
+    const int own_log = (BN == 16 ? 4 : 5) - p.ks_log, own = 1 << own_log;
     uint32_t it = 0, un = 0, sn = 0;
     bool ok = true;
     for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
@@ -857,14 +858,14 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
           // an expert without a slot: its routes get zeros (and a status bit)
           if (wrow < p.N)
             for (int n = 0; n < t.nvalid; ++n)
-              static_cast<uint16_t*>(p.out)[(int64_t)p.g.sorted_ids[(int64_t)t.b * p.g.BN + n] * p.out_ld + wrow] = 0;
+              static_cast<uint16_t*>(p.out)[(int64_t)ld_tab<MODE == 2>(p.g.sorted_ids + (int64_t)t.b * p.g.BN + n) * p.out_ld + wrow] = 0;
           if (row == 0) set_status(status, OES_DEV_BAD_ID);
         }
         continue;
       }
-      // MODE 1, 2: the block's routes, one a lane
+      // MODE 2: the block's routes, one a lane
       int sid = 0;
-      if (MODE != 0 && lane < t.nvalid) sid = p.g.sorted_ids[(int64_t)t.b * p.g.BN + lane];
+      if (MODE == 2 && lane < t.nvalid) sid = ld_tab<true>(p.g.sorted_ids + (int64_t)t.b * p.g.BN + lane);
       float acc[kA][BN];
 #pragma unroll
       for (int i = 0; i < kA; ++i)
@@ -1039,12 +1040,18 @@ int launch_tm(const Fp8Maps& maps, Fp8Params p, cudaStream_t stream) {
   return OES_OK;
 }
 
-// log2 of the CTAs that share a tile: the largest of 8, 4, 2, 1 that keeps
-// every tile resident at once and leaves each CTA at least two blocks of K.
-// units: the most units the launch can have, known on the host.
+// log2 of the CTAs that share a tile: the largest of 8, 4, 2, 1 with every tile
+// resident at once and two blocks of K for each CTA.  Sharing costs about 2 us
+// (the cluster's start, the exchange of sums) and a block 0.35 us, so fewer than
+// 12 blocks are not shared (768 of K: 7.3 us in 128 CTAs, 9.0 in 32 pairs).
+// Clusters of 4 and 8 do not fill the GPU's groups of SMs: 16 clusters of 8 ran
+// in two turns, 18.1 us, where 32 of 4 took 12.9.  units: the most units the
+// launch can have, known on the host.
 int k_shares_log(int64_t units, int nkb) {
+  if (nkb < 12) return 0;
+  const int64_t sms = num_sms();
   for (int l = 3; l > 0; --l)
-    if ((units << l) <= num_sms() && nkb >= (2 << l)) return l;
+    if ((units << l) <= (l == 3 ? sms * 3 / 4 : l == 2 ? sms * 7 / 8 : sms) && nkb >= (2 << l)) return l;
   return 0;
 }
 
@@ -1142,15 +1149,12 @@ extern "C" int moe_fp8_gemm(const uint8_t* xq, int64_t xq_ld, const float* xs, i
   OES_REQUIRE(((uintptr_t)xs & 3) == 0 && ((uintptr_t)ws & 3) == 0 &&
                   ((uintptr_t)out & (dtype == OES_BF16 ? 1 : 3)) == 0,
               "moe_fp8_gemm: a pointer is not aligned to its type");
-  // The token-major kernel once its tiles fill most of the GPU; below that
-  // its few CTAs would each walk the whole of K.
-  const int64_t tiles = (int64_t)ceil_div(T, kTileM) * ceil_div(N, kTmN0);
-  const bool tm = tiles * 4 >= (int64_t)num_sms() * 3;
-  // Else 32 rows a tile while that is one wave of CTAs, 64 after: 200 x 2048 x
-  // 768 takes 7.3 us against 13.0 (32 rows 112 CTAs, 64 rows 64 pairs), 600 x
-  // 1536 x 2048 takes 15.1 us with 64 rows against 18.0.
-  const bool narrow = (int64_t)ceil_div(T, 32) * ceil_div(N, kTileM) <= num_sms();
-  const int bn = tm ? kTileM : T <= 16 ? 16 : narrow ? 32 : 64;
+  // Weight-major tiles of 16 or 32 rows while they are one wave of CTAs, else
+  // token-major ones: 384 x 1536 x 2048 takes 10.9 us weight-major (144 tiles)
+  // and 13.1 token-major, 512 rows 15.1 (in tiles of 64, gone since) and 13.2,
+  // 1024 rows 25.6 and 13.3.
+  const bool tm = T > 16 && (int64_t)ceil_div(T, 32) * ceil_div(N, kTileM) > num_sms();
+  const int bn = tm ? kTileM : T <= 16 ? 16 : 32;
   Fp8Params p{};
   p.g.status = status;
   p.xs = xs;
@@ -1177,6 +1181,5 @@ extern "C" int moe_fp8_gemm(const uint8_t* xq, int64_t xq_ld, const float* xs, i
   if ((rc = encode_tiled(&m.x, u8, 2, xq, dx, sx, bx, CU_TENSOR_MAP_SWIZZLE_128B))) return rc;
   if (tm) return p.out_f32 ? launch_tm<0, float, kTmN0>(m, p, stream) : launch_tm<0, uint16_t, kTmN0>(m, p, stream);
   const int64_t units = (int64_t)p.mt * p.nt;
-  if (bn == 16) return launch_wm<0, 16>(m, p, units, stream);
-  return bn == 32 ? launch_wm<0, 32>(m, p, units, stream) : launch_wm<0, 64>(m, p, units, stream);
+  return bn == 16 ? launch_wm<0, 16>(m, p, units, stream) : launch_wm<0, 32>(m, p, units, stream);
 }

@@ -141,7 +141,10 @@ CASES = [case("one_token", 1, 4, 16, 256, 192), case("one_route", 1, 1, 1, 128, 
          case("narrow", 5, 2, 8, 64, 64), case("wide_blocks", 160, 8, 12, 128, 128),
          case("ragged", 96, 4, 16, 320, 192), case("one_expert", 300, 1, 1, 256, 128),
          case("two_full_blocks", 256, 1, 1, 128, 320), case("long_k", 3, 2, 4, 4096, 128),
-         case("long_i", 130, 2, 4, 128, 2048), case("many_units", 64, 8, 64, 1152, 384)]
+         case("long_i", 130, 2, 4, 128, 2048), case("many_units", 64, 8, 64, 1152, 384),
+         # K shared by a cluster in both products, blocks part full and full
+         case("shared_k", 3, 2, 4, 1600, 2048), case("shared_k_full", 16, 1, 1, 2048, 1600),
+         case("shared_k_two", 24, 2, 8, 1536, 1536)]
 
 
 @pytest.mark.parametrize("cfg", CASES, ids=lambda c: c.name)
@@ -218,6 +221,29 @@ def test_pool_past_4_gib():
     e.pool, e.e2s, e.cfg = pool, cuda(slots), scaled(cfg, S=S)
     assert torch.equal(e.run(), near)
     assert e.status == 0
+
+
+@pytest.mark.parametrize("T", [5, 70])
+def test_nan_and_infinity_stay_with_their_token(T):
+    cfg = case("nan", T, 2, 4, 256, 192)
+    e = Experts(cfg)
+    clean = e.run().clone()
+    e.x[1, 7] = 0x7FC0            # NaN
+    e.x[3, 200] = 0x7F80          # infinity
+    out = e.run()
+    assert e.status == 0
+    bad = torch.isnan(out.float()).any(1)
+    assert bad[1] and bad[3] and int(bad.sum()) == 2
+    keep = ~bad
+    assert torch.equal(out[keep], clean[keep])
+
+
+def test_no_tokens():
+    cfg = case("none", 0, 2, 4, 256, 192)
+    lib()
+    view = oes.routed_experts(0, 4, 16, oes.OES_WFMT_FP8, 16, cfg.row_bytes, cfg.S, 256, 192)
+    oes.moe_grouped_gemm_slots(view, 16, 0, 2, 16, 16, 16, 16, 16, oes.oes_tile_plan(0, 4), 256, 1 << 20, 16, 0)
+    torch.cuda.synchronize()
 
 
 # ------------------------------------------------------------- layer paths
