@@ -116,25 +116,62 @@ __device__ __forceinline__ const float* scales_of(const Fp8Params& p, int slot) 
   return reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(p.ws) + (int64_t)slot * p.g.row_bytes);
 }
 
-// The bounded wait of these kernels.  The loop is in the asm, so that a warp
-// that waits together stays together: written as a loop in C++, with a lane's
-// own exit, each hand-off between MMA and epilogue took 60 cycles longer.
-__device__ __forceinline__ bool bar_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
-  uint32_t ok;
-  asm volatile(
-      "{ .reg .pred p; .reg .u32 n; mov.u32 n, 0;\n"
-      "W%=: mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-      "@p bra D%=;\n"
-      "add.u32 n, n, 1;\n"
-      "setp.lt.u32 p, n, %3;\n"
-      "@p bra W%=;\n"
-      "D%=: selp.u32 %0, 1, 0, p; }"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity), "n"(kWaitLimit)
-      : "memory");
-  if (!ok) set_status(status, OES_DEV_TIMEOUT);
-  return ok != 0;
-}
+// The bounded waits of a CTA's warps, all lanes of a warp together.  One that
+// gives up sets the status and the CTA's flag; from then on no wait lasts and
+// nothing more is loaded, but every warp walks its loops to their end, so that
+// no barrier between warps is left short.  That the first test stands alone,
+// that no wait has an exit of its own and that the flag costs no register
+// matters: with a result to test after each wait 4096 x 8192 x 4096 took 131 us,
+// with a flag in a register 119, like this 116.  LOOP_ASM: the loop in one asm
+// block, 3 % better for the experts' kernels and 10 % worse for the dense one.
+template <bool LOOP_ASM>
+struct Waits {
+  int32_t* status;
+  volatile int* flag;
+  __device__ __forceinline__ bool dead() const { return *flag != 0; }
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
+    if (!mbar_try_wait(bar, parity)) slow(bar, parity);
+  }
+  __device__ __forceinline__ void slow(uint64_t* bar, uint32_t parity) {
+    if (dead()) return;
+    if (LOOP_ASM) {
+      uint32_t ok;
+      asm volatile(
+          "{ .reg .pred p; .reg .u32 n; mov.u32 n, 0;\n"
+          "W%=: mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+          "@p bra D%=;\n"
+          "add.u32 n, n, 1;\n"
+          "setp.lt.u32 p, n, %3;\n"
+          "@p bra W%=;\n"
+          "D%=: selp.u32 %0, 1, 0, p; }"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "n"(kWaitLimit)
+          : "memory");
+      if (!ok) give_up();
+    } else if (!mbar_wait(bar, parity, status)) {
+      *flag = 1;
+    }
+  }
+  __device__ __forceinline__ void give_up() {
+    set_status(status, OES_DEV_TIMEOUT);
+    *flag = 1;
+  }
+  // arrivals and data come from other CTAs of the cluster
+  __device__ __forceinline__ void cluster(uint64_t* bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+      uint32_t ok;
+      asm volatile(
+          "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 "
+          "%0, 1, 0, p; }"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity)
+          : "memory");
+      if (ok || dead()) return;
+      if (i > 64) __nanosleep(32);
+    }
+    give_up();
+  }
+};
 // D[tmem] (+)= A[smem] * B[smem]^T, kind::f8f6f4 (e4m3 inputs, fp32 sums)
 __device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc,
                                           uint32_t idesc, uint32_t accumulate) {
@@ -162,6 +199,10 @@ __device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t (&r)[32]) {
       : "r"(taddr)
       : "memory");
 }
+// The warp's index, in a form the compiler can see is the same for all lanes:
+// what follows from it then needs no registers of each thread (a 256-wide
+// tile's kernel spilled 32 bytes a thread without, 8 with).
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
   asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(r));
@@ -213,21 +254,6 @@ __device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-__device__ __forceinline__ bool mbar_wait_cluster(uint64_t* bar, uint32_t parity, int32_t* status) {
-  for (uint32_t i = 0; i < kWaitLimit; ++i) {
-    uint32_t ok;
-    asm volatile(
-        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 "
-        "%0, 1, 0, p; }"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity)
-        : "memory");
-    if (ok) return true;
-    if (i > 64) __nanosleep(32);
-  }
-  set_status(status, OES_DEV_TIMEOUT);
-  return false;
-}
 __device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
@@ -260,14 +286,6 @@ __host__ __device__ constexpr int tm_threads(int mode) { return mode == 1 ? 512 
 // Registers: the launch gives every thread 65536 / threads; the epilogue
 // warps (128 sums each) take what the other warpgroups give back.
 // MODE 1: 512 x 128 = 128 (56 + 2 x 200 + 56).  Else 384 x 168 = 128 (72 + 2 x 216).
-// The dense kernel keeps the library's wait: it measured 135 us at 4096 x 8192 x
-// 4096 with it and 154 us with the asm loop, the experts' kernels 3 % better
-// with the loop.
-template <int MODE>
-__device__ __forceinline__ bool tm_wait(uint64_t* bar, uint32_t parity, int32_t* status) {
-  return MODE == 0 ? mbar_wait(bar, parity, status) : bar_wait(bar, parity, status);
-}
-
 template <int MODE, typename OT, int TN>
 __global__ void __launch_bounds__(tm_threads(MODE), 1)
     fp8_tm_kernel(const __grid_constant__ Fp8Maps maps, const __grid_constant__ Fp8Params p) {
@@ -290,9 +308,11 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
   float* sc_tab = reinterpret_cast<float*>(stg_all + kTmEpi * 32 * kStgRow);
   __shared__ int s_scan[33];
   __shared__ float s_amax[2][2][kTileM];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int32_t* status = p.g.status;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  __shared__ int s_dead;
+  Waits<MODE != 0> wait{p.g.status, &s_dead};
   if (threadIdx.x == 0) {
+    s_dead = 0;
     for (int s = 0; s < p.ns; ++s) {
       // the weights' TMA, and the rows' TMA or gather threads
       mbar_init(&full[s], 1 + (MODE == 1 ? 128 : 1));
@@ -330,16 +350,15 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- weight producer
       int s = 0, ph = 0;
-      bool ok = true;
-      for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
+      for (int u = blockIdx.x, ui = 0; u < total; u += gridDim.x, ++ui) {
         const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
         if (t.skip) continue;
         const int ra = t.m * (MODE == 1 ? kTileM : TN);
         const int rb = MODE == 1 ? p.N + ra : ra + kTileM;
 #pragma unroll 1
         for (int kb = 0; kb < p.nkb; ++kb) {
-          ok = tm_wait<MODE>(&empty[s], ph ^ 1, status);
-          if (!ok) break;
+          wait(&empty[s], ph ^ 1);
+          if (wait.dead()) break;
           uint8_t* W = stages + s * kStage;
           mbar_arrive_expect_tx(&full[s], TN * kBlkK);
           tma_load_3d(W, &maps.w, &full[s], kb * kBlkK, ra, t.slot);
@@ -354,20 +373,17 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
       // each hand-off took 0.09 us longer.
       int s = 0, ph = 0;
       uint32_t it = 0;
-      bool ok = true;
       const uint32_t idesc = idesc_f8(kTileM, TN);
       const uint64_t desc0 = smem_desc_sw128(smem_u32(stages));
       const bool leader = elect_one();
-      for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
+      for (int u = blockIdx.x, ui = 0; u < total; u += gridDim.x, ++ui) {
         const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
         if (t.skip) continue;
 #pragma unroll 1
         for (int kb = 0; kb < p.nkb; ++kb, ++it) {
           const uint32_t a = it % kBufs;
-          ok = tm_wait<MODE>(&full[s], ph, status);
-          ok = tm_wait<MODE>(&tempty[a], ((it / kBufs) & 1) ^ 1, status) && ok;
-          ok = __all_sync(0xffffffffu, ok);
-          if (!ok) break;
+          wait(&full[s], ph);
+          wait(&tempty[a], ((it / kBufs) & 1) ^ 1);
           tc_fence_after();
           if (MODE == 1) fence_proxy_async_smem();  // cp.async-written rows -> tensor core
           if (leader) {
@@ -387,8 +403,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
       // lane l: rows l + 32 i and, of the weights' 2 x 8 scales, one
       const int nwb = (p.N + 127) / 128;  // blocks of weight rows
       uint32_t n = 0;
-      bool ok = true;
-      for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
+      for (int u = blockIdx.x, ui = 0; u < total; u += gridDim.x, ++ui) {
         const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
         if (t.skip) continue;
         const float* xr[4];
@@ -408,8 +423,8 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
                           (int64_t)(MODE == 1 || wb < nwb ? wb : wb - 1) * p.nkb;
         for (int k0 = 0; k0 < p.nkb; k0 += kTmScK, ++n) {
           const int slot = n % kScSlots;
-          ok = tm_wait<MODE>(&sempty[slot], ((n / kScSlots) & 1) ^ 1, status);
-          if (!ok) break;
+          wait(&sempty[slot], ((n / kScSlots) & 1) ^ 1);
+          if (__any_sync(0xffffffffu, wait.dead())) break;
           float* tab = sc_tab + slot * kTmScFloats;
           const int kn = min(kTmScK, p.nkb - k0);
 #pragma unroll
@@ -425,14 +440,13 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
     } else if (MODE != 1 && warp == 3 && lane == 0) {
       // ------------------------------------------------------ rows producer
       int s = 0, ph = 0;
-      bool ok = true;
-      for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
+      for (int u = blockIdx.x, ui = 0; u < total; u += gridDim.x, ++ui) {
         const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
         if (t.skip) continue;
 #pragma unroll 1
         for (int kb = 0; kb < p.nkb; ++kb) {
-          ok = tm_wait<MODE>(&empty[s], ph ^ 1, status);
-          if (!ok) break;
+          wait(&empty[s], ph ^ 1);
+          if (wait.dead()) break;
           mbar_arrive_expect_tx(&full[s], kTileBytes);
           tma_load_2d(stages + s * kStage + TN * kBlkK, &maps.x, &full[s], kb * kBlkK, t.b * kTileM);
           if (++s == p.ns) { s = 0; ph ^= 1; }
@@ -450,8 +464,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
     uint8_t* const mine = stg + lane * kStgRow;
     uint32_t it = 0, sn = 0;
     int par = 0;
-    bool ok = true;
-    for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
+    for (int u = blockIdx.x, ui = 0; u < total; u += gridDim.x, ++ui) {
       const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
       const bool live = row < t.nvalid;
       const int col0 = t.m * TN + half * kCols;  // MODE 0, 2: first column of this warp
@@ -463,7 +476,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
           uint16_t* y = static_cast<uint16_t*>(p.out) + (int64_t)r * p.out_ld;
           for (int c = col0; c < min(col0 + kCols, p.N); c += 8)
             *reinterpret_cast<uint4*>(y + c) = make_uint4(0, 0, 0, 0);
-          if (row == 0) set_status(status, OES_DEV_BAD_ID);
+          if (row == 0) set_status(p.g.status, OES_DEV_BAD_ID);
         }
         continue;
       }
@@ -480,8 +493,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
 #pragma unroll 1
       for (int k0 = 0; k0 < p.nkb; k0 += kTmScK, ++sn) {
         const int slot = sn % kScSlots;
-        ok = tm_wait<MODE>(&sfull[slot], (sn / kScSlots) & 1, status);
-        if (!ok) break;
+        wait(&sfull[slot], (sn / kScSlots) & 1);
         const float* xt = sc_tab + slot * kTmScFloats + row;
         const float* wt = sc_tab + slot * kTmScFloats + kTmScK * kTileM + (MODE == 1 || TN == 128 ? 0 : half * kTmScK);
         float s0 = xt[0] * wt[0], s1 = MODE == 1 ? xt[0] * wt[kTmScK] : s0;
@@ -489,8 +501,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
 #pragma unroll 1
         for (int ki = 0; ki < kn; ++ki, ++it) {
           const uint32_t a = it % kBufs;
-          ok = tm_wait<MODE>(&tfull[a], (it / kBufs) & 1, status);
-          if (!ok) break;
+          wait(&tfull[a], (it / kBufs) & 1);
           tc_fence_after();
           // the next block's scales come in while this one's sums do
           xt += kTileM;
@@ -525,11 +536,9 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
           s0 = xn * w0;
           s1 = MODE == 1 ? xn * w1 : s0;
         }
-        if (!ok) break;
         __syncwarp();
         if (lane == 0) mbar_arrive(&sempty[slot]);
       }
-      if (!ok) break;
       if (MODE == 1) {
         if (q * 32 >= t.nvalid) continue;  // both warps of the quarter
         // h, the amax of its 128 columns with the other half's warp, codes
@@ -611,8 +620,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
     const int g = threadIdx.x - kTmGatherW0 * 32;
     const int c = g & 7, r0 = g >> 3;
     int s = 0, ph = 0;
-    bool ok = true;
-    for (int u = blockIdx.x, ui = 0; u < total && ok; u += gridDim.x, ++ui) {
+    for (int u = blockIdx.x, ui = 0; u < total; u += gridDim.x, ++ui) {
       const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
       if (t.skip) continue;
       const int n16 = round16(t.nvalid);
@@ -625,9 +633,8 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
       }
 #pragma unroll 1
       for (int kb = 0; kb < p.nkb; ++kb) {
-        if (lane == 0) ok = tm_wait<MODE>(&empty[s], ph ^ 1, status);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
+        wait(&empty[s], ph ^ 1);
+        if (__any_sync(0xffffffffu, wait.dead())) break;
         const uint32_t X = smem_u32(stages + s * kStage + TN * kBlkK);
         const bool in = kb * kBlkK + c * 16 < p.K;
 #pragma unroll
@@ -687,13 +694,15 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
   constexpr int kScFloats = wm_sc_floats(MODE, BN);
   __shared__ int s_scan[33];
   __shared__ float s_amax[2][4][BN];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int32_t* status = p.g.status;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  __shared__ int s_dead;
+  Waits<true> wait{p.g.status, &s_dead};
   // the CTAs of a cluster have neighbouring block indices
   const int ks = 1 << p.ks_log, rank = (int)blockIdx.x & (ks - 1);
   const int worker = (int)blockIdx.x >> p.ks_log, nworkers = (int)gridDim.x >> p.ks_log;
   const int k_lo = (rank * p.nkb) >> p.ks_log, k_hi = ((rank + 1) * p.nkb) >> p.ks_log;
   if (threadIdx.x == 0) {
+    s_dead = 0;
     for (int s = 0; s < p.ns; ++s) {
       mbar_init(&full[s], 1 + (MODE == 1 ? 128 : 1));
       mbar_init(&empty[s], 1);
@@ -740,14 +749,13 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     if (lane == 0) {
       // ---------------------------------------------------- weight producer
       int s = 0, ph = 0;
-      bool ok = true;
-      for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
+      for (int u = worker, ui = 0; u < total; u += nworkers, ++ui) {
         const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
         if (t.skip) continue;
 #pragma unroll 1
         for (int kb = k_lo; kb < k_hi; ++kb) {
-          ok = bar_wait(&empty[s], ph ^ 1, status);
-          if (!ok) break;
+          wait(&empty[s], ph ^ 1);
+          if (wait.dead()) break;
           uint8_t* W = stages + s * kStage;
           mbar_arrive_expect_tx(&full[s], kA * kTileBytes);
           tma_load_3d(W, &maps.w, &full[s], kb * kBlkK, t.m * kTileM, t.slot);
@@ -761,20 +769,17 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     // ---------------------------------------------------------- MMA issuer
     int s = 0, ph = 0;
     uint32_t it = 0;
-    bool ok = true;
     const uint64_t desc0 = smem_desc_sw128(smem_u32(stages));
     const bool leader = elect_one();
-    for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
+    for (int u = worker, ui = 0; u < total; u += nworkers, ++ui) {
       const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
       if (t.skip) continue;
       const uint32_t idesc = idesc_f8(kTileM, round16(t.nvalid));
 #pragma unroll 1
       for (int kb = k_lo; kb < k_hi; ++kb, ++it) {
         const uint32_t a = it % kWmAcc;
-        ok = bar_wait(&full[s], ph, status);
-        ok = bar_wait(&tempty[a], ((it / kWmAcc) & 1) ^ 1, status) && ok;
-        ok = __all_sync(0xffffffffu, ok);
-        if (!ok) break;
+        wait(&full[s], ph);
+        wait(&tempty[a], ((it / kWmAcc) & 1) ^ 1);
         tc_fence_after();
         if (MODE == 1) fence_proxy_async_smem();
         if (leader) {
@@ -798,8 +803,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     if (MODE == 2) pdl_wait();  // h's scales
     const int nwb = (p.N + 127) / 128;
     uint32_t i = 0;
-    bool ok = true;
-    for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
+    for (int u = worker, ui = 0; u < total; u += nworkers, ++ui) {
       const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
       if (t.skip) continue;
       int tk = 0;  // MODE 1: the rows' tokens, one a lane
@@ -807,8 +811,8 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       const float* w = (MODE == 0 ? p.ws : scales_of(p, t.slot)) + (int64_t)t.m * p.nkb;
       for (int k0 = k_lo; k0 < k_hi; k0 += kWmScK, ++i) {
         const int slot = i % kScSlots, k = k0 + lane;
-        ok = bar_wait(&sempty[slot], ((i / kScSlots) & 1) ^ 1, status);
-        if (!ok) break;
+        wait(&sempty[slot], ((i / kScSlots) & 1) ^ 1);
+        if (__any_sync(0xffffffffu, wait.dead())) break;
         float* tab = sc_tab + slot * kScFloats;
         for (int n = 0; n < t.nvalid; ++n) {
           const int r = MODE == 1 ? __shfl_sync(0xffffffffu, tk, n & 31) : t.b * BN + n;
@@ -827,14 +831,13 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       // ------------------------------------------------------ rows producer
       if (MODE == 2) pdl_wait();  // h is the kernel before's output
       int s = 0, ph = 0;
-      bool ok = true;
-      for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
+      for (int u = worker, ui = 0; u < total; u += nworkers, ++ui) {
         const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
         if (t.skip) continue;
 #pragma unroll 1
         for (int kb = k_lo; kb < k_hi; ++kb) {
-          ok = bar_wait(&empty[s], ph ^ 1, status);
-          if (!ok) break;
+          wait(&empty[s], ph ^ 1);
+          if (wait.dead()) break;
           mbar_arrive_expect_tx(&full[s], BN * kBlkK);
           tma_load_2d(stages + s * kStage + kA * kTileBytes, &maps.x, &full[s], kb * kBlkK, t.b * BN);
           if (++s == p.ns) { s = 0; ph ^= 1; }
@@ -849,8 +852,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     // log2 of the columns this CTA finishes, from rank * own
     const int own_log = (BN == 16 ? 4 : 5) - p.ks_log, own = 1 << own_log;
     uint32_t it = 0, un = 0, sn = 0;
-    bool ok = true;
-    for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
+    for (int u = worker, ui = 0; u < total; u += nworkers, ++ui) {
       const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
       const int wrow = t.m * kTileM + row;
       if (t.skip) {
@@ -859,7 +861,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
           if (wrow < p.N)
             for (int n = 0; n < t.nvalid; ++n)
               static_cast<uint16_t*>(p.out)[(int64_t)ld_tab<MODE == 2>(p.g.sorted_ids + (int64_t)t.b * p.g.BN + n) * p.out_ld + wrow] = 0;
-          if (row == 0) set_status(status, OES_DEV_BAD_ID);
+          if (row == 0) set_status(p.g.status, OES_DEV_BAD_ID);
         }
         continue;
       }
@@ -876,11 +878,9 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
         const uint32_t a = it % kWmAcc;
         const int slot = sn % kScSlots, ki = (kb - k_lo) % kWmScK;
         if (ki == 0) {
-          ok = bar_wait(&sfull[slot], (sn / kScSlots) & 1, status);
-          if (!ok) break;
+          wait(&sfull[slot], (sn / kScSlots) & 1);
         }
-        ok = bar_wait(&tfull[a], (it / kWmAcc) & 1, status);
-        if (!ok) break;
+        wait(&tfull[a], (it / kWmAcc) & 1);
         tc_fence_after();
         const float* tab = sc_tab + slot * kScFloats;
         const uint32_t tl = tmem_base + ((uint32_t)(q * 32) << 16) + a * kA * BN;
@@ -912,15 +912,13 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
           ++sn;
         }
       }
-      if (!ok) break;
       // The sums go through shared memory, so that what follows is a loop
       // over columns: unrolled over registers it was 250 KB of code, and
       // fetching it took longer than the product.  Each CTA of a cluster
       // finishes `own` columns: it sends the others theirs and adds up its
       // own in rank order.
       if (ks > 1) {
-        ok = mbar_wait_cluster(&rempty[q], (un & 1) ^ 1, status);
-        if (!ok) break;
+        wait.cluster(&rempty[q], (un & 1) ^ 1);
       }
       {
         const uint32_t base = smem_u32(red) + row * 4;
@@ -937,8 +935,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
         fence_cluster();
         __syncwarp();
         if (lane < ks) mbar_arrive_cluster(map_rank(smem_u32(&rfull[q]), lane));
-        ok = mbar_wait_cluster(&rfull[q], un & 1, status);
-        if (!ok) break;
+        wait.cluster(&rfull[q], un & 1);
       }
       const int n0 = rank << own_log, mine = min(own, t.nvalid - n0);
       auto sum = [&](int i, int j) {
@@ -989,17 +986,15 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     const int g = threadIdx.x - 256;
     const int c = g & 7, n = g >> 3;
     int s = 0, ph = 0;
-    bool ok = true;
-    for (int u = worker, ui = 0; u < total && ok; u += nworkers, ++ui) {
+    for (int u = worker, ui = 0; u < total; u += nworkers, ++ui) {
       const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
       if (t.skip) continue;
       const int tk = n < t.nvalid ? p.g.sorted_ids[(int64_t)t.b * p.g.BN + n] / p.g.k : 0;
       const uint8_t* src = p.x + (int64_t)tk * p.K + c * 16;
 #pragma unroll 1
       for (int kb = k_lo; kb < k_hi; ++kb) {
-        if (lane == 0) ok = bar_wait(&empty[s], ph ^ 1, status);
-        ok = __shfl_sync(0xffffffffu, ok, 0);
-        if (!ok) break;
+        wait(&empty[s], ph ^ 1);
+        if (__any_sync(0xffffffffu, wait.dead())) break;
         const bool in = kb * kBlkK + c * 16 < p.K;
         cp_async16_or_zero(smem_u32(stages + s * kStage + kA * kTileBytes) + n * kBlkK + ((c ^ (n & 7)) << 4),
                            in ? src + kb * kBlkK : src, in);
