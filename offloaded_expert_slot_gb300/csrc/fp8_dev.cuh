@@ -10,9 +10,9 @@
 // NaN code; an infinity makes s infinite, so the whole group reads as NaN.
 //
 // The quotient is taken from the mathematics, four operations a value instead
-// of a full division: with amax = m 2^e, m in [1, 2), and y = RN(1/m),
-//   p = RN(7 v 2^(6-e)),  q0 = RN(p y),  q = RN(q0 + (p - q0 m) y)
-// p - q0 m is exact in an FMA, so q = RN(p/m + d) with |d| below 2^-46 |q|
+// of a full division: with amax = m 2^e, m in [1, 2), and y = 1/m within 2^-23,
+//   p = RN(v (7 2^(6-e))),  q0 = RN(p y),  q = RN(q0 + (p - q0 m) y)
+// p - q0 m is exact in an FMA, so q = RN(p/m + d) with |d| below 2^-44 |q|
 // (Markstein, IBM J. Res. Dev. 34, 1990): a quotient that is an fp32 number
 // comes out exact.  That is what matters here: bf16 values reach exact
 // midpoints between two codes all the time (448 v / amax is a ratio of small
@@ -29,28 +29,28 @@ constexpr float kCodeMax = 448.0f;
 
 struct QuantScale {
   float s;         // what a code stands for: code * s
-  float mul;       // 2^(6-e)
+  float mul;       // 7 2^(6-e)
   float m, rcp_m;  // amax's significand and its reciprocal
 };
 
 __device__ __forceinline__ QuantScale quant_scale(float amax) {
   amax = fmaxf(amax, 0x1p-100f);
   QuantScale q;
-  q.s = __fdiv_rn(amax, kCodeMax);
+  q.s = amax * (1.0f / kCodeMax);  // within 2 units of 2^-24 of the quotient
   const uint32_t b = __float_as_uint(amax);
   if (b == 0x7F800000u) {  // an infinity: finite values get 0, infinities NaN
     q.mul = 0.0f;
     q.m = q.rcp_m = 1.0f;
   } else {
-    q.mul = __uint_as_float((260u - (b >> 23)) << 23);
+    q.mul = 7.0f * __uint_as_float((260u - (b >> 23)) << 23);
     q.m = __uint_as_float((b & 0x007FFFFFu) | 0x3F800000u);
-    q.rcp_m = __frcp_rn(q.m);
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(q.rcp_m) : "f"(q.m));
   }
   return q;
 }
 
 __device__ __forceinline__ float quant_ratio(float v, const QuantScale& q) {
-  const float p = 7.0f * (v * q.mul);
+  const float p = v * q.mul;
   const float q0 = p * q.rcp_m;
   return fmaf(fmaf(-q0, q.m, p), q.rcp_m, q0);
 }
