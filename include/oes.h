@@ -425,9 +425,9 @@ enum { OES_ACT_NONE = 0, OES_ACT_SWIGLU = 1 };
 
 /* Rows to e4m3 codes with one fp32 scale for each group of 128 values.  For
  * each row t and group b (the last group may be short), over the group's
- * values v:  amax = max(|v|, 2^-100), scale[t, b] = amax / 448, and
- * q[t, i] = e4m3(448 v / amax), the quotient rounded to fp32, then to the
- * nearest code, ties to even.  NaN values take no part in amax and get a NaN
+ * values v:  amax = max(|v|, 2^-100), scale[t, b] = amax / 448 (to within two
+ * units in the last place), and q[t, i] = e4m3(448 v / amax), the quotient
+ * rounded to fp32, then to the nearest code, ties to even.  NaN values take no part in amax and get a NaN
  * code; an infinity makes the group's scale infinite (the group reads as
  * NaN).  act = OES_ACT_NONE: v = x[t, i], i < K.  OES_ACT_SWIGLU: rows of x
  * are [gate (K), up (K)] and v = silu(gate) * up in fp32, unrounded.
