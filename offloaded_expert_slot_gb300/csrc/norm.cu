@@ -66,13 +66,18 @@ __global__ void __launch_bounds__(MAXT, norm_ctas(VEC, MAXT)) block_norm_kernel(
   const int nw = blockDim.x >> 5;
   const int64_t step = (int64_t)gridDim.x * (WARP ? nw : 1);
   const float inv_h = 1.0f / (float)p.H;
-  auto row_sum = [&](float s, int which) {
+  // The two buffers take turns: a warp writes one again only past the barrier of
+  // the sum between, which every warp reaches after it has read the first.
+  int turn = 0;
+  auto row_sum = [&](float s) {
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (WARP) return s;
-    if (lane == 0) red[which][warp] = s;
+    float* sums = red[turn];
+    turn ^= 1;
+    if (lane == 0) sums[warp] = s;
     __syncthreads();
-    s = lane < nw ? red[which][lane] : 0.0f;
+    s = lane < nw ? sums[lane] : 0.0f;
 #pragma unroll
     for (int o = MAXT / 64; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     return __shfl_sync(0xffffffffu, s, 0);
@@ -136,7 +141,7 @@ __global__ void __launch_bounds__(MAXT, norm_ctas(VEC, MAXT)) block_norm_kernel(
         for (int j = 0; j < NV; ++j)
 #pragma unroll
           for (int e = 0; e < VEC; ++e) s = fmaf(v[j][e], v[j][e], s);
-        inv = rsqrtf(row_sum(s, 0) * inv_h + p.eps);
+        inv = rsqrtf(row_sum(s) * inv_h + p.eps);
       }
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
@@ -166,7 +171,7 @@ __global__ void __launch_bounds__(MAXT, norm_ctas(VEC, MAXT)) block_norm_kernel(
       for (int j = 0; j < NV; ++j)
 #pragma unroll
         for (int e = 0; e < VEC; ++e) s = fmaf(r[j][e], r[j][e], s);
-      const float inv = rsqrtf(row_sum(s, 1) * inv_h + p.eps);
+      const float inv = rsqrtf(row_sum(s) * inv_h + p.eps);
 #pragma unroll
       for (int j = 0; j < NV; ++j) {
         if (col(j) >= p.H) continue;

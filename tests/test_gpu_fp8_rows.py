@@ -218,6 +218,15 @@ def test_norm_forms(H, kw):
     norm_case(11, H, **kw)
 
 
+@pytest.mark.parametrize("kw", [dict(post=False), dict(pre=False), {}], ids=str)
+@pytest.mark.parametrize("T,H", [(6000, 1024), (3000, 2040), (2000, 1999), (700, 5001), (400, 12001)])
+def test_norm_many_rows_a_cta(T, H, kw):
+    """Each CTA walks many rows, with one reduction a row or two."""
+    lib()
+    norm_case(T, H, pad=1, **kw)
+    norm_case(T, H, **kw)
+
+
 def test_norm_outputs_may_be_left_out_and_stand_in_place():
     lib()
     T, H = 37, 640
