@@ -113,7 +113,7 @@ __device__ __forceinline__ int unit_table(const Fp8Params& p, UnitRec* utab, int
   for (int i = threadIdx.x; i < kMaxUnitsPerCta; i += blockDim.x) {
     const int u = worker + i * nworkers;
     if (u >= total) break;
-    const Unit t = unit_info<MODE == 2>(g, u, nb);
+    const Unit t = unit_info<MODE == 2, true>(g, u, nb);
     utab[i] = UnitRec{t.b, t.m, t.slot, t.nvalid};
   }
   return total;
@@ -339,12 +339,17 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
     tma_prefetch_desc(&maps.w);
     if (MODE != 1) tma_prefetch_desc(&maps.x);
   }
-  pdl_wait();
-  if (MODE != 0 && p.g.filter && p.g.gcount && p.g.gcount[p.g.filter] == 0) return;
+  // The gate and up product releases the down product once its units are known;
+  // a CTA of that starts where one of this ends, and waits for h alone (see the
+  // weight-major kernel).  600 tokens x 10 routes took 159 us so, 162 where it
+  // waits first; 4096 tokens 498 and 502.
+  if (MODE != 2) pdl_wait();
+  if (MODE != 0 && p.g.filter && p.g.gcount && ld_tab<MODE == 2>(p.g.gcount + p.g.filter) == 0) return;
   int nb = 0;
   const int total = unit_table<MODE>(p, utab, s_scan, blockIdx.x, gridDim.x, &nb);
   __syncthreads();
   if ((int)blockIdx.x >= total) return;
+  if (MODE == 1) pdl_trigger();
   if (warp == 2) {
     tmem_alloc(tmem_holder, 512);
     tmem_relinquish();
@@ -412,6 +417,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
       // lane l: rows l + 32 i and, of the weights' 2 x 8 scales, one
       const int nwb = (p.N + 127) / 128;  // blocks of weight rows
       uint32_t n = 0;
+      if (MODE == 2) pdl_wait();  // h's scales
       for (int u = blockIdx.x, ui = 0; u < total; u += gridDim.x, ++ui) {
         const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
         if (t.skip) continue;
@@ -449,6 +455,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
     } else if (MODE != 1 && warp == 3 && lane == 0) {
       // ------------------------------------------------------ rows producer
       int s = 0, ph = 0;
+      if (MODE == 2) pdl_wait();  // h is the kernel before's output
       for (int u = blockIdx.x, ui = 0; u < total; u += gridDim.x, ++ui) {
         const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
         if (t.skip) continue;
@@ -478,7 +485,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
       const bool live = row < t.nvalid;
       const int col0 = t.m * TN + half * kCols;  // MODE 0, 2: first column of this warp
       int r = 0;                                    // row of out (MODE 2: the route)
-      if (MODE == 2 && live) r = p.g.sorted_ids[(int64_t)t.b * p.g.BN + row];
+      if (MODE == 2 && live) r = ld_tab<true>(p.g.sorted_ids + (int64_t)t.b * p.g.BN + row);
       if (t.skip) {
         if (MODE == 2 && live && t.slot != kFiltered) {
           // an expert without a slot: its routes get zeros (and a status bit)
