@@ -743,7 +743,9 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
   // releases it after its set-up): all it reads but h was complete before
   // that kernel passed this wait, so it builds its unit table and streams its
   // first weights now, and only what reads h waits (below).  Tables it reads
-  // without waiting are read through L2.
+  // without waiting are read through L2.  32 tokens x 10 of 512 experts: 187 us,
+  // 193 with the release left to the end where a CTA has more than two units; 64
+  // x 8 of 64: 75 and 80.
   if (MODE != 2) pdl_wait();
   if (MODE != 0 && p.g.filter && p.g.gcount && ld_tab<MODE == 2>(p.g.gcount + p.g.filter) == 0) return;
   int nb = 0;
@@ -759,7 +761,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
   if (ks > 1) cluster_barrier();  // every CTA's barriers are initialised
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
-  if (MODE == 1 && total <= 2 * nworkers) pdl_trigger();
+  if (MODE == 1) pdl_trigger();
 
   if (warp == 0) {
     if (lane == 0) {
