@@ -26,7 +26,7 @@
 //     for gate and up in 120 us, 6.4 TB/s, and 382 MB for down in 68 us, 5.6
 //     TB/s.  When the tiles do not fill the GPU, the CTAs of a cluster share a
 //     tile's K range and add their sums over distributed shared memory in a
-//     fixed order (1 x 1536 x 2048: 5.7 us).
+//     fixed order (1 x 1536 x 2048: 3.9 us).
 #include <algorithm>
 
 #include "common.cuh"
@@ -255,13 +255,17 @@ __device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
   asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
   return r;
 }
-__device__ __forceinline__ void st_cluster(uint32_t addr, float v) {
-  asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+// Into another CTA's shared memory, the bytes counted by a barrier there: whoever
+// waits for that barrier sees them.  With plain stores, a fence and a releasing
+// arrival 1 x 1536 x 2048 took 5.4 us, like this 3.9.
+__device__ __forceinline__ void st_async(uint32_t addr, float v, uint32_t bar) {
+  asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
+               "r"(__float_as_uint(v)), "r"(bar)
+               : "memory");
 }
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-__device__ __forceinline__ void fence_cluster() { asm volatile("fence.acq_rel.cluster;" ::: "memory"); }
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -728,7 +732,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       mbar_init(&tempty[a], 4);
     }
     for (int w = 0; w < 4; ++w) {
-      mbar_init(&rfull[w], ks);
+      mbar_init(&rfull[w], 1);
       mbar_init(&rempty[w], ks);
     }
     for (int a = 0; a < kScSlots; ++a) {
@@ -752,6 +756,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
   const int total = unit_table<MODE>(p, utab, s_scan, worker, nworkers, &nb);
   __syncthreads();
   if (worker >= total) return;  // the whole cluster
+  const bool single = worker + nworkers >= total;
   if (warp == 2) {
     tmem_alloc(tmem_holder, kCols);
     tmem_relinquish();
@@ -869,7 +874,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     const int nwb = (p.N + 127) / 128;
     // log2 of the columns this CTA finishes, from rank * own
     const int own_log = (BN == 16 ? 4 : 5) - p.ks_log, own = 1 << own_log;
-    uint32_t it = 0, un = 0, sn = 0;
+    uint32_t it = 0, un = 0, sn = 0, rn = 0;
     for (int u = worker, ui = 0; u < total; u += nworkers, ++ui) {
       const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
       const int wrow = t.m * kTileM + row;
@@ -935,27 +940,29 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       // fetching it took longer than the product.  Each CTA of a cluster
       // finishes `own` columns: it sends the others theirs and adds up its
       // own in rank order.
+      const int n0 = rank << own_log, mine = min(own, t.nvalid - n0);
+      const uint32_t base = smem_u32(red) + row * 4;
       if (ks > 1) {
         wait.cluster(&rempty[q], (un & 1) ^ 1);
-      }
-      {
-        const uint32_t base = smem_u32(red) + row * 4;
+        if (lane == 0 && mine > 0) mbar_arrive_expect_tx(&rfull[q], ks * kA * mine * 32 * 4);
 #pragma unroll
         for (int n = 0; n < BN; ++n) {
           if (n >= t.nvalid) continue;
           const int d = n >> own_log, j = n & (own - 1);
           const uint32_t to = map_rank(base + (((rank << own_log) + j) * kTileM) * 4, d);
+          const uint32_t bar = map_rank(smem_u32(&rfull[q]), d);
 #pragma unroll
-          for (int i = 0; i < kA; ++i) st_cluster(to + i * (BN * kTileM * 4), acc[i][n]);
+          for (int i = 0; i < kA; ++i) st_async(to + i * (BN * kTileM * 4), acc[i][n], bar);
+        }
+        if (mine > 0) wait.cluster(&rfull[q], rn++ & 1);
+      } else {
+#pragma unroll
+        for (int n = 0; n < BN; ++n) {
+          if (n >= t.nvalid) continue;
+#pragma unroll
+          for (int i = 0; i < kA; ++i) red[(i * BN + n) * kTileM + row] = acc[i][n];
         }
       }
-      if (ks > 1) {
-        fence_cluster();
-        __syncwarp();
-        if (lane < ks) mbar_arrive_cluster(map_rank(smem_u32(&rfull[q]), lane));
-        wait.cluster(&rfull[q], un & 1);
-      }
-      const int n0 = rank << own_log, mine = min(own, t.nvalid - n0);
       auto sum = [&](int i, int j) {
         const float* v = red + (i * BN + j) * kTileM + row;
         float s = v[0];
@@ -993,7 +1000,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
           else static_cast<uint16_t*>(p.out)[o] = (uint16_t)f32_bf16(v);
         }
       }
-      if (ks > 1) {
+      if (ks > 1 && !single) {
         __syncwarp();
         if (lane < ks) mbar_arrive_cluster(map_rank(smem_u32(&rempty[q]), lane));
       }
@@ -1029,8 +1036,9 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, kCols);
   }
-  // no CTA leaves while another may still send to it
-  if (ks > 1) cluster_barrier();
+  // no CTA leaves while another may still send to it (of a single unit's sums
+  // each has waited for all that are sent to it)
+  if (ks > 1 && (!single || wait.dead())) cluster_barrier();
 }
 
 // ------------------------------------------------------------------ launches
@@ -1054,14 +1062,16 @@ int launch_tm(const Fp8Maps& maps, Fp8Params p, cudaStream_t stream) {
 }
 
 // log2 of the CTAs that share a tile: the largest of 8, 4, 2, 1 with every tile
-// resident at once and two blocks of K for each CTA.  Sharing costs about 2 us
-// (the cluster's start, the exchange of sums) and a block 0.35 us, so fewer than
-// 12 blocks are not shared (768 of K: 7.3 us in 128 CTAs, 9.0 in 32 pairs).
-// Clusters of 4 and 8 do not fill the GPU's groups of SMs: 16 clusters of 8 ran
-// in two turns, 18.1 us, where 32 of 4 took 12.9.  units: the most units the
-// launch can have, known on the host.
+// resident at once and two blocks of K for each CTA.  Sharing has a cost (the
+// cluster's start, the exchange of sums), so fewer than 8 blocks are not shared
+// (8 x 1024 x 1024: 4.4 us shared, 4.9 not; 8 x 2048 x 768: 5.0 and 4.4).
+// Clusters of 4 and 8 do not fill the GPU's groups of SMs: 17 clusters of 8 ran
+// in two turns, 16 x 2176 x 4096 in 9.2 us, where 17 of 4 took 5.9.  Nor are
+// tiles shared that take several turns: 64 tokens x 8 of 64 experts took 83 us
+// so, 73 with a tile a CTA.  units: the most units the launch can have, known on
+// the host.
 int k_shares_log(int64_t units, int nkb) {
-  if (nkb < 12) return 0;
+  if (nkb < 8) return 0;
   const int64_t sms = num_sms();
   for (int l = 3; l > 0; --l)
     if ((units << l) <= (l == 3 ? sms * 3 / 4 : l == 2 ? sms * 7 / 8 : sms) && nkb >= (2 << l)) return l;
