@@ -267,9 +267,6 @@ __device__ __forceinline__ void st_async(uint32_t addr, float v, uint32_t bar) {
                "r"(__float_as_uint(v)), "r"(bar)
                : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
-}
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -709,8 +706,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
   uint64_t* tfull = empty + p.ns;
   uint64_t* tempty = tfull + kWmAcc;
   uint64_t* rfull = tempty + kWmAcc;  // [4]: a warp's sums of every CTA of the cluster are in
-  uint64_t* rempty = rfull + 4;       // [4]: every CTA has read what this warp sent
-  uint64_t* sfull = rempty + 4;
+  uint64_t* sfull = rfull + 4;
   uint64_t* sempty = sfull + kScSlots;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(sempty + kScSlots);
   UnitRec* utab = reinterpret_cast<UnitRec*>(tmem_holder + 4);
@@ -735,10 +731,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], 4);
     }
-    for (int w = 0; w < 4; ++w) {
-      mbar_init(&rfull[w], 1);
-      mbar_init(&rempty[w], ks);
-    }
+    for (int w = 0; w < 4; ++w) mbar_init(&rfull[w], 1);
     for (int a = 0; a < kScSlots; ++a) {
       mbar_init(&sfull[a], 32);
       mbar_init(&sempty[a], 4);
@@ -760,7 +753,6 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
   const int total = unit_table<MODE>(p, utab, s_scan, worker, nworkers, &nb);
   __syncthreads();
   if (worker >= total) return;  // the whole cluster
-  const bool single = worker + nworkers >= total;
   if (warp == 2) {
     tmem_alloc(tmem_holder, kCols);
     tmem_relinquish();
@@ -878,7 +870,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     const int nwb = (p.N + 127) / 128;
     // log2 of the columns this CTA finishes, from rank * own
     const int own_log = (BN == 16 ? 4 : 5) - p.ks_log, own = 1 << own_log;
-    uint32_t it = 0, un = 0, sn = 0, rn = 0;
+    uint32_t it = 0, un = 0, sn = 0;
     for (int u = worker, ui = 0; u < total; u += nworkers, ++ui) {
       const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
       const int wrow = t.m * kTileM + row;
@@ -947,7 +939,6 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       const int n0 = rank << own_log, mine = min(own, t.nvalid - n0);
       const uint32_t base = smem_u32(red) + row * 4;
       if (ks > 1) {
-        wait.cluster(&rempty[q], (un & 1) ^ 1);
         if (lane == 0 && mine > 0) mbar_arrive_expect_tx(&rfull[q], ks * kA * mine * 32 * 4);
 #pragma unroll
         for (int n = 0; n < BN; ++n) {
@@ -958,7 +949,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
 #pragma unroll
           for (int i = 0; i < kA; ++i) st_async(to + i * (BN * kTileM * 4), acc[i][n], bar);
         }
-        if (mine > 0) wait.cluster(&rfull[q], rn++ & 1);
+        if (mine > 0) wait.cluster(&rfull[q], 0);  // a cluster has one unit at most
       } else {
 #pragma unroll
         for (int n = 0; n < BN; ++n) {
@@ -1004,10 +995,6 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
           else static_cast<uint16_t*>(p.out)[o] = (uint16_t)f32_bf16(v);
         }
       }
-      if (ks > 1 && !single) {
-        __syncwarp();
-        if (lane < ks) mbar_arrive_cluster(map_rank(smem_u32(&rempty[q]), lane));
-      }
       ++un;
     }
   } else if (MODE == 1 && warp >= 8) {
@@ -1040,9 +1027,9 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     tc_fence_after();
     tmem_dealloc(tmem_base, kCols);
   }
-  // no CTA leaves while another may still send to it (of a single unit's sums
-  // each has waited for all that are sent to it)
-  if (ks > 1 && (!single || wait.dead())) cluster_barrier();
+  // no CTA leaves while another may still send to it: each has waited for all
+  // that is sent to it, unless it gave up
+  if (ks > 1 && wait.dead()) cluster_barrier();
 }
 
 // ------------------------------------------------------------------ launches
@@ -1066,7 +1053,8 @@ int launch_tm(const Fp8Maps& maps, Fp8Params p, cudaStream_t stream) {
 }
 
 // log2 of the CTAs that share a tile: the largest of 8, 4, 2, 1 with every tile
-// resident at once and two blocks of K for each CTA.  Sharing has a cost (the
+// resident at once (so a cluster has one tile at most, and its sums' barriers and
+// buffers are used once) and two blocks of K for each CTA.  Sharing has a cost (the
 // cluster's start, the exchange of sums), so fewer than 8 blocks are not shared
 // (8 x 1024 x 1024: 4.4 us shared, 4.9 not; 8 x 2048 x 768: 5.0 and 4.4).
 // Clusters of 4 and 8 do not fill the GPU's groups of SMs: 17 clusters of 8 ran
