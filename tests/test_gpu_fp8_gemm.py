@@ -131,3 +131,16 @@ def test_gemm_in_a_graph_and_empty():
     torch.cuda.synchronize()
     assert torch.equal(out, want)
     oes.moe_fp8_gemm(0, 16, 0, 0, 16, 0, 16, 0, 16, 0, 16, 0, dtype=oes.OES_BF16)   # no rows
+
+
+@pytest.mark.parametrize("T", [1, 2, 3, 5, 9, 15, 16, 17, 18, 25, 31, 33])
+@pytest.mark.parametrize("K,N", [(1000, 640), (1024, 2200), (1152, 1000), (2000, 384), (4200, 130)])
+def test_gemm_shared_k(T, K, N):
+    """Few tiles over 8 to 33 blocks of K, where several CTAs share a tile, some of
+    them without rows of their own; the same bits from one call after another."""
+    lib()
+    xq, xs, x64, w = operands(T, K, N, seed=5)
+    first = product(xq, xs, K, w, N, torch.float32).clone()
+    check(first, x64, w[2], K)
+    for _ in range(20):
+        assert torch.equal(product(xq, xs, K, w, N, torch.float32), first)
