@@ -25,8 +25,8 @@ struct QuantArgs {
 // VEC 8: 16 lanes hold a group, 8 values each.  VEC 1: a warp holds a group,
 // value lane + 32 i.  Plain rows of 8 take two groups a turn, both loaded before
 // the first is reduced (16384 x 4096 bf16: 44 us, 4.6 TB/s; one at a time 51
-// us).  The others do better with one and more threads (SwiGLU to 4096 x 2048:
-// 9.7 us, two at a time 11.7; 4096 x 2047: 9.2 and 10.4).
+// us).  The others do better with one and more threads (4096 x 2047: 9.2 us, two at a
+// time 10.4).
 template <int VEC, bool SWIGLU, typename XT>
 __global__ void __launch_bounds__(256) fp8_quantize_kernel(const QuantArgs a) {
   pdl_begin();
@@ -116,7 +116,10 @@ __global__ void __launch_bounds__(256) fp8_quantize_kernel(const QuantArgs a) {
 template <int VEC, bool SWIGLU, typename XT>
 int launch_quant(const QuantArgs& a, cudaStream_t stream) {
   const int per_cta = 256 / (VEC == 8 ? 16 : 32);
-  const int grid = (int)std::min<int64_t>(ceil_div64(a.groups, per_cta), (int64_t)num_sms() * 8);
+  // SwiGLU of rows of 8 has registers for six CTAs an SM: at eight 4096 x 2048 took
+  // 12.7 us, at six 11.5 (4096 x 768 4.5 and 4.4)
+  const int per_sm = VEC == 8 && SWIGLU ? 6 : 8;
+  const int grid = (int)std::min<int64_t>(ceil_div64(a.groups, per_cta), (int64_t)num_sms() * per_sm);
   QuantArgs args = a;
   args.step_t = grid * per_cta / a.nb;
   args.step_b = grid * per_cta % a.nb;
