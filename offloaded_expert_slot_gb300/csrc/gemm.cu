@@ -1059,9 +1059,13 @@ __global__ void x_quant_kernel(const uint16_t* __restrict__ x, uint16_t* __restr
 }
 
 // out[t, :] = sum_{j=0..k-1} w[t, j] * y[t*k + j, :], fp32 in j order -> bf16.
-// Rows loaded together: an FP8 call of 4096 x 2048 whose experts are 64 wide took
-// 147 us with six at k = 10 and 104 at k = 6; 153 and 107 with eight.
-constexpr int kCombineBatch = 6;
+// N rows are loaded together: k routes in as few and as equal rounds as rows of
+// eight allow.  A call whose GEMMs are empty, H = 2048, us with six rows, with
+// eight, like this: one token k = 8 10.0, 9.3, 9.3 and k = 10 10.2, 10.2, 9.5; 128
+// tokens k = 8 4.8, 4.7, 4.6; 4096 tokens k = 7 26.8, 27.3, 25.5, k = 8 28.0, 27.8,
+// 27.8 and k = 10 32.5, 36.1, 32.9.
+constexpr int kCombineRows = 8;
+template <int N>
 __global__ void combine_kernel(const uint16_t* __restrict__ y, const float* __restrict__ w,
                                const int32_t* __restrict__ ids, int T, int k, int H, int E,
                                uint16_t* __restrict__ out) {
@@ -1073,15 +1077,15 @@ __global__ void combine_kernel(const uint16_t* __restrict__ y, const float* __re
     const int t = static_cast<int>(i / vec);
     const int c = static_cast<int>(i % vec);
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
-    // six routes' rows are loaded together (every y row exists, so the
+    // N routes' rows are loaded together (every y row exists, so the
     // loads need not wait for the ids), then added in j order, skipping
     // routes outside [0, E)
-    for (int j0 = 0; j0 < k; j0 += kCombineBatch) {
-      uint4 v[kCombineBatch];
-      float wj[kCombineBatch];
-      bool ok[kCombineBatch];
+    for (int j0 = 0; j0 < k; j0 += N) {
+      uint4 v[N];
+      float wj[N];
+      bool ok[N];
 #pragma unroll
-      for (int b = 0; b < kCombineBatch; ++b) {
+      for (int b = 0; b < N; ++b) {
         const int j = j0 + b;
         ok[b] = false;
         if (j < k) {
@@ -1092,7 +1096,7 @@ __global__ void combine_kernel(const uint16_t* __restrict__ y, const float* __re
         }
       }
 #pragma unroll
-      for (int b = 0; b < kCombineBatch; ++b) {
+      for (int b = 0; b < N; ++b) {
         if (!ok[b]) continue;
         const uint32_t u[4] = {v[b].x, v[b].y, v[b].z, v[b].w};
 #pragma unroll
@@ -1522,7 +1526,12 @@ int gemm_combine(const GemmPlan& g, const int32_t* ids, const float* weights, ui
   OES_REQUIRE(ids && weights && out && ((uintptr_t)out & 15) == 0,
               "moe_grouped_gemm_slots: ids, weights and a 16-byte aligned out are required");
   const int64_t nvec = (int64_t)g.T * (g.H / 8);
-  launch_kernel(combine_kernel, (int)std::min<int64_t>(ceil_div64(nvec, 256), (int64_t)num_sms() * 8), 256, 0, stream, g.y, weights, ids, g.T, g.k, g.H, g.E, out);
+  const int grid = (int)std::min<int64_t>(ceil_div64(nvec, 256), (int64_t)num_sms() * 8);
+  static constexpr decltype(&combine_kernel<1>) kernels[kCombineRows] = {
+      combine_kernel<1>, combine_kernel<2>, combine_kernel<3>, combine_kernel<4>,
+      combine_kernel<5>, combine_kernel<6>, combine_kernel<7>, combine_kernel<8>};
+  const int rows = ceil_div(g.k, ceil_div(g.k, kCombineRows));
+  launch_kernel(kernels[rows - 1], grid, 256, 0, stream, g.y, weights, ids, g.T, g.k, g.H, g.E, out);
   OES_CHECK_LAUNCH("combine_kernel");
   return OES_OK;
 }
