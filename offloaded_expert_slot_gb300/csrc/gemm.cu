@@ -1384,15 +1384,10 @@ int gemm_prepare(const oes_routed_experts* v, const uint16_t* x, int T, int k,
       return rc;
     const uint64_t dh[2] = {(uint64_t)I, (uint64_t)cap}, sh[1] = {(uint64_t)I};
     if ((rc = encode_tiled(&m2.b, u8, 2, ws.h, dh, sh, hbox, CU_TENSOR_MAP_SWIZZLE_128B))) return rc;
-    // x, gathered by rows
-    const uint64_t dx[2] = {(uint64_t)H, (uint64_t)T}, sx[1] = {(uint64_t)H};
-    const uint32_t xbox[2] = {128, 1};
-    if ((rc = encode_tiled(&m1.b, u8, 2, ws.x16, dx, sx, xbox, CU_TENSOR_MAP_SWIZZLE_128B))) return rc;
     g->f8.xq = reinterpret_cast<const uint8_t*>(ws.x16);
     g->f8.xs = ws.xs;
     g->f8.hq = reinterpret_cast<uint8_t*>(ws.h);
     g->f8.hs = ws.hs;
-    g->f8.w2_off = row.w2;
     g->f8.s13_off = row.s13;
     g->f8.s2_off = row.s2;
   } else if (!wf) {

@@ -14,7 +14,7 @@ struct GemmMaps {
   CUtensorMap a;   // 16-bit weights [S][rows][K] (bf16 path)
   CUtensorMap q;   // NVFP4 values [S][rows][K/2] bytes
   CUtensorMap sc;  // NVFP4 scales [S][K/64][rows] u32
-  CUtensorMap b;   // GEMM2: h [cap][I]; FP8 GEMM1: x [T][H], a row at a time
+  CUtensorMap b;   // GEMM2: h [cap][I]
 };
 
 struct GemmParams {
@@ -50,7 +50,7 @@ struct Fp8Group {
   const float* xs;    // [T, ceil(H/128)]
   uint8_t* hq;        // [cap, I] codes of h
   float* hs;          // [cap, ceil(I/128)]
-  int64_t w2_off, s13_off, s2_off;  // sections of an expert row
+  int64_t s13_off, s2_off;  // sections of an expert row
 };
 
 // Everything needed to launch GEMM1 / GEMM2 / combine of one call.
