@@ -127,14 +127,20 @@ __device__ __forceinline__ const float* scales_of(const Fp8Params& p, int slot) 
   return reinterpret_cast<const float*>(reinterpret_cast<const uint8_t*>(p.ws) + (int64_t)slot * p.g.row_bytes);
 }
 
+// Polls of the waits below; a test builds this file with few, so that they run out.
+#ifndef OES_FP8_WAIT_POLLS
+#define OES_FP8_WAIT_POLLS kWaitLimit
+#endif
+
 // The bounded waits of a CTA's warps, all lanes of a warp together.  One that
 // gives up sets the status and the CTA's flag; from then on no wait lasts and
 // nothing more is loaded, but every warp walks its loops to their end, so that
-// no barrier between warps is left short.  That the first test stands alone,
-// that no wait has an exit of its own and that the flag costs no register
-// matters: with a result to test after each wait 4096 x 8192 x 4096 took 131 us,
-// with a flag in a register 119, like this 116.  LOOP_ASM: the loop in one asm
-// block, 3 % better for the experts' kernels and 10 % worse for the dense one.
+// no barrier between warps is left short, and drain() then waits for what is in
+// flight.  That the first test stands alone, that no wait has an exit of its own
+// and that the flag costs no register matters: with a result to test after each
+// wait 4096 x 8192 x 4096 took 131 us, with a flag in a register 119, like this
+// 116.  LOOP_ASM: the loop in one asm block, 3 % better for the experts' kernels
+// and 10 % worse for the dense one.
 template <bool LOOP_ASM>
 struct Waits {
   int32_t* status;
@@ -156,10 +162,10 @@ struct Waits {
           "@p bra W%=;\n"
           "D%=: selp.u32 %0, 1, 0, p; }"
           : "=r"(ok)
-          : "r"(smem_u32(bar)), "r"(parity), "n"(kWaitLimit)
+          : "r"(smem_u32(bar)), "r"(parity), "n"(OES_FP8_WAIT_POLLS)
           : "memory");
       if (!ok) give_up();
-    } else if (!mbar_wait(bar, parity, status)) {
+    } else if (!mbar_wait(bar, parity, status, OES_FP8_WAIT_POLLS)) {
       *flag = 1;
     }
   }
@@ -169,7 +175,7 @@ struct Waits {
   }
   // arrivals and data come from other CTAs of the cluster
   __device__ __forceinline__ void cluster(uint64_t* bar, uint32_t parity) {
-    for (uint32_t i = 0; i < kWaitLimit; ++i) {
+    for (uint32_t i = 0; i < OES_FP8_WAIT_POLLS; ++i) {
       uint32_t ok;
       asm volatile(
           "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2; selp.u32 "
@@ -272,6 +278,36 @@ __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
+// Once every role of a CTA in which a wait gave up has ended, by one thread: no
+// copy and no MMA of the CTA outlives its shared memory and TMEM.  fills[r] is
+// the number of stages that producer r filled (0 the weights; then the rows, or in
+// MODE 1 the four gather warps).  A fill's phase ends when all its arrivals and
+// bytes are in; what a producer that stopped before it owes is arrived here, for
+// the ring's last ns fills (the stages of earlier ones were released, so their
+// phases have ended).  mma_done ends with the issuer's last MMA.  Called by the
+// warp that frees the TMEM: by all warps' common tail it took registers from the
+// loops (4096 tokens x 10: 512 us, like this 503).
+template <int MODE>
+__device__ __forceinline__ void drain(uint64_t* full, int ns, const volatile int* fills, uint64_t* mma_done,
+                                      int32_t* status) {
+  constexpr int kProducers = MODE == 1 ? 5 : 2;
+  int most = 0;
+#pragma unroll 1
+  for (int r = 0; r < kProducers; ++r) most = max(most, fills[r]);
+#pragma unroll 1
+  for (int i = max(0, most - ns); i < most; ++i) {
+    uint64_t* bar = &full[i % ns];
+#pragma unroll 1
+    for (int r = 0; r < kProducers; ++r) {
+      if (fills[r] > i) continue;
+#pragma unroll 1
+      for (int n = MODE == 1 && r > 0 ? 32 : 1; n > 0; --n) mbar_arrive(bar);
+    }
+    mbar_wait(bar, (i / ns) & 1, status);
+  }
+  mbar_wait(mma_done, 0, status);
+}
+
 // ============================================================ token-major
 // TN weight rows a tile (MODE 1: 128 gate + 128 up).  TMEM holds 512 / TN
 // blocks' sums.
@@ -323,10 +359,13 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
   __shared__ int s_scan[33];
   __shared__ float s_amax[2][2][kTileM];
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  __shared__ int s_dead;
+  __shared__ int s_dead, s_fills[5];  // see drain()
+  __shared__ uint64_t s_mma_done;
   Waits<MODE != 0> wait{p.g.status, &s_dead};
   if (threadIdx.x == 0) {
     s_dead = 0;
+    for (int r = 0; r < 5; ++r) s_fills[r] = 0;
+    mbar_init(&s_mma_done, 1);
     for (int s = 0; s < p.ns; ++s) {
       // the weights' TMA, and the rows' TMA or gather threads
       mbar_init(&full[s], 1 + (MODE == 1 ? 128 : 1));
@@ -368,7 +407,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
     if (TN == 256) regs_dec<MODE == 1 || sizeof(OT) == 4 ? 56 : 72>();
     if (warp == 0 && lane == 0) {
       // ---------------------------------------------------- weight producer
-      int s = 0, ph = 0;
+      int s = 0, ph = 0;  // the next stage; times around the ring
       for (int u = blockIdx.x, ui = 0; u < total; u += gridDim.x, ++ui) {
         const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
         if (t.skip) continue;
@@ -376,15 +415,16 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
         const int rb = MODE == 1 ? p.N + ra : ra + kTileM;
 #pragma unroll 1
         for (int kb = 0; kb < p.nkb; ++kb) {
-          wait(&empty[s], ph ^ 1);
+          wait(&empty[s], ~ph & 1);
           if (wait.dead()) break;
           uint8_t* W = stages + s * kStage;
           mbar_arrive_expect_tx(&full[s], TN * kBlkK);
           tma_load_3d(W, &maps.w, &full[s], kb * kBlkK, ra, t.slot);
           if (TN == 256) tma_load_3d(W + kTileBytes, &maps.w, &full[s], kb * kBlkK, rb, t.slot);
-          if (++s == p.ns) { s = 0; ph ^= 1; }
+          if (++s == p.ns) { s = 0; ++ph; }
         }
       }
+      s_fills[0] = ph * p.ns + s;
     } else if (warp == 1) {
       // -------------------------------------------------------- MMA issuer
       // The whole warp walks the loop and one elected lane issues, so that the
@@ -417,6 +457,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
           if (++s == p.ns) { s = 0; ph ^= 1; }
         }
       }
+      if (leader) tc_commit(&s_mma_done);
     } else if (warp == 2) {
       // ---------------------------------------------------- scale producer
       // lane l: rows l + 32 i and, of the weights' 2 x 8 scales, one
@@ -459,20 +500,21 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
       cp_async_wait_all();
     } else if (MODE != 1 && warp == 3 && lane == 0) {
       // ------------------------------------------------------ rows producer
-      int s = 0, ph = 0;
+      int s = 0, ph = 0;  // the next stage; times around the ring
       if (MODE == 2) pdl_wait();  // h is the kernel before's output
       for (int u = blockIdx.x, ui = 0; u < total; u += gridDim.x, ++ui) {
         const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
         if (t.skip) continue;
 #pragma unroll 1
         for (int kb = 0; kb < p.nkb; ++kb) {
-          wait(&empty[s], ph ^ 1);
+          wait(&empty[s], ~ph & 1);
           if (wait.dead()) break;
           mbar_arrive_expect_tx(&full[s], kTileBytes);
           tma_load_2d(stages + s * kStage + TN * kBlkK, &maps.x, &full[s], kb * kBlkK, t.b * kTileM);
-          if (++s == p.ns) { s = 0; ph ^= 1; }
+          if (++s == p.ns) { s = 0; ++ph; }
         }
       }
+      s_fills[1] = ph * p.ns + s;
     }
   } else if (warp < kTmGatherW0) {
     if (TN == 256) regs_inc<MODE == 1 ? 200 : sizeof(OT) == 4 ? 224 : 216>();
@@ -640,7 +682,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
     // not silence a NaN code.
     const int g = threadIdx.x - kTmGatherW0 * 32;
     const int c = g & 7, r0 = g >> 3;
-    int s = 0, ph = 0;
+    int s = 0, ph = 0;  // the next stage; times around the ring
     for (int u = blockIdx.x, ui = 0; u < total; u += gridDim.x, ++ui) {
       const Unit t = unit_of<MODE, true>(p, utab, ui, u, nb, kTileM);
       if (t.skip) continue;
@@ -654,7 +696,7 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
       }
 #pragma unroll 1
       for (int kb = 0; kb < p.nkb; ++kb) {
-        wait(&empty[s], ph ^ 1);
+        wait(&empty[s], ~ph & 1);
         if (__any_sync(0xffffffffu, wait.dead())) break;
         const uint32_t X = smem_u32(stages + s * kStage + TN * kBlkK);
         const bool in = kb * kBlkK + c * 16 < p.K;
@@ -664,15 +706,20 @@ __global__ void __launch_bounds__(tm_threads(MODE), 1)
           if (n < n16) cp_async16_or_zero(X + n * kBlkK + ((c ^ (n & 7)) << 4), in ? src[j] + kb * kBlkK : src[j], in);
         }
         cp_async_mbar_arrive(&full[s]);
-        if (++s == p.ns) { s = 0; ph ^= 1; }
+        if (++s == p.ns) { s = 0; ++ph; }
       }
     }
     cp_async_wait_all();
+    if (lane == 0) s_fills[1 + warp - kTmGatherW0] = ph * p.ns + s;
   }
 
   tc_fence_before();
   __syncthreads();
   if (warp == 2) {
+    if (wait.dead()) {
+      if (lane == 0) drain<MODE>(full, p.ns, s_fills, &s_mma_done, p.g.status);
+      __syncwarp();
+    }
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
   }
@@ -715,7 +762,8 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
   __shared__ int s_scan[33];
   __shared__ float s_amax[2][4][BN];
   const int warp = warp_index(), lane = threadIdx.x & 31;
-  __shared__ int s_dead;
+  __shared__ int s_dead, s_fills[5];  // see drain()
+  __shared__ uint64_t s_mma_done;
   Waits<true> wait{p.g.status, &s_dead};
   // the CTAs of a cluster have neighbouring block indices
   const int ks = 1 << p.ks_log, rank = (int)blockIdx.x & (ks - 1);
@@ -723,6 +771,8 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
   const int k_lo = (rank * p.nkb) >> p.ks_log, k_hi = ((rank + 1) * p.nkb) >> p.ks_log;
   if (threadIdx.x == 0) {
     s_dead = 0;
+    for (int r = 0; r < 5; ++r) s_fills[r] = 0;
+    mbar_init(&s_mma_done, 1);
     for (int s = 0; s < p.ns; ++s) {
       mbar_init(&full[s], 1 + (MODE == 1 ? 128 : 1));
       mbar_init(&empty[s], 1);
@@ -763,26 +813,28 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_holder;
   if (MODE == 1) pdl_trigger();
+  bool awaited = false;  // an epilogue warp: the cluster's CTAs send it sums
 
   if (warp == 0) {
     if (lane == 0) {
       // ---------------------------------------------------- weight producer
-      int s = 0, ph = 0;
+      int s = 0, ph = 0;  // the next stage; times around the ring
       for (int u = worker, ui = 0; u < total; u += nworkers, ++ui) {
         const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
         if (t.skip) continue;
 #pragma unroll 1
         for (int kb = k_lo; kb < k_hi; ++kb) {
-          wait(&empty[s], ph ^ 1);
+          wait(&empty[s], ~ph & 1);
           if (wait.dead()) break;
           uint8_t* W = stages + s * kStage;
           mbar_arrive_expect_tx(&full[s], kA * kTileBytes);
           tma_load_3d(W, &maps.w, &full[s], kb * kBlkK, t.m * kTileM, t.slot);
           if (MODE == 1)
             tma_load_3d(W + kTileBytes, &maps.w, &full[s], kb * kBlkK, p.N + t.m * kTileM, t.slot);
-          if (++s == p.ns) { s = 0; ph ^= 1; }
+          if (++s == p.ns) { s = 0; ++ph; }
         }
       }
+      s_fills[0] = ph * p.ns + s;
     }
   } else if (warp == 1) {
     // ---------------------------------------------------------- MMA issuer
@@ -817,6 +869,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
         if (++s == p.ns) { s = 0; ph ^= 1; }
       }
     }
+    if (leader) tc_commit(&s_mma_done);
   } else if (warp == 2) {
     // ------------------------------------------------------ scale producer
     if (MODE == 2) pdl_wait();  // h's scales
@@ -849,19 +902,20 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     if (MODE != 1 && lane == 0) {
       // ------------------------------------------------------ rows producer
       if (MODE == 2) pdl_wait();  // h is the kernel before's output
-      int s = 0, ph = 0;
+      int s = 0, ph = 0;  // the next stage; times around the ring
       for (int u = worker, ui = 0; u < total; u += nworkers, ++ui) {
         const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
         if (t.skip) continue;
 #pragma unroll 1
         for (int kb = k_lo; kb < k_hi; ++kb) {
-          wait(&empty[s], ph ^ 1);
+          wait(&empty[s], ~ph & 1);
           if (wait.dead()) break;
           mbar_arrive_expect_tx(&full[s], BN * kBlkK);
           tma_load_2d(stages + s * kStage + kA * kTileBytes, &maps.x, &full[s], kb * kBlkK, t.b * BN);
-          if (++s == p.ns) { s = 0; ph ^= 1; }
+          if (++s == p.ns) { s = 0; ++ph; }
         }
       }
+      s_fills[1] = ph * p.ns + s;
     }
   } else if (warp >= kEpiW0 && warp < kEpiW0 + 4) {
     // ---------------------------------------------------------- epilogue
@@ -939,7 +993,8 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       const int n0 = rank << own_log, mine = min(own, t.nvalid - n0);
       const uint32_t base = smem_u32(red) + row * 4;
       if (ks > 1) {
-        if (lane == 0 && mine > 0) mbar_arrive_expect_tx(&rfull[q], ks * kA * mine * 32 * 4);
+        awaited = mine > 0;
+        if (lane == 0 && awaited) mbar_arrive_expect_tx(&rfull[q], ks * kA * mine * 32 * 4);
 #pragma unroll
         for (int n = 0; n < BN; ++n) {
           if (n >= t.nvalid) continue;
@@ -949,7 +1004,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
 #pragma unroll
           for (int i = 0; i < kA; ++i) st_async(to + i * (BN * kTileM * 4), acc[i][n], bar);
         }
-        if (mine > 0) wait.cluster(&rfull[q], 0);  // a cluster has one unit at most
+        if (awaited) wait.cluster(&rfull[q], 0);  // a cluster has one unit at most
       } else {
 #pragma unroll
         for (int n = 0; n < BN; ++n) {
@@ -1001,7 +1056,7 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
     // -------------------------------------------- token gather (as above)
     const int g = threadIdx.x - 256;
     const int c = g & 7, n = g >> 3;
-    int s = 0, ph = 0;
+    int s = 0, ph = 0;  // the next stage; times around the ring
     for (int u = worker, ui = 0; u < total; u += nworkers, ++ui) {
       const Unit t = unit_of<MODE, false>(p, utab, ui, u, nb, BN);
       if (t.skip) continue;
@@ -1009,27 +1064,37 @@ __global__ void __launch_bounds__(wm_threads(MODE), 1)
       const uint8_t* src = p.x + (int64_t)tk * p.K + c * 16;
 #pragma unroll 1
       for (int kb = k_lo; kb < k_hi; ++kb) {
-        wait(&empty[s], ph ^ 1);
+        wait(&empty[s], ~ph & 1);
         if (__any_sync(0xffffffffu, wait.dead())) break;
         const bool in = kb * kBlkK + c * 16 < p.K;
         cp_async16_or_zero(smem_u32(stages + s * kStage + kA * kTileBytes) + n * kBlkK + ((c ^ (n & 7)) << 4),
                            in ? src + kb * kBlkK : src, in);
         cp_async_mbar_arrive(&full[s]);
-        if (++s == p.ns) { s = 0; ph ^= 1; }
+        if (++s == p.ns) { s = 0; ++ph; }
       }
     }
     cp_async_wait_all();
+    if (lane == 0) s_fills[1 + warp - 8] = ph * p.ns + s;
   }
 
   tc_fence_before();
   __syncthreads();
   if (warp == 2) {
+    if (wait.dead()) {
+      if (lane == 0) drain<MODE>(full, p.ns, s_fills, &s_mma_done, p.g.status);
+      __syncwarp();
+    }
     tc_fence_after();
     tmem_dealloc(tmem_base, kCols);
   }
-  // no CTA leaves while another may still send to it: each has waited for all
-  // that is sent to it, unless it gave up
-  if (ks > 1 && wait.dead()) cluster_barrier();
+  // No CTA leaves while another may still send to it: each has waited for all that
+  // is sent to it, unless it gave up.  Then it waits until the others have ended
+  // or sent theirs too (they get there: every wait on the way is bounded), and
+  // for what they sent.
+  if (ks > 1 && wait.dead()) {
+    cluster_barrier();
+    if (awaited) mbar_wait(&rfull[warp & 3], 0, p.g.status);
+  }
 }
 
 // ------------------------------------------------------------------ launches
