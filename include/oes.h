@@ -80,7 +80,8 @@ enum {
  * activations are quantised the way moe_fp8_quantize does it: x for each 128
  * values along H, the SwiGLU output h (fp32, unrounded) for each 128 along I.
  * The products of codes are summed in fp32 over each 128 of K, scaled by both
- * scales, and added up in fp32. */
+ * scales, and added up in fp32; each route's output row is rounded once to bf16
+ * before the weighted sum, as in the other formats. */
 enum {
   OES_WFMT_BF16 = 0,
   OES_WFMT_NVFP4 = 1,
@@ -382,10 +383,13 @@ int oes_tile_plan(int R, int E, int *block);
 size_t moe_grouped_gemm_workspace_size(const oes_routed_experts *view, int T, int k);
 
 /* Device pointers to the GEMM's intermediates inside its workspace, for
- * checking the steps: h [capacity, I] (16-bit: bf16 for bf16 weights, f16
- * otherwise; for W4A4 the quantised q * sf), y [T*k, H] bf16, and x16 [T, H]
+ * checking the steps: h [capacity, I] (16-bit: bf16 for bf16 weights, f16 for
+ * NVFP4; for W4A4 the quantised q * sf), y [T*k, H] bf16, and x16 [T, H]
  * f16, the 16-bit copy of x the NVFP4 GEMMs read (for W4A4, q * sf of the
- * quantised x; NULL for bf16 weights).  Any output may be NULL. */
+ * quantised x; NULL for bf16 weights).  For FP8, h [capacity, I] and x16
+ * [T, H] are e4m3 bytes, each followed, from the next multiple of 256 bytes on,
+ * by its fp32 scales [capacity, ceil(I/128)] and [T, ceil(H/128)].  Any output
+ * may be NULL. */
 int moe_grouped_gemm_workspace_views(const oes_routed_experts *view, int T, int k,
                                      void *workspace, uint16_t **h, uint16_t **y,
                                      uint16_t **x16);
@@ -430,7 +434,8 @@ enum { OES_ACT_NONE = 0, OES_ACT_SWIGLU = 1 };
  * rounded to fp32, then to the nearest code, ties to even.  NaN values take no part in amax and get a NaN
  * code; an infinity makes the group's scale infinite (the group reads as
  * NaN).  act = OES_ACT_NONE: v = x[t, i], i < K.  OES_ACT_SWIGLU: rows of x
- * are [gate (K), up (K)] and v = silu(gate) * up in fp32, unrounded.
+ * are [gate (K), up (K)] and v = silu(gate) * up in fp32, unrounded (silu
+ * within 17 units of 2^-24 for every gate; a gate of -inf gives NaN).
  * x: device, dtype OES_BF16 or OES_F32, row stride x_ld values (at least K,
  * or 2 K); q: device bytes, row stride q_ld >= K; scale: device
  * [T, ceil(K/128)] fp32.  T >= 0, 1 <= K <= 2^28.  Rows are read and written

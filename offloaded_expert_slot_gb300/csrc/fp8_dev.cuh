@@ -139,8 +139,8 @@ __device__ __forceinline__ float sigmoid_f32(float g) { return 1.0f / (1.0f + ex
 // below g = -88.7, and its reciprocal is flushed from -87.3 (with it, 4096 tokens x
 // 10 took 491 us, like this 498).  z = 2^t with t = g log2(e) / 2 rounded, and e =
 // z^2 (1 + lo), lo = g - 2 t ln 2 being what the rounding left.  From g = 64 ln 2 on
-// the factor of g is exactly 1.  -inf gives NaN, like the quotient.  Within 17 (measured 8)
-// units of 2^-24, a subnormal result rounded once more.
+// the factor of g is exactly 1.  -inf gives NaN, like the quotient.  Within 17
+// units of 2^-24 (measured: 8), a subnormal result rounded once more.
 __device__ __forceinline__ float silu_f32(float g) {
   constexpr float kHalfLog2e = 0.721347511f, kTwoLn2 = 1.386294365f, kMost = 44.3614197f;
   const float c = fminf(g, kMost), t = c * kHalfLog2e;

@@ -24,7 +24,7 @@
 //     tensor pipe active for 52 % of them.  Tiles of 128 weight rows took 185
 //     us there.  The experts' products are bound by the stream of weights: 4096
 //     tokens x 10 of 512 experts (2048 x 768) read 1.7 GB for gate and up in
-//     292 us, 5.9 TB/s, and move 1.0 GB for down in 159 us, 6.3 TB/s.
+//     300 us, 5.7 TB/s, and move 1.0 GB for down in 156 us, 6.5 TB/s.
 //   weight-major: 128 weight rows x 16 or 32 rows a tile, for few rows, bound
 //     by the stream of weights: 32 tokens x 10 of the same experts read 763 MB
 //     for gate and up in 120 us, 6.4 TB/s, and 382 MB for down in 68 us, 5.6
@@ -217,8 +217,9 @@ __device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t (&r)[32]) {
       : "memory");
 }
 // The warp's index, in a form the compiler can see is the same for all lanes:
-// what follows from it then needs no registers of each thread (a 256-wide
-// tile's kernel spilled 32 bytes a thread without, 8 with).
+// what follows from it then needs no registers of each thread (the dense 256-wide
+// tile's kernel stores 32 bytes a thread to local memory without, 16 with; with
+// fp32 results 80 and none).
 __device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
 __device__ __forceinline__ bool elect_one() {
   uint32_t r;
