@@ -109,5 +109,5 @@ def test_experts(impatient, T, k, E, H, I):
 
 
 def test_waits_ran_out():
-    """The cases above reached the path that they are for."""
-    assert not ran_out or oes.OES_DEV_TIMEOUT in ran_out, ran_out
+    """The cases above, where all have run, reached the path that they are for."""
+    assert len(ran_out) < 9 or oes.OES_DEV_TIMEOUT in ran_out, ran_out
