@@ -422,6 +422,44 @@ int moe_grouped_gemm_slots(const oes_routed_experts *view, const uint16_t *x, in
                            void *workspace, size_t workspace_bytes, uint16_t *out,
                            int32_t *status, oes_stream_t stream);
 
+/* ------------------------------------------------ a layer for few tokens */
+
+/* Most tokens of moe_layer_few_tokens. */
+#define OES_FEW_TOKENS_MAX 16
+
+/* Workspace bytes of moe_layer_few_tokens (0 for arguments it refuses). */
+size_t moe_layer_few_tokens_workspace_size(const oes_routed_experts *view, int T, int k);
+
+/* A whole mixture-of-experts layer for 0 to OES_FEW_TOKENS_MAX tokens whose
+ * experts are in the slot pool (a decode step with a warm cache, or after the
+ * step's ensure and copies), in two launches: the router's top-k as
+ * moe_route_topk has it, and
+ *   out[t] = sum_j weights[t, j] * W2_e (silu(Wg_e x_t) * (Wu_e x_t)),  e = ids[t, j]
+ * over the experts' rows at their slots, rounded to bf16.
+ * logits: device [T, E] of `dtype` (OES_LOGITS_*), then ids and weights
+ * (device [T, k]) receive the routing, bit for bit moe_route_topk's; or NULL,
+ * and ids and weights are read: a route whose id is outside [0, E)
+ * contributes nothing, an expert may stand twice in a token's list, and a token
+ * without a route gets zeros.  A routed expert with e2s outside [0, S) sets
+ * OES_DEV_BAD_ID and its routes give 0.
+ * view->wfmt: OES_WFMT_BF16, OES_WFMT_FP8 or OES_WFMT_NVFP4, rows as above.
+ * Weights are decoded exactly, and the activations are not quantised, in the FP8
+ * format neither (moe_grouped_gemm_slots quantises them there): sums are fp32, h
+ * is rounded once to bf16, out once.  For NVFP4 x and h pass through f16, as
+ * in the other calls (|x| and |h| up to 65504).  The result does not depend on
+ * timing; it is not bit for bit that of moe_grouped_gemm_slots, which rounds each
+ * route's output row to bf16 before the weighted sum.
+ * x: device [T, H] bf16, pool, x and workspace 16-byte aligned; out: device
+ * [T, H] bf16; status: device word or NULL.  H, I multiples of 64 in
+ * [64, 16384], k <= OES_MAX_TOPK (and <= E with logits).  Layers of more than
+ * 512 experts take one launch more for the routing, and rows of x that do not
+ * fit in shared memory together (H above about 4700 for 16 tokens) take two
+ * launches for each group of tokens that do. */
+int moe_layer_few_tokens(const oes_routed_experts *view, const uint16_t *x, int T, int k,
+                         const void *logits, int dtype, int32_t *ids, float *weights,
+                         void *workspace, size_t workspace_bytes, uint16_t *out, int32_t *status,
+                         oes_stream_t stream);
+
 /* ------------------------------------------ 8-bit rows and the block norms */
 
 /* Activations of moe_fp8_quantize. */

@@ -1,0 +1,778 @@
+// moe_layer_few_tokens: a whole mixture-of-experts layer for up to 16 tokens in
+// two launches.
+//
+//   out[t] = sum_j w[t, j] W2_e (silu(Wg_e x_t) * (Wu_e x_t)),   e = ids[t, j]
+//
+// A few tokens reach a few experts each, so the layer is a stream of those
+// experts' weights (one token x 10 of 512 FP8 experts: 47 MB, 7 us at the copy
+// rate), and everything around that stream is latency.  Both kernels read the
+// logits and work out the routing, the experts' slots and the tables of the
+// chunk in every CTA, instead of waiting for a kernel that does (the same
+// device code as moe_route_topk, so the same ids and weights bit for bit).
+//
+//   few_up_kernel    unit = (block, 8 rows of I): the 8 gate rows and the same
+//                    8 up rows are the 16 rows of one matrix instruction, so
+//                    that a lane has both factors of its h.  The CTA's eight
+//                    warps share K.
+//   few_down_kernel  a CTA owns up to 16 rows of the output at a time and goes
+//                    through all blocks for them, its warps sharing
+//                    (block, K) steps; the weighted sum over a token's routes
+//                    is the accumulator.  It is launched while the first kernel
+//                    runs, repeats the routing and fills its queues with W2;
+//                    only the loads of h wait.
+//
+// A block is one expert with at most one route of each token: column c of the
+// matrix instruction is token c, in both kernels.  An expert that a token lists
+// twice gets a second block for the second route.
+//
+// Weights go from memory into a queue of each lane's own (16-byte asynchronous
+// copies, read back by the same lane), so a warp has kept its next steps in
+// flight without registers and without a barrier.  The instructions are the
+// warp-wide m16n8k16: at 8 columns the tensor work is a hundredth of what the
+// stream takes, and tcgen05 tiles (128 weight rows, operands through shared
+// memory and TMEM) gave 9 to 31 % of the copy rate here, held up by their set-up
+// and hand-offs.
+//
+// Weights are exact in 16 bits: bf16 as they are; e4m3 as bf16, their block scales
+// on the fp32 sums of each 128 of K; e2m1 x e4m3 as f16, the global scale on the
+// sums.  h is rounded once, to bf16 (f16 for e2m1 weights), the sums over a
+// token's routes stay in fp32, and out is rounded once.
+#include <algorithm>
+
+#include "common.cuh"
+#include "fp8_dev.cuh"
+#include "gemm_types.h"
+#include "internal.h"
+#include "route_dev.cuh"
+#include "warp_mma.cuh"
+
+namespace oes {
+
+// Logits read through L2: the second kernel reads them while the first still
+// runs (see few_down_kernel).
+struct L2F32 { float v; };
+struct L2Bf16 { uint16_t v; };
+template <int V>
+__device__ __forceinline__ void load_logits(const L2F32* p, float* o) {
+  static_assert(V == 1, "one a load");
+  o[0] = __ldcg(reinterpret_cast<const float*>(p));
+}
+template <int V>
+__device__ __forceinline__ void load_logits(const L2Bf16* p, float* o) {
+  static_assert(V == 1, "one a load");
+  o[0] = bf16_f32(__ldcg(reinterpret_cast<const unsigned short*>(p)));
+}
+
+namespace {
+
+__host__ __device__ constexpr int cdiv(int a, int b) { return (a + b - 1) / b; }
+
+constexpr int kMaxTokens = 16;    // of a call
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kFusedExperts = 512;  // most experts that the kernels route themselves
+constexpr int kRowTile = 16;
+
+// Weight formats.  A step is what a warp takes from its queue at a time: kStepK
+// values of 16 rows, kChunks x 16 bytes a lane, kB x 16 bytes of B a lane and
+// column, and the step's scales behind the weights.
+template <int WF>
+struct Fmt;
+template <>
+struct Fmt<OES_WFMT_BF16> {
+  static constexpr int kStepK = 64, kRowBytes = 128, kChunks = 4, kB = 2, kXPad = 64;
+  static constexpr int kScale = 0;
+  static constexpr bool kF16 = false;
+};
+template <>
+struct Fmt<OES_WFMT_FP8> {
+  static constexpr int kStepK = 128, kRowBytes = 128, kChunks = 4, kB = 4, kXPad = 16;
+  static constexpr int kScale = 64;  // 16 fp32, one a row (few_up: gate, up)
+  static constexpr bool kF16 = false;
+};
+template <>
+struct Fmt<OES_WFMT_NVFP4> {
+  static constexpr int kStepK = 128, kRowBytes = 64, kChunks = 2, kB = 4, kXPad = 16;
+  static constexpr int kScale = 128 + 16;  // [2 x 64 of K][16 rows][4] e4m3, then the global scale
+  static constexpr bool kF16 = true;
+};
+template <int WF>
+__host__ __device__ constexpr int entry_bytes() {
+  return Fmt<WF>::kChunks * 512 + Fmt<WF>::kScale;
+}
+
+struct FewParams {
+  const uint8_t* pool;
+  int64_t row_bytes;
+  const int32_t* e2s;
+  int E, S, H, I, T, k;
+  const uint16_t* x;
+  const void* logits;  // NULL: ids and weights are given
+  int logits_bf16;
+  int32_t* ids;
+  float* weights;
+  uint16_t* h;  // [T k, I]
+  uint16_t* out;
+  int32_t* status;
+  int64_t s13, w2, s2, gs;  // sections of an expert row
+  int x_ld;                 // bytes of a row of x in shared memory
+  int rows_cta;             // few_down: rows of out a CTA owns
+};
+
+// The chunk's tables, in shared memory.
+struct Tables {
+  int32_t* ids;    // [R]
+  float* w;        // [R]
+  int32_t* lead;   // [R] first route of the route's block, -1 for one that does not count
+  int32_t* blk;    // [R] block of a leading route
+  int32_t* slot;   // [R] by block
+  int16_t* route;  // [blocks][8 NG] route of each token in a block, or -1
+  __device__ __forceinline__ Tables(uint8_t* base, int R) {
+    ids = reinterpret_cast<int32_t*>(base);
+    w = reinterpret_cast<float*>(ids + R);
+    lead = reinterpret_cast<int32_t*>(w + R);
+    blk = lead + R;
+    slot = blk + R;
+    route = reinterpret_cast<int16_t*>(slot + R);
+  }
+};
+__host__ __device__ constexpr int tables_bytes(int R, int ng) { return R * (20 + 16 * ng); }
+
+// Routing and tables, by the whole CTA; returns the number of blocks.  One CTA
+// writes the router's outputs and the status (`first`).
+template <int NG>
+__device__ int few_tables(const FewParams& p, const Tables& tb, bool first) {
+  __shared__ uint2 cand[kWarps][33];
+  __shared__ int s_nb;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int R = p.T * p.k;
+  for (int i = tid; i < R * 4 * NG; i += kThreads) reinterpret_cast<int32_t*>(tb.route)[i] = -1;
+  if (p.logits) {
+    for (int t = warp; t < p.T; t += kWarps) {
+      int32_t* ids = tb.ids + t * p.k;
+      float* w = tb.w + t * p.k;
+      if (p.logits_bf16)
+        topk_row_filtered<1, kFusedExperts / 32>(static_cast<const L2Bf16*>(p.logits) + (size_t)t * p.E, p.E, p.k,
+                                                 lane, ids, w, cand[warp]);
+      else
+        topk_row_filtered<1, kFusedExperts / 32>(static_cast<const L2F32*>(p.logits) + (size_t)t * p.E, p.E, p.k,
+                                                 lane, ids, w, cand[warp]);
+    }
+  } else {
+    for (int r = tid; r < R; r += kThreads) {
+      tb.ids[r] = __ldcg(p.ids + r);
+      tb.w[r] = __ldcg(p.weights + r);
+    }
+  }
+  __syncthreads();
+  for (int r = tid; r < R; r += kThreads) {
+    const int e = tb.ids[r];
+    const int t = r / p.k;
+    int lead = -1;
+    if (first && p.logits) {
+      p.ids[r] = e;
+      p.weights[r] = tb.w[r];
+    }
+    if (e >= 0 && e < p.E) {
+      const int slot = __ldcg(p.e2s + e);
+      if (slot >= 0 && slot < p.S) {
+        // this is the token's route number n to e; the block's first route is the
+        // first token's that has as many
+        int n = 0;
+        for (int i = t * p.k; i < r; ++i) n += tb.ids[i] == e;
+        lead = r;
+        for (int u = 0; u < t && lead == r; ++u) {
+          int m = 0;
+          for (int i = u * p.k; i < (u + 1) * p.k; ++i)
+            if (tb.ids[i] == e && m++ == n) {
+              lead = i;
+              break;
+            }
+        }
+        tb.blk[r] = slot;  // a leading route's, until the blocks are numbered
+      } else if (first) {
+        set_status(p.status, OES_DEV_BAD_ID);
+      }
+    }
+    tb.lead[r] = lead;
+  }
+  __syncthreads();
+  if (warp == 0) {
+    int n = 0;
+    for (int r0 = 0; r0 < R; r0 += 32) {
+      const int r = r0 + lane;
+      const bool is = r < R && tb.lead[r] == r;
+      const uint32_t m = __ballot_sync(0xffffffffu, is);
+      if (is) {
+        const int b = n + __popc(m & ((1u << lane) - 1));
+        tb.slot[b] = tb.blk[r];
+        tb.blk[r] = b;
+      }
+      n += __popc(m);
+    }
+    if (lane == 0) s_nb = n;
+  }
+  __syncthreads();
+  for (int r = tid; r < R; r += kThreads) {
+    const int lead = tb.lead[r];
+    if (lead >= 0) tb.route[tb.blk[lead] * 8 * NG + r / p.k] = (int16_t)r;
+  }
+  __syncthreads();
+  return s_nb;
+}
+
+// One step's matrix instructions: the lane's weights from its queue entry,
+// added onto d (row g and g + 8, columns 2t and 2t + 1, of each 8 tokens).
+template <int WF, int NG>
+__device__ __forceinline__ void step_mma(uint32_t entry, const uint4 (&B)[NG][Fmt<WF>::kB], float (&d)[NG][4]) {
+  const int lane = threadIdx.x & 31;
+  const uint32_t mine = entry + lane * 16;
+  if constexpr (WF == OES_WFMT_BF16) {
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const uint4 a = lds128(mine + hh * 1024), b = lds128(mine + hh * 1024 + 512);
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        mma_16816<false>(d[n], a.x, b.x, a.y, b.y, B[n][hh].x, B[n][hh].y);
+        mma_16816<false>(d[n], a.z, b.z, a.w, b.w, B[n][hh].z, B[n][hh].w);
+      }
+    }
+  } else if constexpr (WF == OES_WFMT_FP8) {
+#pragma unroll
+    for (int hh = 0; hh < 2; ++hh) {
+      const uint4 a = lds128(mine + hh * 1024), b = lds128(mine + hh * 1024 + 512);
+      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        uint32_t a0, a2, a1, a3;
+        e4m3x4_bf16x4(aw[i], a0, a2);
+        e4m3x4_bf16x4(bw[i], a1, a3);
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          const uint4& v = B[n][2 * hh + (i >> 1)];
+          mma_16816<false>(d[n], a0, a1, a2, a3, i & 1 ? v.z : v.x, i & 1 ? v.w : v.y);
+        }
+      }
+    }
+  } else {
+    const int g = lane >> 2, t = lane & 3;
+    const uint4 a = lds128(mine), b = lds128(mine + 512);
+    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+    // the lane's 32 values have the scales of groups 2t and 2t + 1 of the step
+    const uint32_t sc = entry + 1024 + (t >> 1) * 64 + g * 4;
+    const uint32_t sa = e4m3x2_f16x2((lds32(sc) >> (16 * (t & 1))) & 0xFFFFu);
+    const uint32_t sb = e4m3x2_f16x2((lds32(sc + 32) >> (16 * (t & 1))) & 0xFFFFu);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t fa = __byte_perm(sa, 0, i < 2 ? 0x1010 : 0x3232), fb = __byte_perm(sb, 0, i < 2 ? 0x1010 : 0x3232);
+      uint32_t oa[4], ob[4];
+      e2m1x8_f16x8(aw[i], oa);
+      e2m1x8_f16x8(bw[i], ob);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        oa[j] = mul_f16x2(oa[j], fa);
+        ob[j] = mul_f16x2(ob[j], fb);
+      }
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+        mma_16816<true>(d[n], oa[0], ob[0], oa[1], ob[1], B[n][i].x, B[n][i].y);
+        mma_16816<true>(d[n], oa[2], ob[2], oa[3], ob[3], B[n][i].z, B[n][i].w);
+      }
+    }
+  }
+}
+
+// The lane's copies of one step: 16 rows' kRowBytes from byte `at` of rows whose
+// first bytes for this lane are r0 (row g) and r1 (row g + 8); a row that is
+// absent (ok0, ok1) and bytes past `row` become zeros.
+template <int WF>
+__device__ __forceinline__ void step_copy(uint32_t entry, const uint8_t* pool, const uint8_t* r0, const uint8_t* r1,
+                                          bool ok0, bool ok1, int at, int row) {
+  const int lane = threadIdx.x & 31, t = lane & 3;
+  const uint32_t mine = entry + lane * 16;
+#pragma unroll
+  for (int hh = 0; hh < Fmt<WF>::kChunks / 2; ++hh) {
+    const int o = at + hh * 64;
+    const bool in = o + 16 * t < row;
+    cp_async16_take(mine + hh * 1024, in && ok0 ? r0 + o : pool, in && ok0);
+    cp_async16_take(mine + hh * 1024 + 512, in && ok1 ? r1 + o : pool, in && ok1);
+  }
+}
+
+// ------------------------------------------------------------------ gate, up
+template <int WF, int NG, int S>
+__global__ void __launch_bounds__(kThreads, 2) few_up_kernel(const FewParams p) {
+  using F = Fmt<WF>;
+  constexpr int kEntry = entry_bytes<WF>();
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* queue = smem + (threadIdx.x >> 5) * (S * kEntry);
+  float* part = reinterpret_cast<float*>(smem + kWarps * S * kEntry);  // [2][warp][lane][4 NG]
+  uint8_t* xs = reinterpret_cast<uint8_t*>(part + 2 * kThreads * 4 * NG);
+  const Tables tb(xs + p.T * p.x_ld, p.T * p.k);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  pdl_wait();
+  pdl_trigger();  // the down kernel; it reads what this kernel waited for, and h after this kernel's end
+  // x, with zeros up to a whole step
+  const int xc = cdiv(p.H, F::kStepK) * (F::kStepK / 8);
+  for (int i = tid; i < p.T * xc; i += kThreads) {
+    const int tok = i / xc, c = i - tok * xc;
+    const bool in = c * 8 < p.H;
+    const uint16_t* src = p.x + (size_t)tok * p.H + (in ? c * 8 : 0);
+    uint8_t* dst = xs + tok * p.x_ld + c * 16;
+    if constexpr (F::kF16) {
+      float v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+      if (in) load_vals<8>(src, v);
+      uint32_t o[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
+      }
+      *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+      cp_async16_take(smem_u32(dst), src, in);
+    }
+  }
+  cp_async_commit();
+  const int nb = few_tables<NG>(p, tb, blockIdx.x == 0);
+  const int groups = p.I / 8, units = nb * groups;
+  const int row = p.H * F::kRowBytes / F::kStepK;  // bytes of a weight row
+  const int ns = cdiv(p.H, F::kStepK);
+
+  // the next step to copy
+  int iu = warp < ns ? (int)blockIdx.x : units, is = warp, at = 0;
+  const uint8_t* base = p.pool;
+  const uint8_t* r0 = p.pool;
+  int rg = 0;
+  auto unit_rows = [&]() {
+    if (iu >= units) return;
+    const int b = iu / groups;
+    rg = (iu - b * groups) * 8;
+    base = p.pool + (int64_t)tb.slot[b] * p.row_bytes;
+    r0 = base + (int64_t)(rg + g) * row + 16 * t;
+  };
+  unit_rows();
+  auto copy_next = [&]() {
+    if (iu < units) {
+      const uint32_t e = smem_u32(queue + at * kEntry);
+      step_copy<WF>(e, p.pool, r0, r0 + (int64_t)p.I * row, true, true, is * F::kRowBytes, row);
+      if constexpr (WF == OES_WFMT_FP8) {
+        const int hb = cdiv(p.H, 128), ib = cdiv(p.I, 128);
+        if (lane < 2)
+          cp_async4_take(e + 2048 + 4 * lane, base + p.s13 + ((int64_t)(lane * ib + (rg >> 7)) * hb + is) * 4, true);
+      }
+      if constexpr (WF == OES_WFMT_NVFP4) {
+        const int r16 = lane & 15, c = 2 * is + (lane >> 4);
+        const bool in = c * 64 < p.H;
+        cp_async4_take(e + 1024 + 4 * lane,
+                       base + p.s13 + ((int64_t)(in ? c : 0) * 2 * p.I + (r16 >> 3) * p.I + rg + (r16 & 7)) * 4, in);
+        if (lane == 0) cp_async4_take(e + 1024 + 128, base + p.gs, true);
+      }
+      is += kWarps;
+      if (is >= ns) {
+        is = warp;
+        iu += gridDim.x;
+        unit_rows();
+      }
+    }
+    cp_async_commit();
+    at = at + 1 == S ? 0 : at + 1;
+  };
+  for (int i = 0; i < S; ++i) copy_next();
+  cp_async_wait<S>();  // x
+  __syncthreads();
+
+  const uint8_t* xb[NG];
+#pragma unroll
+  for (int n = 0; n < NG; ++n) {
+    const int tok = min(8 * n + g, p.T - 1);  // columns past the tokens are not used
+    xb[n] = xs + tok * p.x_ld + (WF == OES_WFMT_BF16 ? 16 : WF == OES_WFMT_FP8 ? 32 : 64) * t;
+  }
+  int from = 0, buf = 0;
+  for (int u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
+    float acc[NG][4];
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+    float gs = 1.0f;
+    for (int s = warp; s < ns; s += kWarps) {
+      cp_async_wait<S - 1>();
+      __syncwarp();  // scales that other lanes copied
+      const uint32_t e = smem_u32(queue + from * kEntry);
+      uint4 B[NG][F::kB];
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int i = 0; i < F::kB; ++i) {
+          const int o = WF == OES_WFMT_BF16 ? 64 * i : WF == OES_WFMT_FP8 ? 128 * (i >> 1) + 16 * (i & 1) : 16 * i;
+          B[n][i] = *reinterpret_cast<const uint4*>(xb[n] + s * (2 * F::kStepK) + o);
+        }
+      if constexpr (WF == OES_WFMT_FP8) {
+        float d[NG][4];
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
+        step_mma<WF, NG>(e, B, d);
+        const float sg = __uint_as_float(lds32(e + 2048)), su = __uint_as_float(lds32(e + 2052));
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(i < 2 ? sg : su, d[n][i], acc[n][i]);
+      } else {
+        step_mma<WF, NG>(e, B, acc);
+        if constexpr (WF == OES_WFMT_NVFP4) gs = __uint_as_float(lds32(e + 1024 + 128));
+      }
+      __syncwarp();
+      from = from + 1 == S ? 0 : from + 1;
+      copy_next();
+    }
+    float* mine = part + ((buf * kWarps + warp) * 32 + lane) * (4 * NG);
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+      *reinterpret_cast<float4*>(mine + 4 * n) =
+          make_float4(gs * acc[n][0], gs * acc[n][1], gs * acc[n][2], gs * acc[n][3]);
+    __syncthreads();
+    if (tid < 64 * NG) {
+      const int col = tid >> 3, r8 = tid & 7, b = u / groups;
+      const int r = tb.route[b * 8 * NG + col];
+      if (r >= 0) {
+        const float* v = part + (buf * kWarps * 32 + r8 * 4 + (col & 7) / 2) * (4 * NG) + (col >> 3) * 4 + (col & 1);
+        float gate = 0.0f, up = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+          gate += v[w * 32 * 4 * NG];
+          up += v[w * 32 * 4 * NG + 2];
+        }
+        const float h = silu_f32(gate) * up;
+        uint16_t bits;
+        if constexpr (F::kF16) asm("cvt.rn.f16.f32 %0, %1;" : "=h"(bits) : "f"(h));
+        else bits = (uint16_t)f32_bf16(h);
+        p.h[(int64_t)r * p.I + (u - b * groups) * 8 + r8] = bits;
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------- down
+// Launched early: every CTA of few_up_kernel has passed its own wait then, so all
+// that was written before it (logits, routes, the slot map, x, the pool) is
+// complete, and this kernel reads it through L2 without waiting.  h is
+// few_up_kernel's, and is read after the wait.
+template <int WF, int NG, int S>
+__global__ void __launch_bounds__(kThreads, 2) few_down_kernel(const FewParams p) {
+  using F = Fmt<WF>;
+  constexpr int kEntry = entry_bytes<WF>();
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* queue = smem + (threadIdx.x >> 5) * (S * kEntry);
+  float* part = reinterpret_cast<float*>(smem + kWarps * S * kEntry);  // [2][warp][lane][4 NG]
+  const Tables tb(reinterpret_cast<uint8_t*>(part + 2 * kThreads * 4 * NG), p.T * p.k);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const int nb = few_tables<NG>(p, tb, false);
+  const int row = p.I * F::kRowBytes / F::kStepK;
+  const int ns = cdiv(p.I, F::kStepK);
+  const int row_lo = blockIdx.x * p.rows_cta, row_hi = min(p.H, row_lo + p.rows_cta);
+
+  // a place in the warp's steps: (block, step) in turns of kWarps, and the tile
+  struct Place {
+    int b, s, row0;
+  };
+  auto first = [&](int row0) {
+    Place q{0, warp, row0};
+    while (q.s >= ns) {
+      q.s -= ns;
+      ++q.b;
+    }
+    return q;
+  };
+  auto next = [&](Place& q) {
+    q.s += kWarps;
+    while (q.s >= ns) {
+      q.s -= ns;
+      ++q.b;
+    }
+    if (q.b >= nb) q = first(q.row0 + kRowTile);
+  };
+  const bool any = first(0).b < nb;  // whether the warp has a step in each tile
+
+  Place c = first(row_lo);
+  int at = 0;
+  auto copy_next = [&]() {
+    if (any && c.row0 < row_hi) {
+      const uint32_t e = smem_u32(queue + at * kEntry);
+      const uint8_t* base = p.pool + (int64_t)tb.slot[c.b] * p.row_bytes;
+      const uint8_t* w = base + p.w2 + (int64_t)(c.row0 + g) * row + 16 * t;
+      step_copy<WF>(e, p.pool, w, w + 8 * (int64_t)row, c.row0 + g < row_hi, c.row0 + g + 8 < row_hi, c.s * F::kRowBytes, row);
+      if constexpr (WF == OES_WFMT_FP8) {
+        const int r = c.row0 + lane;
+        if (lane < kRowTile)
+          cp_async4_take(e + 2048 + 4 * lane,
+                         base + p.s2 + ((int64_t)(r < row_hi ? r >> 7 : 0) * ns + c.s) * 4, r < row_hi);
+      }
+      if constexpr (WF == OES_WFMT_NVFP4) {
+        const int r = c.row0 + (lane & 15), k64 = 2 * c.s + (lane >> 4);
+        const bool in = r < row_hi && k64 * 64 < p.I;
+        cp_async4_take(e + 1024 + 4 * lane, base + p.s2 + (in ? (int64_t)k64 * p.H + r : 0) * 4, in);
+        if (lane == 0) cp_async4_take(e + 1024 + 128, base + p.gs + 4, true);
+      }
+      next(c);
+    }
+    cp_async_commit();
+    at = at + 1 == S ? 0 : at + 1;
+  };
+  for (int i = 0; i < S; ++i) copy_next();
+  pdl_wait();  // h
+
+  auto load_h = [&](const Place& q, uint4 (&B)[NG][F::kB]) {
+#pragma unroll
+    for (int n = 0; n < NG; ++n) {
+      const int r = any && q.row0 < row_hi ? tb.route[q.b * 8 * NG + 8 * n + g] : -1;
+#pragma unroll
+      for (int i = 0; i < F::kB; ++i) {
+        const int k = q.s * F::kStepK + (WF == OES_WFMT_BF16  ? 32 * i + 8 * t
+                                         : WF == OES_WFMT_FP8 ? 64 * (i >> 1) + 16 * t + 8 * (i & 1)
+                                                              : 32 * t + 8 * i);
+        B[n][i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r >= 0 && k < p.I) B[n][i] = __ldcg(reinterpret_cast<const uint4*>(p.h + (int64_t)r * p.I + k));
+      }
+    }
+  };
+  uint4 B[NG][F::kB];
+  Place q = first(row_lo);
+  load_h(q, B);
+  int from = 0, buf = 0;
+  for (int row0 = row_lo; row0 < row_hi; row0 += kRowTile, buf ^= 1) {
+    float acc[NG][4];
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+    while (any && q.row0 == row0) {
+      const int b = q.b;
+      next(q);
+      uint4 Bn[NG][F::kB];
+      load_h(q, Bn);  // the next step's, while this one is multiplied
+      cp_async_wait<S - 1>();
+      __syncwarp();
+      const uint32_t e = smem_u32(queue + from * kEntry);
+      float d[NG][4];
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
+      step_mma<WF, NG>(e, B, d);
+      float s0 = 1.0f, s1 = 1.0f;
+      if constexpr (WF == OES_WFMT_FP8) {
+        s0 = __uint_as_float(lds32(e + 2048 + 4 * g));
+        s1 = __uint_as_float(lds32(e + 2048 + 32 + 4 * g));
+      }
+      if constexpr (WF == OES_WFMT_NVFP4) s0 = s1 = __uint_as_float(lds32(e + 1024 + 128));
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          // a token without a route in this block takes nothing from it, not
+          // even a NaN of its weights
+          const int r = tb.route[b * 8 * NG + 8 * n + 2 * t + j];
+          if (r >= 0) {
+            const float w = tb.w[r];
+            acc[n][j] = fmaf(w, s0 * d[n][j], acc[n][j]);
+            acc[n][2 + j] = fmaf(w, s1 * d[n][2 + j], acc[n][2 + j]);
+          }
+        }
+      __syncwarp();
+      from = from + 1 == S ? 0 : from + 1;
+      copy_next();
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int i = 0; i < F::kB; ++i) B[n][i] = Bn[n][i];
+    }
+    float* mine = part + ((buf * kWarps + warp) * 32 + lane) * (4 * NG);
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+      *reinterpret_cast<float4*>(mine + 4 * n) = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+    __syncthreads();
+    for (int i = tid; i < kRowTile * p.T; i += kThreads) {
+      const int r16 = i & 15, tok = i >> 4;
+      if (row0 + r16 >= row_hi) continue;
+      const float* v = part + (buf * kWarps * 32 + (r16 & 7) * 4 + (tok & 7) / 2) * (4 * NG) + (tok >> 3) * 4 +
+                       (r16 >> 3) * 2 + (tok & 1);
+      float s = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s += v[w * 32 * 4 * NG];
+      p.out[(int64_t)tok * p.H + row0 + r16] = (uint16_t)f32_bf16(s);
+    }
+  }
+}
+
+// ------------------------------------------------------------------ launches
+constexpr size_t kSmemMost = 227 * 1024 - 3 * 1024;  // beside the kernels' static shared memory
+
+template <int WF>
+int x_stride(int H) {
+  using F = Fmt<WF>;
+  // rows a bank's width apart, so that the eight lanes of a phase never meet
+  return ceil_div(H, F::kStepK) * F::kStepK * 2 + F::kXPad;
+}
+
+template <int WF, int NG, int S>
+size_t up_smem(int T, int k, int H) {
+  return (size_t)kWarps * S * entry_bytes<WF>() + 2 * kThreads * 16 * NG + (size_t)T * x_stride<WF>(H) +
+         tables_bytes(T * k, NG);
+}
+
+template <int WF, int NG, int S>
+int launch_up(const FewParams& p, cudaStream_t stream) {
+  const size_t smem = up_smem<WF, NG, S>(p.T, p.k, p.H);
+  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(few_up_kernel<WF, NG, S>), smem,
+                                "few_up_kernel: shared memory limit");
+  if (rc) return rc;
+  const int64_t units = (int64_t)p.T * p.k * (p.I / 8);
+  launch_kernel(few_up_kernel<WF, NG, S>, (int)std::min<int64_t>(num_sms(), units), kThreads, smem, stream, p);
+  OES_CHECK_LAUNCH("few_up_kernel");
+  return OES_OK;
+}
+
+// One group of tokens: both kernels.
+template <int WF, int NG>
+int launch_few(FewParams p, cudaStream_t stream) {
+  constexpr int S = 5;
+  p.x_ld = x_stride<WF>(p.H);
+  const int rc = up_smem<WF, NG, S>(p.T, p.k, p.H) <= kSmemMost ? launch_up<WF, NG, S>(p, stream)
+                                                                : launch_up<WF, NG, 2>(p, stream);
+  if (rc) return rc;
+  const size_t smem = (size_t)kWarps * S * entry_bytes<WF>() + 2 * kThreads * 16 * NG + tables_bytes(p.T * p.k, NG);
+  const int rc2 = set_max_dynamic_smem(reinterpret_cast<const void*>(few_down_kernel<WF, NG, S>), smem,
+                                       "few_down_kernel: shared memory limit");
+  if (rc2) return rc2;
+  p.rows_cta = ceil_div(p.H, num_sms());
+  launch_kernel(few_down_kernel<WF, NG, S>, ceil_div(p.H, p.rows_cta), kThreads, smem, stream, p);
+  OES_CHECK_LAUNCH("few_down_kernel");
+  return OES_OK;
+}
+
+// Most tokens whose rows of x fit beside the queues.
+template <int WF>
+int group_tokens(int T, int k, int H) {
+  int n = T;
+  while (n > 1 && (n > 8 ? up_smem<WF, 2, 2>(n, k, H) : up_smem<WF, 1, 2>(n, k, H)) > kSmemMost) --n;
+  return n;
+}
+
+template <int WF>
+int run_few(FewParams p, cudaStream_t stream) {
+  const int T = p.T, groups = ceil_div(T, group_tokens<WF>(T, p.k, p.H)), per = ceil_div(T, groups);
+  for (int t0 = 0; t0 < T; t0 += per) {
+    FewParams q = p;
+    q.T = std::min(per, T - t0);
+    q.x += (size_t)t0 * p.H;
+    q.out += (size_t)t0 * p.H;
+    q.ids += (size_t)t0 * p.k;
+    q.weights += (size_t)t0 * p.k;
+    if (p.logits) q.logits = static_cast<const uint8_t*>(p.logits) + (size_t)t0 * p.E * (p.logits_bf16 ? 2 : 4);
+    const int rc = q.T > 8 ? launch_few<WF, 2>(q, stream) : launch_few<WF, 1>(q, stream);
+    if (rc) return rc;
+  }
+  return OES_OK;
+}
+
+}  // namespace
+}  // namespace oes
+
+using namespace oes;
+
+namespace {
+// The view's own limits; shared by the size query and the call.
+int check_view(const oes_routed_experts* v, int T, int k, const char* who) {
+  OES_REQUIRE(v, "%s: null view", who);
+  OES_REQUIRE(v->E >= 1 && v->E <= OES_MAX_EXPERTS && v->S >= 1, "%s: bad E=%d S=%d", who, v->E, v->S);
+  OES_REQUIRE(v->H >= 64 && v->I >= 64 && v->H % 64 == 0 && v->I % 64 == 0 && v->H <= 16384 && v->I <= 16384,
+              "%s: H=%d I=%d must be multiples of 64 in [64, 16384]", who, v->H, v->I);
+  OES_REQUIRE(v->wfmt >= OES_WFMT_BF16 && v->wfmt <= OES_WFMT_FP8, "%s: bad wfmt %d", who, v->wfmt);
+  OES_REQUIRE(T >= 0 && k >= 1 && k <= OES_MAX_TOPK, "%s: bad T=%d k=%d", who, T, k);
+  if (v->wfmt == OES_WFMT_NVFP4_W4A4) {
+    set_error("%s: activations are not quantised here (OES_WFMT_NVFP4 reads the same rows)", who);
+    return OES_ERR_UNSUPPORTED;
+  }
+  if (T > OES_FEW_TOKENS_MAX) {
+    set_error("%s: %d tokens, at most %d", who, T, OES_FEW_TOKENS_MAX);
+    return OES_ERR_UNSUPPORTED;
+  }
+  return OES_OK;
+}
+static_assert(OES_FEW_TOKENS_MAX == kMaxTokens, "tokens a call");
+}  // namespace
+
+extern "C" size_t moe_layer_few_tokens_workspace_size(const oes_routed_experts* v, int T, int k) {
+  if (check_view(v, T, k, "moe_layer_few_tokens_workspace_size")) return 0;
+  return ((size_t)T * k * v->I * 2 + 255) / 256 * 256;
+}
+
+extern "C" int moe_layer_few_tokens(const oes_routed_experts* v, const uint16_t* x, int T, int k, const void* logits,
+                                    int dtype, int32_t* ids, float* weights, void* workspace, size_t workspace_bytes,
+                                    uint16_t* out, int32_t* status, oes_stream_t stream) {
+  const char* who = "moe_layer_few_tokens";
+  int rc = check_view(v, T, k, who);
+  if (rc) return rc;
+  OES_REQUIRE(dtype == OES_LOGITS_F32 || dtype == OES_LOGITS_BF16, "%s: unknown logits type %d", who, dtype);
+  OES_REQUIRE(!logits || k <= v->E, "%s: k=%d of E=%d experts", who, k, v->E);
+  if (T == 0) return OES_OK;
+  OES_REQUIRE(v->pool && v->e2s && x && ids && weights && workspace && out, "%s: null pointer", who);
+  const Fp8Row f8 = fp8_row(v->H, v->I);
+  const int64_t hi = (int64_t)v->H * v->I;
+  FewParams p{};
+  int64_t need;
+  if (v->wfmt == OES_WFMT_BF16) {
+    p.w2 = 4 * hi;
+    need = 6 * hi;
+  } else if (v->wfmt == OES_WFMT_FP8) {
+    p.s13 = f8.s13;
+    p.w2 = f8.w2;
+    p.s2 = f8.s2;
+    need = f8.end;
+  } else {
+    p.s13 = hi;
+    p.w2 = p.s13 + hi / 8;
+    p.s2 = p.w2 + hi / 2;
+    p.gs = p.s2 + hi / 16;
+    need = p.gs + 16;
+  }
+  OES_REQUIRE(v->row_bytes >= need && v->row_bytes % 16 == 0, "%s: row_bytes %lld (layout needs %lld, multiple of 16)",
+              who, (long long)v->row_bytes, (long long)need);
+  OES_REQUIRE(((uintptr_t)v->pool & 15) == 0 && ((uintptr_t)x & 15) == 0 && ((uintptr_t)workspace & 15) == 0,
+              "%s: pool, x and workspace must be 16-byte aligned", who);
+  OES_REQUIRE((((uintptr_t)ids | (uintptr_t)weights | (uintptr_t)v->e2s | (uintptr_t)status) & 3) == 0 &&
+                  ((uintptr_t)out & 1) == 0 && ((uintptr_t)logits & (dtype == OES_LOGITS_F32 ? 3 : 1)) == 0,
+              "%s: a pointer is not aligned to its type", who);
+  const size_t bytes = moe_layer_few_tokens_workspace_size(v, T, k);
+  OES_REQUIRE(workspace_bytes >= bytes, "%s: workspace %zu < %zu bytes", who, workspace_bytes, bytes);
+  p.pool = static_cast<const uint8_t*>(v->pool);
+  p.row_bytes = v->row_bytes;
+  p.e2s = v->e2s;
+  p.E = v->E;
+  p.S = v->S;
+  p.H = v->H;
+  p.I = v->I;
+  p.T = T;
+  p.k = k;
+  p.x = x;
+  p.logits = logits;
+  p.logits_bf16 = dtype == OES_LOGITS_BF16;
+  p.ids = ids;
+  p.weights = weights;
+  p.h = static_cast<uint16_t*>(workspace);
+  p.out = out;
+  p.status = status;
+  if (logits && v->E > kFusedExperts) {
+    // wider rows are routed by the router's own kernel: held 16 a lane, a row of 512
+    // fits these kernels' registers
+    if ((rc = moe_route_topk(logits, dtype, T, v->E, k, ids, weights, stream))) return rc;
+    p.logits = nullptr;
+  }
+  if (v->wfmt == OES_WFMT_BF16) return run_few<OES_WFMT_BF16>(p, stream);
+  if (v->wfmt == OES_WFMT_FP8) return run_few<OES_WFMT_FP8>(p, stream);
+  return run_few<OES_WFMT_NVFP4>(p, stream);
+}

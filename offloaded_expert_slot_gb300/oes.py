@@ -33,6 +33,7 @@ OES_QUERY_MAX = 128
 OES_MAX_TOPK = 32
 OES_MAX_EXPERTS = 4096
 OES_MAX_SLOTS = 8192
+OES_FEW_TOKENS_MAX = 16
 
 _ERR_NAMES = {1: "OES_ERR_INVALID_ARG", 2: "OES_ERR_UNSUPPORTED", 3: "OES_ERR_CUDA",
               4: "OES_ERR_CAPACITY"}
@@ -123,6 +124,9 @@ _SIGS = {
     "oes_stage_plan_layer": (_i, [_vp, _i, C.POINTER(_i), _vp, C.POINTER(_i)]),
     "moe_layers_forward_staged": (_i, [_vp, _vp, _vp, C.POINTER(LayerDesc), C.POINTER(Chunk), _vp,
                                        _vp]),
+    "moe_layer_few_tokens_workspace_size": (_sz, [C.POINTER(RoutedExperts), _i, _i]),
+    "moe_layer_few_tokens": (_i, [C.POINTER(RoutedExperts), _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _sz, _vp, _vp,
+                                  _vp]),
     "moe_fp8_quantize": (_i, [_vp, _i, _i64, _i, _i, _i, _vp, _i64, _vp, _vp]),
     "moe_fp8_gemm": (_i, [_vp, _i64, _vp, _i, _i, _vp, _i64, _vp, _i, _vp, _i, _i64, _vp, _vp]),
     "moe_block_norm": (_i, [C.POINTER(BlockNorm), _vp]),
@@ -360,6 +364,27 @@ def moe_grouped_gemm_slots(view: RoutedExperts, x, T, k, ids, weights, sorted_id
     _call("moe_grouped_gemm_slots", C.byref(view), _ptr(x), T, k, _ptr(ids), _ptr(weights),
           _ptr(sorted_ids), _ptr(block_expert), _ptr(n_post_pad), B, _ptr(workspace),
           workspace_bytes, _ptr(out), _ptr(status), _stream(stream))
+
+
+# ------------------------------------------------- a layer for few tokens
+def moe_layer_few_tokens_workspace_size(view: RoutedExperts, T, k) -> int:
+    return int(load().moe_layer_few_tokens_workspace_size(C.byref(view), T, k))
+
+
+_logits_types: dict = {}      # dtype object -> OES_LOGITS_*
+
+
+def moe_layer_few_tokens(view: RoutedExperts, x, T, k, ids, weights, workspace, workspace_bytes, out, status=None,
+                         logits=None, stream=None, dtype=None):
+    """With logits, ids and weights receive the routing; without, they are read.
+    dtype: OES_LOGITS_*, or None to take it from the logits array."""
+    if dtype is None:
+        t = getattr(logits, "dtype", None)
+        dtype = _logits_types.get(t)
+        if dtype is None:
+            dtype = _logits_types[t] = _logits_type(logits)
+    _call("moe_layer_few_tokens", C.byref(view), _ptr(x), T, k, _ptr(logits), dtype, _ptr(ids), _ptr(weights),
+          _ptr(workspace), workspace_bytes, _ptr(out), _ptr(status), _stream(stream))
 
 
 # --------------------------------------------- 8-bit rows and block norms
