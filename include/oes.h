@@ -497,6 +497,38 @@ int moe_fp8_gemm(const uint8_t *xq, int64_t xq_ld, const float *xs, int T, int K
                  int64_t wq_ld, const float *ws, int N, void *out, int dtype, int64_t out_ld,
                  int32_t *status, oes_stream_t stream);
 
+/* Rows to 8-bit integers with one fp32 scale a row (a token).  For each row t,
+ * over its values v:  amax = max(|v|, 2^-100), scale[t] = amax / 127, and
+ * q[t, i] = the integer nearest to the real number 127 v / amax, ties to even.
+ * A row with a NaN or an infinity gets a NaN scale and codes of 0 (the row reads as
+ * NaN).  act, x, dtype, x_ld as in moe_fp8_quantize (for OES_ACT_SWIGLU, v is
+ * fp32); q: device, row stride q_ld >= K; scale: device [T] fp32.  T >= 0,
+ * 1 <= K <= 2^28.  Rows are read and written 8 values at a time when K, strides and
+ * addresses allow it (K a multiple of 8; x and its rows 16-byte, q and its rows
+ * 8-byte aligned). */
+int moe_int8_quantize(const void *x, int dtype, int64_t x_ld, int T, int K, int act, int8_t *q,
+                      int64_t q_ld, float *scale, oes_stream_t stream);
+
+/* Workspace bytes of moe_int8_gemm (0 for few rows, and for sizes it refuses). */
+size_t moe_int8_gemm_workspace_size(int T, int K, int N);
+
+/* The matrix product of 8-bit integer rows with a scale for each token and each
+ * channel, as a shared expert or a projection beside the routed experts uses it:
+ *   out[t, n] = sum_k xq[t, k] * wq[n, k] * xs[t] * ws[n]
+ * The sum is the exact integer; it is converted to fp32, multiplied by xs and then
+ * by ws, and rounded to out's type.
+ * xq: device [T, K], row stride xq_ld bytes, xs: device [T] fp32
+ * (moe_int8_quantize); wq: device [N, K], row stride wq_ld bytes, ws: device [N]
+ * fp32; codes may be any of -128..127; out: device [T, N] of dtype OES_BF16 or
+ * OES_F32, row stride out_ld values.  xq and wq are 16-byte aligned and their row
+ * strides multiples of 16 (bytes past K in a row are not read).  workspace: device
+ * scratch of moe_int8_gemm_workspace_size(T, K, N) bytes, 256-byte aligned (NULL
+ * where that is 0); calls that may overlap need their own.  T >= 0,
+ * 1 <= K <= 65536, 1 <= N <= 2^24.  status: device word or NULL. */
+int moe_int8_gemm(const int8_t *xq, int64_t xq_ld, const float *xs, int T, int K, const int8_t *wq,
+                  int64_t wq_ld, const float *ws, int N, void *out, int dtype, int64_t out_ld,
+                  void *workspace, size_t workspace_bytes, int32_t *status, oes_stream_t stream);
+
 /* Gates of moe_block_norm: none; one fp32 value a token (gate[t * gate_ld]:
  * a column of moe_gate_logits' output does); one bf16 value a channel,
  * gate[h]; one bf16 value each, gate[t * gate_ld + h]. */

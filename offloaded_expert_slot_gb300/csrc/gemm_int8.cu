@@ -1,0 +1,549 @@
+// moe_int8_gemm: matrix products of 8-bit integer rows, a scale for each row of
+// both sides:
+//
+//   out[t, n] = xs[t] ws[n] sum_k x[t, k] w[n, k]
+//
+// GB300's tensor cores have no fast integer products, and need none here: f16
+// holds every 8-bit integer exactly, its products are below 2^14 and exact in the
+// tensor core, and fp32 sums of up to 1024 of them stay below 2^24, where
+// integers are exact.  So the sums of at most 1024 of K come from f16 matrix
+// instructions and are added up as 32-bit integers: the sum is the integer, whatever
+// the order, at the f16 rate.
+//
+//   int8_stream_kernel  few rows: a CTA takes 16 weight rows at a time, its warps
+//                       share K and stream the weights through queues of their
+//                       own (as in few_tokens.cu), x stands in shared memory as
+//                       f16.  Bound by the stream of weights.
+//   int8_tm_kernel      more rows: 128 rows x 256 (or 64) weight rows a tile on
+//                       tcgen05, operands by TMA from f16 copies of both that
+//                       int8_to_f16_kernel leaves in the workspace.
+#include <algorithm>
+
+#include "common.cuh"
+#include "fp8_dev.cuh"
+#include "tc_dev.cuh"
+#include "warp_mma.cuh"
+
+namespace oes {
+namespace {
+
+// ================================================================= few rows
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kQueue = 4;       // steps in flight a warp
+constexpr int kStepK = 128;
+constexpr int kEntry = 2048;    // 16 rows of a step
+
+struct StreamArgs {
+  const int8_t* x;
+  int64_t x_ld;
+  const float* xs;
+  const int8_t* w;
+  int64_t w_ld;
+  const float* ws;
+  int T, K, N;
+  void* out;
+  int64_t out_ld;
+  int rows_cta, x_row;  // weight rows a CTA owns; bytes of a row of x in shared memory
+};
+
+__host__ __device__ constexpr int64_t stream_x_row(int K) { return (int64_t)(K + kStepK - 1) / kStepK * kStepK * 2 + 16; }
+int64_t stream_smem(int T, int K) {
+  const int ng = T <= 8 ? 1 : T <= 16 ? 2 : 4;
+  return kWarps * kQueue * kEntry + 2 * kThreads * 16 * ng + T * stream_x_row(K);
+}
+
+template <int NG, typename OT>
+__global__ void __launch_bounds__(kThreads, 1) int8_stream_kernel(const StreamArgs p) {
+  extern __shared__ __align__(128) uint8_t smem[];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  const uint32_t queue = smem_u32(smem + warp * (kQueue * kEntry)) + lane * 16;
+  int32_t* part = reinterpret_cast<int32_t*>(smem + kWarps * kQueue * kEntry);  // [2][warp][lane][4 NG]
+  uint8_t* xs = reinterpret_cast<uint8_t*>(part + 2 * kThreads * 4 * NG);
+  const int ns = (p.K + kStepK - 1) / kStepK;
+  const int row_lo = blockIdx.x * p.rows_cta, row_hi = min(p.N, row_lo + p.rows_cta);
+  pdl_begin();
+
+  // the next step to copy
+  int ct = row_lo, cs = warp, at = 0;
+  auto copy_next = [&]() {
+    if (cs < ns && ct < row_hi) {
+      const int8_t* r0 = p.w + (int64_t)(ct + g) * p.w_ld;
+      const bool ok0 = ct + g < row_hi, ok1 = ct + g + 8 < row_hi;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const int k = cs * kStepK + hh * 64 + 16 * t;
+        const int n = max(0, min(16, p.K - k));
+        cp_async16_part(queue + at * kEntry + hh * 1024, ok0 && n > 0 ? r0 + k : p.w, ok0 ? n : 0);
+        cp_async16_part(queue + at * kEntry + hh * 1024 + 512, ok1 && n > 0 ? r0 + 8 * p.w_ld + k : p.w, ok1 ? n : 0);
+      }
+      cs += kWarps;
+      if (cs >= ns) {
+        cs = warp;
+        ct += 16;
+      }
+    }
+    cp_async_commit();
+    at = (at + 1) % kQueue;
+  };
+  for (int i = 0; i < kQueue; ++i) copy_next();
+
+  // x as f16, zeros past K (which silence what a weight's row holds there)
+  const int xc = ns * (kStepK / 16);
+  for (int i = tid; i < p.T * xc; i += kThreads) {
+    const int tok = i / xc, k = (i - tok * xc) * 16;
+    const int8_t* src = p.x + (int64_t)tok * p.x_ld + k;
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (k + 16 <= p.K) {
+      const uint4 v = *reinterpret_cast<const uint4*>(src);
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+      for (int j = 0; j < 16 && k + j < p.K; ++j) w[j >> 2] |= (uint32_t)(uint8_t)src[j] << (8 * (j & 3));
+    }
+    uint32_t o[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s8x4_f16x4(w[j], o[2 * j], o[2 * j + 1]);
+    uint4* dst = reinterpret_cast<uint4*>(xs + (int64_t)tok * p.x_row + 2 * k);
+    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+  }
+  __syncthreads();
+
+  uint32_t xb[NG];
+#pragma unroll
+  for (int n = 0; n < NG; ++n) xb[n] = smem_u32(xs + (int64_t)min(8 * n + g, p.T - 1) * p.x_row) + 32 * t;
+  int from = 0, buf = 0;
+  for (int row0 = row_lo; row0 < row_hi; row0 += 16, buf ^= 1) {
+    int32_t acc[NG][4];
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0;
+    for (int s = warp; s < ns; s += kWarps) {
+      cp_async_wait<kQueue - 1>();
+      float d[NG][4];
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
+#pragma unroll
+      for (int hh = 0; hh < 2; ++hh) {
+        const uint4 a = lds128(queue + from * kEntry + hh * 1024), b = lds128(queue + from * kEntry + hh * 1024 + 512);
+        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+        uint32_t m[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          s8x4_f16x4(aw[i], m[i][0], m[i][2]);
+          s8x4_f16x4(bw[i], m[i][1], m[i][3]);
+        }
+#pragma unroll
+        for (int n = 0; n < NG; ++n) {
+          const uint32_t xa = xb[n] + s * (2 * kStepK) + hh * 128;
+          const uint4 u = lds128(xa), v = lds128(xa + 16);
+          mma_16816<true>(d[n], m[0][0], m[0][1], m[0][2], m[0][3], u.x, u.y);
+          mma_16816<true>(d[n], m[1][0], m[1][1], m[1][2], m[1][3], u.z, u.w);
+          mma_16816<true>(d[n], m[2][0], m[2][1], m[2][2], m[2][3], v.x, v.y);
+          mma_16816<true>(d[n], m[3][0], m[3][1], m[3][2], m[3][3], v.z, v.w);
+        }
+      }
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[n][i] += __float2int_rn(d[n][i]);
+      from = (from + 1) % kQueue;
+      copy_next();
+    }
+    int32_t* mine = part + ((buf * kWarps + warp) * 32 + lane) * (4 * NG);
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+      *reinterpret_cast<int4*>(mine + 4 * n) = make_int4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+    __syncthreads();
+    for (int i = tid; i < 16 * p.T; i += kThreads) {
+      const int r16 = i & 15, tok = i >> 4, n = row0 + r16;
+      if (n >= row_hi) continue;
+      const int32_t* v = part + (buf * kWarps * 32 + (r16 & 7) * 4 + (tok & 7) / 2) * (4 * NG) + (tok >> 3) * 4 +
+                         (r16 >> 3) * 2 + (tok & 1);
+      int32_t sum = 0;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) sum += v[w * 32 * 4 * NG];
+      const float o = (float)sum * p.xs[tok] * p.ws[n];
+      if constexpr (sizeof(OT) == 2) static_cast<uint16_t*>(p.out)[tok * p.out_ld + n] = (uint16_t)f32_bf16(o);
+      else static_cast<float*>(p.out)[tok * p.out_ld + n] = o;
+    }
+  }
+}
+
+// ================================================================ more rows
+struct CvtArgs {
+  const int8_t* src[2];  // x, w
+  int64_t ld[2];
+  uint16_t* dst[2];      // rows of Kp values
+  int rows0;             // of x
+  int64_t rows;          // of both
+  int K, Kp;
+  int step_r, step_c;    // the chunks of the whole grid, in rows and chunks
+};
+
+// Rows of codes to rows of f16, zeros from K to Kp (a multiple of 64).
+__global__ void __launch_bounds__(256) int8_to_f16_kernel(const CvtArgs a) {
+  pdl_begin();
+  const int nc = a.Kp / 16;
+  const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  int64_t r = first / nc;
+  int c = (int)(first - r * nc);
+  while (r < a.rows) {
+    const int o = r >= a.rows0;
+    const int64_t row = o ? r - a.rows0 : r;
+    const int8_t* src = a.src[o] + row * a.ld[o] + c * 16;
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    if (c * 16 + 16 <= a.K) {
+      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
+      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+    } else {
+      for (int j = 0; j < 16 && c * 16 + j < a.K; ++j) w[j >> 2] |= (uint32_t)(uint8_t)src[j] << (8 * (j & 3));
+    }
+    uint32_t v[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s8x4_f16x4(w[j], v[2 * j], v[2 * j + 1]);
+    uint4* dst = reinterpret_cast<uint4*>(a.dst[o] + row * a.Kp + c * 16);
+    dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+    r += a.step_r;
+    c += a.step_c;
+    if (c >= nc) {
+      c -= nc;
+      ++r;
+    }
+  }
+}
+
+constexpr int kTileM = 128;
+constexpr int kBlkBytes = 128;        // 64 f16 of K, a pipeline stage's row
+constexpr int kDrain = 16;            // stages (1024 of K) a TMEM buffer sums
+constexpr int kEpiW0 = 4, kEpi = 8;   // epilogue warps: two a TMEM lane quarter
+constexpr int kTmThreads = (kEpiW0 + kEpi) * 32;
+
+struct TmMaps {
+  CUtensorMap x, w;  // f16 [T][Kp], [N][Kp]
+};
+struct TmArgs {
+  const float* xs;
+  const float* ws;
+  int T, N, nkb;  // nkb: stages of K
+  int mt, nt;
+  void* out;
+  int64_t out_ld;
+  int vec;  // out's rows and their pieces are multiples of 16 bytes
+  int ns;
+  int32_t* status;
+};
+
+template <typename OT, int TN>
+__global__ void __launch_bounds__(kTmThreads, 1)
+    int8_tm_kernel(const __grid_constant__ TmMaps maps, const __grid_constant__ TmArgs p) {
+  constexpr int kStage = (kTileM + TN) * kBlkBytes;
+  constexpr int kBufs = 512 / TN;
+  constexpr int kCols = TN / 2;  // columns of an epilogue warp
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* stg_all = stages + p.ns * kStage;  // 2 KB an epilogue warp
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + kEpi * 2048);
+  uint64_t* empty = full + p.ns;
+  uint64_t* tfull = empty + p.ns;
+  uint64_t* tempty = tfull + kBufs;
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_dead, s_fills;
+  __shared__ uint64_t s_mma_done;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  Waits<false> wait{p.status, &s_dead};
+  if (threadIdx.x == 0) {
+    s_dead = s_fills = 0;
+    mbar_init(&s_mma_done, 1);
+    for (int s = 0; s < p.ns; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < kBufs; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], kEpi);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.x);
+    tma_prefetch_desc(&maps.w);
+  }
+  if (warp == 2) {
+    tmem_alloc(&s_tmem, 512);
+    tmem_relinquish();
+    tc_fence_before();
+  }
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = s_tmem;
+  pdl_wait();  // the f16 copies
+  const int total = p.mt * p.nt;
+
+  if (warp < kEpiW0) {
+    if (TN == 256) regs_dec<sizeof(OT) == 4 ? 56 : 72>();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer
+      int s = 0, ph = 0;
+      for (int u = blockIdx.x; u < total; u += gridDim.x) {
+        // row tiles fastest: the CTAs of a wave share a few weight tiles
+        const int m = u % p.mt, n = u / p.mt;
+#pragma unroll 1
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          wait(&empty[s], ~ph & 1);
+          if (wait.dead()) break;
+          uint8_t* X = stages + s * kStage;
+          mbar_arrive_expect_tx(&full[s], kStage);
+          tma_load_2d(X, &maps.x, &full[s], kb * 64, m * kTileM);
+#pragma unroll
+          for (int j = 0; j < TN; j += 64)
+            tma_load_2d(X + (kTileM + j) * kBlkBytes, &maps.w, &full[s], kb * 64, n * TN + j);
+          if (++s == p.ns) { s = 0; ++ph; }
+        }
+      }
+      s_fills = ph * p.ns + s;
+    } else if (warp == 1) {
+      // -------------------------------------------------------- MMA issuer
+      int s = 0, ph = 0;
+      uint32_t it = 0;
+      const uint32_t idesc = idesc_f16(0, kTileM, TN);
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(stages));
+      const bool leader = elect_one();
+      for (int u = blockIdx.x; u < total; u += gridDim.x) {
+#pragma unroll 1
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          const uint32_t a = it % kBufs;
+          const bool opens = kb % kDrain == 0, closes = (kb + 1) % kDrain == 0 || kb + 1 == p.nkb;
+          if (opens) wait(&tempty[a], ((it / kBufs) & 1) ^ 1);
+          wait(&full[s], ph);
+          tc_fence_after();
+          if (leader) {
+            const uint64_t xd = desc0 + (uint32_t)(s * (kStage >> 4)), wd = xd + (kTileM * kBlkBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              tc_mma_f16(tmem_base + a * TN, xd + 2 * kk, wd + 2 * kk, idesc, opens && kk == 0 ? 0u : 1u);
+            tc_commit(&empty[s]);
+            if (closes) tc_commit(&tfull[a]);
+          }
+          __syncwarp();
+          if (closes) ++it;
+          if (++s == p.ns) { s = 0; ph ^= 1; }
+        }
+      }
+      if (leader) tc_commit(&s_mma_done);
+    }
+  } else {
+    if (TN == 256) regs_inc<sizeof(OT) == 4 ? 224 : 216>();
+    // ---------------------------------------------------------- epilogue
+    const int q = warp & 3, half = (warp - kEpiW0) >> 2;
+    const int row = q * 32 + lane;  // TMEM lane = row of the tile
+    uint8_t* const stg = stg_all + (warp - kEpiW0) * 2048;
+    const int nd = (p.nkb + kDrain - 1) / kDrain;
+    uint32_t it = 0;
+    for (int u = blockIdx.x; u < total; u += gridDim.x) {
+      const int m0 = u % p.mt * kTileM, n0 = u / p.mt * TN + half * kCols;
+      const int nvalid = min(kTileM, p.T - m0);
+      const bool on = q * 32 < nvalid && n0 < p.N;
+      int32_t acc[kCols];
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) acc[j] = 0;
+#pragma unroll 1
+      for (int d = 0; d < nd; ++d, ++it) {
+        const uint32_t a = it % kBufs;
+        wait(&tfull[a], (it / kBufs) & 1);
+        tc_fence_after();
+        if (on) {
+          const uint32_t tl = tmem_base + ((uint32_t)(q * 32) << 16) + a * TN + half * kCols;
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld_32(tl + c * 32, r);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[c * 32 + j] += __float2int_rn(__uint_as_float(r[j]));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[a]);
+      }
+      if (!on) continue;
+      // results leave in pieces of 64 bytes of 32 rows, turned around in shared
+      // memory so that whole sectors are stored
+      constexpr int kPer = 64 / (int)sizeof(OT), kVec = 16 / (int)sizeof(OT);
+      const float xscale = row < nvalid ? __ldg(p.xs + m0 + row) : 0.0f;
+#pragma unroll
+      for (int pc = 0; pc < kCols / kPer; ++pc) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t w[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            constexpr int kEach = 4 / (int)sizeof(OT);  // values a word
+            float v[kEach];
+#pragma unroll
+            for (int e = 0; e < kEach; ++e) {
+              const int j = pc * kPer + c * kVec + i * kEach + e;
+              v[e] = (float)acc[j] * xscale * __ldg(p.ws + min(n0 + j, p.N - 1));
+            }
+            if constexpr (sizeof(OT) == 2) w[i] = f32x2_bf16x2(v[0], v[1]);
+            else w[i] = __float_as_uint(v[0]);
+          }
+          *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int rr = 8 * i + (lane >> 2), c = lane & 3;
+          const int col = n0 + pc * kPer + c * kVec;
+          const uint8_t* from = stg + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4);
+          if (q * 32 + rr < nvalid && col < p.N) {
+            OT* o = static_cast<OT*>(p.out) + (int64_t)(m0 + q * 32 + rr) * p.out_ld + col;
+            if (p.vec && col + kVec <= p.N) {
+              *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(from);
+            } else {
+#pragma unroll 1
+              for (int e = 0; e < min(kVec, p.N - col); ++e) o[e] = reinterpret_cast<const OT*>(from)[e];
+            }
+          }
+        }
+        __syncwarp();
+      }
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 2) {
+    if (wait.dead()) {
+      // a wait gave up: no copy and no MMA of the CTA outlives its shared memory and TMEM
+      if (lane == 0) {
+        const int fills = *(volatile int*)&s_fills;
+        for (int i = max(0, fills - p.ns); i < fills; ++i) mbar_wait(&full[i % p.ns], (i / p.ns) & 1, p.status);
+        mbar_wait(&s_mma_done, 0, p.status);
+      }
+      __syncwarp();
+    }
+    tc_fence_after();
+    tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// ------------------------------------------------------------------ launches
+constexpr size_t kSmemMost = 227 * 1024 - 1024;  // beside the kernels' static shared memory
+constexpr int kStreamRows = 32;
+
+bool few_rows(int T, int K) { return T <= kStreamRows && stream_smem(T, K) <= (int64_t)kSmemMost; }
+int64_t padded_k(int K) { return ceil_div64(K, 64) * 64; }
+size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+template <int NG, typename OT>
+int launch_stream(StreamArgs a, cudaStream_t stream) {
+  const size_t smem = (size_t)stream_smem(a.T, a.K);
+  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(int8_stream_kernel<NG, OT>), smem,
+                                "int8_stream_kernel: shared memory limit");
+  if (rc) return rc;
+  a.x_row = (int)stream_x_row(a.K);
+  a.rows_cta = ceil_div(a.N, num_sms());
+  launch_kernel(int8_stream_kernel<NG, OT>, ceil_div(a.N, a.rows_cta), kThreads, smem, stream, a);
+  OES_CHECK_LAUNCH("int8_stream_kernel");
+  return OES_OK;
+}
+
+template <typename OT, int TN>
+int launch_tm(const TmMaps& maps, TmArgs a, cudaStream_t stream) {
+  constexpr int stage = (kTileM + TN) * kBlkBytes;
+  const size_t fixed = 1024 + kEpi * 2048 + 64 * 8;
+  a.ns = (int)std::min<size_t>(8, (kSmemMost - fixed) / stage);
+  const size_t smem = fixed + (size_t)a.ns * stage;
+  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(int8_tm_kernel<OT, TN>), smem,
+                                "int8_tm_kernel: shared memory limit");
+  if (rc) return rc;
+  launch_kernel(int8_tm_kernel<OT, TN>, std::min(num_sms(), a.mt * a.nt), kTmThreads, smem, stream, maps, a);
+  OES_CHECK_LAUNCH("int8_tm_kernel");
+  return OES_OK;
+}
+
+template <typename OT>
+int run_stream(const StreamArgs& a, cudaStream_t stream) {
+  return a.T <= 8 ? launch_stream<1, OT>(a, stream) : a.T <= 16 ? launch_stream<2, OT>(a, stream)
+                                                                : launch_stream<4, OT>(a, stream);
+}
+
+bool sizes_ok(int T, int K, int N) { return T >= 0 && K >= 1 && K <= 65536 && N >= 1 && N <= (1 << 24); }
+
+}  // namespace
+}  // namespace oes
+
+using namespace oes;
+
+extern "C" size_t moe_int8_gemm_workspace_size(int T, int K, int N) {
+  if (!sizes_ok(T, K, N) || T == 0 || few_rows(T, K)) return 0;
+  return align256((size_t)T * padded_k(K) * 2) + align256((size_t)N * padded_k(K) * 2);
+}
+
+extern "C" int moe_int8_gemm(const int8_t* xq, int64_t xq_ld, const float* xs, int T, int K, const int8_t* wq,
+                             int64_t wq_ld, const float* ws, int N, void* out, int dtype, int64_t out_ld,
+                             void* workspace, size_t workspace_bytes, int32_t* status, oes_stream_t stream) {
+  OES_REQUIRE(sizes_ok(T, K, N), "moe_int8_gemm: bad T=%d N=%d K=%d", T, N, K);
+  OES_REQUIRE(dtype == OES_BF16 || dtype == OES_F32, "moe_int8_gemm: bad dtype %d", dtype);
+  if (T == 0) return OES_OK;
+  OES_REQUIRE(xq && xs && wq && ws && out, "moe_int8_gemm: null pointer");
+  OES_REQUIRE(xq_ld >= K && wq_ld >= K && out_ld >= N, "moe_int8_gemm: a row stride is smaller than its row");
+  OES_REQUIRE(((uintptr_t)xq & 15) == 0 && ((uintptr_t)wq & 15) == 0 && xq_ld % 16 == 0 && wq_ld % 16 == 0,
+              "moe_int8_gemm: xq and wq must be 16-byte aligned with strides of a multiple of 16");
+  OES_REQUIRE((((uintptr_t)xs | (uintptr_t)ws | (uintptr_t)status) & 3) == 0 &&
+                  ((uintptr_t)out & (dtype == OES_BF16 ? 1 : 3)) == 0,
+              "moe_int8_gemm: a pointer is not aligned to its type");
+  const size_t need = moe_int8_gemm_workspace_size(T, K, N);
+  OES_REQUIRE(need == 0 || (workspace && ((uintptr_t)workspace & 255) == 0 && workspace_bytes >= need),
+              "moe_int8_gemm: a 256-byte aligned workspace of %zu bytes is required", need);
+  if (few_rows(T, K)) {
+    StreamArgs a{xq, xq_ld, xs, wq, wq_ld, ws, T, K, N, out, out_ld, 0, 0};
+    return dtype == OES_BF16 ? run_stream<uint16_t>(a, stream) : run_stream<float>(a, stream);
+  }
+  const int64_t Kp = padded_k(K);
+  uint16_t* xf = static_cast<uint16_t*>(workspace);
+  uint16_t* wf = reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(workspace) + align256((size_t)T * Kp * 2));
+  TmArgs a{};
+  a.xs = xs;
+  a.ws = ws;
+  a.T = T;
+  a.N = N;
+  a.nkb = (int)(Kp / 64);
+  a.mt = ceil_div(T, kTileM);
+  const bool wide = (int64_t)a.mt * ceil_div(N, 256) >= num_sms();
+  a.nt = ceil_div(N, wide ? 256 : 64);
+  OES_REQUIRE((int64_t)a.mt * a.nt <= 0x7FFFFFFF - 4096, "moe_int8_gemm: too many tiles (T=%d N=%d)", T, N);
+  a.out = out;
+  a.out_ld = out_ld;
+  const int vec = dtype == OES_F32 ? 4 : 8;
+  a.vec = ((uintptr_t)out & 15) == 0 && out_ld % vec == 0;
+  a.status = status;
+  TmMaps m;
+  const uint64_t dx[2] = {(uint64_t)Kp, (uint64_t)T}, dw[2] = {(uint64_t)Kp, (uint64_t)N}, st[1] = {(uint64_t)Kp * 2};
+  const uint32_t bx[2] = {64, kTileM}, bw[2] = {64, 64};
+  int rc = encode_tiled(&m.x, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, xf, dx, st, bx, CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc) return rc;
+  if ((rc = encode_tiled(&m.w, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 2, wf, dw, st, bw, CU_TENSOR_MAP_SWIZZLE_128B))) return rc;
+  CvtArgs c{};
+  c.src[0] = xq;
+  c.src[1] = wq;
+  c.ld[0] = xq_ld;
+  c.ld[1] = wq_ld;
+  c.dst[0] = xf;
+  c.dst[1] = wf;
+  c.rows0 = T;
+  c.rows = (int64_t)T + N;
+  c.K = K;
+  c.Kp = (int)Kp;
+  const int grid = (int)std::min<int64_t>(ceil_div64(c.rows * (Kp / 16), 256), (int64_t)num_sms() * 8);
+  c.step_r = (int)((int64_t)grid * 256 / (Kp / 16));
+  c.step_c = (int)((int64_t)grid * 256 % (Kp / 16));
+  launch_kernel(int8_to_f16_kernel, grid, 256, 0, stream, c);
+  OES_CHECK_LAUNCH("int8_to_f16_kernel");
+  if (wide) return dtype == OES_BF16 ? launch_tm<uint16_t, 256>(m, a, stream) : launch_tm<float, 256>(m, a, stream);
+  return dtype == OES_BF16 ? launch_tm<uint16_t, 64>(m, a, stream) : launch_tm<float, 64>(m, a, stream);
+}

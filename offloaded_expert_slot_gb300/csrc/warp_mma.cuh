@@ -21,6 +21,10 @@ __device__ __forceinline__ void cp_async16_take(uint32_t dst_smem, const void* s
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "r"(take ? 16 : 0)
                : "memory");
 }
+// the first n <= 16 bytes, zeros behind them
+__device__ __forceinline__ void cp_async16_part(uint32_t dst_smem, const void* src, int n) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst_smem), "l"(src), "r"(n) : "memory");
+}
 __device__ __forceinline__ void cp_async4_take(uint32_t dst_smem, const void* src, bool take) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst_smem), "l"(src), "r"(take ? 4 : 0)
                : "memory");
@@ -97,6 +101,14 @@ __device__ __forceinline__ void e2m1x8_f16x8(uint32_t w, uint32_t (&o)[4]) {
       "cvt.rn.f16x2.e2m1x2 %3, b3; }"
       : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3])
       : "r"(w));
+}
+// four 8-bit integers -> two f16x2, exact: f16 numbers from 1024 to 2047 are 1024
+// plus their low bits, so a byte v + 128 behind 0x64 reads as v + 1152
+__device__ __forceinline__ void s8x4_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  const uint32_t u = w ^ 0x80808080u;
+  asm("{ .reg .b32 c; mov.b32 c, 0x64806480; sub.rn.f16x2 %0, %2, c; sub.rn.f16x2 %1, %3, c; }"
+      : "=r"(lo), "=r"(hi)
+      : "r"(__byte_perm(u, 0x64646464u, 0x4140)), "r"(__byte_perm(u, 0x64646464u, 0x4342)));
 }
 __device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t r;

@@ -129,6 +129,9 @@ _SIGS = {
                                   _vp]),
     "moe_fp8_quantize": (_i, [_vp, _i, _i64, _i, _i, _i, _vp, _i64, _vp, _vp]),
     "moe_fp8_gemm": (_i, [_vp, _i64, _vp, _i, _i, _vp, _i64, _vp, _i, _vp, _i, _i64, _vp, _vp]),
+    "moe_int8_quantize": (_i, [_vp, _i, _i64, _i, _i, _i, _vp, _i64, _vp, _vp]),
+    "moe_int8_gemm_workspace_size": (_sz, [_i, _i, _i]),
+    "moe_int8_gemm": (_i, [_vp, _i64, _vp, _i, _i, _vp, _i64, _vp, _i, _vp, _i, _i64, _vp, _sz, _vp, _vp]),
     "moe_block_norm": (_i, [C.POINTER(BlockNorm), _vp]),
     "moe_layer_forward": (_i, [_vp, _vp, _vp, _vp, _i, C.POINTER(LayerDesc), C.POINTER(Chunk), _i,
                                _i, _vp, _vp, C.POINTER(_i)]),
@@ -418,6 +421,24 @@ def moe_fp8_gemm(xq, xq_ld, xs, T, K, wq, wq_ld, ws, N, out, out_ld, status=None
     """dtype: OES_F32 or OES_BF16 of out, or None to take it from the array."""
     _call("moe_fp8_gemm", _ptr(xq), xq_ld, _ptr(xs), T, K, _ptr(wq), wq_ld, _ptr(ws), N, _ptr(out),
           _elem_type(out, "moe_fp8_gemm", dtype), out_ld, _ptr(status), _stream(stream))
+
+
+def moe_int8_quantize(x, x_ld, T, K, act, q, q_ld, scale, stream=None, dtype=None):
+    """dtype: OES_F32 or OES_BF16 of x, or None to take it from the array."""
+    _call("moe_int8_quantize", _ptr(x), _elem_type(x, "moe_int8_quantize", dtype), x_ld, T, K, act,
+          _ptr(q), q_ld, _ptr(scale), _stream(stream))
+
+
+def moe_int8_gemm_workspace_size(T, K, N) -> int:
+    return int(load().moe_int8_gemm_workspace_size(T, K, N))
+
+
+def moe_int8_gemm(xq, xq_ld, xs, T, K, wq, wq_ld, ws, N, out, out_ld, workspace=None, workspace_bytes=0,
+                  status=None, stream=None, dtype=None):
+    """dtype: OES_F32 or OES_BF16 of out, or None to take it from the array."""
+    _call("moe_int8_gemm", _ptr(xq), xq_ld, _ptr(xs), T, K, _ptr(wq), wq_ld, _ptr(ws), N, _ptr(out),
+          _elem_type(out, "moe_int8_gemm", dtype), out_ld, _ptr(workspace), workspace_bytes, _ptr(status),
+          _stream(stream))
 
 
 def block_norm(T, H, residual, residual_ld=None, y=None, y_ld=None, post_weight=None,
