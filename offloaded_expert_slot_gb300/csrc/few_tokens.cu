@@ -33,9 +33,12 @@
 // memory and TMEM) gave 9 to 31 % of the copy rate here, held up by their set-up
 // and hand-offs.
 //
-// Weights are exact in 16 bits: bf16 as they are; e4m3 as bf16, their block scales
-// on the fp32 sums of each 128 of K; e2m1 x e4m3 as f16, the global scale on the
-// sums.  h is rounded once, to bf16 (f16 for e2m1 weights), the sums over a
+// Weights are exact in 16 bits: bf16 as they are; e4m3 as f16, their block scales on
+// the fp32 sums of each 128 of K; e2m1 x e4m3 as f16, the global scale on the sums.
+// For bf16 weights x is taken as it is and h as two bf16 numbers, the second what
+// rounding to the first left (a bf16 h alone would add as much error as out's own
+// rounding does).  For the others x and h are f16 numbers with a power of two for
+// each 128 (f16_group).  h passes between the kernels in fp32, the sums over a
 // token's routes stay in fp32, and out is rounded once.
 #include <algorithm>
 
@@ -74,25 +77,27 @@ constexpr int kFusedExperts = 512;  // most experts that the kernels route thems
 constexpr int kRowTile = 16;
 
 // Weight formats.  A step is what a warp takes from its queue at a time: kStepK
-// values of 16 rows, kChunks x 16 bytes a lane, kB x 16 bytes of B a lane and
-// column, and the step's scales behind the weights.
+// values of 16 rows, kChunks x 16 bytes a lane, the step's scales behind them; of
+// the activations a lane needs 2 x kB x 16 bytes for each column, half a step at a
+// time.  kF16: the activations are f16 numbers with a power of two for each 128
+// (see f16_group), else bf16.
 template <int WF>
 struct Fmt;
 template <>
 struct Fmt<OES_WFMT_BF16> {
-  static constexpr int kStepK = 64, kRowBytes = 128, kChunks = 4, kB = 2, kXPad = 64;
+  static constexpr int kStepK = 64, kRowBytes = 128, kChunks = 4, kB = 1, kXPad = 64;
   static constexpr int kScale = 0;
   static constexpr bool kF16 = false;
 };
 template <>
 struct Fmt<OES_WFMT_FP8> {
-  static constexpr int kStepK = 128, kRowBytes = 128, kChunks = 4, kB = 4, kXPad = 16;
+  static constexpr int kStepK = 128, kRowBytes = 128, kChunks = 4, kB = 2, kXPad = 16;
   static constexpr int kScale = 64;  // 16 fp32, one a row (few_up: gate, up)
-  static constexpr bool kF16 = false;
+  static constexpr bool kF16 = true;
 };
 template <>
 struct Fmt<OES_WFMT_NVFP4> {
-  static constexpr int kStepK = 128, kRowBytes = 64, kChunks = 2, kB = 4, kXPad = 16;
+  static constexpr int kStepK = 128, kRowBytes = 64, kChunks = 2, kB = 2, kXPad = 16;
   static constexpr int kScale = 128 + 16;  // [2 x 64 of K][16 rows][4] e4m3, then the global scale
   static constexpr bool kF16 = true;
 };
@@ -111,12 +116,14 @@ struct FewParams {
   int logits_bf16;
   int32_t* ids;
   float* weights;
-  uint16_t* h;  // [T k, I]
+  float* h;  // [T k, I]
   uint16_t* out;
   int32_t* status;
   int64_t s13, w2, s2, gs;  // sections of an expert row
   int x_ld;                 // bytes of a row of x in shared memory
   int rows_cta;             // few_down: rows of out a CTA owns
+  int k_steps, h_bytes;     // few_down: steps of K a group of h spans; a buffer's bytes
+  int h_bufs;
 };
 
 // The chunk's tables, in shared memory.
@@ -127,16 +134,20 @@ struct Tables {
   int32_t* blk;    // [R] block of a leading route
   int32_t* slot;   // [R] by block
   int16_t* route;  // [blocks][8 NG] route of each token in a block, or -1
-  __device__ __forceinline__ Tables(uint8_t* base, int R) {
+  int16_t* order;  // [R] few_down: the routes that count, block after block
+  int16_t* cum;    // [blocks + 1] few_down: a block's first place there
+  __device__ __forceinline__ Tables(uint8_t* base, int R, int ng) {
     ids = reinterpret_cast<int32_t*>(base);
     w = reinterpret_cast<float*>(ids + R);
     lead = reinterpret_cast<int32_t*>(w + R);
     blk = lead + R;
     slot = blk + R;
     route = reinterpret_cast<int16_t*>(slot + R);
+    order = route + R * 8 * ng;
+    cum = order + R;
   }
 };
-__host__ __device__ constexpr int tables_bytes(int R, int ng) { return R * (20 + 16 * ng); }
+__host__ __device__ constexpr int tables_bytes(int R, int ng) { return R * (24 + 16 * ng) + 4; }
 
 // Routing and tables, by the whole CTA; returns the number of blocks.  One CTA
 // writes the router's outputs and the status (`first`).
@@ -221,50 +232,50 @@ __device__ int few_tables(const FewParams& p, const Tables& tb, bool first) {
   return s_nb;
 }
 
-// One step's matrix instructions: the lane's weights from its queue entry,
-// added onto d (row g and g + 8, columns 2t and 2t + 1, of each 8 tokens).
-template <int WF, int NG>
-__device__ __forceinline__ void step_mma(uint32_t entry, const uint4 (&B)[NG][Fmt<WF>::kB], float (&d)[NG][4]) {
+// The matrix instructions of half a step: the lane's weights from its queue entry,
+// added onto d (row g and g + 8, columns 2t and 2t + 1, of each 8 tokens).  B are
+// the lane's values of the columns, L what their rounding to bf16 left (LO).
+template <int WF, int NG, bool LO>
+__device__ __forceinline__ void half_mma(uint32_t entry, int hh, const uint4 (&B)[NG][Fmt<WF>::kB],
+                                         const uint4 (&L)[NG][Fmt<WF>::kB], float (&d)[NG][4]) {
   const int lane = threadIdx.x & 31;
   const uint32_t mine = entry + lane * 16;
   if constexpr (WF == OES_WFMT_BF16) {
+    const uint4 a = lds128(mine + hh * 1024), b = lds128(mine + hh * 1024 + 512);
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const uint4 a = lds128(mine + hh * 1024), b = lds128(mine + hh * 1024 + 512);
-#pragma unroll
-      for (int n = 0; n < NG; ++n) {
-        mma_16816<false>(d[n], a.x, b.x, a.y, b.y, B[n][hh].x, B[n][hh].y);
-        mma_16816<false>(d[n], a.z, b.z, a.w, b.w, B[n][hh].z, B[n][hh].w);
+    for (int n = 0; n < NG; ++n) {
+      mma_16816<false>(d[n], a.x, b.x, a.y, b.y, B[n][0].x, B[n][0].y);
+      mma_16816<false>(d[n], a.z, b.z, a.w, b.w, B[n][0].z, B[n][0].w);
+      if (LO) {
+        mma_16816<false>(d[n], a.x, b.x, a.y, b.y, L[n][0].x, L[n][0].y);
+        mma_16816<false>(d[n], a.z, b.z, a.w, b.w, L[n][0].z, L[n][0].w);
       }
     }
   } else if constexpr (WF == OES_WFMT_FP8) {
+    const uint4 a = lds128(mine + hh * 1024), b = lds128(mine + hh * 1024 + 512);
+    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-    for (int hh = 0; hh < 2; ++hh) {
-      const uint4 a = lds128(mine + hh * 1024), b = lds128(mine + hh * 1024 + 512);
-      const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+    for (int i = 0; i < 4; ++i) {
+      uint32_t a0, a2, a1, a3;
+      e4m3x4_f16x4(aw[i], a0, a2);
+      e4m3x4_f16x4(bw[i], a1, a3);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        uint32_t a0, a2, a1, a3;
-        e4m3x4_bf16x4(aw[i], a0, a2);
-        e4m3x4_bf16x4(bw[i], a1, a3);
-#pragma unroll
-        for (int n = 0; n < NG; ++n) {
-          const uint4& v = B[n][2 * hh + (i >> 1)];
-          mma_16816<false>(d[n], a0, a1, a2, a3, i & 1 ? v.z : v.x, i & 1 ? v.w : v.y);
-        }
+      for (int n = 0; n < NG; ++n) {
+        const uint4& v = B[n][i >> 1];
+        mma_16816<true>(d[n], a0, a1, a2, a3, i & 1 ? v.z : v.x, i & 1 ? v.w : v.y);
       }
     }
   } else {
     const int g = lane >> 2, t = lane & 3;
-    const uint4 a = lds128(mine), b = lds128(mine + 512);
-    const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+    const uint2 a = lds64(mine + hh * 8), b = lds64(mine + 512 + hh * 8);
+    const uint32_t aw[2] = {a.x, a.y}, bw[2] = {b.x, b.y};
     // the lane's 32 values have the scales of groups 2t and 2t + 1 of the step
     const uint32_t sc = entry + 1024 + (t >> 1) * 64 + g * 4;
     const uint32_t sa = e4m3x2_f16x2((lds32(sc) >> (16 * (t & 1))) & 0xFFFFu);
     const uint32_t sb = e4m3x2_f16x2((lds32(sc + 32) >> (16 * (t & 1))) & 0xFFFFu);
+    const uint32_t fa = __byte_perm(sa, 0, hh ? 0x3232 : 0x1010), fb = __byte_perm(sb, 0, hh ? 0x3232 : 0x1010);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t fa = __byte_perm(sa, 0, i < 2 ? 0x1010 : 0x3232), fb = __byte_perm(sb, 0, i < 2 ? 0x1010 : 0x3232);
+    for (int i = 0; i < 2; ++i) {
       uint32_t oa[4], ob[4];
       e2m1x8_f16x8(aw[i], oa);
       e2m1x8_f16x8(bw[i], ob);
@@ -280,6 +291,13 @@ __device__ __forceinline__ void step_mma(uint32_t entry, const uint4 (&B)[NG][Fm
       }
     }
   }
+}
+
+// First value along K, within a step, of 16-byte piece i of the lane's half hh.
+template <int WF>
+__device__ __forceinline__ int piece_k(int hh, int i) {
+  const int t = threadIdx.x & 3;
+  return WF == OES_WFMT_BF16 ? 32 * hh + 8 * t : WF == OES_WFMT_FP8 ? 64 * hh + 16 * t + 8 * i : 32 * t + 16 * hh + 8 * i;
 }
 
 // The lane's copies of one step: 16 rows' kRowBytes from byte `at` of rows whose
@@ -299,81 +317,127 @@ __device__ __forceinline__ void step_copy(uint32_t entry, const uint8_t* pool, c
   }
 }
 
+// Activations for 8- and 4-bit weights: f16 numbers with one power of two for each
+// 128 along K, chosen so that the largest is in [2^14, 2^15).  The sums of a step
+// span just such 128, so the factor goes to the sums.  A number keeps 11
+// significant bits down to 2^-29 of its group's largest, and nothing leaves f16's
+// range, whatever the activations' own.  The group is 16 neighbouring lanes' 8
+// values each; returns the factor that undoes it.  A NaN stays one and counts for
+// nothing else, an infinity stays one.
+__device__ __forceinline__ float f16_group(const float (&v)[8], uint4& out) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+#pragma unroll
+  for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const uint32_t ex = min(max(__float_as_uint(m) >> 23, 27u), 254u);  // 2^-100 at least
+  const float f = __uint_as_float((268u - ex) << 23);
+  uint32_t o[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(v[2 * i + 1] * f), "f"(v[2 * i] * f));
+  out = make_uint4(o[0], o[1], o[2], o[3]);
+  return __uint_as_float((ex - 14u) << 23);
+}
+
 // ------------------------------------------------------------------ gate, up
+// The (block, 8 rows of I) of the chunk are dealt out in runs, and a CTA takes two
+// neighbours at a time where they are of one block: both use the same columns.
 template <int WF, int NG, int S>
 __global__ void __launch_bounds__(kThreads, 2) few_up_kernel(const FewParams p) {
   using F = Fmt<WF>;
   constexpr int kEntry = entry_bytes<WF>();
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* queue = smem + (threadIdx.x >> 5) * (S * kEntry);
-  float* part = reinterpret_cast<float*>(smem + kWarps * S * kEntry);  // [2][warp][lane][4 NG]
-  uint8_t* xs = reinterpret_cast<uint8_t*>(part + 2 * kThreads * 4 * NG);
-  const Tables tb(xs + p.T * p.x_ld, p.T * p.k);
+  float* part = reinterpret_cast<float*>(smem + kWarps * S * kEntry);  // [2][warp][lane][2][4 NG]
+  uint8_t* xs = reinterpret_cast<uint8_t*>(part + 2 * kThreads * 8 * NG);
+  float* xf = reinterpret_cast<float*>(xs + p.T * p.x_ld);  // [T][ns] factors of x (kF16)
+  const int ns = cdiv(p.H, F::kStepK);
+  const Tables tb(reinterpret_cast<uint8_t*>(xf + (F::kF16 ? p.T * ns : 0)), p.T * p.k, NG);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   pdl_wait();
   pdl_trigger();  // the down kernel; it reads what this kernel waited for, and h after this kernel's end
   // x, with zeros up to a whole step
-  const int xc = cdiv(p.H, F::kStepK) * (F::kStepK / 8);
-  for (int i = tid; i < p.T * xc; i += kThreads) {
-    const int tok = i / xc, c = i - tok * xc;
-    const bool in = c * 8 < p.H;
-    const uint16_t* src = p.x + (size_t)tok * p.H + (in ? c * 8 : 0);
+  const int xc = ns * (F::kStepK / 8);
+  for (int i0 = 0; i0 < p.T * xc; i0 += kThreads) {
+    const int i = i0 + tid, tok = i / xc, c = i - tok * xc;
+    const bool live = i < p.T * xc, in = live && c * 8 < p.H;
+    const uint16_t* src = p.x + (in ? (size_t)tok * p.H + c * 8 : 0);
     uint8_t* dst = xs + tok * p.x_ld + c * 16;
     if constexpr (F::kF16) {
       float v[8];
 #pragma unroll
       for (int j = 0; j < 8; ++j) v[j] = 0.0f;
       if (in) load_vals<8>(src, v);
-      uint32_t o[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[j]) : "f"(v[2 * j + 1]), "f"(v[2 * j]));
+      uint4 o;
+      const float f = f16_group(v, o);
+      if (live) {
+        *reinterpret_cast<uint4*>(dst) = o;
+        if ((c & 15) == 0) xf[tok * ns + (c >> 4)] = f;
       }
-      *reinterpret_cast<uint4*>(dst) = make_uint4(o[0], o[1], o[2], o[3]);
-    } else {
+    } else if (live) {
       cp_async16_take(smem_u32(dst), src, in);
     }
   }
   cp_async_commit();
   const int nb = few_tables<NG>(p, tb, blockIdx.x == 0);
-  const int groups = p.I / 8, units = nb * groups;
+  const int per = p.I / 8, units = nb * per;  // groups of 8 rows: of a block, and in all
+  const int lo = (int)((int64_t)blockIdx.x * units / gridDim.x), hi = (int)((int64_t)(blockIdx.x + 1) * units / gridDim.x);
   const int row = p.H * F::kRowBytes / F::kStepK;  // bytes of a weight row
-  const int ns = cdiv(p.H, F::kStepK);
 
-  // the next step to copy
-  int iu = warp < ns ? (int)blockIdx.x : units, is = warp, at = 0;
+  // A place in the CTA's groups: group j, n (1 or 2) of them taken together, of
+  // block b, from group r of it
+  struct Place {
+    int j, n, b, r;
+  };
+  auto at_group = [&](int j, int b, int r) {
+    if (r >= per) {
+      r -= per;
+      ++b;
+    }
+    return Place{j, j + 1 < hi && r + 1 < per ? 2 : 1, b, r};
+  };
+  const Place start = at_group(lo, lo / per, lo % per);
+
+  // the next step to copy: of place c, step cs, group cm of the place
+  Place c = start;
+  int cs = warp, cm = 0, at = 0;
   const uint8_t* base = p.pool;
   const uint8_t* r0 = p.pool;
-  int rg = 0;
-  auto unit_rows = [&]() {
-    if (iu >= units) return;
-    const int b = iu / groups;
-    rg = (iu - b * groups) * 8;
-    base = p.pool + (int64_t)tb.slot[b] * p.row_bytes;
-    r0 = base + (int64_t)(rg + g) * row + 16 * t;
+  auto set_rows = [&]() {
+    if (c.j >= hi || warp >= ns) return;
+    base = p.pool + (int64_t)tb.slot[c.b] * p.row_bytes;
+    r0 = base + (int64_t)(c.r * 8 + g) * row + 16 * t;
   };
-  unit_rows();
+  set_rows();
+  const int64_t up = (int64_t)p.I * row;
   auto copy_next = [&]() {
-    if (iu < units) {
+    if (c.j < hi && warp < ns) {
       const uint32_t e = smem_u32(queue + at * kEntry);
-      step_copy<WF>(e, p.pool, r0, r0 + (int64_t)p.I * row, true, true, is * F::kRowBytes, row);
+      const uint8_t* w = r0 + (cm ? 8 * row : 0);
+      step_copy<WF>(e, p.pool, w, w + up, true, true, cs * F::kRowBytes, row);
       if constexpr (WF == OES_WFMT_FP8) {
-        const int hb = cdiv(p.H, 128), ib = cdiv(p.I, 128);
+        const int ib = cdiv(p.I, 128);
         if (lane < 2)
-          cp_async4_take(e + 2048 + 4 * lane, base + p.s13 + ((int64_t)(lane * ib + (rg >> 7)) * hb + is) * 4, true);
+          cp_async4_take(e + 2048 + 4 * lane,
+                         base + p.s13 + ((int64_t)(lane * ib + (((c.r + cm) * 8) >> 7)) * ns + cs) * 4, true);
       }
       if constexpr (WF == OES_WFMT_NVFP4) {
-        const int r16 = lane & 15, c = 2 * is + (lane >> 4);
-        const bool in = c * 64 < p.H;
+        const int r16 = lane & 15, k64 = 2 * cs + (lane >> 4);
+        const bool in = k64 * 64 < p.H;
         cp_async4_take(e + 1024 + 4 * lane,
-                       base + p.s13 + ((int64_t)(in ? c : 0) * 2 * p.I + (r16 >> 3) * p.I + rg + (r16 & 7)) * 4, in);
+                       base + p.s13 + ((int64_t)(in ? k64 : 0) * 2 * p.I + (r16 >> 3) * p.I + (c.r + cm) * 8 + (r16 & 7)) * 4,
+                       in);
         if (lane == 0) cp_async4_take(e + 1024 + 128, base + p.gs, true);
       }
-      is += kWarps;
-      if (is >= ns) {
-        is = warp;
-        iu += gridDim.x;
-        unit_rows();
+      if (++cm == c.n) {
+        cm = 0;
+        cs += kWarps;
+        if (cs >= ns) {
+          cs = warp;
+          c = at_group(c.j + c.n, c.b, c.r + c.n);
+          set_rows();
+        }
       }
     }
     cp_async_commit();
@@ -383,74 +447,97 @@ __global__ void __launch_bounds__(kThreads, 2) few_up_kernel(const FewParams p) 
   cp_async_wait<S>();  // x
   __syncthreads();
 
-  const uint8_t* xb[NG];
+  // columns past the tokens are not used: any row does
+  uint32_t xb[NG];
+  const float* xfc[NG][2];
 #pragma unroll
   for (int n = 0; n < NG; ++n) {
-    const int tok = min(8 * n + g, p.T - 1);  // columns past the tokens are not used
-    xb[n] = xs + tok * p.x_ld + (WF == OES_WFMT_BF16 ? 16 : WF == OES_WFMT_FP8 ? 32 : 64) * t;
+    xb[n] = smem_u32(xs + min(8 * n + g, p.T - 1) * p.x_ld) + 2 * piece_k<WF>(0, 0);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) xfc[n][j] = xf + min(8 * n + 2 * t + j, p.T - 1) * ns;
   }
   int from = 0, buf = 0;
-  for (int u = blockIdx.x; u < units; u += gridDim.x, buf ^= 1) {
-    float acc[NG][4];
+  for (Place q = start; q.j < hi; q = at_group(q.j + q.n, q.b, q.r + q.n), buf ^= 1) {
+    float acc[2][NG][4];
 #pragma unroll
-    for (int n = 0; n < NG; ++n)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    float gs = 1.0f;
-    for (int s = warp; s < ns; s += kWarps) {
-      cp_async_wait<S - 1>();
-      __syncwarp();  // scales that other lanes copied
-      const uint32_t e = smem_u32(queue + from * kEntry);
-      uint4 B[NG][F::kB];
+    for (int m = 0; m < 2; ++m)
 #pragma unroll
       for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int i = 0; i < F::kB; ++i) {
-          const int o = WF == OES_WFMT_BF16 ? 64 * i : WF == OES_WFMT_FP8 ? 128 * (i >> 1) + 16 * (i & 1) : 16 * i;
-          B[n][i] = *reinterpret_cast<const uint4*>(xb[n] + s * (2 * F::kStepK) + o);
+        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
+    float gs = 1.0f;
+    for (int s = warp; s < ns; s += kWarps) {
+      uint4 B[2][NG][F::kB];
+      float f[NG][2];
+#pragma unroll
+      for (int n = 0; n < NG; ++n) {
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int i = 0; i < F::kB; ++i)
+            B[hh][n][i] = lds128(xb[n] + 2 * (s * F::kStepK + piece_k<WF>(hh, i) - piece_k<WF>(0, 0)));
+        if (F::kF16) {
+          f[n][0] = xfc[n][0][s];
+          f[n][1] = xfc[n][1][s];
         }
-      if constexpr (WF == OES_WFMT_FP8) {
-        float d[NG][4];
-#pragma unroll
-        for (int n = 0; n < NG; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
-        step_mma<WF, NG>(e, B, d);
-        const float sg = __uint_as_float(lds32(e + 2048)), su = __uint_as_float(lds32(e + 2052));
-#pragma unroll
-        for (int n = 0; n < NG; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) acc[n][i] = fmaf(i < 2 ? sg : su, d[n][i], acc[n][i]);
-      } else {
-        step_mma<WF, NG>(e, B, acc);
-        if constexpr (WF == OES_WFMT_NVFP4) gs = __uint_as_float(lds32(e + 1024 + 128));
       }
-      __syncwarp();
-      from = from + 1 == S ? 0 : from + 1;
-      copy_next();
-    }
-    float* mine = part + ((buf * kWarps + warp) * 32 + lane) * (4 * NG);
 #pragma unroll
-    for (int n = 0; n < NG; ++n)
-      *reinterpret_cast<float4*>(mine + 4 * n) =
-          make_float4(gs * acc[n][0], gs * acc[n][1], gs * acc[n][2], gs * acc[n][3]);
+      for (int m = 0; m < 2; ++m) {
+        if (m >= q.n) continue;
+        cp_async_wait<S - 1>();
+        if (F::kScale) __syncwarp();  // scales that other lanes copied
+        const uint32_t e = smem_u32(queue + from * kEntry);
+        if constexpr (F::kF16) {
+          float d[NG][4];
+#pragma unroll
+          for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
+          half_mma<WF, NG, false>(e, 0, B[0], B[0], d);
+          half_mma<WF, NG, false>(e, 1, B[1], B[1], d);
+          float sg = 1.0f, su = 1.0f;
+          if constexpr (WF == OES_WFMT_FP8) {
+            const uint2 sc = lds64(e + 2048);
+            sg = __uint_as_float(sc.x);
+            su = __uint_as_float(sc.y);
+          } else {
+            gs = __uint_as_float(lds32(e + 1024 + 128));
+          }
+#pragma unroll
+          for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              acc[m][n][i] = fmaf((i < 2 ? sg : su) * f[n][i & 1], d[n][i], acc[m][n][i]);
+        } else {
+          half_mma<WF, NG, false>(e, 0, B[0], B[0], acc[m]);
+          half_mma<WF, NG, false>(e, 1, B[1], B[1], acc[m]);
+        }
+        if (F::kScale) __syncwarp();
+        from = from + 1 == S ? 0 : from + 1;
+        copy_next();
+      }
+    }
+    float* mine = part + ((buf * kWarps + warp) * 32 + lane) * (8 * NG);
+#pragma unroll
+    for (int m = 0; m < 2; ++m)
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+        if (m < q.n)
+          *reinterpret_cast<float4*>(mine + (m * NG + n) * 4) =
+              make_float4(gs * acc[m][n][0], gs * acc[m][n][1], gs * acc[m][n][2], gs * acc[m][n][3]);
     __syncthreads();
-    if (tid < 64 * NG) {
-      const int col = tid >> 3, r8 = tid & 7, b = u / groups;
-      const int r = tb.route[b * 8 * NG + col];
+    const int col = (tid >> 3) & (8 * NG - 1), r8 = tid & 7, m = tid / (64 * NG);
+    if (m < q.n) {
+      const int r = tb.route[q.b * 8 * NG + col];
       if (r >= 0) {
-        const float* v = part + (buf * kWarps * 32 + r8 * 4 + (col & 7) / 2) * (4 * NG) + (col >> 3) * 4 + (col & 1);
-        float gate = 0.0f, up = 0.0f;
+        const float* v = part + (buf * kWarps * 32 + r8 * 4 + (col & 7) / 2) * (8 * NG) + (m * NG + (col >> 3)) * 4 + (col & 1);
+        float gate = 0.0f, upv = 0.0f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          gate += v[w * 32 * 4 * NG];
-          up += v[w * 32 * 4 * NG + 2];
+          gate += v[w * 32 * 8 * NG];
+          upv += v[w * 32 * 8 * NG + 2];
         }
-        const float h = silu_f32(gate) * up;
-        uint16_t bits;
-        if constexpr (F::kF16) asm("cvt.rn.f16.f32 %0, %1;" : "=h"(bits) : "f"(h));
-        else bits = (uint16_t)f32_bf16(h);
-        p.h[(int64_t)r * p.I + (u - b * groups) * 8 + r8] = bits;
+        p.h[(int64_t)r * p.I + (q.r + m) * 8 + r8] = silu_f32(gate) * upv;
       }
     }
   }
@@ -461,134 +548,299 @@ __global__ void __launch_bounds__(kThreads, 2) few_up_kernel(const FewParams p) 
 // that was written before it (logits, routes, the slot map, x, the pool) is
 // complete, and this kernel reads it through L2 without waiting.  h is
 // few_up_kernel's, and is read after the wait.
+//
+// h goes through shared memory a group at a time: whole blocks, as many as their
+// routes' rows fit kHPieces pieces of 8 values a thread, over k_steps steps of K.
+// A group is loaded into registers while the group before it is multiplied, and
+// stored behind it in the form that the instructions take.  (Loaded by each lane
+// for itself, half a step ahead, its latency set the pace: 16 tokens x 10 of 200 bf16
+// experts ran at 1.9 TB/s.)  Within a group the warps share its (block, step)
+// in runs, so that a warp seldom changes the block.
+constexpr int kHPieces = 4;
+
 template <int WF, int NG, int S>
-__global__ void __launch_bounds__(kThreads, 2) few_down_kernel(const FewParams p) {
+__global__ void __launch_bounds__(kThreads) __maxnreg__(NG == 1 ? 144 : 208) few_down_kernel(const FewParams p) {
   using F = Fmt<WF>;
   constexpr int kEntry = entry_bytes<WF>();
+  constexpr int kParts = F::kF16 ? 1 : 2;
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* queue = smem + (threadIdx.x >> 5) * (S * kEntry);
   float* part = reinterpret_cast<float*>(smem + kWarps * S * kEntry);  // [2][warp][lane][4 NG]
-  const Tables tb(reinterpret_cast<uint8_t*>(part + 2 * kThreads * 4 * NG), p.T * p.k);
+  uint8_t* hbuf = reinterpret_cast<uint8_t*>(part + 2 * kThreads * 4 * NG);  // [h_bufs][h_bytes]
+  const Tables tb(hbuf + p.h_bufs * p.h_bytes, p.T * p.k, NG);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const int nb = few_tables<NG>(p, tb, false);
   const int row = p.I * F::kRowBytes / F::kStepK;
   const int ns = cdiv(p.I, F::kStepK);
   const int row_lo = blockIdx.x * p.rows_cta, row_hi = min(p.H, row_lo + p.rows_cta);
-
-  // a place in the warp's steps: (block, step) in turns of kWarps, and the tile
-  struct Place {
-    int b, s, row0;
-  };
-  auto first = [&](int row0) {
-    Place q{0, warp, row0};
-    while (q.s >= ns) {
-      q.s -= ns;
-      ++q.b;
+  if (warp == 0) {  // the order of the routes that count
+    int n = 0;
+    for (int b = 0; b < nb; ++b) {
+      const int r = lane < 8 * NG ? tb.route[b * 8 * NG + lane] : -1;
+      const uint32_t m = __ballot_sync(0xffffffffu, r >= 0);
+      if (lane == 0) tb.cum[b] = (int16_t)n;
+      if (r >= 0) tb.order[n + __popc(m & ((1u << lane) - 1))] = (int16_t)r;
+      n += __popc(m);
     }
-    return q;
-  };
-  auto next = [&](Place& q) {
-    q.s += kWarps;
-    while (q.s >= ns) {
-      q.s -= ns;
-      ++q.b;
-    }
-    if (q.b >= nb) q = first(q.row0 + kRowTile);
-  };
-  const bool any = first(0).b < nb;  // whether the warp has a step in each tile
+    if (lane == 0) tb.cum[nb] = (int16_t)n;
+  }
+  __syncthreads();
 
-  Place c = first(row_lo);
+  // A group: blocks [b0, b1) over steps k0 .. k0 + kn, for the tile of rows row0
+  struct Group {
+    int b0, b1, k0, kn, row0;
+  };
+  auto group_at = [&](int row0, int k0, int b0) {
+    if (b0 >= nb) {
+      b0 = 0;
+      k0 += p.k_steps;
+      if (k0 >= ns) {
+        k0 = 0;
+        row0 += kRowTile;
+      }
+    }
+    Group o{b0, b0, k0, min(p.k_steps, ns - k0), nb > 0 ? row0 : row_hi};
+    if (o.row0 >= row_hi) return o;
+    const int lim = tb.cum[b0] + kHPieces * kThreads / (o.kn * (F::kStepK / 8));
+    int l = b0 + 1, h = nb;  // the last block whose routes fit; the first one's always do
+    while (l < h) {
+      const int mid = (l + h + 1) >> 1;
+      if (tb.cum[mid] <= lim) l = mid;
+      else h = mid - 1;
+    }
+    o.b1 = l;
+    return o;
+  };
+  // The warp's run within a group: `rem` (block, step) from block b, step s on
+  struct Run {
+    int b, s, rem;
+  };
+  auto run_of = [&](const Group& o) {
+    if (o.row0 >= row_hi) return Run{0, 0, 0};
+    const int n = (o.b1 - o.b0) * o.kn, i0 = warp * n / kWarps, i1 = (warp + 1) * n / kWarps;
+    const int b = i0 / o.kn;
+    return Run{o.b0 + b, i0 - b * o.kn, i1 - i0};
+  };
+
+  // the next step to copy
+  Group cg = group_at(row_lo, 0, 0);
+  Run c = run_of(cg);
   int at = 0;
+  const uint8_t* base = p.pool;
+  const uint8_t* w0 = p.pool;
+  bool ok0 = false, ok1 = false;
+  auto set_rows = [&]() {
+    while (c.rem == 0 && cg.row0 < row_hi) {
+      cg = group_at(cg.row0, cg.k0, cg.b1);
+      c = run_of(cg);
+    }
+    if (cg.row0 >= row_hi) return;
+    base = p.pool + (int64_t)tb.slot[c.b] * p.row_bytes;
+    w0 = base + p.w2 + (int64_t)(cg.row0 + g) * row + 16 * t;
+    ok0 = cg.row0 + g < row_hi;
+    ok1 = cg.row0 + g + 8 < row_hi;
+  };
+  set_rows();
   auto copy_next = [&]() {
-    if (any && c.row0 < row_hi) {
+    if (c.rem > 0) {
       const uint32_t e = smem_u32(queue + at * kEntry);
-      const uint8_t* base = p.pool + (int64_t)tb.slot[c.b] * p.row_bytes;
-      const uint8_t* w = base + p.w2 + (int64_t)(c.row0 + g) * row + 16 * t;
-      step_copy<WF>(e, p.pool, w, w + 8 * (int64_t)row, c.row0 + g < row_hi, c.row0 + g + 8 < row_hi, c.s * F::kRowBytes, row);
+      const int s = cg.k0 + c.s;
+      step_copy<WF>(e, p.pool, w0, w0 + 8 * row, ok0, ok1, s * F::kRowBytes, row);
       if constexpr (WF == OES_WFMT_FP8) {
-        const int r = c.row0 + lane;
+        const int r = cg.row0 + lane;
         if (lane < kRowTile)
-          cp_async4_take(e + 2048 + 4 * lane,
-                         base + p.s2 + ((int64_t)(r < row_hi ? r >> 7 : 0) * ns + c.s) * 4, r < row_hi);
+          cp_async4_take(e + 2048 + 4 * lane, base + p.s2 + ((int64_t)(r < row_hi ? r >> 7 : 0) * ns + s) * 4,
+                         r < row_hi);
       }
       if constexpr (WF == OES_WFMT_NVFP4) {
-        const int r = c.row0 + (lane & 15), k64 = 2 * c.s + (lane >> 4);
+        const int r = cg.row0 + (lane & 15), k64 = 2 * s + (lane >> 4);
         const bool in = r < row_hi && k64 * 64 < p.I;
         cp_async4_take(e + 1024 + 4 * lane, base + p.s2 + (in ? (int64_t)k64 * p.H + r : 0) * 4, in);
         if (lane == 0) cp_async4_take(e + 1024 + 128, base + p.gs + 4, true);
       }
-      next(c);
+      --c.rem;
+      if (++c.s == cg.kn) {
+        c.s = 0;
+        ++c.b;
+      }
+      if (c.s == 0 || c.rem == 0) set_rows();
     }
     cp_async_commit();
     at = at + 1 == S ? 0 : at + 1;
   };
   for (int i = 0; i < S; ++i) copy_next();
-  pdl_wait();  // h
 
-  auto load_h = [&](const Place& q, uint4 (&B)[NG][F::kB]) {
+  // Rows of h in a buffer are ppr pieces of 16 bytes and one more, so that rows do
+  // not start in the same bank; bf16 rows come in two parts, and f16 rows' factors
+  // stand behind all rows.
+  float hv[kHPieces][8];
+  auto load_h = [&](const Group& o) {
+    const int ppr = o.kn * (F::kStepK / 8), j0 = tb.cum[o.b0], n = (tb.cum[o.b1] - j0) * ppr;
 #pragma unroll
-    for (int n = 0; n < NG; ++n) {
-      const int r = any && q.row0 < row_hi ? tb.route[q.b * 8 * NG + 8 * n + g] : -1;
+    for (int i = 0; i < kHPieces; ++i) {
+      const int x = tid + i * kThreads, rw = x / ppr, k = o.k0 * F::kStepK + (x - rw * ppr) * 8;
 #pragma unroll
-      for (int i = 0; i < F::kB; ++i) {
-        const int k = q.s * F::kStepK + (WF == OES_WFMT_BF16  ? 32 * i + 8 * t
-                                         : WF == OES_WFMT_FP8 ? 64 * (i >> 1) + 16 * t + 8 * (i & 1)
-                                                              : 32 * t + 8 * i);
-        B[n][i] = make_uint4(0u, 0u, 0u, 0u);
-        if (r >= 0 && k < p.I) B[n][i] = __ldcg(reinterpret_cast<const uint4*>(p.h + (int64_t)r * p.I + k));
+      for (int j = 0; j < 8; ++j) hv[i][j] = 0.0f;
+      if (x < n && k < p.I) {
+        const float4* h = reinterpret_cast<const float4*>(p.h + (int64_t)tb.order[j0 + rw] * p.I + k);
+        const float4 a = __ldcg(h), b = __ldcg(h + 1);
+        hv[i][0] = a.x; hv[i][1] = a.y; hv[i][2] = a.z; hv[i][3] = a.w;
+        hv[i][4] = b.x; hv[i][5] = b.y; hv[i][6] = b.z; hv[i][7] = b.w;
       }
     }
   };
-  uint4 B[NG][F::kB];
-  Place q = first(row_lo);
-  load_h(q, B);
-  int from = 0, buf = 0;
+  auto store_h = [&](const Group& o, uint8_t* dst) {
+    const int ppr = o.kn * (F::kStepK / 8), rows = tb.cum[o.b1] - tb.cum[o.b0];
+    float* factors = reinterpret_cast<float*>(dst + rows * kParts * (ppr + 1) * 16);
+#pragma unroll
+    for (int i = 0; i < kHPieces; ++i) {
+      if (i * kThreads >= rows * ppr) break;
+      const int x = tid + i * kThreads, rw = x / ppr, pc = x - rw * ppr;
+      uint4* to = reinterpret_cast<uint4*>(dst + (rw * kParts * (ppr + 1) + pc) * 16);
+      if constexpr (F::kF16) {
+        uint4 v;
+        const float f = f16_group(hv[i], v);
+        if (rw < rows) {
+          *to = v;
+          if ((pc & 15) == 0) factors[rw * o.kn + (pc >> 4)] = f;
+        }
+      } else if (rw < rows) {
+        uint32_t a[4], b[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          a[j] = f32x2_bf16x2(hv[i][2 * j], hv[i][2 * j + 1]);
+          const float x0 = bf16_f32(a[j] & 0xFFFFu), x1 = __uint_as_float(a[j] & 0xFFFF0000u);
+          // an infinity leaves nothing (and not the NaN of its difference)
+          b[j] = f32x2_bf16x2(fabsf(x0) < INFINITY ? hv[i][2 * j] - x0 : 0.0f,
+                              fabsf(x1) < INFINITY ? hv[i][2 * j + 1] - x1 : 0.0f);
+        }
+        to[0] = make_uint4(a[0], a[1], a[2], a[3]);
+        to[ppr + 1] = make_uint4(b[0], b[1], b[2], b[3]);
+      }
+    }
+  };
+
+  pdl_wait();  // h
+  Group cur = group_at(row_lo, 0, 0);
+  if (cur.row0 < row_hi) {
+    load_h(cur);
+    store_h(cur, hbuf);
+    __syncthreads();
+  }
+  int from = 0, buf = 0, hb = 0;
   for (int row0 = row_lo; row0 < row_hi; row0 += kRowTile, buf ^= 1) {
     float acc[NG][4];
 #pragma unroll
     for (int n = 0; n < NG; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    while (any && q.row0 == row0) {
-      const int b = q.b;
-      next(q);
-      uint4 Bn[NG][F::kB];
-      load_h(q, Bn);  // the next step's, while this one is multiplied
-      cp_async_wait<S - 1>();
-      __syncwarp();
-      const uint32_t e = smem_u32(queue + from * kEntry);
-      float d[NG][4];
+    while (cur.row0 == row0) {
+      const Group nx = group_at(cur.row0, cur.k0, cur.b1);
+      const bool more = nx.row0 < row_hi;
+      // what the one buffer holds serves every tile of rows
+      if (more && p.h_bufs > 1) load_h(nx);
+      const int ppr = cur.kn * (F::kStepK / 8), j0 = tb.cum[cur.b0], line = kParts * (ppr + 1) * 16;
+      const uint32_t hs = smem_u32(hbuf + hb * p.h_bytes);
+      const uint32_t hf = hs + (tb.cum[cur.b1] - j0) * line;  // the factors
+      Run q = run_of(cur);
+      while (q.rem > 0) {
+        // this lane's columns in block q.b: column g's row of h, and whether columns
+        // 2t and 2t + 1 have a route, its weight and its factors
+        uint32_t hrow[NG], hfc[NG][2];
+        bool has[NG];
+        float w[NG][2];
+        int place = tb.cum[q.b] - j0;
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+        for (int n = 0; n < NG; ++n) {
+          const int r = tb.route[q.b * 8 * NG + 8 * n + (lane & 7)];
+          const uint32_t m = __ballot_sync(0xffffffffu, r >= 0) & 0xFFu;
+          has[n] = (m >> g) & 1u;
+          hrow[n] = hs + (has[n] ? place + __popc(m & ((1u << g) - 1)) : 0) * line + 2 * piece_k<WF>(0, 0);
+          const float wr = r >= 0 ? tb.w[r] : 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
-      step_mma<WF, NG>(e, B, d);
-      float s0 = 1.0f, s1 = 1.0f;
-      if constexpr (WF == OES_WFMT_FP8) {
-        s0 = __uint_as_float(lds32(e + 2048 + 4 * g));
-        s1 = __uint_as_float(lds32(e + 2048 + 32 + 4 * g));
-      }
-      if constexpr (WF == OES_WFMT_NVFP4) s0 = s1 = __uint_as_float(lds32(e + 1024 + 128));
-#pragma unroll
-      for (int n = 0; n < NG; ++n)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          // a token without a route in this block takes nothing from it, not
-          // even a NaN of its weights
-          const int r = tb.route[b * 8 * NG + 8 * n + 2 * t + j];
-          if (r >= 0) {
-            const float w = tb.w[r];
-            acc[n][j] = fmaf(w, s0 * d[n][j], acc[n][j]);
-            acc[n][2 + j] = fmaf(w, s1 * d[n][2 + j], acc[n][2 + j]);
+          for (int j = 0; j < 2; ++j) {
+            const int col = 2 * t + j;
+            w[n][j] = __shfl_sync(0xffffffffu, wr, col);
+            const bool hc = (m >> col) & 1u;
+            hfc[n][j] = hc ? hf + (place + __popc(m & ((1u << col) - 1))) * cur.kn * 4 : 0u;
           }
+          place += __popc(m);
         }
-      __syncwarp();
-      from = from + 1 == S ? 0 : from + 1;
-      copy_next();
+        float blk[NG][4];
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+        for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int i = 0; i < F::kB; ++i) B[n][i] = Bn[n][i];
+          for (int i = 0; i < 4; ++i) blk[n][i] = 0.0f;
+        float gs = 1.0f;
+        const int end = min(cur.kn, q.s + q.rem);
+        q.rem -= end - q.s;
+        for (int s = q.s; s < end; ++s) {
+          uint4 B[2][NG][F::kB], L[2][NG][F::kB];
+          float f[NG][2];
+#pragma unroll
+          for (int n = 0; n < NG; ++n) {
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+              for (int i = 0; i < F::kB; ++i) {
+                B[hh][n][i] = L[hh][n][i] = make_uint4(0u, 0u, 0u, 0u);
+                if (has[n]) {
+                  const uint32_t a = hrow[n] + 2 * (s * F::kStepK + piece_k<WF>(hh, i) - piece_k<WF>(0, 0));
+                  B[hh][n][i] = lds128(a);
+                  if (kParts == 2) L[hh][n][i] = lds128(a + (ppr + 1) * 16);
+                }
+              }
+            if (F::kF16) {
+#pragma unroll
+              for (int j = 0; j < 2; ++j) f[n][j] = hfc[n][j] ? __uint_as_float(lds32(hfc[n][j] + 4 * s)) : 0.0f;
+            }
+          }
+          cp_async_wait<S - 1>();
+          if (F::kScale) __syncwarp();  // scales that other lanes copied
+          const uint32_t e = smem_u32(queue + from * kEntry);
+          if constexpr (F::kF16) {
+            float d[NG][4];
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
+            half_mma<WF, NG, false>(e, 0, B[0], B[0], d);
+            half_mma<WF, NG, false>(e, 1, B[1], B[1], d);
+            float s0 = 1.0f, s1 = 1.0f;
+            if constexpr (WF == OES_WFMT_FP8) {
+              s0 = __uint_as_float(lds32(e + 2048 + 4 * g));
+              s1 = __uint_as_float(lds32(e + 2048 + 32 + 4 * g));
+            } else {
+              gs = __uint_as_float(lds32(e + 1024 + 128));
+            }
+#pragma unroll
+            for (int n = 0; n < NG; ++n)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) blk[n][i] = fmaf((i < 2 ? s0 : s1) * f[n][i & 1], d[n][i], blk[n][i]);
+          } else {
+            half_mma<WF, NG, true>(e, 0, B[0], L[0], blk);
+            half_mma<WF, NG, true>(e, 1, B[1], L[1], blk);
+          }
+          if (F::kScale) __syncwarp();
+          from = from + 1 == S ? 0 : from + 1;
+          copy_next();
+        }
+        // a token without a route in this block takes nothing from it, not even a
+        // NaN of its weights
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            if (hfc[n][i & 1]) acc[n][i] = fmaf(w[n][i & 1] * gs, blk[n][i], acc[n][i]);
+        q.s = 0;
+        ++q.b;
+      }
+      if (more && p.h_bufs > 1) {
+        hb ^= 1;
+        store_h(nx, hbuf + hb * p.h_bytes);
+        __syncthreads();
+      }
+      cur = nx;
     }
     float* mine = part + ((buf * kWarps + warp) * 32 + lane) * (4 * NG);
 #pragma unroll
@@ -620,8 +872,9 @@ int x_stride(int H) {
 
 template <int WF, int NG, int S>
 size_t up_smem(int T, int k, int H) {
-  return (size_t)kWarps * S * entry_bytes<WF>() + 2 * kThreads * 16 * NG + (size_t)T * x_stride<WF>(H) +
-         tables_bytes(T * k, NG);
+  using F = Fmt<WF>;
+  return (size_t)kWarps * S * entry_bytes<WF>() + 2 * kThreads * 32 * NG + (size_t)T * x_stride<WF>(H) +
+         (F::kF16 ? 4 * T * ceil_div(H, F::kStepK) : 0) + tables_bytes(T * k, NG);
 }
 
 template <int WF, int NG, int S>
@@ -630,7 +883,7 @@ int launch_up(const FewParams& p, cudaStream_t stream) {
   int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(few_up_kernel<WF, NG, S>), smem,
                                 "few_up_kernel: shared memory limit");
   if (rc) return rc;
-  const int64_t units = (int64_t)p.T * p.k * (p.I / 8);
+  const int64_t units = (int64_t)p.T * p.k * (p.I / 8);  // at most
   launch_kernel(few_up_kernel<WF, NG, S>, (int)std::min<int64_t>(num_sms(), units), kThreads, smem, stream, p);
   OES_CHECK_LAUNCH("few_up_kernel");
   return OES_OK;
@@ -639,12 +892,27 @@ int launch_up(const FewParams& p, cudaStream_t stream) {
 // One group of tokens: both kernels.
 template <int WF, int NG>
 int launch_few(FewParams p, cudaStream_t stream) {
-  constexpr int S = 5;
+  constexpr int S = 4;
   p.x_ld = x_stride<WF>(p.H);
   const int rc = up_smem<WF, NG, S>(p.T, p.k, p.H) <= kSmemMost ? launch_up<WF, NG, S>(p, stream)
                                                                 : launch_up<WF, NG, 2>(p, stream);
   if (rc) return rc;
-  const size_t smem = (size_t)kWarps * S * entry_bytes<WF>() + 2 * kThreads * 16 * NG + tables_bytes(p.T * p.k, NG);
+  // every block's routes (one of each token at most) fit a buffer
+  using F = Fmt<WF>;
+  constexpr int parts = F::kF16 ? 1 : 2, step = F::kStepK / 8, most = kHPieces * kThreads;
+  const int ns = ceil_div(p.I, F::kStepK);
+  p.k_steps = std::min(ns, most / (p.T * step));
+  auto group_bytes = [&](int kn) {  // of the routes over kn steps
+    const int rows = std::min(p.T * p.k, most / (kn * step));
+    return rows * (parts * (kn * step + 1) * 16 + (F::kF16 ? 4 * kn : 0));
+  };
+  p.h_bytes = group_bytes(p.k_steps);
+  if (ns % p.k_steps) p.h_bytes = std::max(p.h_bytes, group_bytes(ns % p.k_steps));
+  p.h_bytes = (p.h_bytes + 15) / 16 * 16;
+  // one buffer where it holds the whole of h
+  p.h_bufs = p.k_steps == ns && p.T * p.k * ns * step <= most ? 1 : 2;
+  const size_t smem = (size_t)kWarps * S * entry_bytes<WF>() + 2 * kThreads * 16 * NG + (size_t)p.h_bufs * p.h_bytes +
+                      tables_bytes(p.T * p.k, NG);
   const int rc2 = set_max_dynamic_smem(reinterpret_cast<const void*>(few_down_kernel<WF, NG, S>), smem,
                                        "few_down_kernel: shared memory limit");
   if (rc2) return rc2;
@@ -708,7 +976,7 @@ static_assert(OES_FEW_TOKENS_MAX == kMaxTokens, "tokens a call");
 
 extern "C" size_t moe_layer_few_tokens_workspace_size(const oes_routed_experts* v, int T, int k) {
   if (check_view(v, T, k, "moe_layer_few_tokens_workspace_size")) return 0;
-  return ((size_t)T * k * v->I * 2 + 255) / 256 * 256;
+  return ((size_t)T * k * v->I * 4 + 255) / 256 * 256;
 }
 
 extern "C" int moe_layer_few_tokens(const oes_routed_experts* v, const uint16_t* x, int T, int k, const void* logits,
@@ -763,7 +1031,7 @@ extern "C" int moe_layer_few_tokens(const oes_routed_experts* v, const uint16_t*
   p.logits_bf16 = dtype == OES_LOGITS_BF16;
   p.ids = ids;
   p.weights = weights;
-  p.h = static_cast<uint16_t*>(workspace);
+  p.h = static_cast<float*>(workspace);
   p.out = out;
   p.status = status;
   if (logits && v->E > kFusedExperts) {

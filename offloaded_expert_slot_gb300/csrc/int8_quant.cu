@@ -34,18 +34,33 @@ struct Int8QuantArgs {
   float* s;
 };
 
-__device__ __forceinline__ int int8_code(float v, float rcp, float amax) {
-  const float f = v * rcp;
-  const float n = rintf(f);
-  int c = (int)n;
-  if (fabsf(f - n) > 0.5f - 0x1p-14f) {
-    const float a = fabsf(v), m = floorf(fabsf(f));
-    const double lhs = 254.0 * (double)a, rhs = (2.0 * (double)m + 1.0) * (double)amax;
-    int r = (int)m;
-    if (lhs > rhs || (lhs == rhs && (r & 1))) ++r;
-    c = v < 0.0f ? -r : r;
+// The code of one value, exactly: m or m + 1, m = floor(|f|).  Out of line, since
+// one chunk in a thousand comes here.
+__device__ __noinline__ int int8_code_exact(float v, float rcp, float amax) {
+  const float a = fabsf(v), m = floorf(a * rcp);
+  const double lhs = 254.0 * (double)a, rhs = (2.0 * (double)m + 1.0) * (double)amax;
+  int c = (int)m;
+  if (lhs > rhs || (lhs == rhs && (c & 1))) ++c;
+  return v < 0.0f ? -c : c;
+}
+
+// V codes, one in each low byte.  Adding 3 2^22 leaves the nearest integer of v rcp
+// (an FMA: the product unrounded) in the low bits of the sum, in two's complement;
+// d is how far it is from there.
+template <int V>
+__device__ __forceinline__ void int8_codes(const float (&v)[V], float rcp, float amax, uint32_t (&code)[V]) {
+  constexpr float kMagic = 12582912.0f;
+  float far = 0.0f;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const float t = fmaf(v[i], rcp, kMagic);
+    far = fmaxf(far, fabsf(fmaf(v[i], rcp, -(t - kMagic))));
+    code[i] = __float_as_uint(t);
   }
-  return c;
+  if (far > 0.5f - 0x1p-14f) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) code[i] = (uint32_t)int8_code_exact(v[i], rcp, amax);
+  }
 }
 
 // The values of chunk c of a row (V at a time), K past its end as zeros.
@@ -113,9 +128,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) int8_quantize_kernel(co
     if (tid == 0) a.s[t] = odd ? __int_as_float(0x7FFFFFFF) : __fdiv_rn(amax, 127.0f);
     int8_t* q = a.q + t * a.q_ld;
     auto put = [&](int c, float (&w)[V]) {
-      int code[V];
+      uint32_t code[V];
+      int8_codes<V>(w, rcp, amax, code);
+      if (odd) {
 #pragma unroll
-      for (int i = 0; i < V; ++i) code[i] = odd ? 0 : int8_code(w[i], rcp, amax);
+        for (int i = 0; i < V; ++i) code[i] = 0u;
+      }
       if constexpr (V == 8) {
         uint32_t o[2];
 #pragma unroll

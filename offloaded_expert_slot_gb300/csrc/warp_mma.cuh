@@ -41,6 +41,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
   asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
   asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -72,24 +77,11 @@ __device__ __forceinline__ uint32_t e4m3x2_f16x2(uint32_t two) {
   asm("{ .reg .b16 h; cvt.u16.u32 h, %1; cvt.rn.f16x2.e4m3x2 %0, h; }" : "=r"(r) : "r"(two));
   return r;
 }
-// four e4m3 codes -> two bf16x2, exact (a code has 4 significant bits, and
-// its value's fp32 form has nothing past the upper half); NaN stays NaN
-__device__ __forceinline__ void e4m3x4_bf16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
-  uint32_t f0, f1, f2, f3;
-  asm("{ .reg .b16 a, b, p, q, r, s; .reg .b32 u, v;\n"
-      "mov.b32 {a, b}, %4;\n"
-      "cvt.rn.f16x2.e4m3x2 u, a;\n"
-      "cvt.rn.f16x2.e4m3x2 v, b;\n"
-      "mov.b32 {p, q}, u;\n"
-      "mov.b32 {r, s}, v;\n"
-      "cvt.f32.f16 %0, p;\n"
-      "cvt.f32.f16 %1, q;\n"
-      "cvt.f32.f16 %2, r;\n"
-      "cvt.f32.f16 %3, s; }"
-      : "=r"(f0), "=r"(f1), "=r"(f2), "=r"(f3)
+// four e4m3 codes -> two f16x2, exact; NaN stays NaN
+__device__ __forceinline__ void e4m3x4_f16x4(uint32_t w, uint32_t& lo, uint32_t& hi) {
+  asm("{ .reg .b16 a, b; mov.b32 {a, b}, %2; cvt.rn.f16x2.e4m3x2 %0, a; cvt.rn.f16x2.e4m3x2 %1, b; }"
+      : "=r"(lo), "=r"(hi)
       : "r"(w));
-  lo = __byte_perm(f0, f1, 0x7632);
-  hi = __byte_perm(f2, f3, 0x7632);
 }
 // eight e2m1 codes (element 2i in the low nibble of byte i) -> four f16x2, exact
 __device__ __forceinline__ void e2m1x8_f16x8(uint32_t w, uint32_t (&o)[4]) {

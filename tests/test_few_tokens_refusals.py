@@ -33,7 +33,7 @@ def call(v, **kw):
     (dict(weights=0), 1), (dict(workspace=0), 1), (dict(out=0), 1), (dict(x=P + 8), 1), (dict(workspace=P + 8), 1),
     (dict(ids=P + 2), 1), (dict(weights=P + 1), 1), (dict(out=P + 1), 1), (dict(status=P + 2), 1),
     (dict(logits=P + 2), 1), (dict(logits=P + 1, dtype=1), 1), (dict(dtype=2), 1), (dict(dtype=-1), 1),
-    (dict(workspace_bytes=4 * 2 * 128 * 2 - 1), 1)], ids=str)
+    (dict(workspace_bytes=4 * 2 * 128 * 4 - 1), 1)], ids=str)
 def test_call_refuses(kw, code):
     with pytest.raises(oes.OesError) as e:
         call(view(), **kw)
@@ -58,7 +58,7 @@ def test_null_view_and_sizes():
     assert oes.load().moe_layer_few_tokens(None, P, 1, 1, P, 0, P, P, P, 1 << 20, P, P, None) == oes.OES_ERR_INVALID_ARG
     assert oes.load().moe_layer_few_tokens_workspace_size(None, 1, 1) == 0
     v = view()
-    assert oes.moe_layer_few_tokens_workspace_size(v, 4, 2) >= 4 * 2 * 128 * 2
+    assert oes.moe_layer_few_tokens_workspace_size(v, 4, 2) >= 4 * 2 * 128 * 4
     for T, k in ((17, 2), (-1, 2), (4, 0), (4, 33)):
         assert oes.moe_layer_few_tokens_workspace_size(v, T, k) == 0
     assert oes.moe_layer_few_tokens_workspace_size(view(wfmt=oes.OES_WFMT_NVFP4_W4A4), 4, 2) == 0
