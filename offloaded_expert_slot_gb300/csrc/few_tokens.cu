@@ -71,8 +71,6 @@ namespace {
 __host__ __device__ constexpr int cdiv(int a, int b) { return (a + b - 1) / b; }
 
 constexpr int kMaxTokens = 16;    // of a call
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kFusedExperts = 512;  // most experts that the kernels route themselves
 constexpr int kRowTile = 16;
 
@@ -122,8 +120,6 @@ struct FewParams {
   int64_t s13, w2, s2, gs;  // sections of an expert row
   int x_ld;                 // bytes of a row of x in shared memory
   int rows_cta;             // few_down: rows of out a CTA owns
-  int k_steps, h_bytes;     // few_down: steps of K a group of h spans; a buffer's bytes
-  int h_bufs;
 };
 
 // The chunk's tables, in shared memory.
@@ -136,6 +132,7 @@ struct Tables {
   int16_t* route;  // [blocks][8 NG] route of each token in a block, or -1
   int16_t* order;  // [R] few_down: the routes that count, block after block
   int16_t* cum;    // [blocks + 1] few_down: a block's first place there
+  uint16_t* has;   // [blocks] few_down: which tokens have a route in a block
   __device__ __forceinline__ Tables(uint8_t* base, int R, int ng) {
     ids = reinterpret_cast<int32_t*>(base);
     w = reinterpret_cast<float*>(ids + R);
@@ -145,21 +142,22 @@ struct Tables {
     route = reinterpret_cast<int16_t*>(slot + R);
     order = route + R * 8 * ng;
     cum = order + R;
+    has = reinterpret_cast<uint16_t*>(cum + R + 1);
   }
 };
-__host__ __device__ constexpr int tables_bytes(int R, int ng) { return R * (24 + 16 * ng) + 4; }
+__host__ __device__ constexpr int tables_bytes(int R, int ng) { return R * (26 + 16 * ng) + 4; }
 
 // Routing and tables, by the whole CTA; returns the number of blocks.  One CTA
 // writes the router's outputs and the status (`first`).
 template <int NG>
 __device__ int few_tables(const FewParams& p, const Tables& tb, bool first) {
-  __shared__ uint2 cand[kWarps][33];
+  __shared__ uint2 cand[kMaxTokens][33];
   __shared__ int s_nb;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
   const int R = p.T * p.k;
-  for (int i = tid; i < R * 4 * NG; i += kThreads) reinterpret_cast<int32_t*>(tb.route)[i] = -1;
+  for (int i = tid; i < R * 4 * NG; i += nt) reinterpret_cast<int32_t*>(tb.route)[i] = -1;
   if (p.logits) {
-    for (int t = warp; t < p.T; t += kWarps) {
+    for (int t = warp; t < p.T; t += nt >> 5) {
       int32_t* ids = tb.ids + t * p.k;
       float* w = tb.w + t * p.k;
       if (p.logits_bf16)
@@ -170,13 +168,13 @@ __device__ int few_tables(const FewParams& p, const Tables& tb, bool first) {
                                                  lane, ids, w, cand[warp]);
     }
   } else {
-    for (int r = tid; r < R; r += kThreads) {
+    for (int r = tid; r < R; r += nt) {
       tb.ids[r] = __ldcg(p.ids + r);
       tb.w[r] = __ldcg(p.weights + r);
     }
   }
   __syncthreads();
-  for (int r = tid; r < R; r += kThreads) {
+  for (int r = tid; r < R; r += nt) {
     const int e = tb.ids[r];
     const int t = r / p.k;
     int lead = -1;
@@ -224,7 +222,7 @@ __device__ int few_tables(const FewParams& p, const Tables& tb, bool first) {
     if (lane == 0) s_nb = n;
   }
   __syncthreads();
-  for (int r = tid; r < R; r += kThreads) {
+  for (int r = tid; r < R; r += nt) {
     const int lead = tb.lead[r];
     if (lead >= 0) tb.route[tb.blk[lead] * 8 * NG + r / p.k] = (int16_t)r;
   }
@@ -341,20 +339,23 @@ __device__ __forceinline__ float f16_group(const float (&v)[8], uint4& out) {
 }
 
 // ------------------------------------------------------------------ gate, up
-// The (block, 8 rows of I) of the chunk are dealt out in runs, and a CTA takes two
-// neighbours at a time where they are of one block: both use the same columns.
-template <int WF, int NG, int S>
-__global__ void __launch_bounds__(kThreads, 2) few_up_kernel(const FewParams p) {
+// A unit is 8 rows of I of a block.  The chunk's units are dealt out to the CTAs in
+// runs.  KS 1: each warp takes units of its own, and a lane ends with both factors of
+// its h; no barrier after the tables.  KS W: the CTA's warps share the K range of a unit
+// and add their sums, for chunks with few units (see launch_few).
+template <int WF, int NG, int W, int KS, int S>
+__global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_up_kernel(const FewParams p) {
   using F = Fmt<WF>;
+  constexpr int kThreads = W * 32;
   constexpr int kEntry = entry_bytes<WF>();
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* queue = smem + (threadIdx.x >> 5) * (S * kEntry);
-  float* part = reinterpret_cast<float*>(smem + kWarps * S * kEntry);  // [2][warp][lane][2][4 NG]
-  uint8_t* xs = reinterpret_cast<uint8_t*>(part + 2 * kThreads * 8 * NG);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  uint8_t* queue = smem + warp * (S * kEntry);
+  float* part = reinterpret_cast<float*>(smem + W * S * kEntry);  // KS > 1: [2][warp][lane][4 NG]
+  uint8_t* xs = reinterpret_cast<uint8_t*>(part + (KS > 1 ? 2 * kThreads * 4 * NG : 0));
   float* xf = reinterpret_cast<float*>(xs + p.T * p.x_ld);  // [T][ns] factors of x (kF16)
   const int ns = cdiv(p.H, F::kStepK);
   const Tables tb(reinterpret_cast<uint8_t*>(xf + (F::kF16 ? p.T * ns : 0)), p.T * p.k, NG);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   pdl_wait();
   pdl_trigger();  // the down kernel; it reads what this kernel waited for, and h after this kernel's end
   // x, with zeros up to a whole step
@@ -381,63 +382,61 @@ __global__ void __launch_bounds__(kThreads, 2) few_up_kernel(const FewParams p) 
   }
   cp_async_commit();
   const int nb = few_tables<NG>(p, tb, blockIdx.x == 0);
-  const int per = p.I / 8, units = nb * per;  // groups of 8 rows: of a block, and in all
+  const int per = p.I / 8, units = nb * per;
   const int lo = (int)((int64_t)blockIdx.x * units / gridDim.x), hi = (int)((int64_t)(blockIdx.x + 1) * units / gridDim.x);
   const int row = p.H * F::kRowBytes / F::kStepK;  // bytes of a weight row
+  constexpr int kNext = KS > 1 ? 1 : W;            // to the warp's next unit
+  const int s0 = KS > 1 ? warp : 0;
 
-  // A place in the CTA's groups: group j, n (1 or 2) of them taken together, of
-  // block b, from group r of it
+  // A place in the warp's units: unit j, rows 8 r of block b
   struct Place {
-    int j, n, b, r;
+    int j, b, r;
   };
-  auto at_group = [&](int j, int b, int r) {
-    if (r >= per) {
-      r -= per;
-      ++b;
+  auto next = [&](Place& q) {
+    q.j += kNext;
+    q.r += kNext;
+    while (q.r >= per) {
+      q.r -= per;
+      ++q.b;
     }
-    return Place{j, j + 1 < hi && r + 1 < per ? 2 : 1, b, r};
   };
-  const Place start = at_group(lo, lo / per, lo % per);
+  Place q{lo + (KS > 1 ? 0 : warp), 0, 0};
+  q.b = q.j / per;
+  q.r = q.j - q.b * per;
 
-  // the next step to copy: of place c, step cs, group cm of the place
-  Place c = start;
-  int cs = warp, cm = 0, at = 0;
+  // the next step to copy: step cs of place c
+  Place c = q;
+  int cs = s0, at = 0;
   const uint8_t* base = p.pool;
-  const uint8_t* r0 = p.pool;
+  const uint8_t* w0 = p.pool;
+  const int64_t up = (int64_t)p.I * row;
   auto set_rows = [&]() {
-    if (c.j >= hi || warp >= ns) return;
+    if (c.j >= hi || s0 >= ns) return;
     base = p.pool + (int64_t)tb.slot[c.b] * p.row_bytes;
-    r0 = base + (int64_t)(c.r * 8 + g) * row + 16 * t;
+    w0 = base + (int64_t)(c.r * 8 + g) * row + 16 * t;
   };
   set_rows();
-  const int64_t up = (int64_t)p.I * row;
   auto copy_next = [&]() {
-    if (c.j < hi && warp < ns) {
+    if (c.j < hi && s0 < ns) {
       const uint32_t e = smem_u32(queue + at * kEntry);
-      const uint8_t* w = r0 + (cm ? 8 * row : 0);
-      step_copy<WF>(e, p.pool, w, w + up, true, true, cs * F::kRowBytes, row);
+      step_copy<WF>(e, p.pool, w0, w0 + up, true, true, cs * F::kRowBytes, row);
       if constexpr (WF == OES_WFMT_FP8) {
         const int ib = cdiv(p.I, 128);
         if (lane < 2)
-          cp_async4_take(e + 2048 + 4 * lane,
-                         base + p.s13 + ((int64_t)(lane * ib + (((c.r + cm) * 8) >> 7)) * ns + cs) * 4, true);
+          cp_async4_take(e + 2048 + 4 * lane, base + p.s13 + ((int64_t)(lane * ib + ((c.r * 8) >> 7)) * ns + cs) * 4, true);
       }
       if constexpr (WF == OES_WFMT_NVFP4) {
         const int r16 = lane & 15, k64 = 2 * cs + (lane >> 4);
         const bool in = k64 * 64 < p.H;
         cp_async4_take(e + 1024 + 4 * lane,
-                       base + p.s13 + ((int64_t)(in ? k64 : 0) * 2 * p.I + (r16 >> 3) * p.I + (c.r + cm) * 8 + (r16 & 7)) * 4,
-                       in);
+                       base + p.s13 + ((int64_t)(in ? k64 : 0) * 2 * p.I + (r16 >> 3) * p.I + c.r * 8 + (r16 & 7)) * 4, in);
         if (lane == 0) cp_async4_take(e + 1024 + 128, base + p.gs, true);
       }
-      if (++cm == c.n) {
-        cm = 0;
-        cs += kWarps;
-        if (cs >= ns) {
-          cs = warp;
-          c = at_group(c.j + c.n, c.b, c.r + c.n);
-          set_rows();
-        }
+      cs += KS;
+      if (cs >= ns) {
+        cs = s0;
+        next(c);
+        set_rows();
       }
     }
     cp_async_commit();
@@ -448,96 +447,94 @@ __global__ void __launch_bounds__(kThreads, 2) few_up_kernel(const FewParams p) 
   __syncthreads();
 
   // columns past the tokens are not used: any row does
-  uint32_t xb[NG];
-  const float* xfc[NG][2];
+  uint32_t xb[NG], xfc[NG][2];
 #pragma unroll
   for (int n = 0; n < NG; ++n) {
     xb[n] = smem_u32(xs + min(8 * n + g, p.T - 1) * p.x_ld) + 2 * piece_k<WF>(0, 0);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) xfc[n][j] = xf + min(8 * n + 2 * t + j, p.T - 1) * ns;
+    for (int j = 0; j < 2; ++j) xfc[n][j] = smem_u32(xf + min(8 * n + 2 * t + j, p.T - 1) * ns);
   }
   int from = 0, buf = 0;
-  for (Place q = start; q.j < hi; q = at_group(q.j + q.n, q.b, q.r + q.n), buf ^= 1) {
-    float acc[2][NG][4];
+  for (; q.j < hi; next(q), buf ^= 1) {
+    float acc[NG][4];
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
+    float gs = 1.0f;
+    for (int s = s0; s < ns; s += KS) {
+      cp_async_wait<S - 1>();
+      if (F::kScale) __syncwarp();  // scales that other lanes copied
+      const uint32_t e = smem_u32(queue + from * kEntry);
+      float d[NG][4];
 #pragma unroll
       for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][n][i] = 0.0f;
-    float gs = 1.0f;
-    for (int s = warp; s < ns; s += kWarps) {
-      uint4 B[2][NG][F::kB];
-      float f[NG][2];
+        for (int i = 0; i < 4; ++i) d[n][i] = F::kF16 ? 0.0f : acc[n][i];
 #pragma unroll
-      for (int n = 0; n < NG; ++n) {
+      for (int hh = 0; hh < 2; ++hh) {
+        uint4 B[NG][F::kB];
 #pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
+        for (int n = 0; n < NG; ++n)
 #pragma unroll
           for (int i = 0; i < F::kB; ++i)
-            B[hh][n][i] = lds128(xb[n] + 2 * (s * F::kStepK + piece_k<WF>(hh, i) - piece_k<WF>(0, 0)));
-        if (F::kF16) {
-          f[n][0] = xfc[n][0][s];
-          f[n][1] = xfc[n][1][s];
-        }
+            B[n][i] = lds128(xb[n] + 2 * (s * F::kStepK + piece_k<WF>(hh, i) - piece_k<WF>(0, 0)));
+        half_mma<WF, NG, false>(e, hh, B, B, d);
       }
-#pragma unroll
-      for (int m = 0; m < 2; ++m) {
-        if (m >= q.n) continue;
-        cp_async_wait<S - 1>();
-        if (F::kScale) __syncwarp();  // scales that other lanes copied
-        const uint32_t e = smem_u32(queue + from * kEntry);
-        if constexpr (F::kF16) {
-          float d[NG][4];
-#pragma unroll
-          for (int n = 0; n < NG; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
-          half_mma<WF, NG, false>(e, 0, B[0], B[0], d);
-          half_mma<WF, NG, false>(e, 1, B[1], B[1], d);
-          float sg = 1.0f, su = 1.0f;
-          if constexpr (WF == OES_WFMT_FP8) {
-            const uint2 sc = lds64(e + 2048);
-            sg = __uint_as_float(sc.x);
-            su = __uint_as_float(sc.y);
-          } else {
-            gs = __uint_as_float(lds32(e + 1024 + 128));
-          }
-#pragma unroll
-          for (int n = 0; n < NG; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              acc[m][n][i] = fmaf((i < 2 ? sg : su) * f[n][i & 1], d[n][i], acc[m][n][i]);
+      if constexpr (F::kF16) {
+        float sg = 1.0f, su = 1.0f;
+        if constexpr (WF == OES_WFMT_FP8) {
+          const uint2 sc = lds64(e + 2048);
+          sg = __uint_as_float(sc.x);
+          su = __uint_as_float(sc.y);
         } else {
-          half_mma<WF, NG, false>(e, 0, B[0], B[0], acc[m]);
-          half_mma<WF, NG, false>(e, 1, B[1], B[1], acc[m]);
+          gs = __uint_as_float(lds32(e + 1024 + 128));
         }
-        if (F::kScale) __syncwarp();
-        from = from + 1 == S ? 0 : from + 1;
-        copy_next();
-      }
-    }
-    float* mine = part + ((buf * kWarps + warp) * 32 + lane) * (8 * NG);
 #pragma unroll
-    for (int m = 0; m < 2; ++m)
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float f = __uint_as_float(lds32(xfc[n][j] + 4 * s));
+            acc[n][j] = fmaf(sg * f, d[n][j], acc[n][j]);
+            acc[n][2 + j] = fmaf(su * f, d[n][2 + j], acc[n][2 + j]);
+          }
+      } else {
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[n][i] = d[n][i];
+      }
+      if (F::kScale) __syncwarp();
+      from = from + 1 == S ? 0 : from + 1;
+      copy_next();
+    }
+    if constexpr (KS == 1) {
 #pragma unroll
       for (int n = 0; n < NG; ++n)
-        if (m < q.n)
-          *reinterpret_cast<float4*>(mine + (m * NG + n) * 4) =
-              make_float4(gs * acc[m][n][0], gs * acc[m][n][1], gs * acc[m][n][2], gs * acc[m][n][3]);
-    __syncthreads();
-    const int col = (tid >> 3) & (8 * NG - 1), r8 = tid & 7, m = tid / (64 * NG);
-    if (m < q.n) {
-      const int r = tb.route[q.b * 8 * NG + col];
-      if (r >= 0) {
-        const float* v = part + (buf * kWarps * 32 + r8 * 4 + (col & 7) / 2) * (8 * NG) + (m * NG + (col >> 3)) * 4 + (col & 1);
-        float gate = 0.0f, upv = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kWarps; ++w) {
-          gate += v[w * 32 * 8 * NG];
-          upv += v[w * 32 * 8 * NG + 2];
+        for (int j = 0; j < 2; ++j) {
+          const int r = tb.route[q.b * 8 * NG + 8 * n + 2 * t + j];
+          if (r >= 0) p.h[(int64_t)r * p.I + q.r * 8 + g] = silu_f32(gs * acc[n][j]) * (gs * acc[n][2 + j]);
         }
-        p.h[(int64_t)r * p.I + (q.r + m) * 8 + r8] = silu_f32(gate) * upv;
+    } else {
+      float* mine = part + ((buf * W + warp) * 32 + lane) * (4 * NG);
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+        *reinterpret_cast<float4*>(mine + 4 * n) =
+            make_float4(gs * acc[n][0], gs * acc[n][1], gs * acc[n][2], gs * acc[n][3]);
+      __syncthreads();
+      if (tid < 64 * NG) {
+        const int col = tid >> 3, r8 = tid & 7, r = tb.route[q.b * 8 * NG + col];
+        if (r >= 0) {
+          const float* v = part + (buf * W * 32 + r8 * 4 + (col & 7) / 2) * (4 * NG) + (col >> 3) * 4 + (col & 1);
+          float gate = 0.0f, upv = 0.0f;
+#pragma unroll
+          for (int w = 0; w < W; ++w) {
+            gate += v[w * 32 * 4 * NG];
+            upv += v[w * 32 * 4 * NG + 2];
+          }
+          p.h[(int64_t)r * p.I + q.r * 8 + r8] = silu_f32(gate) * upv;
+        }
       }
     }
   }
@@ -549,26 +546,36 @@ __global__ void __launch_bounds__(kThreads, 2) few_up_kernel(const FewParams p) 
 // complete, and this kernel reads it through L2 without waiting.  h is
 // few_up_kernel's, and is read after the wait.
 //
-// h goes through shared memory a group at a time: whole blocks, as many as their
-// routes' rows fit kHPieces pieces of 8 values a thread, over k_steps steps of K.
-// A group is loaded into registers while the group before it is multiplied, and
-// stored behind it in the form that the instructions take.  (Loaded by each lane
-// for itself, half a step ahead, its latency set the pace: 16 tokens x 10 of 200 bf16
-// experts ran at 1.9 TB/s.)  Within a group the warps share its (block, step)
-// in runs, so that a warp seldom changes the block.
-constexpr int kHPieces = 4;
+// The (block, step of K) of a tile of rows are dealt out to the CTA's warps in runs.
+// For each, the warp brings the rows of h of the block's tokens into a place of its own
+// in shared memory, in the form that the instructions take; they are loaded into
+// registers while the step before is multiplied (the first kHold of them: few
+// blocks have more).  (Loaded by each lane as it needs them, their latency set the
+// pace, 16 tokens x 10 of 200 bf16 experts ran at 1.9 TB/s; staged by the CTA for several
+// blocks at a time, the barriers and the bookkeeping did.)
+constexpr int kHold = 4;  // rows of h
 
-template <int WF, int NG, int S>
-__global__ void __launch_bounds__(kThreads) __maxnreg__(NG == 1 ? 144 : 208) few_down_kernel(const FewParams p) {
+template <int WF, int NG>
+__host__ __device__ constexpr int hold_bytes() {  // a warp's place for h: rows, then factors
   using F = Fmt<WF>;
+  return 8 * NG * ((F::kF16 ? 1 : 2) * (F::kStepK * 2 + 16) + (F::kF16 ? 16 : 0));
+}
+
+template <int WF, int NG, int W, int S>
+__global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_down_kernel(const FewParams p) {
+  using F = Fmt<WF>;
+  constexpr int kThreads = W * 32;
   constexpr int kEntry = entry_bytes<WF>();
   constexpr int kParts = F::kF16 ? 1 : 2;
+  constexpr int kPart = F::kStepK * 2 + 16, kLine = kParts * kPart;  // a row of h: its parts a bank's width apart
+  constexpr int kRowLanes = F::kStepK / 8, kRowsAt = 32 / kRowLanes;  // lanes a row, rows a pass
   extern __shared__ __align__(128) uint8_t smem[];
-  uint8_t* queue = smem + (threadIdx.x >> 5) * (S * kEntry);
-  float* part = reinterpret_cast<float*>(smem + kWarps * S * kEntry);  // [2][warp][lane][4 NG]
-  uint8_t* hbuf = reinterpret_cast<uint8_t*>(part + 2 * kThreads * 4 * NG);  // [h_bufs][h_bytes]
-  const Tables tb(hbuf + p.h_bufs * p.h_bytes, p.T * p.k, NG);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+  uint8_t* queue = smem + warp * (S * kEntry);
+  uint8_t* hrows = smem + W * S * kEntry + warp * hold_bytes<WF, NG>();
+  float* hf = reinterpret_cast<float*>(hrows + 8 * NG * kLine);  // factors (kF16)
+  float* part = reinterpret_cast<float*>(smem + W * (S * kEntry + hold_bytes<WF, NG>()));  // [warp][lane][4 NG]
+  const Tables tb(reinterpret_cast<uint8_t*>(part + kThreads * 4 * NG), p.T * p.k, NG);
   const int nb = few_tables<NG>(p, tb, false);
   const int row = p.I * F::kRowBytes / F::kStepK;
   const int ns = cdiv(p.I, F::kStepK);
@@ -578,7 +585,10 @@ __global__ void __launch_bounds__(kThreads) __maxnreg__(NG == 1 ? 144 : 208) few
     for (int b = 0; b < nb; ++b) {
       const int r = lane < 8 * NG ? tb.route[b * 8 * NG + lane] : -1;
       const uint32_t m = __ballot_sync(0xffffffffu, r >= 0);
-      if (lane == 0) tb.cum[b] = (int16_t)n;
+      if (lane == 0) {
+        tb.cum[b] = (int16_t)n;
+        tb.has[b] = (uint16_t)m;
+      }
       if (r >= 0) tb.order[n + __popc(m & ((1u << lane) - 1))] = (int16_t)r;
       n += __popc(m);
     }
@@ -586,263 +596,214 @@ __global__ void __launch_bounds__(kThreads) __maxnreg__(NG == 1 ? 144 : 208) few
   }
   __syncthreads();
 
-  // A group: blocks [b0, b1) over steps k0 .. k0 + kn, for the tile of rows row0
-  struct Group {
-    int b0, b1, k0, kn, row0;
+  // A place in the warp's run of a tile: i of [.., i1), step s of block b
+  const int n_all = nb * ns, i0 = (int)((int64_t)warp * n_all / W), i1 = (int)((int64_t)(warp + 1) * n_all / W);
+  struct Place {
+    int i, b, s, row0;
   };
-  auto group_at = [&](int row0, int k0, int b0) {
-    if (b0 >= nb) {
-      b0 = 0;
-      k0 += p.k_steps;
-      if (k0 >= ns) {
-        k0 = 0;
-        row0 += kRowTile;
-      }
+  Place start{i0, i0 / max(ns, 1), 0, i0 < i1 ? row_lo : row_hi};
+  start.s = i0 - start.b * ns;
+  auto next = [&](Place& q) {
+    if (++q.s == ns) {
+      q.s = 0;
+      ++q.b;
     }
-    Group o{b0, b0, k0, min(p.k_steps, ns - k0), nb > 0 ? row0 : row_hi};
-    if (o.row0 >= row_hi) return o;
-    const int lim = tb.cum[b0] + kHPieces * kThreads / (o.kn * (F::kStepK / 8));
-    int l = b0 + 1, h = nb;  // the last block whose routes fit; the first one's always do
-    while (l < h) {
-      const int mid = (l + h + 1) >> 1;
-      if (tb.cum[mid] <= lim) l = mid;
-      else h = mid - 1;
+    if (++q.i == i1) {
+      const int r = q.row0 + kRowTile;
+      q = start;
+      q.row0 = r;
     }
-    o.b1 = l;
-    return o;
-  };
-  // The warp's run within a group: `rem` (block, step) from block b, step s on
-  struct Run {
-    int b, s, rem;
-  };
-  auto run_of = [&](const Group& o) {
-    if (o.row0 >= row_hi) return Run{0, 0, 0};
-    const int n = (o.b1 - o.b0) * o.kn, i0 = warp * n / kWarps, i1 = (warp + 1) * n / kWarps;
-    const int b = i0 / o.kn;
-    return Run{o.b0 + b, i0 - b * o.kn, i1 - i0};
   };
 
   // the next step to copy
-  Group cg = group_at(row_lo, 0, 0);
-  Run c = run_of(cg);
+  Place c = start;
   int at = 0;
   const uint8_t* base = p.pool;
   const uint8_t* w0 = p.pool;
   bool ok0 = false, ok1 = false;
   auto set_rows = [&]() {
-    while (c.rem == 0 && cg.row0 < row_hi) {
-      cg = group_at(cg.row0, cg.k0, cg.b1);
-      c = run_of(cg);
-    }
-    if (cg.row0 >= row_hi) return;
+    if (c.row0 >= row_hi) return;
     base = p.pool + (int64_t)tb.slot[c.b] * p.row_bytes;
-    w0 = base + p.w2 + (int64_t)(cg.row0 + g) * row + 16 * t;
-    ok0 = cg.row0 + g < row_hi;
-    ok1 = cg.row0 + g + 8 < row_hi;
+    w0 = base + p.w2 + (int64_t)(c.row0 + g) * row + 16 * t;
+    ok0 = c.row0 + g < row_hi;
+    ok1 = c.row0 + g + 8 < row_hi;
   };
   set_rows();
   auto copy_next = [&]() {
-    if (c.rem > 0) {
+    if (c.row0 < row_hi) {
       const uint32_t e = smem_u32(queue + at * kEntry);
-      const int s = cg.k0 + c.s;
-      step_copy<WF>(e, p.pool, w0, w0 + 8 * row, ok0, ok1, s * F::kRowBytes, row);
+      step_copy<WF>(e, p.pool, w0, w0 + 8 * row, ok0, ok1, c.s * F::kRowBytes, row);
       if constexpr (WF == OES_WFMT_FP8) {
-        const int r = cg.row0 + lane;
+        const int r = c.row0 + lane;
         if (lane < kRowTile)
-          cp_async4_take(e + 2048 + 4 * lane, base + p.s2 + ((int64_t)(r < row_hi ? r >> 7 : 0) * ns + s) * 4,
+          cp_async4_take(e + 2048 + 4 * lane, base + p.s2 + ((int64_t)(r < row_hi ? r >> 7 : 0) * ns + c.s) * 4,
                          r < row_hi);
       }
       if constexpr (WF == OES_WFMT_NVFP4) {
-        const int r = cg.row0 + (lane & 15), k64 = 2 * s + (lane >> 4);
+        const int r = c.row0 + (lane & 15), k64 = 2 * c.s + (lane >> 4);
         const bool in = r < row_hi && k64 * 64 < p.I;
         cp_async4_take(e + 1024 + 4 * lane, base + p.s2 + (in ? (int64_t)k64 * p.H + r : 0) * 4, in);
         if (lane == 0) cp_async4_take(e + 1024 + 128, base + p.gs + 4, true);
       }
-      --c.rem;
-      if (++c.s == cg.kn) {
-        c.s = 0;
-        ++c.b;
-      }
-      if (c.s == 0 || c.rem == 0) set_rows();
+      const int i = c.i;
+      next(c);
+      if (c.s == 0 || c.i != i + 1) set_rows();
     }
     cp_async_commit();
     at = at + 1 == S ? 0 : at + 1;
   };
   for (int i = 0; i < S; ++i) copy_next();
 
-  // Rows of h in a buffer are ppr pieces of 16 bytes and one more, so that rows do
-  // not start in the same bank; bf16 rows come in two parts, and f16 rows' factors
-  // stand behind all rows.
-  float hv[kHPieces][8];
-  auto load_h = [&](const Group& o) {
-    const int ppr = o.kn * (F::kStepK / 8), j0 = tb.cum[o.b0], n = (tb.cum[o.b1] - j0) * ppr;
+  // Row j of a place's block: 8 values of this lane, loaded and stored
+  constexpr int kPass = (kHold + kRowsAt - 1) / kRowsAt;
+  const int hl = lane / kRowLanes, hp = lane % kRowLanes;
+  auto load_row = [&](const Place& q, int j, float (&v)[8]) {
 #pragma unroll
-    for (int i = 0; i < kHPieces; ++i) {
-      const int x = tid + i * kThreads, rw = x / ppr, k = o.k0 * F::kStepK + (x - rw * ppr) * 8;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) hv[i][j] = 0.0f;
-      if (x < n && k < p.I) {
-        const float4* h = reinterpret_cast<const float4*>(p.h + (int64_t)tb.order[j0 + rw] * p.I + k);
-        const float4 a = __ldcg(h), b = __ldcg(h + 1);
-        hv[i][0] = a.x; hv[i][1] = a.y; hv[i][2] = a.z; hv[i][3] = a.w;
-        hv[i][4] = b.x; hv[i][5] = b.y; hv[i][6] = b.z; hv[i][7] = b.w;
-      }
+    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+    const int first = tb.cum[q.b], k = q.s * F::kStepK + hp * 8;
+    if (j < tb.cum[q.b + 1] - first && k < p.I) {
+      const float4* h = reinterpret_cast<const float4*>(p.h + (int64_t)tb.order[first + j] * p.I + k);
+      const float4 a = __ldcg(h), b = __ldcg(h + 1);
+      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     }
   };
-  auto store_h = [&](const Group& o, uint8_t* dst) {
-    const int ppr = o.kn * (F::kStepK / 8), rows = tb.cum[o.b1] - tb.cum[o.b0];
-    float* factors = reinterpret_cast<float*>(dst + rows * kParts * (ppr + 1) * 16);
+  auto store_row = [&](int j, const float (&v)[8]) {
+    uint4* to = reinterpret_cast<uint4*>(hrows + j * kLine + hp * 16);
+    if constexpr (F::kF16) {
+      uint4 o;
+      const float f = f16_group(v, o);
+      *to = o;
+      if (hp == 0) hf[j] = f;
+    } else {
+      uint32_t a[4], b[4];
 #pragma unroll
-    for (int i = 0; i < kHPieces; ++i) {
-      if (i * kThreads >= rows * ppr) break;
-      const int x = tid + i * kThreads, rw = x / ppr, pc = x - rw * ppr;
-      uint4* to = reinterpret_cast<uint4*>(dst + (rw * kParts * (ppr + 1) + pc) * 16);
-      if constexpr (F::kF16) {
-        uint4 v;
-        const float f = f16_group(hv[i], v);
-        if (rw < rows) {
-          *to = v;
-          if ((pc & 15) == 0) factors[rw * o.kn + (pc >> 4)] = f;
-        }
-      } else if (rw < rows) {
-        uint32_t a[4], b[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          a[j] = f32x2_bf16x2(hv[i][2 * j], hv[i][2 * j + 1]);
-          const float x0 = bf16_f32(a[j] & 0xFFFFu), x1 = __uint_as_float(a[j] & 0xFFFF0000u);
-          // an infinity leaves nothing (and not the NaN of its difference)
-          b[j] = f32x2_bf16x2(fabsf(x0) < INFINITY ? hv[i][2 * j] - x0 : 0.0f,
-                              fabsf(x1) < INFINITY ? hv[i][2 * j + 1] - x1 : 0.0f);
-        }
-        to[0] = make_uint4(a[0], a[1], a[2], a[3]);
-        to[ppr + 1] = make_uint4(b[0], b[1], b[2], b[3]);
+      for (int i = 0; i < 4; ++i) {
+        a[i] = f32x2_bf16x2(v[2 * i], v[2 * i + 1]);
+        const float x0 = bf16_f32(a[i] & 0xFFFFu), x1 = __uint_as_float(a[i] & 0xFFFF0000u);
+        // an infinity leaves nothing (and not the NaN of its difference)
+        b[i] = f32x2_bf16x2(fabsf(x0) < INFINITY ? v[2 * i] - x0 : 0.0f, fabsf(x1) < INFINITY ? v[2 * i + 1] - x1 : 0.0f);
       }
+      to[0] = make_uint4(a[0], a[1], a[2], a[3]);
+      to[kPart / 16] = make_uint4(b[0], b[1], b[2], b[3]);
+    }
+  };
+  float hv[kPass][8];
+  auto load_h = [&](const Place& q) {
+    if (q.row0 >= row_hi) return;
+#pragma unroll
+    for (int i = 0; i < kPass; ++i) load_row(q, i * kRowsAt + hl, hv[i]);
+  };
+  auto store_h = [&](const Place& q) {
+    const int n = tb.cum[q.b + 1] - tb.cum[q.b];
+#pragma unroll
+    for (int i = 0; i < kPass; ++i)
+      if (i * kRowsAt < n) store_row(i * kRowsAt + hl, hv[i]);
+#pragma unroll 1
+    for (int j = kPass * kRowsAt; j < n; j += kRowsAt) {
+      float v[8];
+      load_row(q, j + hl, v);
+      store_row(j + hl, v);
     }
   };
 
   pdl_wait();  // h
-  Group cur = group_at(row_lo, 0, 0);
-  if (cur.row0 < row_hi) {
-    load_h(cur);
-    store_h(cur, hbuf);
-    __syncthreads();
-  }
-  int from = 0, buf = 0, hb = 0;
-  for (int row0 = row_lo; row0 < row_hi; row0 += kRowTile, buf ^= 1) {
+  Place q = start;
+  load_h(q);
+  int from = 0;
+  for (int row0 = row_lo; row0 < row_hi; row0 += kRowTile) {
     float acc[NG][4];
 #pragma unroll
     for (int n = 0; n < NG; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    while (cur.row0 == row0) {
-      const Group nx = group_at(cur.row0, cur.k0, cur.b1);
-      const bool more = nx.row0 < row_hi;
-      // what the one buffer holds serves every tile of rows
-      if (more && p.h_bufs > 1) load_h(nx);
-      const int ppr = cur.kn * (F::kStepK / 8), j0 = tb.cum[cur.b0], line = kParts * (ppr + 1) * 16;
-      const uint32_t hs = smem_u32(hbuf + hb * p.h_bytes);
-      const uint32_t hf = hs + (tb.cum[cur.b1] - j0) * line;  // the factors
-      Run q = run_of(cur);
-      while (q.rem > 0) {
-        // this lane's columns in block q.b: column g's row of h, and whether columns
-        // 2t and 2t + 1 have a route, its weight and its factors
-        uint32_t hrow[NG], hfc[NG][2];
-        bool has[NG];
-        float w[NG][2];
-        int place = tb.cum[q.b] - j0;
+    while (q.row0 == row0) {
+      // this lane's columns in the block: column g's row of h, and for columns 2t and
+      // 2t + 1 whether they have a route, its weight and its row's factor; a column
+      // without a route takes any row, its sums are not used
+      const int b = q.b;
+      const uint32_t m = tb.has[b];
+      uint32_t hrow[NG], hfc[NG][2];
+      float w[NG][2];
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-          const int r = tb.route[q.b * 8 * NG + 8 * n + (lane & 7)];
-          const uint32_t m = __ballot_sync(0xffffffffu, r >= 0) & 0xFFu;
-          has[n] = (m >> g) & 1u;
-          hrow[n] = hs + (has[n] ? place + __popc(m & ((1u << g) - 1)) : 0) * line + 2 * piece_k<WF>(0, 0);
-          const float wr = r >= 0 ? tb.w[r] : 0.0f;
+      for (int n = 0; n < NG; ++n) {
+        auto row_of = [&](int col) { return (m >> col) & 1u ? __popc(m & ((1u << col) - 1)) : 0; };
+        hrow[n] = smem_u32(hrows) + row_of(8 * n + g) * kLine + 2 * piece_k<WF>(0, 0);
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const int col = 2 * t + j;
-            w[n][j] = __shfl_sync(0xffffffffu, wr, col);
-            const bool hc = (m >> col) & 1u;
-            hfc[n][j] = hc ? hf + (place + __popc(m & ((1u << col) - 1))) * cur.kn * 4 : 0u;
-          }
-          place += __popc(m);
+        for (int j = 0; j < 2; ++j) {
+          const int col = 8 * n + 2 * t + j;
+          w[n][j] = (m >> col) & 1u ? tb.w[tb.route[b * 8 * NG + col]] : 0.0f;
+          hfc[n][j] = smem_u32(hf + row_of(col));
         }
-        float blk[NG][4];
+      }
+      float blk[NG][4];
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) blk[n][i] = 0.0f;
+      float gs = 1.0f;
+      do {
+        __syncwarp();  // the step before has read its rows of h
+        store_h(q);
+        next(q);
+        load_h(q);
+        cp_async_wait<S - 1>();
+        __syncwarp();  // rows of h, and scales, that other lanes brought
+        const uint32_t e = smem_u32(queue + from * kEntry);
+        float d[NG][4];
 #pragma unroll
         for (int n = 0; n < NG; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) blk[n][i] = 0.0f;
-        float gs = 1.0f;
-        const int end = min(cur.kn, q.s + q.rem);
-        q.rem -= end - q.s;
-        for (int s = q.s; s < end; ++s) {
-          uint4 B[2][NG][F::kB], L[2][NG][F::kB];
-          float f[NG][2];
+          for (int i = 0; i < 4; ++i) d[n][i] = F::kF16 ? 0.0f : blk[n][i];
 #pragma unroll
-          for (int n = 0; n < NG; ++n) {
+        for (int hh = 0; hh < 2; ++hh) {
+          uint4 B[NG][F::kB], L[NG][F::kB];
 #pragma unroll
-            for (int hh = 0; hh < 2; ++hh)
+          for (int n = 0; n < NG; ++n)
 #pragma unroll
-              for (int i = 0; i < F::kB; ++i) {
-                B[hh][n][i] = L[hh][n][i] = make_uint4(0u, 0u, 0u, 0u);
-                if (has[n]) {
-                  const uint32_t a = hrow[n] + 2 * (s * F::kStepK + piece_k<WF>(hh, i) - piece_k<WF>(0, 0));
-                  B[hh][n][i] = lds128(a);
-                  if (kParts == 2) L[hh][n][i] = lds128(a + (ppr + 1) * 16);
-                }
-              }
-            if (F::kF16) {
-#pragma unroll
-              for (int j = 0; j < 2; ++j) f[n][j] = hfc[n][j] ? __uint_as_float(lds32(hfc[n][j] + 4 * s)) : 0.0f;
+            for (int i = 0; i < F::kB; ++i) {
+              const uint32_t a = hrow[n] + 2 * (piece_k<WF>(hh, i) - piece_k<WF>(0, 0));
+              B[n][i] = lds128(a);
+              L[n][i] = kParts == 2 ? lds128(a + kPart) : B[n][i];
             }
-          }
-          cp_async_wait<S - 1>();
-          if (F::kScale) __syncwarp();  // scales that other lanes copied
-          const uint32_t e = smem_u32(queue + from * kEntry);
-          if constexpr (F::kF16) {
-            float d[NG][4];
-#pragma unroll
-            for (int n = 0; n < NG; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
-            half_mma<WF, NG, false>(e, 0, B[0], B[0], d);
-            half_mma<WF, NG, false>(e, 1, B[1], B[1], d);
-            float s0 = 1.0f, s1 = 1.0f;
-            if constexpr (WF == OES_WFMT_FP8) {
-              s0 = __uint_as_float(lds32(e + 2048 + 4 * g));
-              s1 = __uint_as_float(lds32(e + 2048 + 32 + 4 * g));
-            } else {
-              gs = __uint_as_float(lds32(e + 1024 + 128));
-            }
-#pragma unroll
-            for (int n = 0; n < NG; ++n)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) blk[n][i] = fmaf((i < 2 ? s0 : s1) * f[n][i & 1], d[n][i], blk[n][i]);
+          half_mma<WF, NG, kParts == 2>(e, hh, B, L, d);
+        }
+        if constexpr (F::kF16) {
+          float s0 = 1.0f, s1 = 1.0f;
+          if constexpr (WF == OES_WFMT_FP8) {
+            s0 = __uint_as_float(lds32(e + 2048 + 4 * g));
+            s1 = __uint_as_float(lds32(e + 2048 + 32 + 4 * g));
           } else {
-            half_mma<WF, NG, true>(e, 0, B[0], L[0], blk);
-            half_mma<WF, NG, true>(e, 1, B[1], L[1], blk);
+            gs = __uint_as_float(lds32(e + 1024 + 128));
           }
-          if (F::kScale) __syncwarp();
-          from = from + 1 == S ? 0 : from + 1;
-          copy_next();
+#pragma unroll
+          for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+              const float f = __uint_as_float(lds32(hfc[n][j]));
+              blk[n][j] = fmaf(s0 * f, d[n][j], blk[n][j]);
+              blk[n][2 + j] = fmaf(s1 * f, d[n][2 + j], blk[n][2 + j]);
+            }
+        } else {
+#pragma unroll
+          for (int n = 0; n < NG; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) blk[n][i] = d[n][i];
         }
-        // a token without a route in this block takes nothing from it, not even a
-        // NaN of its weights
+        if (F::kScale) __syncwarp();
+        from = from + 1 == S ? 0 : from + 1;
+        copy_next();
+      } while (q.b == b && q.row0 == row0 && q.s != 0);
+      // a token without a route in this block takes nothing from it, not even a NaN of
+      // its weights
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i)
-            if (hfc[n][i & 1]) acc[n][i] = fmaf(w[n][i & 1] * gs, blk[n][i], acc[n][i]);
-        q.s = 0;
-        ++q.b;
-      }
-      if (more && p.h_bufs > 1) {
-        hb ^= 1;
-        store_h(nx, hbuf + hb * p.h_bytes);
-        __syncthreads();
-      }
-      cur = nx;
+        for (int i = 0; i < 4; ++i)
+          if ((m >> (8 * n + 2 * t + (i & 1))) & 1u) acc[n][i] = fmaf(w[n][i & 1] * gs, blk[n][i], acc[n][i]);
     }
-    float* mine = part + ((buf * kWarps + warp) * 32 + lane) * (4 * NG);
+    if (row0 > row_lo) __syncthreads();  // the tile before has read its sums
+    float* mine = part + (warp * 32 + lane) * (4 * NG);
 #pragma unroll
     for (int n = 0; n < NG; ++n)
       *reinterpret_cast<float4*>(mine + 4 * n) = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
@@ -850,18 +811,17 @@ __global__ void __launch_bounds__(kThreads) __maxnreg__(NG == 1 ? 144 : 208) few
     for (int i = tid; i < kRowTile * p.T; i += kThreads) {
       const int r16 = i & 15, tok = i >> 4;
       if (row0 + r16 >= row_hi) continue;
-      const float* v = part + (buf * kWarps * 32 + (r16 & 7) * 4 + (tok & 7) / 2) * (4 * NG) + (tok >> 3) * 4 +
-                       (r16 >> 3) * 2 + (tok & 1);
+      const float* v = part + ((r16 & 7) * 4 + (tok & 7) / 2) * (4 * NG) + (tok >> 3) * 4 + (r16 >> 3) * 2 + (tok & 1);
       float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += v[w * 32 * 4 * NG];
+      for (int w = 0; w < W; ++w) s += v[w * 32 * 4 * NG];
       p.out[(int64_t)tok * p.H + row0 + r16] = (uint16_t)f32_bf16(s);
     }
   }
 }
 
 // ------------------------------------------------------------------ launches
-constexpr size_t kSmemMost = 227 * 1024 - 3 * 1024;  // beside the kernels' static shared memory
+constexpr size_t kSmemMost = 227 * 1024 - 5 * 1024;  // beside the kernels' static shared memory
 
 template <int WF>
 int x_stride(int H) {
@@ -870,54 +830,47 @@ int x_stride(int H) {
   return ceil_div(H, F::kStepK) * F::kStepK * 2 + F::kXPad;
 }
 
-template <int WF, int NG, int S>
+template <int WF, int NG, int W, int KS, int S>
 size_t up_smem(int T, int k, int H) {
   using F = Fmt<WF>;
-  return (size_t)kWarps * S * entry_bytes<WF>() + 2 * kThreads * 32 * NG + (size_t)T * x_stride<WF>(H) +
+  return (size_t)W * S * entry_bytes<WF>() + (KS > 1 ? 2 * W * 32 * 16 * NG : 0) + (size_t)T * x_stride<WF>(H) +
          (F::kF16 ? 4 * T * ceil_div(H, F::kStepK) : 0) + tables_bytes(T * k, NG);
 }
 
-template <int WF, int NG, int S>
+template <int WF, int NG, int W, int KS, int S>
 int launch_up(const FewParams& p, cudaStream_t stream) {
-  const size_t smem = up_smem<WF, NG, S>(p.T, p.k, p.H);
-  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(few_up_kernel<WF, NG, S>), smem,
+  const size_t smem = up_smem<WF, NG, W, KS, S>(p.T, p.k, p.H);
+  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(few_up_kernel<WF, NG, W, KS, S>), smem,
                                 "few_up_kernel: shared memory limit");
   if (rc) return rc;
   const int64_t units = (int64_t)p.T * p.k * (p.I / 8);  // at most
-  launch_kernel(few_up_kernel<WF, NG, S>, (int)std::min<int64_t>(num_sms(), units), kThreads, smem, stream, p);
+  launch_kernel(few_up_kernel<WF, NG, W, KS, S>, (int)std::min<int64_t>(num_sms(), units), W * 32, smem, stream, p);
   OES_CHECK_LAUNCH("few_up_kernel");
   return OES_OK;
 }
 
+#ifndef OES_V
+#define OES_V 0
+#endif
 // One group of tokens: both kernels.
 template <int WF, int NG>
 int launch_few(FewParams p, cudaStream_t stream) {
-  constexpr int S = 4;
   p.x_ld = x_stride<WF>(p.H);
-  const int rc = up_smem<WF, NG, S>(p.T, p.k, p.H) <= kSmemMost ? launch_up<WF, NG, S>(p, stream)
-                                                                : launch_up<WF, NG, 2>(p, stream);
+  const int64_t units = (int64_t)p.T * p.k * (p.I / 8);  // of few_up, at most
+  int rc;
+  if (up_smem<WF, NG, 16, 1, 3>(p.T, p.k, p.H) > kSmemMost) rc = launch_up<WF, NG, 8, 8, 2>(p, stream);
+  else if (OES_V == 1 && NG == 1 && units <= 8 * num_sms()) rc = launch_up<WF, NG, 8, 8, 5>(p, stream);
+  else if (OES_V == 2 && NG == 1 && units <= 8 * num_sms()) rc = launch_up<WF, NG, 8, 1, 5>(p, stream);
+  else rc = launch_up<WF, NG, 16, 1, 3>(p, stream);
   if (rc) return rc;
-  // every block's routes (one of each token at most) fit a buffer
-  using F = Fmt<WF>;
-  constexpr int parts = F::kF16 ? 1 : 2, step = F::kStepK / 8, most = kHPieces * kThreads;
-  const int ns = ceil_div(p.I, F::kStepK);
-  p.k_steps = std::min(ns, most / (p.T * step));
-  auto group_bytes = [&](int kn) {  // of the routes over kn steps
-    const int rows = std::min(p.T * p.k, most / (kn * step));
-    return rows * (parts * (kn * step + 1) * 16 + (F::kF16 ? 4 * kn : 0));
-  };
-  p.h_bytes = group_bytes(p.k_steps);
-  if (ns % p.k_steps) p.h_bytes = std::max(p.h_bytes, group_bytes(ns % p.k_steps));
-  p.h_bytes = (p.h_bytes + 15) / 16 * 16;
-  // one buffer where it holds the whole of h
-  p.h_bufs = p.k_steps == ns && p.T * p.k * ns * step <= most ? 1 : 2;
-  const size_t smem = (size_t)kWarps * S * entry_bytes<WF>() + 2 * kThreads * 16 * NG + (size_t)p.h_bufs * p.h_bytes +
+  constexpr int W = 16, S = 3;
+  const size_t smem = (size_t)W * (S * entry_bytes<WF>() + hold_bytes<WF, NG>()) + W * 32 * 16 * NG +
                       tables_bytes(p.T * p.k, NG);
-  const int rc2 = set_max_dynamic_smem(reinterpret_cast<const void*>(few_down_kernel<WF, NG, S>), smem,
-                                       "few_down_kernel: shared memory limit");
-  if (rc2) return rc2;
+  rc = set_max_dynamic_smem(reinterpret_cast<const void*>(few_down_kernel<WF, NG, W, S>), smem,
+                            "few_down_kernel: shared memory limit");
+  if (rc) return rc;
   p.rows_cta = ceil_div(p.H, num_sms());
-  launch_kernel(few_down_kernel<WF, NG, S>, ceil_div(p.H, p.rows_cta), kThreads, smem, stream, p);
+  launch_kernel(few_down_kernel<WF, NG, W, S>, ceil_div(p.H, p.rows_cta), W * 32, smem, stream, p);
   OES_CHECK_LAUNCH("few_down_kernel");
   return OES_OK;
 }
@@ -926,7 +879,7 @@ int launch_few(FewParams p, cudaStream_t stream) {
 template <int WF>
 int group_tokens(int T, int k, int H) {
   int n = T;
-  while (n > 1 && (n > 8 ? up_smem<WF, 2, 2>(n, k, H) : up_smem<WF, 1, 2>(n, k, H)) > kSmemMost) --n;
+  while (n > 1 && (n > 8 ? up_smem<WF, 2, 8, 8, 2>(n, k, H) : up_smem<WF, 1, 8, 8, 2>(n, k, H)) > kSmemMost) --n;
   return n;
 }
 
