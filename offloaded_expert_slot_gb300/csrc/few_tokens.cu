@@ -73,6 +73,7 @@ __host__ __device__ constexpr int cdiv(int a, int b) { return (a + b - 1) / b; }
 constexpr int kMaxTokens = 16;    // of a call
 constexpr int kFusedExperts = 512;  // most experts that the kernels route themselves
 constexpr int kRowTile = 16;
+constexpr int W = 16;  // warps of a CTA
 
 // Weight formats.  A step is what a warp takes from its queue at a time: kStepK
 // values of 16 rows, kChunks x 16 bytes a lane, the step's scales behind them; of
@@ -118,116 +119,264 @@ struct FewParams {
   uint16_t* out;
   int32_t* status;
   int64_t s13, w2, s2, gs;  // sections of an expert row
+  uint8_t* tables;          // from few_up to few_down: the number of blocks, and 16 bytes on the tables
   int x_ld;                 // bytes of a row of x in shared memory
   int rows_cta;             // few_down: rows of out a CTA owns
 };
 
-// The chunk's tables, in shared memory.
+// The chunk's tables, in shared memory.  A block's first route leads it.
 struct Tables {
   int32_t* ids;    // [R]
   float* w;        // [R]
   int32_t* lead;   // [R] first route of the route's block, -1 for one that does not count
   int32_t* blk;    // [R] block of a leading route
-  int32_t* slot;   // [R] by block
-  int16_t* route;  // [blocks][8 NG] route of each token in a block, or -1
+  int32_t* slot;   // [blocks]
+  uint32_t* has;   // [blocks] which tokens have a route in the block
+  int16_t* route;  // [blocks][8 NG] route of each token in the block, or -1
   int16_t* order;  // [R] few_down: the routes that count, block after block
-  int16_t* cum;    // [blocks + 1] few_down: a block's first place there
-  uint16_t* has;   // [blocks] few_down: which tokens have a route in a block
+  int16_t* cum;    // [blocks] few_down: a block's first place there
   __device__ __forceinline__ Tables(uint8_t* base, int R, int ng) {
     ids = reinterpret_cast<int32_t*>(base);
     w = reinterpret_cast<float*>(ids + R);
     lead = reinterpret_cast<int32_t*>(w + R);
     blk = lead + R;
     slot = blk + R;
-    route = reinterpret_cast<int16_t*>(slot + R);
+    has = reinterpret_cast<uint32_t*>(slot + R);
+    route = reinterpret_cast<int16_t*>(has + R);
     order = route + R * 8 * ng;
     cum = order + R;
-    has = reinterpret_cast<uint16_t*>(cum + R + 1);
   }
 };
-__host__ __device__ constexpr int tables_bytes(int R, int ng) { return R * (26 + 16 * ng) + 4; }
+__host__ __device__ constexpr int tables_bytes(int R, int ng) { return (R * (28 + 16 * ng) + 15) / 16 * 16; }
+
+// One token's top-k by one warp, the ids and weights of topk_row_filtered bit for bit
+// (the same threshold, the same order of the candidates, topk_write), made for a single
+// row's latency: candidates find their places by ballots instead of a counter in
+// shared memory, whose round trips a lone warp has nothing to hide behind, and rank
+// themselves against broadcasts.  E <= 512; cand: 32 entries of the warp's own.
+template <typename LT>
+__device__ __forceinline__ void topk_few(const LT* __restrict__ row, int E, int k, int lane, int32_t* ids, float* w,
+                                         uint64_t* cand) {
+  constexpr int Q = kFusedExperts / 32;
+  float v[Q];
+#pragma unroll
+  for (int j = 0; j < Q; ++j) {
+    v[j] = __int_as_float(0x7fffffff);  // NaN: no expert
+    if (lane + 32 * j < E) load_logits<1>(row + lane + 32 * j, v + j);
+  }
+  float m = -INFINITY;  // fmaxf skips NaN
+#pragma unroll
+  for (int j = 0; j < Q; ++j) m = fmaxf(m, v[j]);
+  // the lane maxima in descending order; tau the k-th
+#pragma unroll
+  for (int size = 2; size <= 32; size <<= 1)
+#pragma unroll
+    for (int d = size >> 1; d > 0; d >>= 1) {
+      const float o = __shfl_xor_sync(0xffffffffu, m, d);
+      m = (((lane & d) == 0) == ((lane & size) == 0)) ? fmaxf(m, o) : fminf(m, o);
+    }
+  const float tau = __shfl_sync(0xffffffffu, m, k - 1);
+  int n = 0;
+  if (tau > -INFINITY) {
+#pragma unroll
+    for (int j = 0; j < Q; ++j) {
+      const uint32_t at = __ballot_sync(0xffffffffu, v[j] >= tau);
+      const int place = n + __popc(at & ((1u << lane) - 1));
+      if (v[j] >= tau && place < 32)  // larger key first, then the lower id
+        cand[place] = ((uint64_t)logit_key(v[j]) << 32) | (uint32_t)~(lane + 32 * j);
+      n += __popc(at);
+    }
+  }
+  if (n == 0 || n > 32) {  // few numbers above -inf, or many equal ones: in rounds
+    uint32_t key[Q];
+#pragma unroll
+    for (int j = 0; j < Q; ++j) key[j] = lane + 32 * j < E ? logit_key(v[j]) : 0u;
+    topk_rounds<Q, 1>(key, k, lane, ids, w);
+    return;
+  }
+  __syncwarp();
+  const uint64_t mine = lane < n ? cand[lane] : 0;
+  int r = 0;
+#pragma unroll 8
+  for (int c = 0; c < n; ++c) r += cand[c] > mine;
+  __syncwarp();
+  if (lane < n && r < k) cand[r] = mine;
+  __syncwarp();
+  const uint64_t won = lane < k ? cand[lane] : 0;
+  topk_write((uint32_t)(won >> 32), ~(uint32_t)won, k, lane, ids, w);
+}
 
 // Routing and tables, by the whole CTA; returns the number of blocks.  One CTA
-// writes the router's outputs and the status (`first`).
-template <int NG>
-__device__ int few_tables(const FewParams& p, const Tables& tb, bool first) {
-  __shared__ uint2 cand[kMaxTokens][33];
-  __shared__ int s_nb;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
-  const int R = p.T * p.k;
-  for (int i = tid; i < R * 4 * NG; i += nt) reinterpret_cast<int32_t*>(tb.route)[i] = -1;
-  if (p.logits) {
-    for (int t = warp; t < p.T; t += nt >> 5) {
+// writes the router's outputs and the status (`first`).  scratch: shared memory, one
+// word an expert, two with logits.  Beside the routing, the warps that have no token
+// run side(i, n), i of n threads (with a token for every warp, all do, behind it).
+template <int NG, typename Side>
+__device__ __forceinline__ int few_tables(const FewParams& p, const Tables& tb, uint8_t* scratch, bool first,
+                                          const Side& side) {
+  __shared__ uint64_t cand[kMaxTokens][32];
+  __shared__ int s_leads[OES_FEW_TOKENS_MAX * OES_MAX_TOPK / 32 + 1];
+  __shared__ int s_one;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x, nw = nt >> 5;
+  const int R = p.T * p.k, chunks = cdiv(R, 32);
+  int32_t* fst = reinterpret_cast<int32_t*>(scratch);  // [E] the first route to each expert
+  int32_t* map = fst + p.E;                            // [E] the slot map, with logits
+  const int routers = p.logits && p.T < nw ? p.T : 0;
+  auto init = [&](int i0, int n) {
+    for (int i = i0; i < p.E; i += n) {
+      fst[i] = 0x7FFFFFFF;
+      if (p.logits) cp_async4_take(smem_u32(map + i), p.e2s + i, true);
+    }
+    for (int i = i0; i < R * 4 * NG; i += n) reinterpret_cast<int32_t*>(tb.route)[i] = -1;
+    for (int i = i0; i < R; i += n) {
+      tb.has[i] = 0u;
+      if (!p.logits) {
+        tb.ids[i] = __ldcg(p.ids + i);
+        tb.w[i] = __ldcg(p.weights + i);
+      }
+    }
+    side(i0, n);
+  };
+  if (warp >= routers && routers > 0) {
+    init(tid - routers * 32, nt - routers * 32);
+  } else if (p.logits) {
+    for (int t = warp; t < p.T; t += nw) {
       int32_t* ids = tb.ids + t * p.k;
       float* w = tb.w + t * p.k;
       if (p.logits_bf16)
-        topk_row_filtered<1, kFusedExperts / 32>(static_cast<const L2Bf16*>(p.logits) + (size_t)t * p.E, p.E, p.k,
-                                                 lane, ids, w, cand[warp]);
+        topk_few(static_cast<const L2Bf16*>(p.logits) + (size_t)t * p.E, p.E, p.k, lane, ids, w, cand[warp]);
       else
-        topk_row_filtered<1, kFusedExperts / 32>(static_cast<const L2F32*>(p.logits) + (size_t)t * p.E, p.E, p.k,
-                                                 lane, ids, w, cand[warp]);
-    }
-  } else {
-    for (int r = tid; r < R; r += nt) {
-      tb.ids[r] = __ldcg(p.ids + r);
-      tb.w[r] = __ldcg(p.weights + r);
+        topk_few(static_cast<const L2F32*>(p.logits) + (size_t)t * p.E, p.E, p.k, lane, ids, w, cand[warp]);
     }
   }
+  if (routers == 0) init(tid, nt);
+  cp_async_wait<0>();
   __syncthreads();
+  if (p.logits && p.T == 1) {
+    // one token, distinct experts: where all have slots, block r is route r
+    if (warp == 0) {
+      const int e = lane < R ? tb.ids[lane] : 0;
+      const int slot = lane < R ? map[e] : 0;
+      const bool all = __all_sync(0xffffffffu, slot >= 0 && slot < p.S);
+      if (all && lane < R) {
+        tb.slot[lane] = slot;
+        tb.lead[lane] = tb.blk[lane] = lane;
+        tb.has[lane] = 1u;
+        tb.route[lane * 8 * NG] = (int16_t)lane;
+        if (first) {
+          p.ids[lane] = e;
+          p.weights[lane] = tb.w[lane];
+        }
+      }
+      if (lane == 0) s_one = all;
+    }
+    __syncthreads();
+    if (s_one) return R;
+  }
   for (int r = tid; r < R; r += nt) {
     const int e = tb.ids[r];
-    const int t = r / p.k;
-    int lead = -1;
     if (first && p.logits) {
       p.ids[r] = e;
       p.weights[r] = tb.w[r];
     }
+    int n = -1;  // this is the token's route number n to e
     if (e >= 0 && e < p.E) {
-      const int slot = __ldcg(p.e2s + e);
+      const int slot = p.logits ? map[e] : __ldcg(p.e2s + e);
       if (slot >= 0 && slot < p.S) {
-        // this is the token's route number n to e; the block's first route is the
-        // first token's that has as many
-        int n = 0;
-        for (int i = t * p.k; i < r; ++i) n += tb.ids[i] == e;
-        lead = r;
-        for (int u = 0; u < t && lead == r; ++u) {
-          int m = 0;
-          for (int i = u * p.k; i < (u + 1) * p.k; ++i)
-            if (tb.ids[i] == e && m++ == n) {
-              lead = i;
-              break;
-            }
-        }
+        n = 0;
+        if (!p.logits)
+          for (int i = r / p.k * p.k; i < r; ++i) n += tb.ids[i] == e;
+        if (n == 0) atomicMin(&fst[e], r);
         tb.blk[r] = slot;  // a leading route's, until the blocks are numbered
       } else if (first) {
         set_status(p.status, OES_DEV_BAD_ID);
       }
     }
-    tb.lead[r] = lead;
+    tb.lead[r] = n;
   }
   __syncthreads();
-  if (warp == 0) {
-    int n = 0;
-    for (int r0 = 0; r0 < R; r0 += 32) {
-      const int r = r0 + lane;
-      const bool is = r < R && tb.lead[r] == r;
-      const uint32_t m = __ballot_sync(0xffffffffu, is);
-      if (is) {
-        const int b = n + __popc(m & ((1u << lane) - 1));
-        tb.slot[b] = tb.blk[r];
-        tb.blk[r] = b;
+  // the block's first route is the first token's that has as many to e
+  for (int c = warp; c < chunks; c += nw) {
+    const int r = c * 32 + lane;
+    int lead = -1;
+    if (r < R) {
+      const int n = tb.lead[r];
+      if (n >= 0) {
+        const int e = tb.ids[r];
+        lead = r;
+        if (n == 0) {
+          lead = fst[e];
+        } else {
+          for (int u = 0; u < r / p.k && lead == r; ++u) {
+            int m = 0;
+            for (int i = u * p.k; i < (u + 1) * p.k; ++i)
+              if (tb.ids[i] == e && m++ == n) {
+                lead = i;
+                break;
+              }
+          }
+        }
       }
-      n += __popc(m);
+      tb.lead[r] = lead;
     }
-    if (lane == 0) s_nb = n;
+    const uint32_t m = __ballot_sync(0xffffffffu, r < R && lead == r);
+    if (lane == 0) s_leads[c] = __popc(m);
+  }
+  __syncthreads();
+  for (int c = warp; c < chunks; c += nw) {
+    const int r = c * 32 + lane;
+    const bool is = r < R && tb.lead[r] == r;
+    const uint32_t m = __ballot_sync(0xffffffffu, is);
+    const int before = __reduce_add_sync(0xffffffffu, lane < c ? s_leads[lane] : 0);
+    if (is) {
+      const int b = before + __popc(m & ((1u << lane) - 1));
+      tb.slot[b] = tb.blk[r];
+      tb.blk[r] = b;
+    }
   }
   __syncthreads();
   for (int r = tid; r < R; r += nt) {
     const int lead = tb.lead[r];
-    if (lead >= 0) tb.route[tb.blk[lead] * 8 * NG + r / p.k] = (int16_t)r;
+    if (lead >= 0) {
+      const int b = tb.blk[lead], t = r / p.k;
+      tb.route[b * 8 * NG + t] = (int16_t)r;
+      atomicOr(&tb.has[b], 1u << t);
+    }
   }
   __syncthreads();
-  return s_nb;
+  int nb = 0;
+  for (int c = 0; c < chunks; ++c) nb += s_leads[c];
+  return nb;
+}
+
+// The routes that count in the order of their blocks, for few_down.
+template <int NG>
+__device__ void few_order(const FewParams& p, const Tables& tb, int nb) {
+  __shared__ int s_sums[OES_FEW_TOKENS_MAX * OES_MAX_TOPK / 32 + 1];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, nt = blockDim.x;
+  const int chunks = cdiv(nb, 32), nw = nt >> 5;
+  for (int c = warp; c < chunks; c += nw) {
+    const int b = c * 32 + lane;
+    const int n = b < nb ? __popc(tb.has[b]) : 0;
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += u;
+    }
+    if (b < nb) tb.cum[b] = (int16_t)(sum - n);
+    if (lane == 31) s_sums[c] = sum;
+  }
+  __syncthreads();
+  for (int c = warp; c < chunks; c += nw) {
+    const int before = __reduce_add_sync(0xffffffffu, lane < c ? s_sums[lane] : 0);
+    if (c * 32 + lane < nb) tb.cum[c * 32 + lane] += (int16_t)before;
+  }
+  __syncthreads();
+  for (int i = tid; i < nb * 8 * NG; i += nt) {
+    const int b = i / (8 * NG), t = i % (8 * NG), r = tb.route[i];
+    if (r >= 0) tb.order[tb.cum[b] + __popc(tb.has[b] & ((1u << t) - 1))] = (int16_t)r;
+  }
+  __syncthreads();
 }
 
 // The matrix instructions of half a step: the lane's weights from its queue entry,
@@ -340,11 +489,11 @@ __device__ __forceinline__ float f16_group(const float (&v)[8], uint4& out) {
 
 // ------------------------------------------------------------------ gate, up
 // A unit is 8 rows of I of a block.  The chunk's units are dealt out to the CTAs in
-// runs.  KS 1: each warp takes units of its own, and a lane ends with both factors of
-// its h; no barrier after the tables.  KS W: the CTA's warps share the K range of a unit
-// and add their sums, for chunks with few units (see launch_few).
-template <int WF, int NG, int W, int KS, int S>
-__global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_up_kernel(const FewParams p) {
+// runs, and a CTA's to its teams of KS warps, which share the unit's K range.  KS 1: a
+// lane ends with both factors of its h, and no barrier follows the tables.  More where
+// there are few units (see launch_few): one warp has 16 KB in flight at most.
+template <int WF, int NG, int KS, int S>
+__global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
   using F = Fmt<WF>;
   constexpr int kThreads = W * 32;
   constexpr int kEntry = entry_bytes<WF>();
@@ -360,33 +509,34 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_up_kernel(const Fe
   pdl_trigger();  // the down kernel; it reads what this kernel waited for, and h after this kernel's end
   // x, with zeros up to a whole step
   const int xc = ns * (F::kStepK / 8);
-  for (int i0 = 0; i0 < p.T * xc; i0 += kThreads) {
-    const int i = i0 + tid, tok = i / xc, c = i - tok * xc;
-    const bool live = i < p.T * xc, in = live && c * 8 < p.H;
-    const uint16_t* src = p.x + (in ? (size_t)tok * p.H + c * 8 : 0);
-    uint8_t* dst = xs + tok * p.x_ld + c * 16;
-    if constexpr (F::kF16) {
-      float v[8];
+  auto load_x = [&](int first, int n) {
+    for (int i0 = first & ~31; i0 < p.T * xc; i0 += n) {
+      const int i = i0 + lane, tok = i / xc, c = i - tok * xc;
+      const bool live = i < p.T * xc, in = live && c * 8 < p.H;
+      const uint16_t* src = p.x + (in ? (size_t)tok * p.H + c * 8 : 0);
+      uint8_t* dst = xs + tok * p.x_ld + c * 16;
+      if constexpr (F::kF16) {
+        float v[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-      if (in) load_vals<8>(src, v);
-      uint4 o;
-      const float f = f16_group(v, o);
-      if (live) {
-        *reinterpret_cast<uint4*>(dst) = o;
-        if ((c & 15) == 0) xf[tok * ns + (c >> 4)] = f;
+        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
+        if (in) load_vals<8>(src, v);
+        uint4 o;
+        const float f = f16_group(v, o);
+        if (live) {
+          *reinterpret_cast<uint4*>(dst) = o;
+          if ((c & 15) == 0) xf[tok * ns + (c >> 4)] = f;
+        }
+      } else if (live) {
+        cp_async16_take(smem_u32(dst), src, in);
       }
-    } else if (live) {
-      cp_async16_take(smem_u32(dst), src, in);
     }
-  }
-  cp_async_commit();
-  const int nb = few_tables<NG>(p, tb, blockIdx.x == 0);
+  };
+  const int nb = few_tables<NG>(p, tb, smem, blockIdx.x == 0, load_x);
   const int per = p.I / 8, units = nb * per;
   const int lo = (int)((int64_t)blockIdx.x * units / gridDim.x), hi = (int)((int64_t)(blockIdx.x + 1) * units / gridDim.x);
   const int row = p.H * F::kRowBytes / F::kStepK;  // bytes of a weight row
-  constexpr int kNext = KS > 1 ? 1 : W;            // to the warp's next unit
-  const int s0 = KS > 1 ? warp : 0;
+  constexpr int kNext = W / KS;  // to the team's next unit
+  const int team = warp / KS, s0 = warp % KS;
 
   // A place in the warp's units: unit j, rows 8 r of block b
   struct Place {
@@ -400,7 +550,7 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_up_kernel(const Fe
       ++q.b;
     }
   };
-  Place q{lo + (KS > 1 ? 0 : warp), 0, 0};
+  Place q{lo + team, 0, 0};
   q.b = q.j / per;
   q.r = q.j - q.b * per;
 
@@ -443,8 +593,13 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_up_kernel(const Fe
     at = at + 1 == S ? 0 : at + 1;
   };
   for (int i = 0; i < S; ++i) copy_next();
-  cp_async_wait<S>();  // x
-  __syncthreads();
+  if (blockIdx.x == 0) {
+    // the tables, for the down kernel
+    few_order<NG>(p, tb, nb);
+    if (tid == 0) *reinterpret_cast<int32_t*>(p.tables) = nb;
+    for (int i = tid; i < tables_bytes(p.T * p.k, NG) / 4; i += kThreads)
+      reinterpret_cast<int32_t*>(p.tables + 16)[i] = tb.ids[i];
+  }
 
   // columns past the tokens are not used: any row does
   uint32_t xb[NG], xfc[NG][2];
@@ -466,11 +621,14 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_up_kernel(const Fe
       cp_async_wait<S - 1>();
       if (F::kScale) __syncwarp();  // scales that other lanes copied
       const uint32_t e = smem_u32(queue + from * kEntry);
-      float d[NG][4];
+      float d[NG][4], d1[NG][4];  // two chains of instructions
 #pragma unroll
       for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) d[n][i] = F::kF16 ? 0.0f : acc[n][i];
+        for (int i = 0; i < 4; ++i) {
+          d[n][i] = F::kF16 ? 0.0f : acc[n][i];
+          d1[n][i] = 0.0f;
+        }
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
         uint4 B[NG][F::kB];
@@ -479,8 +637,12 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_up_kernel(const Fe
 #pragma unroll
           for (int i = 0; i < F::kB; ++i)
             B[n][i] = lds128(xb[n] + 2 * (s * F::kStepK + piece_k<WF>(hh, i) - piece_k<WF>(0, 0)));
-        half_mma<WF, NG, false>(e, hh, B, B, d);
+        half_mma<WF, NG, false>(e, hh, B, B, hh ? d1 : d);
       }
+#pragma unroll
+      for (int n = 0; n < NG; ++n)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[n][i] += d1[n][i];
       if constexpr (F::kF16) {
         float sg = 1.0f, su = 1.0f;
         if constexpr (WF == OES_WFMT_FP8) {
@@ -522,14 +684,15 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_up_kernel(const Fe
       for (int n = 0; n < NG; ++n)
         *reinterpret_cast<float4*>(mine + 4 * n) =
             make_float4(gs * acc[n][0], gs * acc[n][1], gs * acc[n][2], gs * acc[n][3]);
-      __syncthreads();
-      if (tid < 64 * NG) {
-        const int col = tid >> 3, r8 = tid & 7, r = tb.route[q.b * 8 * NG + col];
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(KS * 32) : "memory");
+      const int tt = tid - team * KS * 32;
+      if (tt < 64 * NG) {
+        const int col = tt >> 3, r8 = tt & 7, r = tb.route[q.b * 8 * NG + col];
         if (r >= 0) {
-          const float* v = part + (buf * W * 32 + r8 * 4 + (col & 7) / 2) * (4 * NG) + (col >> 3) * 4 + (col & 1);
+          const float* v = part + ((buf * W + team * KS) * 32 + r8 * 4 + (col & 7) / 2) * (4 * NG) + (col >> 3) * 4 + (col & 1);
           float gate = 0.0f, upv = 0.0f;
 #pragma unroll
-          for (int w = 0; w < W; ++w) {
+          for (int w = 0; w < KS; ++w) {
             gate += v[w * 32 * 4 * NG];
             upv += v[w * 32 * 4 * NG + 2];
           }
@@ -541,67 +704,71 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_up_kernel(const Fe
 }
 
 // ---------------------------------------------------------------------- down
-// Launched early: every CTA of few_up_kernel has passed its own wait then, so all
-// that was written before it (logits, routes, the slot map, x, the pool) is
-// complete, and this kernel reads it through L2 without waiting.  h is
-// few_up_kernel's, and is read after the wait.
-//
 // The (block, step of K) of a tile of rows are dealt out to the CTA's warps in runs.
-// For each, the warp brings the rows of h of the block's tokens into a place of its own
-// in shared memory, in the form that the instructions take; they are loaded into
-// registers while the step before is multiplied (the first kHold of them: few
-// blocks have more).  (Loaded by each lane as it needs them, their latency set the
-// pace, 16 tokens x 10 of 200 bf16 experts ran at 1.9 TB/s; staged by the CTA for several
-// blocks at a time, the barriers and the bookkeeping did.)
-constexpr int kHold = 4;  // rows of h
+// The rows of h of a step's tokens come through the warp's queue too, in fp32, the
+// first kRing of them (few blocks have more; those are loaded when they are needed),
+// and are put into the form that the instructions take where they lie.  (Loaded by
+// each lane as it needs them, their latency set the pace: 16 tokens x 10 of 200 bf16
+// experts ran at 1.9 TB/s; one step ahead, 4 tokens x 10 of 512 NVFP4 experts at 2.2.
+// Staged by the CTA for several blocks at a time, barriers and bookkeeping did.)
+constexpr int kRing = 2;  // rows of h of a step in the queue
 
-template <int WF, int NG>
-__host__ __device__ constexpr int hold_bytes() {  // a warp's place for h: rows, then factors
-  using F = Fmt<WF>;
-  return 8 * NG * ((F::kF16 ? 1 : 2) * (F::kStepK * 2 + 16) + (F::kF16 ? 16 : 0));
+// A row of h: kRow bytes, fp32 or in its form; kLine bytes of its form alone, in parts
+// kPart apart (bf16 rows have two), which spread over the banks.
+template <int WF>
+struct HRow {
+  static constexpr int kParts = Fmt<WF>::kF16 ? 1 : 2;
+  static constexpr int kPart = Fmt<WF>::kStepK * 2 + 16, kLine = kParts * kPart;
+  static constexpr int kRow = Fmt<WF>::kF16 ? Fmt<WF>::kStepK * 4 + 16 : kLine;
+};
+template <int WF, int NG, int S>
+__host__ __device__ constexpr int down_warp_bytes() {  // queue, rows of h in it, further rows, factors
+  return S * (entry_bytes<WF>() + kRing * HRow<WF>::kRow) + (8 * NG - kRing) * HRow<WF>::kLine + 32 * NG;
 }
 
-template <int WF, int NG, int W, int S>
-__global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_down_kernel(const FewParams p) {
+template <int WF, int NG, int S>
+__global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) {
   using F = Fmt<WF>;
   constexpr int kThreads = W * 32;
   constexpr int kEntry = entry_bytes<WF>();
-  constexpr int kParts = F::kF16 ? 1 : 2;
-  constexpr int kPart = F::kStepK * 2 + 16, kLine = kParts * kPart;  // a row of h: its parts a bank's width apart
-  constexpr int kRowLanes = F::kStepK / 8, kRowsAt = 32 / kRowLanes;  // lanes a row, rows a pass
+  constexpr int kParts = HRow<WF>::kParts, kPart = HRow<WF>::kPart, kLine = HRow<WF>::kLine, kRow = HRow<WF>::kRow;
+  constexpr int kRowLanes = F::kStepK / 8, kRowsAt = 32 / kRowLanes;  // 8 values a lane: lanes a row, rows at a time
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  uint8_t* queue = smem + warp * (S * kEntry);
-  uint8_t* hrows = smem + W * S * kEntry + warp * hold_bytes<WF, NG>();
-  float* hf = reinterpret_cast<float*>(hrows + 8 * NG * kLine);  // factors (kF16)
-  float* part = reinterpret_cast<float*>(smem + W * (S * kEntry + hold_bytes<WF, NG>()));  // [warp][lane][4 NG]
+  uint8_t* queue = smem + warp * down_warp_bytes<WF, NG, S>();
+  uint8_t* ring = queue + S * kEntry;                    // [S][kRing] rows of h
+  uint8_t* more = ring + S * kRing * kRow;               // rows past those
+  float* hf = reinterpret_cast<float*>(more + (8 * NG - kRing) * kLine);  // factors (kF16)
+  float* part = reinterpret_cast<float*>(smem + W * down_warp_bytes<WF, NG, S>());  // [warp][lane][4 NG]
   const Tables tb(reinterpret_cast<uint8_t*>(part + kThreads * 4 * NG), p.T * p.k, NG);
-  const int nb = few_tables<NG>(p, tb, false);
+  pdl_wait();
+  // The tables as few_up_kernel left them.  A workspace that another call writes at the
+  // same time would be a mistake of the caller's, which no address may follow: whatever
+  // stands here, indexes are kept within their ranges.
+  const int R = p.T * p.k, nb = min(max(__ldcg(reinterpret_cast<const int32_t*>(p.tables)), 0), R);
+  for (int i = tid; i < tables_bytes(R, NG) / 16; i += kThreads)
+    reinterpret_cast<int4*>(tb.ids)[i] = __ldcg(reinterpret_cast<const int4*>(p.tables + 16) + i);
+  __syncthreads();
+  for (int i = tid; i < nb; i += kThreads) {
+    if ((uint32_t)tb.slot[i] >= (uint32_t)p.S) tb.slot[i] = 0;
+    tb.has[i] &= (1u << p.T) - 1u;
+    tb.cum[i] = (int16_t)min(max((int)tb.cum[i], 0), R - __popc(tb.has[i]));
+  }
+  for (int i = tid; i < R; i += kThreads)
+    if ((uint32_t)tb.order[i] >= (uint32_t)R) tb.order[i] = 0;
+  for (int i = tid; i < nb * 8 * NG; i += kThreads)
+    if (tb.route[i] >= R) tb.route[i] = 0;
+  __syncthreads();
   const int row = p.I * F::kRowBytes / F::kStepK;
   const int ns = cdiv(p.I, F::kStepK);
   const int row_lo = blockIdx.x * p.rows_cta, row_hi = min(p.H, row_lo + p.rows_cta);
-  if (warp == 0) {  // the order of the routes that count
-    int n = 0;
-    for (int b = 0; b < nb; ++b) {
-      const int r = lane < 8 * NG ? tb.route[b * 8 * NG + lane] : -1;
-      const uint32_t m = __ballot_sync(0xffffffffu, r >= 0);
-      if (lane == 0) {
-        tb.cum[b] = (int16_t)n;
-        tb.has[b] = (uint16_t)m;
-      }
-      if (r >= 0) tb.order[n + __popc(m & ((1u << lane) - 1))] = (int16_t)r;
-      n += __popc(m);
-    }
-    if (lane == 0) tb.cum[nb] = (int16_t)n;
-  }
-  __syncthreads();
 
   // A place in the warp's run of a tile: i of [.., i1), step s of block b
   const int n_all = nb * ns, i0 = (int)((int64_t)warp * n_all / W), i1 = (int)((int64_t)(warp + 1) * n_all / W);
   struct Place {
     int i, b, s, row0;
   };
-  Place start{i0, i0 / max(ns, 1), 0, i0 < i1 ? row_lo : row_hi};
+  Place start{i0, i0 / ns, 0, i0 < i1 ? row_lo : row_hi};
   start.s = i0 - start.b * ns;
   auto next = [&](Place& q) {
     if (++q.s == ns) {
@@ -629,22 +796,37 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_down_kernel(const 
     ok1 = c.row0 + g + 8 < row_hi;
   };
   set_rows();
+  auto copy_w = [&]() {
+    const uint32_t e = smem_u32(queue + at * kEntry);
+    step_copy<WF>(e, p.pool, w0, w0 + 8 * row, ok0, ok1, c.s * F::kRowBytes, row);
+    if constexpr (WF == OES_WFMT_FP8) {
+      const int r = c.row0 + lane;
+      if (lane < kRowTile)
+        cp_async4_take(e + 2048 + 4 * lane, base + p.s2 + ((int64_t)(r < row_hi ? r >> 7 : 0) * ns + c.s) * 4, r < row_hi);
+    }
+    if constexpr (WF == OES_WFMT_NVFP4) {
+      const int r = c.row0 + (lane & 15), k64 = 2 * c.s + (lane >> 4);
+      const bool in = r < row_hi && k64 * 64 < p.I;
+      cp_async4_take(e + 1024 + 4 * lane, base + p.s2 + (in ? (int64_t)k64 * p.H + r : 0) * 4, in);
+      if (lane == 0) cp_async4_take(e + 1024 + 128, base + p.gs + 4, true);
+    }
+  };
+  // the first kRing rows of h of place q, zeros past I and for rows that are not
+  auto copy_h = [&](const Place& q, int slot) {
+    const int first = tb.cum[q.b], n = __popc(tb.has[q.b]);
+    constexpr int kLanes = F::kStepK / 4;  // 16 bytes a lane
+#pragma unroll
+    for (int j = 0; j < kRing; j += 32 / kLanes) {
+      const int rw = j + lane / kLanes, k = q.s * F::kStepK + lane % kLanes * 4;
+      const bool in = rw < n && k < p.I;
+      cp_async16_take(smem_u32(ring + (slot * kRing + rw) * kRow) + lane % kLanes * 16,
+                      p.h + (in ? (int64_t)tb.order[first + rw] * p.I + k : 0), in);
+    }
+  };
   auto copy_next = [&]() {
     if (c.row0 < row_hi) {
-      const uint32_t e = smem_u32(queue + at * kEntry);
-      step_copy<WF>(e, p.pool, w0, w0 + 8 * row, ok0, ok1, c.s * F::kRowBytes, row);
-      if constexpr (WF == OES_WFMT_FP8) {
-        const int r = c.row0 + lane;
-        if (lane < kRowTile)
-          cp_async4_take(e + 2048 + 4 * lane, base + p.s2 + ((int64_t)(r < row_hi ? r >> 7 : 0) * ns + c.s) * 4,
-                         r < row_hi);
-      }
-      if constexpr (WF == OES_WFMT_NVFP4) {
-        const int r = c.row0 + (lane & 15), k64 = 2 * c.s + (lane >> 4);
-        const bool in = r < row_hi && k64 * 64 < p.I;
-        cp_async4_take(e + 1024 + 4 * lane, base + p.s2 + (in ? (int64_t)k64 * p.H + r : 0) * 4, in);
-        if (lane == 0) cp_async4_take(e + 1024 + 128, base + p.gs + 4, true);
-      }
+      copy_w();
+      copy_h(c, at);
       const int i = c.i;
       next(c);
       if (c.s == 0 || c.i != i + 1) set_rows();
@@ -654,28 +836,18 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_down_kernel(const 
   };
   for (int i = 0; i < S; ++i) copy_next();
 
-  // Row j of a place's block: 8 values of this lane, loaded and stored
-  constexpr int kPass = (kHold + kRowsAt - 1) / kRowsAt;
+  // 8 values of row j of the block to their form, at `to`
   const int hl = lane / kRowLanes, hp = lane % kRowLanes;
-  auto load_row = [&](const Place& q, int j, float (&v)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-    const int first = tb.cum[q.b], k = q.s * F::kStepK + hp * 8;
-    if (j < tb.cum[q.b + 1] - first && k < p.I) {
-      const float4* h = reinterpret_cast<const float4*>(p.h + (int64_t)tb.order[first + j] * p.I + k);
-      const float4 a = __ldcg(h), b = __ldcg(h + 1);
-      v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-      v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-    }
-  };
-  auto store_row = [&](int j, const float (&v)[8]) {
-    uint4* to = reinterpret_cast<uint4*>(hrows + j * kLine + hp * 16);
+  auto form = [&](const float (&v)[8], uint8_t* to, int j, bool live) {
+    uint4* o = reinterpret_cast<uint4*>(to + hp * 16);
     if constexpr (F::kF16) {
-      uint4 o;
-      const float f = f16_group(v, o);
-      *to = o;
-      if (hp == 0) hf[j] = f;
-    } else {
+      uint4 x;
+      const float f = f16_group(v, x);
+      if (live) {
+        *o = x;
+        if (hp == 0) hf[j] = f;
+      }
+    } else if (live) {
       uint32_t a[4], b[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -684,32 +856,38 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_down_kernel(const 
         // an infinity leaves nothing (and not the NaN of its difference)
         b[i] = f32x2_bf16x2(fabsf(x0) < INFINITY ? v[2 * i] - x0 : 0.0f, fabsf(x1) < INFINITY ? v[2 * i + 1] - x1 : 0.0f);
       }
-      to[0] = make_uint4(a[0], a[1], a[2], a[3]);
-      to[kPart / 16] = make_uint4(b[0], b[1], b[2], b[3]);
+      o[0] = make_uint4(a[0], a[1], a[2], a[3]);
+      o[kPart / 16] = make_uint4(b[0], b[1], b[2], b[3]);
     }
   };
-  float hv[kPass][8];
-  auto load_h = [&](const Place& q) {
-    if (q.row0 >= row_hi) return;
-#pragma unroll
-    for (int i = 0; i < kPass; ++i) load_row(q, i * kRowsAt + hl, hv[i]);
-  };
-  auto store_h = [&](const Place& q) {
-    const int n = tb.cum[q.b + 1] - tb.cum[q.b];
-#pragma unroll
-    for (int i = 0; i < kPass; ++i)
-      if (i * kRowsAt < n) store_row(i * kRowsAt + hl, hv[i]);
+  // all rows of h of place q: those in the queue where they lie, the others here
+  auto form_rows = [&](const Place& q, int slot) {
+    const int first = tb.cum[q.b], n = __popc(tb.has[q.b]);
+    uint8_t* rows = ring + slot * kRing * kRow;
+    float v[8];
+    const float4* raw = reinterpret_cast<const float4*>(rows + min(hl, kRing - 1) * kRow + hp * 32);
+    const float4 x = raw[0], y = raw[1];
+    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    __syncwarp();  // read by all before it is written over
+    form(v, rows + hl * kRow, hl, hl < kRing);
 #pragma unroll 1
-    for (int j = kPass * kRowsAt; j < n; j += kRowsAt) {
-      float v[8];
-      load_row(q, j + hl, v);
-      store_row(j + hl, v);
+    for (int j = kRing; j < n; j += kRowsAt) {
+      const int k = q.s * F::kStepK + hp * 8;
+      const bool live = j + hl < n;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+      if (live && k < p.I) {
+        const float4* h = reinterpret_cast<const float4*>(p.h + (int64_t)tb.order[first + j + hl] * p.I + k);
+        const float4 a = __ldcg(h), b = __ldcg(h + 1);
+        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+      }
+      form(v, more + (j + hl - kRing) * kLine, j + hl, live);
     }
   };
 
-  pdl_wait();  // h
   Place q = start;
-  load_h(q);
   int from = 0;
   for (int row0 = row_lo; row0 < row_hi; row0 += kRowTile) {
     float acc[NG][4];
@@ -723,16 +901,18 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_down_kernel(const 
       // without a route takes any row, its sums are not used
       const int b = q.b;
       const uint32_t m = tb.has[b];
-      uint32_t hrow[NG], hfc[NG][2];
+      uint32_t hrow[NG], hslot[NG], hfc[NG][2];
       float w[NG][2];
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         auto row_of = [&](int col) { return (m >> col) & 1u ? __popc(m & ((1u << col) - 1)) : 0; };
-        hrow[n] = smem_u32(hrows) + row_of(8 * n + g) * kLine + 2 * piece_k<WF>(0, 0);
+        const int r = row_of(8 * n + g);
+        hslot[n] = r < kRing ? kRing * kRow : 0;
+        hrow[n] = smem_u32(r < kRing ? ring + r * kRow : more + (r - kRing) * kLine) + 2 * piece_k<WF>(0, 0);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int col = 8 * n + 2 * t + j;
-          w[n][j] = (m >> col) & 1u ? tb.w[tb.route[b * 8 * NG + col]] : 0.0f;
+          w[n][j] = (m >> col) & 1u ? tb.w[max((int)tb.route[b * 8 * NG + col], 0)] : 0.0f;
           hfc[n][j] = smem_u32(hf + row_of(col));
         }
       }
@@ -743,18 +923,19 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_down_kernel(const 
         for (int i = 0; i < 4; ++i) blk[n][i] = 0.0f;
       float gs = 1.0f;
       do {
-        __syncwarp();  // the step before has read its rows of h
-        store_h(q);
-        next(q);
-        load_h(q);
         cp_async_wait<S - 1>();
-        __syncwarp();  // rows of h, and scales, that other lanes brought
+        __syncwarp();  // what other lanes brought
+        form_rows(q, from);
+        __syncwarp();
         const uint32_t e = smem_u32(queue + from * kEntry);
-        float d[NG][4];
+        float d[NG][4], d1[NG][4];  // two chains of instructions
 #pragma unroll
         for (int n = 0; n < NG; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[n][i] = F::kF16 ? 0.0f : blk[n][i];
+          for (int i = 0; i < 4; ++i) {
+            d[n][i] = F::kF16 ? 0.0f : blk[n][i];
+            d1[n][i] = 0.0f;
+          }
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
           uint4 B[NG][F::kB], L[NG][F::kB];
@@ -762,12 +943,16 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_down_kernel(const 
           for (int n = 0; n < NG; ++n)
 #pragma unroll
             for (int i = 0; i < F::kB; ++i) {
-              const uint32_t a = hrow[n] + 2 * (piece_k<WF>(hh, i) - piece_k<WF>(0, 0));
+              const uint32_t a = hrow[n] + from * hslot[n] + 2 * (piece_k<WF>(hh, i) - piece_k<WF>(0, 0));
               B[n][i] = lds128(a);
               L[n][i] = kParts == 2 ? lds128(a + kPart) : B[n][i];
             }
-          half_mma<WF, NG, kParts == 2>(e, hh, B, L, d);
+          half_mma<WF, NG, kParts == 2>(e, hh, B, L, hh ? d1 : d);
         }
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[n][i] += d1[n][i];
         if constexpr (F::kF16) {
           float s0 = 1.0f, s1 = 1.0f;
           if constexpr (WF == OES_WFMT_FP8) {
@@ -790,9 +975,10 @@ __global__ void __launch_bounds__(W * 32, W == 8 ? 2 : 1) few_down_kernel(const 
 #pragma unroll
             for (int i = 0; i < 4; ++i) blk[n][i] = d[n][i];
         }
-        if (F::kScale) __syncwarp();
+        __syncwarp();  // read by all before the queue's entry is filled again
         from = from + 1 == S ? 0 : from + 1;
         copy_next();
+        next(q);
       } while (q.b == b && q.row0 == row0 && q.s != 0);
       // a token without a route in this block takes nothing from it, not even a NaN of
       // its weights
@@ -830,56 +1016,68 @@ int x_stride(int H) {
   return ceil_div(H, F::kStepK) * F::kStepK * 2 + F::kXPad;
 }
 
-template <int WF, int NG, int W, int KS, int S>
+template <int WF, int NG, int KS, int S>
 size_t up_smem(int T, int k, int H) {
   using F = Fmt<WF>;
   return (size_t)W * S * entry_bytes<WF>() + (KS > 1 ? 2 * W * 32 * 16 * NG : 0) + (size_t)T * x_stride<WF>(H) +
          (F::kF16 ? 4 * T * ceil_div(H, F::kStepK) : 0) + tables_bytes(T * k, NG);
 }
 
-template <int WF, int NG, int W, int KS, int S>
+template <int WF, int NG, int KS, int S>
 int launch_up(const FewParams& p, cudaStream_t stream) {
-  const size_t smem = up_smem<WF, NG, W, KS, S>(p.T, p.k, p.H);
-  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(few_up_kernel<WF, NG, W, KS, S>), smem,
+  const size_t smem = up_smem<WF, NG, KS, S>(p.T, p.k, p.H);
+  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(few_up_kernel<WF, NG, KS, S>), smem,
                                 "few_up_kernel: shared memory limit");
   if (rc) return rc;
   const int64_t units = (int64_t)p.T * p.k * (p.I / 8);  // at most
-  launch_kernel(few_up_kernel<WF, NG, W, KS, S>, (int)std::min<int64_t>(num_sms(), units), W * 32, smem, stream, p);
+  launch_kernel(few_up_kernel<WF, NG, KS, S>, (int)std::min<int64_t>(num_sms(), units), W * 32, smem, stream, p);
   OES_CHECK_LAUNCH("few_up_kernel");
   return OES_OK;
 }
 
-#ifndef OES_V
-#define OES_V 0
-#endif
+template <int WF, int NG, int S>
+size_t down_smem(int T, int k) {
+  return (size_t)W * down_warp_bytes<WF, NG, S>() + W * 32 * 16 * NG + tables_bytes(T * k, NG);
+}
+template <int WF, int NG, int S>
+int launch_down(const FewParams& p, cudaStream_t stream) {
+  const size_t smem = down_smem<WF, NG, S>(p.T, p.k);
+  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(few_down_kernel<WF, NG, S>), smem,
+                                      "few_down_kernel: shared memory limit");
+  if (rc) return rc;
+  launch_kernel(few_down_kernel<WF, NG, S>, ceil_div(p.H, p.rows_cta), W * 32, smem, stream, p);
+  OES_CHECK_LAUNCH("few_down_kernel");
+  return OES_OK;
+}
+
 // One group of tokens: both kernels.
 template <int WF, int NG>
 int launch_few(FewParams p, cudaStream_t stream) {
   p.x_ld = x_stride<WF>(p.H);
-  const int64_t units = (int64_t)p.T * p.k * (p.I / 8);  // of few_up, at most
-  int rc;
-  if (up_smem<WF, NG, 16, 1, 3>(p.T, p.k, p.H) > kSmemMost) rc = launch_up<WF, NG, 8, 8, 2>(p, stream);
-  else if (OES_V == 1 && NG == 1 && units <= 8 * num_sms()) rc = launch_up<WF, NG, 8, 8, 5>(p, stream);
-  else if (OES_V == 2 && NG == 1 && units <= 8 * num_sms()) rc = launch_up<WF, NG, 8, 1, 5>(p, stream);
-  else rc = launch_up<WF, NG, 16, 1, 3>(p, stream);
-  if (rc) return rc;
-  constexpr int W = 16, S = 3;
-  const size_t smem = (size_t)W * (S * entry_bytes<WF>() + hold_bytes<WF, NG>()) + W * 32 * 16 * NG +
-                      tables_bytes(p.T * p.k, NG);
-  rc = set_max_dynamic_smem(reinterpret_cast<const void*>(few_down_kernel<WF, NG, W, S>), smem,
-                            "few_down_kernel: shared memory limit");
-  if (rc) return rc;
   p.rows_cta = ceil_div(p.H, num_sms());
-  launch_kernel(few_down_kernel<WF, NG, W, S>, ceil_div(p.H, p.rows_cta), W * 32, smem, stream, p);
-  OES_CHECK_LAUNCH("few_down_kernel");
-  return OES_OK;
+  // Warps a unit: one of a CTA's sixteen keeps 16 KB in flight, so that few units on an
+  // SM do not fill it.  Up to two units an SM: 1 token x 2 experts of 2048 x 128, bf16,
+  // takes 8.7 us with 16 warps a unit and 11.8 with one, 1 x 1 of 4096 x 512 10.7 and
+  // 17.1; up to eight: 1 x 10 of 2048 x 768 24.4 us with 4 and 25.1 with one (with 16,
+  // in FP8, 19.3 against 17.3).
+  const int64_t units = (int64_t)p.T * p.k * (p.I / 8);  // at most
+  const auto fits = [&](size_t smem) { return smem <= kSmemMost; };
+  int rc;
+  if (units <= 2 * num_sms()) rc = launch_up<WF, NG, 16, 2>(p, stream);
+  else if (units <= 8 * num_sms() && fits(up_smem<WF, NG, 4, 3>(p.T, p.k, p.H))) rc = launch_up<WF, NG, 4, 3>(p, stream);
+  else if (fits(up_smem<WF, NG, 1, 4>(p.T, p.k, p.H))) rc = launch_up<WF, NG, 1, 4>(p, stream);
+  else rc = launch_up<WF, NG, 1, 2>(p, stream);
+  if (rc) return rc;
+  if constexpr (NG == 2)  // with eight tokens three steps always fit
+    if (!fits(down_smem<WF, NG, 3>(p.T, p.k))) return launch_down<WF, NG, 2>(p, stream);
+  return launch_down<WF, NG, 3>(p, stream);
 }
 
 // Most tokens whose rows of x fit beside the queues.
 template <int WF>
 int group_tokens(int T, int k, int H) {
   int n = T;
-  while (n > 1 && (n > 8 ? up_smem<WF, 2, 8, 8, 2>(n, k, H) : up_smem<WF, 1, 8, 8, 2>(n, k, H)) > kSmemMost) --n;
+  while (n > 1 && (n > 8 ? up_smem<WF, 2, 16, 2>(n, k, H) : up_smem<WF, 1, 16, 2>(n, k, H)) > kSmemMost) --n;
   return n;
 }
 
@@ -928,8 +1126,9 @@ static_assert(OES_FEW_TOKENS_MAX == kMaxTokens, "tokens a call");
 }  // namespace
 
 extern "C" size_t moe_layer_few_tokens_workspace_size(const oes_routed_experts* v, int T, int k) {
-  if (check_view(v, T, k, "moe_layer_few_tokens_workspace_size")) return 0;
-  return ((size_t)T * k * v->I * 4 + 255) / 256 * 256;
+  if (check_view(v, T, k, "moe_layer_few_tokens_workspace_size") || T == 0) return 0;
+  // h, then the tables of a group of tokens
+  return ((size_t)T * k * v->I * 4 + 16 + tables_bytes(T * k, 2) + 255) / 256 * 256;
 }
 
 extern "C" int moe_layer_few_tokens(const oes_routed_experts* v, const uint16_t* x, int T, int k, const void* logits,
@@ -985,6 +1184,7 @@ extern "C" int moe_layer_few_tokens(const oes_routed_experts* v, const uint16_t*
   p.ids = ids;
   p.weights = weights;
   p.h = static_cast<float*>(workspace);
+  p.tables = reinterpret_cast<uint8_t*>(p.h + (size_t)T * k * v->I);
   p.out = out;
   p.status = status;
   if (logits && v->E > kFusedExperts) {
