@@ -184,36 +184,52 @@ struct CvtArgs {
   int step_r, step_c;    // the chunks of the whole grid, in rows and chunks
 };
 
-// Rows of codes to rows of f16, zeros from K to Kp (a multiple of 64).
+// Rows of codes to rows of f16, zeros from K to Kp (a multiple of 64): 8 codes a
+// thread, so that a warp's loads and stores are each one piece of memory (with 16, whose
+// stores are every other 16 bytes, 4096 and 8192 rows of 4096 took 45 us).  kCvt
+// chunks a thread are loaded before the first is stored.
+constexpr int kCvt = 4;
 __global__ void __launch_bounds__(256) int8_to_f16_kernel(const CvtArgs a) {
   pdl_begin();
-  const int nc = a.Kp / 16;
+  const int nc = a.Kp / 8;
   const int64_t first = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   int64_t r = first / nc;
   int c = (int)(first - r * nc);
   while (r < a.rows) {
-    const int o = r >= a.rows0;
-    const int64_t row = o ? r - a.rows0 : r;
-    const int8_t* src = a.src[o] + row * a.ld[o] + c * 16;
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (c * 16 + 16 <= a.K) {
-      const uint4 v = __ldg(reinterpret_cast<const uint4*>(src));
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else {
-      for (int j = 0; j < 16 && c * 16 + j < a.K; ++j) w[j >> 2] |= (uint32_t)(uint8_t)src[j] << (8 * (j & 3));
-    }
-    uint32_t v[8];
+    uint2 w[kCvt];
+    uint16_t* dst[kCvt];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s8x4_f16x4(w[j], v[2 * j], v[2 * j + 1]);
-    uint4* dst = reinterpret_cast<uint4*>(a.dst[o] + row * a.Kp + c * 16);
-    dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
-    dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
-    r += a.step_r;
-    c += a.step_c;
-    if (c >= nc) {
-      c -= nc;
-      ++r;
+    for (int i = 0; i < kCvt; ++i) {
+      w[i] = make_uint2(0u, 0u);
+      dst[i] = nullptr;
+      if (r < a.rows) {
+        const int o = r >= a.rows0;
+        const int64_t row = o ? r - a.rows0 : r;
+        const int8_t* src = a.src[o] + row * a.ld[o] + c * 8;
+        dst[i] = a.dst[o] + row * a.Kp + c * 8;
+        if (c * 8 + 8 <= a.K) {
+          w[i] = __ldg(reinterpret_cast<const uint2*>(src));
+        } else {
+          uint32_t v[2] = {0u, 0u};
+          for (int j = 0; j < 8 && c * 8 + j < a.K; ++j) v[j >> 2] |= (uint32_t)(uint8_t)src[j] << (8 * (j & 3));
+          w[i] = make_uint2(v[0], v[1]);
+        }
+      }
+      r += a.step_r;
+      c += a.step_c;
+      if (c >= nc) {
+        c -= nc;
+        ++r;
+      }
     }
+#pragma unroll
+    for (int i = 0; i < kCvt; ++i)
+      if (dst[i]) {
+        uint32_t v[4];
+        s8x4_f16x4(w[i].x, v[0], v[1]);
+        s8x4_f16x4(w[i].y, v[2], v[3]);
+        *reinterpret_cast<uint4*>(dst[i]) = make_uint4(v[0], v[1], v[2], v[3]);
+      }
   }
 }
 
@@ -394,19 +410,23 @@ __global__ void __launch_bounds__(kTmThreads, 1)
           *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
         __syncwarp();
+        if (p.vec && n0 + (pc + 1) * kPer <= p.N) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int rr = 8 * i + (lane >> 2), c = lane & 3;
-          const int col = n0 + pc * kPer + c * kVec;
-          const uint8_t* from = stg + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4);
-          if (q * 32 + rr < nvalid && col < p.N) {
-            OT* o = static_cast<OT*>(p.out) + (int64_t)(m0 + q * 32 + rr) * p.out_ld + col;
-            if (p.vec && col + kVec <= p.N) {
-              *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(from);
-            } else {
-#pragma unroll 1
-              for (int e = 0; e < min(kVec, p.N - col); ++e) o[e] = reinterpret_cast<const OT*>(from)[e];
-            }
+          for (int i = 0; i < 4; ++i) {
+            const int rr = 8 * i + (lane >> 2), c = lane & 3;
+            const uint8_t* from = stg + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4);
+            if (q * 32 + rr < nvalid)
+              *reinterpret_cast<uint4*>(static_cast<OT*>(p.out) + (int64_t)(m0 + q * 32 + rr) * p.out_ld + n0 + pc * kPer + c * kVec) =
+                  *reinterpret_cast<const uint4*>(from);
+          }
+        } else {
+          // single values, neighbouring lanes neighbouring columns
+          constexpr int kRows = 32 / kPer;  // rows at a time
+#pragma unroll 4
+          for (int i = 0; i < 32; i += kRows) {
+            const int rr = i + lane / kPer, e = lane % kPer, col = n0 + pc * kPer + e;
+            const OT v = reinterpret_cast<const OT*>(stg + rr * 64 + ((e / kVec ^ ((rr >> 1) & 3)) << 4))[e % kVec];
+            if (q * 32 + rr < nvalid && col < p.N) static_cast<OT*>(p.out)[(int64_t)(m0 + q * 32 + rr) * p.out_ld + col] = v;
           }
         }
         __syncwarp();
@@ -539,9 +559,9 @@ extern "C" int moe_int8_gemm(const int8_t* xq, int64_t xq_ld, const float* xs, i
   c.rows = (int64_t)T + N;
   c.K = K;
   c.Kp = (int)Kp;
-  const int grid = (int)std::min<int64_t>(ceil_div64(c.rows * (Kp / 16), 256), (int64_t)num_sms() * 8);
-  c.step_r = (int)((int64_t)grid * 256 / (Kp / 16));
-  c.step_c = (int)((int64_t)grid * 256 % (Kp / 16));
+  const int grid = (int)std::min<int64_t>(ceil_div64(c.rows * (Kp / 8), 256), (int64_t)num_sms() * 8);
+  c.step_r = (int)((int64_t)grid * 256 / (Kp / 8));
+  c.step_c = (int)((int64_t)grid * 256 % (Kp / 8));
   launch_kernel(int8_to_f16_kernel, grid, 256, 0, stream, c);
   OES_CHECK_LAUNCH("int8_to_f16_kernel");
   if (wide) return dtype == OES_BF16 ? launch_tm<uint16_t, 256>(m, a, stream) : launch_tm<float, 256>(m, a, stream);
