@@ -10,11 +10,11 @@
 // instructions and are added up as 32-bit integers: the sum is the integer, whatever
 // the order, at the f16 rate.
 //
-//   int8_stream_kernel  few rows: a CTA takes 16 weight rows at a time, its warps
-//                       share K and stream the weights through queues of their
-//                       own (as in few_tokens.cu), x stands in shared memory as
-//                       f16.  Bound by the stream of weights.
-//   int8_tm_kernel      more rows: 128 rows x 256 (or 64) weight rows a tile on
+//   int8_stream_kernel  few rows: warps stream the weights through queues of their
+//                       own (as in few_tokens.cu) into warp-wide instructions, x
+//                       stands in shared memory as f16.  One launch, and the weights
+//                       are read once as they are.
+//   int8_tm_kernel      more rows: 128 rows x 256, 128 or 64 weight rows a tile on
 //                       tcgen05, operands by TMA from f16 copies of both that
 //                       int8_to_f16_kernel leaves in the workspace.
 #include <algorithm>
@@ -28,11 +28,20 @@ namespace oes {
 namespace {
 
 // ================================================================= few rows
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
-constexpr int kQueue = 4;       // steps in flight a warp
+// A CTA takes 8 NG tokens and rows_cta rows of w.  Its 16 warps are 16 >> wk_log
+// groups; a group takes 16 weight rows (one side of the matrix instruction) at a time and
+// shares their K range.  Weights go through queues of each lane's own, codes as they are,
+// and become f16 on their way to the instruction.  The tokens stand in shared memory as f16, in
+// two chunks of K; where K has more, each group has one tile of rows, and chunk after
+// chunk is loaded into registers under the products of the chunk two before it.
+constexpr int W = 16;
+constexpr int kThreads = W * 32;
 constexpr int kStepK = 128;
 constexpr int kEntry = 2048;    // 16 rows of a step
+constexpr int kHold = 4;        // 16 codes each: a thread's share of a chunk
+constexpr int kTokensMost = 32;  // of a CTA
+
+__host__ __device__ constexpr int chunk_steps(int ng) { return 32 / ng; }  // 8 NG tokens x 128 x this = kHold x 16 x kThreads
 
 struct StreamArgs {
   const int8_t* x;
@@ -44,133 +53,242 @@ struct StreamArgs {
   int T, K, N;
   void* out;
   int64_t out_ld;
-  int rows_cta, x_row;  // weight rows a CTA owns; bytes of a row of x in shared memory
+  int rows_cta, wk_log;  // weight rows a CTA owns; 2^wk_log warps share a tile's K range
+  int x_row;             // bytes of a token's row of a chunk in shared memory
 };
 
-__host__ __device__ constexpr int64_t stream_x_row(int K) { return (int64_t)(K + kStepK - 1) / kStepK * kStepK * 2 + 16; }
-int64_t stream_smem(int T, int K) {
-  const int ng = T <= 8 ? 1 : T <= 16 ? 2 : 4;
-  return kWarps * kQueue * kEntry + 2 * kThreads * 16 * ng + T * stream_x_row(K);
-}
-
-template <int NG, typename OT>
+template <int NG, typename OT, int kQueue>
 __global__ void __launch_bounds__(kThreads, 1) int8_stream_kernel(const StreamArgs p) {
+  constexpr int kSteps = chunk_steps(NG);
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t queue = smem_u32(smem + warp * (kQueue * kEntry)) + lane * 16;
-  int32_t* part = reinterpret_cast<int32_t*>(smem + kWarps * kQueue * kEntry);  // [2][warp][lane][4 NG]
-  uint8_t* xs = reinterpret_cast<uint8_t*>(part + 2 * kThreads * 4 * NG);
-  const int ns = (p.K + kStepK - 1) / kStepK;
+  uint8_t* xs = smem + W * kQueue * kEntry;             // [2 chunks][8 NG][x_row]
+  int32_t* part = reinterpret_cast<int32_t*>(xs);       // afterwards [warp][lane][4 NG]
+  const int wk = warp & ((1 << p.wk_log) - 1), wm = warp >> p.wk_log, groups = W >> p.wk_log, share = 1 << p.wk_log;
+  const int ns = (p.K + kStepK - 1) / kStepK, chunks = (ns + kSteps - 1) / kSteps;
   const int row_lo = blockIdx.x * p.rows_cta, row_hi = min(p.N, row_lo + p.rows_cta);
+  const int tok0 = blockIdx.y * 8 * NG, toks = min(8 * NG, p.T - tok0);
+  __shared__ float s_xs[kTokensMost], s_ws[W * 16];  // scales, where warps share tiles (at most 16 of them)
   pdl_begin();
 
-  // the next step to copy
-  int ct = row_lo, cs = warp, at = 0;
+  // The next step to copy: of the tile at row ct, chunk cc, step cs.  A chunk's steps
+  // go round the group's warps.
+  int ct = row_lo + wm * 16, cc = 0, cs = wk, at = 0;
+  const int8_t* r0 = p.w;
+  bool ok0 = false, ok1 = false;
+  auto steps_of = [&](int c) { return min(kSteps, ns - c * kSteps); };
+  auto set_rows = [&]() {
+    r0 = p.w + (int64_t)(ct + g) * p.w_ld + 16 * t;
+    ok0 = ct + g < row_hi;
+    ok1 = ct + g + 8 < row_hi;
+  };
+  auto skip_empty = [&]() {  // to the warp's next step
+    while (ct < row_hi && cs >= steps_of(cc)) {
+      cs = wk;
+      if (++cc == chunks) {
+        cc = 0;
+        ct += 16 * groups;
+        set_rows();
+      }
+    }
+  };
+  set_rows();
+  skip_empty();
   auto copy_next = [&]() {
-    if (cs < ns && ct < row_hi) {
-      const int8_t* r0 = p.w + (int64_t)(ct + g) * p.w_ld;
-      const bool ok0 = ct + g < row_hi, ok1 = ct + g + 8 < row_hi;
+    if (ct < row_hi) {
+      const int k = (cc * kSteps + cs) * kStepK;
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh) {
-        const int k = cs * kStepK + hh * 64 + 16 * t;
-        const int n = max(0, min(16, p.K - k));
-        cp_async16_part(queue + at * kEntry + hh * 1024, ok0 && n > 0 ? r0 + k : p.w, ok0 ? n : 0);
-        cp_async16_part(queue + at * kEntry + hh * 1024 + 512, ok1 && n > 0 ? r0 + 8 * p.w_ld + k : p.w, ok1 ? n : 0);
+        const int o = k + hh * 64, n = max(0, min(16, p.K - o - 16 * t));
+        cp_async16_part(queue + at * kEntry + hh * 1024, ok0 && n > 0 ? r0 + o : p.w, ok0 ? n : 0);
+        cp_async16_part(queue + at * kEntry + hh * 1024 + 512, ok1 && n > 0 ? r0 + 8 * p.w_ld + o : p.w, ok1 ? n : 0);
       }
-      cs += kWarps;
-      if (cs >= ns) {
-        cs = warp;
-        ct += 16;
-      }
+      cs += share;
+      skip_empty();
     }
     cp_async_commit();
     at = (at + 1) % kQueue;
   };
   for (int i = 0; i < kQueue; ++i) copy_next();
 
-  // x as f16, zeros past K (which silence what a weight's row holds there)
-  const int xc = ns * (kStepK / 16);
-  for (int i = tid; i < p.T * xc; i += kThreads) {
-    const int tok = i / xc, k = (i - tok * xc) * 16;
-    const int8_t* src = p.x + (int64_t)tok * p.x_ld + k;
-    uint32_t w[4] = {0u, 0u, 0u, 0u};
-    if (k + 16 <= p.K) {
-      const uint4 v = *reinterpret_cast<const uint4*>(src);
-      w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
-    } else {
-      for (int j = 0; j < 16 && k + j < p.K; ++j) w[j >> 2] |= (uint32_t)(uint8_t)src[j] << (8 * (j & 3));
-    }
-    uint32_t o[8];
+  // Chunk c of the tokens: 16 codes a piece, zeros past K (which silence what a weight's
+  // row holds there)
+  const int per = min(kSteps, ns) * (kStepK / 16);  // pieces of a token's row
+  const int tok_0 = tid / per, pc_0 = tid - tok_0 * per, tok_d = kThreads / per, pc_d = kThreads - tok_d * per;
+  uint4 held[kHold];
+  auto load_x = [&](int c) {
+    int tok = tok_0, pc = pc_0;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s8x4_f16x4(w[j], o[2 * j], o[2 * j + 1]);
-    uint4* dst = reinterpret_cast<uint4*>(xs + (int64_t)tok * p.x_row + 2 * k);
-    dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
-    dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+    for (int i = 0; i < kHold; ++i) {
+      const int k = c * kSteps * kStepK + pc * 16;
+      held[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (tok < toks && k < p.K) {
+        const int8_t* src = p.x + (int64_t)(tok0 + tok) * p.x_ld + k;
+        if (k + 16 <= p.K) {
+          held[i] = __ldg(reinterpret_cast<const uint4*>(src));
+        } else {
+          uint32_t w[4] = {0u, 0u, 0u, 0u};
+          for (int j = 0; k + j < p.K; ++j) w[j >> 2] |= (uint32_t)(uint8_t)src[j] << (8 * (j & 3));
+          held[i] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+      }
+      tok += tok_d;
+      pc += pc_d;
+      if (pc >= per) {
+        pc -= per;
+        ++tok;
+      }
+    }
+  };
+  auto store_x = [&](int c) {
+    uint8_t* to = xs + (c & 1) * (8 * NG * p.x_row);
+    int tok = tok_0, pc = pc_0;
+#pragma unroll
+    for (int i = 0; i < kHold; ++i) {
+      if (tok < toks) {
+        uint32_t o[8];
+        s8x4_f16x4(held[i].x, o[0], o[1]);
+        s8x4_f16x4(held[i].y, o[2], o[3]);
+        s8x4_f16x4(held[i].z, o[4], o[5]);
+        s8x4_f16x4(held[i].w, o[6], o[7]);
+        uint4* dst = reinterpret_cast<uint4*>(to + tok * p.x_row + pc * 32);
+        dst[0] = make_uint4(o[0], o[1], o[2], o[3]);
+        dst[1] = make_uint4(o[4], o[5], o[6], o[7]);
+      }
+      tok += tok_d;
+      pc += pc_d;
+      if (pc >= per) {
+        pc -= per;
+        ++tok;
+      }
+    }
+  };
+  load_x(0);
+  if (share > 1) {
+    if (tid < toks) s_xs[tid] = __ldg(p.xs + tok0 + tid);
+    if (tid < row_hi - row_lo) s_ws[tid] = __ldg(p.ws + row_lo + tid);
+  }
+  store_x(0);
+  if (chunks > 1) {
+    load_x(1);
+    store_x(1);
   }
   __syncthreads();
 
   uint32_t xb[NG];
 #pragma unroll
-  for (int n = 0; n < NG; ++n) xb[n] = smem_u32(xs + (int64_t)min(8 * n + g, p.T - 1) * p.x_row) + 32 * t;
-  int from = 0, buf = 0;
-  for (int row0 = row_lo; row0 < row_hi; row0 += 16, buf ^= 1) {
-    int32_t acc[NG][4];
+  for (int n = 0; n < NG; ++n) xb[n] = smem_u32(xs + min(8 * n + g, toks - 1) * p.x_row) + 32 * t;
+  auto store_out = [&](int n, int tok, int32_t sum, float xscale, float wscale) {
+    const float o = (float)sum * xscale * wscale;
+    const int64_t at = (int64_t)(tok0 + tok) * p.out_ld + n;
+    if constexpr (sizeof(OT) == 2) static_cast<uint16_t*>(p.out)[at] = (uint16_t)f32_bf16(o);
+    else static_cast<float*>(p.out)[at] = o;
+  };
+  int from = 0;
+  int32_t acc[NG][4];
+  // the sums of the tile at row0; all warps come here together where chunks are reloaded
+  auto tile = [&](int row0) {
+    float d[NG][4];  // sums of up to 8 steps (1024 of K), integers below 2^24
+    int steps_in = 0;
 #pragma unroll
     for (int n = 0; n < NG; ++n)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[n][i] = 0;
-    for (int s = warp; s < ns; s += kWarps) {
-      cp_async_wait<kQueue - 1>();
-      float d[NG][4];
+      for (int i = 0; i < 4; ++i) {
+        acc[n][i] = 0;
+        d[n][i] = 0.0f;
+      }
+    auto drain = [&]() {
 #pragma unroll
       for (int n = 0; n < NG; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[n][i] = 0.0f;
-#pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        const uint4 a = lds128(queue + from * kEntry + hh * 1024), b = lds128(queue + from * kEntry + hh * 1024 + 512);
-        const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
-        uint32_t m[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-          s8x4_f16x4(aw[i], m[i][0], m[i][2]);
-          s8x4_f16x4(bw[i], m[i][1], m[i][3]);
+          acc[n][i] += __float2int_rn(d[n][i]);
+          d[n][i] = 0.0f;
         }
+    };
+    for (int c = 0; c < chunks; ++c) {
+      if (c + 2 < chunks) load_x(c + 2);
+      const uint32_t xo = (c & 1) * (8 * NG * p.x_row);
+      const int steps = row0 < row_hi ? steps_of(c) : 0;
+      for (int s = wk; s < steps; s += share) {
+        cp_async_wait<kQueue - 1>();
 #pragma unroll
-        for (int n = 0; n < NG; ++n) {
-          const uint32_t xa = xb[n] + s * (2 * kStepK) + hh * 128;
-          const uint4 u = lds128(xa), v = lds128(xa + 16);
-          mma_16816<true>(d[n], m[0][0], m[0][1], m[0][2], m[0][3], u.x, u.y);
-          mma_16816<true>(d[n], m[1][0], m[1][1], m[1][2], m[1][3], u.z, u.w);
-          mma_16816<true>(d[n], m[2][0], m[2][1], m[2][2], m[2][3], v.x, v.y);
-          mma_16816<true>(d[n], m[3][0], m[3][1], m[3][2], m[3][3], v.z, v.w);
+        for (int hh = 0; hh < 2; ++hh) {
+          const uint4 a = lds128(queue + from * kEntry + hh * 1024), b = lds128(queue + from * kEntry + hh * 1024 + 512);
+          const uint32_t aw[4] = {a.x, a.y, a.z, a.w}, bw[4] = {b.x, b.y, b.z, b.w};
+          uint32_t m[4][4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            s8x4_f16x4(aw[i], m[i][0], m[i][2]);
+            s8x4_f16x4(bw[i], m[i][1], m[i][3]);
+          }
+#pragma unroll
+          for (int n = 0; n < NG; ++n) {
+            const uint32_t xa = xb[n] + xo + s * (2 * kStepK) + hh * 128;
+            const uint4 u = lds128(xa), v = lds128(xa + 16);
+            mma_16816<true>(d[n], m[0][0], m[0][1], m[0][2], m[0][3], u.x, u.y);
+            mma_16816<true>(d[n], m[1][0], m[1][1], m[1][2], m[1][3], u.z, u.w);
+            mma_16816<true>(d[n], m[2][0], m[2][1], m[2][2], m[2][3], v.x, v.y);
+            mma_16816<true>(d[n], m[3][0], m[3][1], m[3][2], m[3][3], v.z, v.w);
+          }
         }
+        if (++steps_in == 1024 / kStepK) {
+          drain();
+          steps_in = 0;
+        }
+        from = (from + 1) % kQueue;
+        copy_next();
       }
+      if (c + 2 < chunks) {
+        __syncthreads();  // chunk c has been read by all; chunk c + 1, stored before, may be
+        store_x(c + 2);
+        if (c + 3 == chunks) __syncthreads();  // no other sync before it is read
+      }
+    }
+    drain();
+  };
+  const int first = row_lo + wm * 16;
+  if (share == 1) {
+    float xsc[NG][2];
+#pragma unroll
+    for (int n = 0; n < NG; ++n)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) xsc[n][j] = __ldg(p.xs + tok0 + min(8 * n + 2 * t + j, toks - 1));
+    int row0 = first;
+    do {
+      const float w0 = __ldg(p.ws + min(row0 + g, p.N - 1)), w1 = __ldg(p.ws + min(row0 + g + 8, p.N - 1));
+      if (row0 < row_hi || chunks > 2) tile(row0);
 #pragma unroll
       for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[n][i] += __float2int_rn(d[n][i]);
-      from = (from + 1) % kQueue;
-      copy_next();
-    }
-    int32_t* mine = part + ((buf * kWarps + warp) * 32 + lane) * (4 * NG);
+        for (int i = 0; i < 4; ++i) {
+          const int tok = 8 * n + 2 * t + (i & 1), r = row0 + g + 8 * (i >> 1);
+          if (tok < toks && r < row_hi) store_out(r, tok, acc[n][i], xsc[n][i & 1], i < 2 ? w0 : w1);
+        }
+      row0 += 16 * groups;
+    } while (row0 < row_hi);  // once, for all warps, where chunks are reloaded
+    return;
+  }
+  // one tile a group at most: its warps' sums go where the tokens were
+  tile(first);
+  __syncthreads();
+  int32_t* mine = part + (warp * 32 + lane) * (4 * NG);
 #pragma unroll
-    for (int n = 0; n < NG; ++n)
-      *reinterpret_cast<int4*>(mine + 4 * n) = make_int4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
-    __syncthreads();
-    for (int i = tid; i < 16 * p.T; i += kThreads) {
-      const int r16 = i & 15, tok = i >> 4, n = row0 + r16;
-      if (n >= row_hi) continue;
-      const int32_t* v = part + (buf * kWarps * 32 + (r16 & 7) * 4 + (tok & 7) / 2) * (4 * NG) + (tok >> 3) * 4 +
+  for (int n = 0; n < NG; ++n)
+    *reinterpret_cast<int4*>(mine + 4 * n) = make_int4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
+  __syncthreads();
+  // half a warp a token: 16 rows of a tile
+  const int r16 = lane & 15;
+  for (int m = 0; row_lo + 16 * m < row_hi; ++m)
+    for (int tok = 2 * warp + (lane >> 4); tok < toks; tok += 2 * W) {
+      const int32_t* v = part + (m * share * 32 + (r16 & 7) * 4 + (tok & 7) / 2) * (4 * NG) + (tok >> 3) * 4 +
                          (r16 >> 3) * 2 + (tok & 1);
       int32_t sum = 0;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) sum += v[w * 32 * 4 * NG];
-      const float o = (float)sum * p.xs[tok] * p.ws[n];
-      if constexpr (sizeof(OT) == 2) static_cast<uint16_t*>(p.out)[tok * p.out_ld + n] = (uint16_t)f32_bf16(o);
-      else static_cast<float*>(p.out)[tok * p.out_ld + n] = o;
+      for (int w = 0; w < share; ++w) sum += v[w * 32 * 4 * NG];
+      const int r = 16 * m + r16;
+      if (row_lo + r < row_hi) store_out(row_lo + r, tok, sum, s_xs[tok], s_ws[r]);
     }
-  }
 }
 
 // ================================================================ more rows
@@ -452,24 +570,67 @@ __global__ void __launch_bounds__(kTmThreads, 1)
 }
 
 // ------------------------------------------------------------------ launches
-constexpr size_t kSmemMost = 227 * 1024 - 1024;  // beside the kernels' static shared memory
-constexpr int kStreamRows = 32;
+constexpr size_t kSmemMost = 227 * 1024 - 2048;  // beside the kernels' static shared memory
 
-bool few_rows(int T, int K) { return T <= kStreamRows && stream_smem(T, K) <= (int64_t)kSmemMost; }
+// How few rows are cut up: NG groups of 8 tokens a CTA, weight rows a CTA, warps that
+// share a tile.  false: the tensor-memory kernel's.  A function of the sizes alone (the
+// workspace's size follows it, also where there is no GPU).
+constexpr int kSms = 152;
+struct Cut {
+  int ng, tiles, rows, wk_log;
+};
+bool stream_cut(int T, int K, int N, Cut* c) {
+  c->ng = T <= 8 ? 1 : T <= 16 ? 2 : 4;
+  c->tiles = ceil_div(T, 8 * c->ng);
+  if (c->tiles > kSms) return false;
+  c->rows = ceil_div(N, kSms / c->tiles);
+  if (c->tiles > 1) c->rows = ceil_div(c->rows, 16) * 16;
+  int groups = 1;  // of warps, one for each tile of 16 rows, at most 16
+  while (groups < W && groups * 16 < c->rows) groups *= 2;
+  c->wk_log = 0;
+  for (int g = groups; g < W; g *= 2) ++c->wk_log;
+  const int64_t chunks = ceil_div(ceil_div(K, kStepK), chunk_steps(c->ng));
+  if (chunks > 2 && groups * 16 < c->rows) return false;  // chunks are loaded again for one tile only
+  // Both ways' times, in us, as they were measured over 30 sizes.  The stream: 3.9 and
+  // 0.09 for each step (16 weight rows x 128 of K) of a CTA.  The tensor-memory kernel:
+  // its two launches, the f16 copies' 3 bytes a code, 0.13 for each 64 of K.
+  //   rows x K x N         stream  tensor       rows x K x N       stream  tensor
+  //   32 x 4096 x 8192      17.5    37.7        200 x 768 x 2048     8.1     8.9
+  //   64 x 512 x 512         4.5     6.1        256 x 4096 x 4096   36.5    29.3
+  //   128 x 4096 x 4096     23.4    29.0        512 x 512 x 512      5.6     6.6
+  //   128 x 2048 x 2048      9.7    14.8        512 x 1024 x 1024    9.8     9.6
+  const double stream = 3.9 + 0.09 * ceil_div(c->rows, 16) * ceil_div(K, kStepK);
+  const double tensor = 5.8 + 1.2 * (0.13 * ceil_div(K, 64) + 3.0 * ((double)T + N) * K / 4.5e6);
+  return stream <= tensor;
+}
+int stream_x_row(int K, int ng) { return std::min(ceil_div(K, kStepK), chunk_steps(ng)) * kStepK * 2 + 16; }
+bool few_rows(int T, int K, int N) {
+  Cut c;
+  return T > 0 && stream_cut(T, K, N, &c);
+}
 int64_t padded_k(int K) { return ceil_div64(K, 64) * 64; }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-template <int NG, typename OT>
-int launch_stream(StreamArgs a, cudaStream_t stream) {
-  const size_t smem = (size_t)stream_smem(a.T, a.K);
-  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(int8_stream_kernel<NG, OT>), smem,
+template <int NG, typename OT, int kQueue>
+int launch_stream_of(const StreamArgs& a, const Cut& c, size_t smem, cudaStream_t stream) {
+  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(int8_stream_kernel<NG, OT, kQueue>), smem,
                                 "int8_stream_kernel: shared memory limit");
   if (rc) return rc;
-  a.x_row = (int)stream_x_row(a.K);
-  a.rows_cta = ceil_div(a.N, num_sms());
-  launch_kernel(int8_stream_kernel<NG, OT>, ceil_div(a.N, a.rows_cta), kThreads, smem, stream, a);
+  launch_kernel(int8_stream_kernel<NG, OT, kQueue>, dim3(ceil_div(a.N, c.rows), c.tiles), kThreads, smem, stream, a);
   OES_CHECK_LAUNCH("int8_stream_kernel");
   return OES_OK;
+}
+template <int NG, typename OT>
+int launch_stream(StreamArgs a, const Cut& c, cudaStream_t stream) {
+  a.x_row = stream_x_row(a.K, NG);
+  a.rows_cta = c.rows;
+  a.wk_log = c.wk_log;
+  const size_t sums = c.wk_log ? (size_t)kThreads * 16 * NG : 0;
+  const int chunks = ceil_div(ceil_div(a.K, kStepK), chunk_steps(NG));
+  const size_t fixed = std::max(sums, (size_t)std::min(chunks, 2) * 8 * NG * a.x_row);
+  // as deep a queue as fits
+  if (fixed + W * 4 * kEntry <= kSmemMost) return launch_stream_of<NG, OT, 4>(a, c, fixed + W * 4 * kEntry, stream);
+  return launch_stream_of<NG, OT, 2>(a, c, fixed + W * 2 * kEntry, stream);
 }
 
 template <typename OT, int TN>
@@ -487,9 +648,9 @@ int launch_tm(const TmMaps& maps, TmArgs a, cudaStream_t stream) {
 }
 
 template <typename OT>
-int run_stream(const StreamArgs& a, cudaStream_t stream) {
-  return a.T <= 8 ? launch_stream<1, OT>(a, stream) : a.T <= 16 ? launch_stream<2, OT>(a, stream)
-                                                                : launch_stream<4, OT>(a, stream);
+int run_stream(const StreamArgs& a, const Cut& c, cudaStream_t stream) {
+  return c.ng == 1 ? launch_stream<1, OT>(a, c, stream) : c.ng == 2 ? launch_stream<2, OT>(a, c, stream)
+                                                                    : launch_stream<4, OT>(a, c, stream);
 }
 
 bool sizes_ok(int T, int K, int N) { return T >= 0 && K >= 1 && K <= 65536 && N >= 1 && N <= (1 << 24); }
@@ -500,7 +661,7 @@ bool sizes_ok(int T, int K, int N) { return T >= 0 && K >= 1 && K <= 65536 && N 
 using namespace oes;
 
 extern "C" size_t moe_int8_gemm_workspace_size(int T, int K, int N) {
-  if (!sizes_ok(T, K, N) || T == 0 || few_rows(T, K)) return 0;
+  if (!sizes_ok(T, K, N) || T == 0 || few_rows(T, K, N)) return 0;
   return align256((size_t)T * padded_k(K) * 2) + align256((size_t)N * padded_k(K) * 2);
 }
 
@@ -520,9 +681,10 @@ extern "C" int moe_int8_gemm(const int8_t* xq, int64_t xq_ld, const float* xs, i
   const size_t need = moe_int8_gemm_workspace_size(T, K, N);
   OES_REQUIRE(need == 0 || (workspace && ((uintptr_t)workspace & 255) == 0 && workspace_bytes >= need),
               "moe_int8_gemm: a 256-byte aligned workspace of %zu bytes is required", need);
-  if (few_rows(T, K)) {
-    StreamArgs a{xq, xq_ld, xs, wq, wq_ld, ws, T, K, N, out, out_ld, 0, 0};
-    return dtype == OES_BF16 ? run_stream<uint16_t>(a, stream) : run_stream<float>(a, stream);
+  Cut cut;
+  if (stream_cut(T, K, N, &cut)) {
+    StreamArgs a{xq, xq_ld, xs, wq, wq_ld, ws, T, K, N, out, out_ld, 0, 0, 0};
+    return dtype == OES_BF16 ? run_stream<uint16_t>(a, cut, stream) : run_stream<float>(a, cut, stream);
   }
   const int64_t Kp = padded_k(K);
   uint16_t* xf = static_cast<uint16_t*>(workspace);
@@ -534,8 +696,12 @@ extern "C" int moe_int8_gemm(const int8_t* xq, int64_t xq_ld, const float* xs, i
   a.N = N;
   a.nkb = (int)(Kp / 64);
   a.mt = ceil_div(T, kTileM);
-  const bool wide = (int64_t)a.mt * ceil_div(N, 256) >= num_sms();
-  a.nt = ceil_div(N, wide ? 256 : 64);
+  // Weight rows a tile: the widest whose tiles leave at most a third of the SMs idle.
+  // 1024 x 4096 x 4096 takes 42.7 us with 256 (128 tiles), 52 with 128 and 77 with 64; 512
+  // x 2048 x 4096 25.8, 20.4 and 25.7; 256 x 4096 x 4096 39.7, 32.2 and 29.3.
+  const int enough = num_sms() * 2 / 3;
+  const int tn = (int64_t)a.mt * ceil_div(N, 256) >= enough ? 256 : (int64_t)a.mt * ceil_div(N, 128) >= enough ? 128 : 64;
+  a.nt = ceil_div(N, tn);
   OES_REQUIRE((int64_t)a.mt * a.nt <= 0x7FFFFFFF - 4096, "moe_int8_gemm: too many tiles (T=%d N=%d)", T, N);
   a.out = out;
   a.out_ld = out_ld;
@@ -564,6 +730,7 @@ extern "C" int moe_int8_gemm(const int8_t* xq, int64_t xq_ld, const float* xs, i
   c.step_c = (int)((int64_t)grid * 256 % (Kp / 8));
   launch_kernel(int8_to_f16_kernel, grid, 256, 0, stream, c);
   OES_CHECK_LAUNCH("int8_to_f16_kernel");
-  if (wide) return dtype == OES_BF16 ? launch_tm<uint16_t, 256>(m, a, stream) : launch_tm<float, 256>(m, a, stream);
+  if (tn == 256) return dtype == OES_BF16 ? launch_tm<uint16_t, 256>(m, a, stream) : launch_tm<float, 256>(m, a, stream);
+  if (tn == 128) return dtype == OES_BF16 ? launch_tm<uint16_t, 128>(m, a, stream) : launch_tm<float, 128>(m, a, stream);
   return dtype == OES_BF16 ? launch_tm<uint16_t, 64>(m, a, stream) : launch_tm<float, 64>(m, a, stream);
 }

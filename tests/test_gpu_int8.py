@@ -150,10 +150,13 @@ def run_gemm(xq, xs, wq, ws, K, out_dtype, out_pad=0, stream=None, work=None):
     return out[:T, :N].cpu()
 
 
+# few rows: one token to 32, a chunk of K or many, tiles of one row to many, tiles of 32
+# tokens; more rows: tiles of 64, 128 and 256 weight rows, one sum of 1024 of K or several
 GEMMS = [(1, 1, 1), (1, 2048, 1536), (7, 100, 64), (8, 768, 2048), (9, 129, 300), (16, 4096, 200), (17, 1000, 333),
          (32, 768, 2048), (32, 1990, 77), (32, 4096, 500), (33, 64, 64), (1, 65536, 40), (5, 65536, 33), (20, 65536, 65),
          (200, 768, 2048), (129, 1025, 257), (601, 1999, 1001), (128, 2048, 128), (300, 63, 1500), (1, 127, 5000),
-         (2, 3000, 40000), (1500, 1100, 4000), (40, 9000, 9001)]
+         (2, 3000, 40000), (1500, 1100, 4000), (40, 9000, 9001), (33, 2049, 1000), (100, 5000, 300), (4096, 250, 256), (255, 512, 512), (64, 700, 20000),
+         (600, 1500, 2600), (257, 4100, 4100), (1030, 2050, 1700), (2049, 1500, 1030)]
 
 
 @pytest.mark.parametrize("size", GEMMS, ids=str)
@@ -196,8 +199,8 @@ def test_scales_of_any_value():
 
 
 def test_unaligned_output_rows():
-    xq, xn, xs, xsn, wq, wn, ws, wsn = gemm_inputs(140, 256, 300, 2)
-    for T in (6, 140):
+    xq, xn, xs, xsn, wq, wn, ws, wsn = gemm_inputs(1400, 256, 300, 2)
+    for T in (6, 140, 1400):
         nb = oes.moe_int8_gemm_workspace_size(T, 256, 300)
         work = torch.empty(nb + 1, dtype=torch.uint8, device="cuda")
         flat = torch.full((T * 301 + 7,), 3.0, dtype=torch.bfloat16, device="cuda")
@@ -215,14 +218,14 @@ def test_no_rows():
 
 
 def test_streams_and_two_calls_at_once():
-    a, b = gemm_inputs(200, 768, 2048, 5), gemm_inputs(700, 640, 3000, 6)
+    a, b = gemm_inputs(900, 768, 2048, 5), gemm_inputs(700, 640, 3000, 6)
     sa, sb = torch.cuda.Stream(), torch.cuda.Stream()
     outs = []
     for s in (sa, sb):
         s.wait_stream(torch.cuda.current_stream())
     keep = []
     for _ in range(5):
-        for s, m, (T, K, N) in ((sa, a, (200, 768, 2048)), (sb, b, (700, 640, 3000))):
+        for s, m, (T, K, N) in ((sa, a, (900, 768, 2048)), (sb, b, (700, 640, 3000))):
             with torch.cuda.stream(s):
                 nb = oes.moe_int8_gemm_workspace_size(T, K, N)
                 work = torch.empty(nb, dtype=torch.uint8, device="cuda")
@@ -235,7 +238,7 @@ def test_streams_and_two_calls_at_once():
         assert torch.equal(out.cpu(), product(m[1], m[3], m[5], m[7], torch.bfloat16))
 
 
-@pytest.mark.parametrize("T", [1, 32, 200])
+@pytest.mark.parametrize("T", [1, 32, 200, 1500])
 def test_linear_replayed_from_a_graph(T):
     """Rows to codes and the product, captured once and replayed on new rows; two
     graphs share the workspace."""

@@ -4,6 +4,7 @@ import pytest
 from offloaded_expert_slot_gb300 import build, oes
 
 P = 4096          # an aligned address; nothing is launched
+MANY = dict(T=4096, K=4096, N=4096, xq_ld=4096, wq_ld=4096, out_ld=4096)      # a size that needs a workspace
 
 
 @pytest.fixture(scope="module", autouse=True)
@@ -33,9 +34,9 @@ def test_quantize_refuses(kw):
                                 dict(xs=0), dict(wq=0), dict(ws=0), dict(out=0), dict(xq=P + 8), dict(wq=P + 4),
                                 dict(xq_ld=136), dict(wq_ld=200), dict(xq_ld=112), dict(wq_ld=0), dict(out_ld=63),
                                 dict(xs=P + 1), dict(ws=P + 2), dict(out=P + 1), dict(dtype=5), dict(status=P + 2),
-                                dict(dtype=oes.OES_F32, out=P + 2), dict(T=200), dict(T=200, workspace=P),
-                                dict(T=200, workspace=P + 16, bytes=1 << 20),
-                                dict(T=200, workspace=P, bytes=2 * (200 + 64) * 128 - 1)], ids=str)
+                                dict(dtype=oes.OES_F32, out=P + 2), MANY, dict(MANY, workspace=P),
+                                dict(MANY, workspace=P + 16, bytes=1 << 30),
+                                dict(MANY, workspace=P, bytes=2 * (4096 + 4096) * 4096 - 1)], ids=str)
 def test_gemm_refuses(kw):
     a = dict(xq=P, xq_ld=128, xs=P, T=4, K=128, wq=P, wq_ld=128, ws=P, N=64, out=P, out_ld=64, workspace=0, bytes=0,
              status=0, dtype=oes.OES_BF16)
@@ -46,7 +47,7 @@ def test_gemm_refuses(kw):
 
 def test_workspace_sizes():
     assert oes.moe_int8_gemm_workspace_size(1, 2048, 1536) == 0                     # few rows
-    assert oes.moe_int8_gemm_workspace_size(200, 768, 2048) >= 2 * 768 * (200 + 2048)
+    assert oes.moe_int8_gemm_workspace_size(4096, 4096, 4096) >= 2 * 4096 * (4096 + 4096)
     for T, K, N in ((-1, 16, 16), (4, 0, 16), (4, 65537, 16), (4, 16, 0), (4, 16, (1 << 24) + 1), (0, 16, 16)):
         assert oes.moe_int8_gemm_workspace_size(T, K, N) == 0
 
