@@ -28,20 +28,17 @@ namespace oes {
 namespace {
 
 // ================================================================= few rows
-// A CTA takes 8 NG tokens and rows_cta rows of w.  Its 16 warps are 16 >> wk_log
+// A CTA takes 8 NG tokens and rows_cta rows of w.  Its W warps are W >> wk_log
 // groups; a group takes 16 weight rows (one side of the matrix instruction) at a time and
 // shares their K range.  Weights go through queues of each lane's own, codes as they are,
 // and become f16 on their way to the instruction.  The tokens stand in shared memory as f16, in
 // two chunks of K; where K has more, each group has one tile of rows, and chunk after
 // chunk is loaded into registers under the products of the chunk two before it.
-constexpr int W = 16;
-constexpr int kThreads = W * 32;
 constexpr int kStepK = 128;
 constexpr int kEntry = 2048;    // 16 rows of a step
-constexpr int kHold = 4;        // 16 codes each: a thread's share of a chunk
 constexpr int kTokensMost = 32;  // of a CTA
 
-__host__ __device__ constexpr int chunk_steps(int ng) { return 32 / ng; }  // 8 NG tokens x 128 x this = kHold x 16 x kThreads
+__host__ __device__ constexpr int chunk_steps(int ng) { return 32 / ng; }  // a chunk is 32 KB of codes
 
 struct StreamArgs {
   const int8_t* x;
@@ -57,9 +54,10 @@ struct StreamArgs {
   int x_row;             // bytes of a token's row of a chunk in shared memory
 };
 
-template <int NG, typename OT, int kQueue>
-__global__ void __launch_bounds__(kThreads, 1) int8_stream_kernel(const StreamArgs p) {
-  constexpr int kSteps = chunk_steps(NG);
+template <int NG, typename OT, int W, int kQueue>
+__global__ void __launch_bounds__(W * 32, 1) int8_stream_kernel(const StreamArgs p) {
+  constexpr int kSteps = chunk_steps(NG), kThreads = W * 32;
+  constexpr int kHold = 8 * NG * kSteps * kStepK / (16 * kThreads);  // 16 codes each: a thread's share of a chunk
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
   const uint32_t queue = smem_u32(smem + warp * (kQueue * kEntry)) + lane * 16;
@@ -69,7 +67,7 @@ __global__ void __launch_bounds__(kThreads, 1) int8_stream_kernel(const StreamAr
   const int ns = (p.K + kStepK - 1) / kStepK, chunks = (ns + kSteps - 1) / kSteps;
   const int row_lo = blockIdx.x * p.rows_cta, row_hi = min(p.N, row_lo + p.rows_cta);
   const int tok0 = blockIdx.y * 8 * NG, toks = min(8 * NG, p.T - tok0);
-  __shared__ float s_xs[kTokensMost], s_ws[W * 16];  // scales, where warps share tiles (at most 16 of them)
+  __shared__ float s_xs[kTokensMost], s_ws[W * 16];  // scales, where warps share tiles
   pdl_begin();
 
   // The next step to copy: of the tile at row ct, chunk cc, step cs.  A chunk's steps
@@ -577,7 +575,7 @@ constexpr size_t kSmemMost = 227 * 1024 - 2048;  // beside the kernels' static s
 // workspace's size follows it, also where there is no GPU).
 constexpr int kSms = 152;
 struct Cut {
-  int ng, tiles, rows, wk_log;
+  int ng, tiles, rows, warps, wk_log;
 };
 bool stream_cut(int T, int K, int N, Cut* c) {
   c->ng = T <= 8 ? 1 : T <= 16 ? 2 : 4;
@@ -585,19 +583,23 @@ bool stream_cut(int T, int K, int N, Cut* c) {
   if (c->tiles > kSms) return false;
   c->rows = ceil_div(N, kSms / c->tiles);
   if (c->tiles > 1) c->rows = ceil_div(c->rows, 16) * 16;
-  int groups = 1;  // of warps, one for each tile of 16 rows, at most 16
-  while (groups < W && groups * 16 < c->rows) groups *= 2;
+  // Short rows are done before 16 warps have set themselves up: 200 x 768 x 2048 takes 6.2
+  // us with 8 and 8.1 with 16, 1024 x 512 x 512 5.6 and 7.5, 1 x 2048 x 1536 3.5 and 3.2,
+  // 128 x 2048 x 2048 10.9 and 9.8.
+  c->warps = K <= 1024 ? 8 : 16;
+  int groups = 1;  // of warps, one for each tile of 16 rows, at most all
+  while (groups < c->warps && groups * 16 < c->rows) groups *= 2;
   c->wk_log = 0;
-  for (int g = groups; g < W; g *= 2) ++c->wk_log;
+  for (int g = groups; g < c->warps; g *= 2) ++c->wk_log;
   const int64_t chunks = ceil_div(ceil_div(K, kStepK), chunk_steps(c->ng));
   if (chunks > 2 && groups * 16 < c->rows) return false;  // chunks are loaded again for one tile only
   // Both ways' times, in us, as they were measured over 30 sizes.  The stream: 3.9 and
   // 0.09 for each step (16 weight rows x 128 of K) of a CTA.  The tensor-memory kernel:
   // its two launches, the f16 copies' 3 bytes a code, 0.13 for each 64 of K.
   //   rows x K x N         stream  tensor       rows x K x N       stream  tensor
-  //   32 x 4096 x 8192      17.5    37.7        200 x 768 x 2048     8.1     8.9
-  //   64 x 512 x 512         4.5     6.1        256 x 4096 x 4096   36.5    29.3
-  //   128 x 4096 x 4096     23.4    29.0        512 x 512 x 512      5.6     6.6
+  //   32 x 4096 x 8192      17.5    37.7        200 x 768 x 2048     6.2     8.9
+  //   64 x 512 x 512         4.0     6.1        256 x 4096 x 4096   36.5    29.3
+  //   128 x 4096 x 4096     23.4    29.0        1024 x 512 x 512     5.6     7.2
   //   128 x 2048 x 2048      9.7    14.8        512 x 1024 x 1024    9.8     9.6
   const double stream = 3.9 + 0.09 * ceil_div(c->rows, 16) * ceil_div(K, kStepK);
   const double tensor = 5.8 + 1.2 * (0.13 * ceil_div(K, 64) + 3.0 * ((double)T + N) * K / 4.5e6);
@@ -611,12 +613,13 @@ bool few_rows(int T, int K, int N) {
 int64_t padded_k(int K) { return ceil_div64(K, 64) * 64; }
 size_t align256(size_t n) { return (n + 255) / 256 * 256; }
 
-template <int NG, typename OT, int kQueue>
-int launch_stream_of(const StreamArgs& a, const Cut& c, size_t smem, cudaStream_t stream) {
-  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(int8_stream_kernel<NG, OT, kQueue>), smem,
+template <int NG, typename OT, int W, int kQueue>
+int launch_stream_of(const StreamArgs& a, const Cut& c, size_t fixed, cudaStream_t stream) {
+  const size_t smem = fixed + W * kQueue * kEntry;
+  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(int8_stream_kernel<NG, OT, W, kQueue>), smem,
                                 "int8_stream_kernel: shared memory limit");
   if (rc) return rc;
-  launch_kernel(int8_stream_kernel<NG, OT, kQueue>, dim3(ceil_div(a.N, c.rows), c.tiles), kThreads, smem, stream, a);
+  launch_kernel(int8_stream_kernel<NG, OT, W, kQueue>, dim3(ceil_div(a.N, c.rows), c.tiles), W * 32, smem, stream, a);
   OES_CHECK_LAUNCH("int8_stream_kernel");
   return OES_OK;
 }
@@ -625,12 +628,13 @@ int launch_stream(StreamArgs a, const Cut& c, cudaStream_t stream) {
   a.x_row = stream_x_row(a.K, NG);
   a.rows_cta = c.rows;
   a.wk_log = c.wk_log;
-  const size_t sums = c.wk_log ? (size_t)kThreads * 16 * NG : 0;
+  const size_t sums = c.wk_log ? (size_t)c.warps * 32 * 16 * NG : 0;
   const int chunks = ceil_div(ceil_div(a.K, kStepK), chunk_steps(NG));
   const size_t fixed = std::max(sums, (size_t)std::min(chunks, 2) * 8 * NG * a.x_row);
+  if (c.warps == 8) return launch_stream_of<NG, OT, 8, 4>(a, c, fixed, stream);
   // as deep a queue as fits
-  if (fixed + W * 4 * kEntry <= kSmemMost) return launch_stream_of<NG, OT, 4>(a, c, fixed + W * 4 * kEntry, stream);
-  return launch_stream_of<NG, OT, 2>(a, c, fixed + W * 2 * kEntry, stream);
+  if (fixed + 16 * 4 * kEntry <= kSmemMost) return launch_stream_of<NG, OT, 16, 4>(a, c, fixed, stream);
+  return launch_stream_of<NG, OT, 16, 2>(a, c, fixed, stream);
 }
 
 template <typename OT, int TN>
