@@ -16,7 +16,10 @@
 //                       are read once as they are.
 //   int8_tm_kernel      more rows: 128 rows x 256, 128 or 64 weight rows a tile on
 //                       tcgen05, operands by TMA from f16 copies of both that
-//                       int8_to_f16_kernel leaves in the workspace.
+//                       int8_to_f16_kernel leaves in the workspace (4096 and 8192
+//                       rows of 4096: 20 us).
+//   int8_pair_kernel    the same for the largest: 256 x 256 a pair of SMs; 4096 x 4096
+//                       x 8192 159 us, 1.73 PFLOP/s, 1.52 with the copies.
 #include <algorithm>
 
 #include "common.cuh"
@@ -370,6 +373,58 @@ struct TmArgs {
   int32_t* status;
 };
 
+// A warp's part of a tile, 32 rows of kCols sums: scaled, and out.  Results leave in
+// pieces of 64 bytes of 32 rows, turned around in shared memory (stg, 2 KB) so that whole
+// sectors are stored.
+template <typename OT, int kCols>
+__device__ __forceinline__ void store_tile(const TmArgs& p, const int32_t (&acc)[kCols], uint8_t* stg, int q, int m0,
+                                           int n0, int nvalid) {
+  const int lane = threadIdx.x & 31, row = q * 32 + lane;
+  constexpr int kPer = 64 / (int)sizeof(OT), kVec = 16 / (int)sizeof(OT);
+  const float xscale = row < nvalid ? __ldg(p.xs + m0 + row) : 0.0f;
+#pragma unroll
+  for (int pc = 0; pc < kCols / kPer; ++pc) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      uint32_t w[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        constexpr int kEach = 4 / (int)sizeof(OT);  // values a word
+        float v[kEach];
+#pragma unroll
+        for (int e = 0; e < kEach; ++e) {
+          const int j = pc * kPer + c * kVec + i * kEach + e;
+          v[e] = (float)acc[j] * xscale * __ldg(p.ws + min(n0 + j, p.N - 1));
+        }
+        if constexpr (sizeof(OT) == 2) w[i] = f32x2_bf16x2(v[0], v[1]);
+        else w[i] = __float_as_uint(v[0]);
+      }
+      *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    __syncwarp();
+    if (p.vec && n0 + (pc + 1) * kPer <= p.N) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int rr = 8 * i + (lane >> 2), c = lane & 3;
+        const uint8_t* from = stg + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4);
+        if (q * 32 + rr < nvalid)
+          *reinterpret_cast<uint4*>(static_cast<OT*>(p.out) + (int64_t)(m0 + q * 32 + rr) * p.out_ld + n0 + pc * kPer + c * kVec) =
+              *reinterpret_cast<const uint4*>(from);
+      }
+    } else {
+      // single values, neighbouring lanes neighbouring columns
+      constexpr int kRows = 32 / kPer;  // rows at a time
+#pragma unroll 4
+      for (int i = 0; i < 32; i += kRows) {
+        const int rr = i + lane / kPer, e = lane % kPer, col = n0 + pc * kPer + e;
+        const OT v = reinterpret_cast<const OT*>(stg + rr * 64 + ((e / kVec ^ ((rr >> 1) & 3)) << 4))[e % kVec];
+        if (q * 32 + rr < nvalid && col < p.N) static_cast<OT*>(p.out)[(int64_t)(m0 + q * 32 + rr) * p.out_ld + col] = v;
+      }
+    }
+    __syncwarp();
+  }
+}
+
 template <typename OT, int TN>
 __global__ void __launch_bounds__(kTmThreads, 1)
     int8_tm_kernel(const __grid_constant__ TmMaps maps, const __grid_constant__ TmArgs p) {
@@ -469,8 +524,7 @@ __global__ void __launch_bounds__(kTmThreads, 1)
   } else {
     if (TN == 256) regs_inc<sizeof(OT) == 4 ? 224 : 216>();
     // ---------------------------------------------------------- epilogue
-    const int q = warp & 3, half = (warp - kEpiW0) >> 2;
-    const int row = q * 32 + lane;  // TMEM lane = row of the tile
+    const int q = warp & 3, half = (warp - kEpiW0) >> 2;  // 32 q + lane: TMEM lane and row of the tile
     uint8_t* const stg = stg_all + (warp - kEpiW0) * 2048;
     const int nd = (p.nkb + kDrain - 1) / kDrain;
     uint32_t it = 0;
@@ -502,51 +556,7 @@ __global__ void __launch_bounds__(kTmThreads, 1)
         if (lane == 0) mbar_arrive(&tempty[a]);
       }
       if (!on) continue;
-      // results leave in pieces of 64 bytes of 32 rows, turned around in shared
-      // memory so that whole sectors are stored
-      constexpr int kPer = 64 / (int)sizeof(OT), kVec = 16 / (int)sizeof(OT);
-      const float xscale = row < nvalid ? __ldg(p.xs + m0 + row) : 0.0f;
-#pragma unroll
-      for (int pc = 0; pc < kCols / kPer; ++pc) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t w[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            constexpr int kEach = 4 / (int)sizeof(OT);  // values a word
-            float v[kEach];
-#pragma unroll
-            for (int e = 0; e < kEach; ++e) {
-              const int j = pc * kPer + c * kVec + i * kEach + e;
-              v[e] = (float)acc[j] * xscale * __ldg(p.ws + min(n0 + j, p.N - 1));
-            }
-            if constexpr (sizeof(OT) == 2) w[i] = f32x2_bf16x2(v[0], v[1]);
-            else w[i] = __float_as_uint(v[0]);
-          }
-          *reinterpret_cast<uint4*>(stg + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
-        __syncwarp();
-        if (p.vec && n0 + (pc + 1) * kPer <= p.N) {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int rr = 8 * i + (lane >> 2), c = lane & 3;
-            const uint8_t* from = stg + rr * 64 + ((c ^ ((rr >> 1) & 3)) << 4);
-            if (q * 32 + rr < nvalid)
-              *reinterpret_cast<uint4*>(static_cast<OT*>(p.out) + (int64_t)(m0 + q * 32 + rr) * p.out_ld + n0 + pc * kPer + c * kVec) =
-                  *reinterpret_cast<const uint4*>(from);
-          }
-        } else {
-          // single values, neighbouring lanes neighbouring columns
-          constexpr int kRows = 32 / kPer;  // rows at a time
-#pragma unroll 4
-          for (int i = 0; i < 32; i += kRows) {
-            const int rr = i + lane / kPer, e = lane % kPer, col = n0 + pc * kPer + e;
-            const OT v = reinterpret_cast<const OT*>(stg + rr * 64 + ((e / kVec ^ ((rr >> 1) & 3)) << 4))[e % kVec];
-            if (q * 32 + rr < nvalid && col < p.N) static_cast<OT*>(p.out)[(int64_t)(m0 + q * 32 + rr) * p.out_ld + col] = v;
-          }
-        }
-        __syncwarp();
-      }
+      store_tile<OT, kCols>(p, acc, stg, q, m0, n0, nvalid);
     }
   }
 
@@ -564,6 +574,230 @@ __global__ void __launch_bounds__(kTmThreads, 1)
     }
     tc_fence_after();
     tmem_dealloc(tmem_base, 512);
+  }
+}
+
+// ----- two SMs on one tile
+// 256 rows x 256 weight rows a pair of CTAs.  A matrix instruction of the pair
+// (cta_group::2, issued by the CTA of rank 0) takes 128 rows of x and 128 weight rows from each
+// one's shared memory and leaves 128 x 256 sums in each one's tensor memory, so that a
+// stage is 32 KB a CTA where a tile of its own takes 48: one SM's tile moved 96 bytes a
+// clock into its shared memory and as many out of it, and the tensor pipe was active for 72 %.
+//
+// Both CTAs' loads are counted by the barriers of rank 0, which issues; the instructions'
+// completion is told to both.  (With the loads counted by barriers of each CTA's own and
+// passed on by a thread of rank 1, whose releasing arrivals took 0.8 us each, 4096 x 8192 x
+// 4096 took 442 us.)
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ uint32_t addr_in_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
+  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
+}
+__device__ __forceinline__ void pair_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void pair_mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
+                                             uint32_t accumulate) {
+  asm volatile(
+      "{ .reg .pred p; setp.ne.b32 p, %4, 0; tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p; }" ::"r"(d_tmem),
+      "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+// a box into this CTA's shared memory, its bytes counted by a barrier of either CTA
+__device__ __forceinline__ void pair_load_2d(void* dst, const CUtensorMap* m, uint32_t cluster_bar, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%3, "
+      "%4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(m)), "r"(cluster_bar), "r"(x), "r"(y)
+      : "memory");
+}
+// one arrival at this barrier in both CTAs once all earlier instructions are done
+__device__ __forceinline__ void pair_commit(uint64_t* bar) {
+  asm volatile(
+      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+          smem_u32(bar)),
+      "h"((uint16_t)3)
+      : "memory");
+}
+
+template <typename OT>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTmThreads, 1)
+    int8_pair_kernel(const __grid_constant__ TmMaps maps, const __grid_constant__ TmArgs p) {
+  constexpr int kTile = 256, kStage = 2 * kTileM * kBlkBytes, kBufs = 2, kCols = 128;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* stg_all = stages + p.ns * kStage;  // 2 KB an epilogue warp
+  uint64_t* full = reinterpret_cast<uint64_t*>(stg_all + kEpi * 2048);
+  uint64_t* empty = full + p.ns;
+  uint64_t* tfull = empty + p.ns;
+  uint64_t* tempty = tfull + kBufs;  // rank 0: both CTAs' warps have read
+  __shared__ uint32_t s_tmem;
+  __shared__ int s_dead, s_fills;
+  __shared__ uint64_t s_mma_done;
+  const int warp = warp_index(), lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  Waits<false> wait{p.status, &s_dead};
+  if (threadIdx.x == 0) {
+    s_dead = s_fills = 0;
+    mbar_init(&s_mma_done, 1);
+    for (int s = 0; s < p.ns; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < kBufs; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 2 * kEpi);
+    }
+    fence_mbar_init();
+    tma_prefetch_desc(&maps.x);
+    tma_prefetch_desc(&maps.w);
+  }
+  if (warp == 2) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&s_tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+    tc_fence_before();
+  }
+  __syncthreads();
+  pair_barrier();  // the other CTA's barriers and tensor memory are there
+  tc_fence_after();
+  const uint32_t tmem_base = s_tmem;
+  pdl_wait();  // the f16 copies
+  const int total = p.mt * p.nt, first = blockIdx.x >> 1, step = gridDim.x >> 1;
+
+  if (warp < kEpiW0) {
+    regs_dec<sizeof(OT) == 4 ? 56 : 72>();
+    if (warp == 0 && lane == 0) {
+      // ---------------------------------------------------------- producer
+      int s = 0, ph = 0;
+      for (int u = first; u < total; u += step) {
+        const int m = (u % p.mt) * kTile + rank * kTileM, n = (u / p.mt) * kTile + rank * 128;
+#pragma unroll 1
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          wait(&empty[s], ~ph & 1);
+          if (wait.dead()) break;
+          // Rank 0 expects both CTAs' bytes.  Rank 1's may come first: its stage was released
+          // with rank 0's, and the phase does not end before rank 0's arrival.
+          uint8_t* X = stages + s * kStage;
+          const uint32_t bar = addr_in_rank(smem_u32(&full[s]), 0);
+          if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
+          pair_load_2d(X, &maps.x, bar, kb * 64, m);
+          pair_load_2d(X + kTileM * kBlkBytes, &maps.w, bar, kb * 64, n);
+          pair_load_2d(X + (kTileM + 64) * kBlkBytes, &maps.w, bar, kb * 64, n + 64);
+          if (++s == p.ns) { s = 0; ++ph; }
+        }
+      }
+      s_fills = ph * p.ns + s;
+    } else if (warp == 1 && rank == 0) {
+      // -------------------------------------------------------- MMA issuer
+      int s = 0, ph = 0;
+      uint32_t it = 0;
+      const uint32_t idesc = idesc_f16(0, kTile, kTile);
+      const uint64_t desc0 = smem_desc_sw128(smem_u32(stages));
+      const bool leader = elect_one();
+      for (int u = first; u < total; u += step) {
+#pragma unroll 1
+        for (int kb = 0; kb < p.nkb; ++kb) {
+          const uint32_t a = it % kBufs;
+          const bool opens = kb % kDrain == 0, closes = (kb + 1) % kDrain == 0 || kb + 1 == p.nkb;
+          if (opens) wait(&tempty[a], ((it / kBufs) & 1) ^ 1);
+          wait(&full[s], ph);
+          tc_fence_after();
+          // Once a wait has given up nothing is released, so that rank 1's loads stop too.
+          if (leader && !wait.dead()) {
+            const uint64_t xd = desc0 + (uint32_t)(s * (kStage >> 4)), wd = xd + (kTileM * kBlkBytes >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              pair_mma_f16(tmem_base + a * kTile, xd + 2 * kk, wd + 2 * kk, idesc, opens && kk == 0 ? 0u : 1u);
+            pair_commit(&empty[s]);
+            if (closes) pair_commit(&tfull[a]);
+          }
+          __syncwarp();
+          if (closes) ++it;
+          if (++s == p.ns) { s = 0; ph ^= 1; }
+        }
+      }
+      if (leader) pair_commit(&s_mma_done);
+    }
+  } else {
+    regs_inc<sizeof(OT) == 4 ? 224 : 216>();
+    // ---------------------------------------------------------- epilogue
+    const int q = warp & 3, half = (warp - kEpiW0) >> 2;
+    uint8_t* const stg = stg_all + (warp - kEpiW0) * 2048;
+    const int nd = (p.nkb + kDrain - 1) / kDrain;
+    uint32_t it = 0;
+    for (int u = first; u < total; u += step) {
+      const int m0 = (u % p.mt) * kTile + rank * kTileM, n0 = (u / p.mt) * kTile + half * kCols;
+      const int nvalid = min(kTileM, p.T - m0);
+      const bool on = q * 32 < nvalid && n0 < p.N;
+      int32_t acc[kCols];
+#pragma unroll
+      for (int j = 0; j < kCols; ++j) acc[j] = 0;
+#pragma unroll 1
+      for (int d = 0; d < nd; ++d, ++it) {
+        const uint32_t a = it % kBufs;
+        wait(&tfull[a], (it / kBufs) & 1);
+        tc_fence_after();
+        if (on) {
+          const uint32_t tl = tmem_base + ((uint32_t)(q * 32) << 16) + a * kTile + half * kCols;
+#pragma unroll
+          for (int c = 0; c < kCols / 32; ++c) {
+            uint32_t r[32];
+            tmem_ld_32(tl + c * 32, r);
+            tc_wait_ld();
+#pragma unroll
+            for (int j = 0; j < 32; ++j) acc[c * 32 + j] += __float2int_rn(__uint_as_float(r[j]));
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) {
+          if (rank == 0) mbar_arrive(&tempty[a]);
+          else arrive_remote(addr_in_rank(smem_u32(&tempty[a]), 0));
+        }
+      }
+      if (on) store_tile<OT, kCols>(p, acc, stg, q, m0, n0, nvalid);
+    }
+  }
+
+  tc_fence_before();
+  __syncthreads();
+  // No copy outlives the shared memory it goes to, no instruction the tensor memory or what
+  // it reads, no arrival the CTA it goes to.
+  if (warp == 2 && lane == 0) mbar_wait(&s_mma_done, 0, p.status);
+  __syncwarp();
+  pair_barrier();
+  if (rank == 0 && threadIdx.x == 0) {
+    int theirs, their_dead;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(theirs) : "r"(addr_in_rank(smem_u32(&s_fills), 1)));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(their_dead) : "r"(addr_in_rank(smem_u32(&s_dead), 1)));
+    if (s_dead || their_dead) {
+      // A wait gave up, and one producer may have stopped before the other: what a phase
+      // of the last ns is short of is made up, then its bytes are waited for.
+      const int mine = s_fills, most = max(mine, theirs);
+      for (int i = max(0, most - p.ns); i < most; ++i) {
+        uint64_t* bar = &full[i % p.ns];
+        if (i >= mine) mbar_arrive_expect_tx(bar, kStage);
+        if (i >= theirs)
+          asm volatile("mbarrier.complete_tx.relaxed.cluster.shared::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)), "r"(kStage)
+                       : "memory");
+        mbar_wait(bar, (i / p.ns) & 1, p.status);
+      }
+    }
+  }
+  __syncthreads();
+  pair_barrier();
+  if (warp == 2) {
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem_base) : "memory");
   }
 }
 
@@ -652,6 +886,20 @@ int launch_tm(const TmMaps& maps, TmArgs a, cudaStream_t stream) {
 }
 
 template <typename OT>
+int launch_pair(const TmMaps& maps, TmArgs a, cudaStream_t stream) {
+  constexpr int stage = 2 * kTileM * kBlkBytes;
+  const size_t fixed = 1024 + kEpi * 2048 + 64 * 8;
+  a.ns = (int)std::min<size_t>(8, (kSmemMost - fixed) / stage);
+  const size_t smem = fixed + (size_t)a.ns * stage;
+  int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(int8_pair_kernel<OT>), smem,
+                                "int8_pair_kernel: shared memory limit");
+  if (rc) return rc;
+  launch_kernel(int8_pair_kernel<OT>, 2 * std::min(num_sms() / 2, a.mt * a.nt), kTmThreads, smem, stream, maps, a);
+  OES_CHECK_LAUNCH("int8_pair_kernel");
+  return OES_OK;
+}
+
+template <typename OT>
 int run_stream(const StreamArgs& a, const Cut& c, cudaStream_t stream) {
   return c.ng == 1 ? launch_stream<1, OT>(a, c, stream) : c.ng == 2 ? launch_stream<2, OT>(a, c, stream)
                                                                     : launch_stream<4, OT>(a, c, stream);
@@ -734,6 +982,12 @@ extern "C" int moe_int8_gemm(const int8_t* xq, int64_t xq_ld, const float* xs, i
   c.step_c = (int)((int64_t)grid * 256 % (Kp / 8));
   launch_kernel(int8_to_f16_kernel, grid, 256, 0, stream, c);
   OES_CHECK_LAUNCH("int8_to_f16_kernel");
+  // Pairs of SMs where every pair has a tile and K is long: 4096 x 4096 x 8192 takes 181 us,
+  // 192 with tiles of one SM, 2048 x 4096 x 4096 66 and 68; 4096 x 768 x 2048 28 and 26.
+  if (tn == 256 && K >= 2048 && (int64_t)ceil_div(T, 256) * a.nt >= num_sms() / 2) {
+    a.mt = ceil_div(T, 256);
+    return dtype == OES_BF16 ? launch_pair<uint16_t>(m, a, stream) : launch_pair<float>(m, a, stream);
+  }
   if (tn == 256) return dtype == OES_BF16 ? launch_tm<uint16_t, 256>(m, a, stream) : launch_tm<float, 256>(m, a, stream);
   if (tn == 128) return dtype == OES_BF16 ? launch_tm<uint16_t, 128>(m, a, stream) : launch_tm<float, 128>(m, a, stream);
   return dtype == OES_BF16 ? launch_tm<uint16_t, 64>(m, a, stream) : launch_tm<float, 64>(m, a, stream);

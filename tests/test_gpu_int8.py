@@ -156,7 +156,8 @@ GEMMS = [(1, 1, 1), (1, 2048, 1536), (7, 100, 64), (8, 768, 2048), (9, 129, 300)
          (32, 768, 2048), (32, 1990, 77), (32, 4096, 500), (33, 64, 64), (1, 65536, 40), (5, 65536, 33), (20, 65536, 65),
          (200, 768, 2048), (129, 1025, 257), (601, 1999, 1001), (128, 2048, 128), (300, 63, 1500), (1, 127, 5000),
          (2, 3000, 40000), (1500, 1100, 4000), (40, 9000, 9001), (33, 2049, 1000), (100, 5000, 300), (4096, 250, 256), (255, 512, 512), (64, 700, 20000),
-         (600, 1500, 2600), (257, 4100, 4100), (1030, 2050, 1700), (2049, 1500, 1030)]
+         (600, 1500, 2600), (257, 4100, 4100), (1030, 2050, 1700), (2049, 1500, 1030),
+         (2100, 2100, 2500), (2305, 4096, 2047)]
 
 
 @pytest.mark.parametrize("size", GEMMS, ids=str)

@@ -32,7 +32,7 @@ def impatient(tmp_path_factory):
     return handle
 
 
-@pytest.mark.parametrize("T,K,N", [(900, 768, 2048), (700, 4096, 6000), (1300, 2500, 4100), (300, 4096, 4096)])
+@pytest.mark.parametrize("T,K,N", [(900, 768, 2048), (700, 4096, 6000), (1300, 2500, 4100), (300, 4096, 4096), (2300, 2100, 3000)])
 def test_products(impatient, T, K, N):
     xq, _, xs, _, wq, _, ws, _ = gemm_inputs(T, K, N, 7)
     nb = oes.moe_int8_gemm_workspace_size(T, K, N)
