@@ -380,9 +380,9 @@ __device__ void few_order(const FewParams& p, const Tables& tb, int nb) {
 }
 
 // The matrix instructions of half a step: the lane's weights from its queue entry,
-// added onto d (row g and g + 8, columns 2t and 2t + 1, of each 8 tokens).  B are
-// the lane's values of the columns, L what their rounding to bf16 left (LO).
-template <int WF, int NG, bool LO>
+// added onto d (row g and g + 8, columns 2t and 2t + 1, of each 8 tokens), or FRESH from
+// zero.  B are the lane's values of the columns, L what their rounding to bf16 left (LO).
+template <int WF, int NG, bool LO, bool FRESH>
 __device__ __forceinline__ void half_mma(uint32_t entry, int hh, const uint4 (&B)[NG][Fmt<WF>::kB],
                                          const uint4 (&L)[NG][Fmt<WF>::kB], float (&d)[NG][4]) {
   const int lane = threadIdx.x & 31;
@@ -391,7 +391,7 @@ __device__ __forceinline__ void half_mma(uint32_t entry, int hh, const uint4 (&B
     const uint4 a = lds128(mine + hh * 1024), b = lds128(mine + hh * 1024 + 512);
 #pragma unroll
     for (int n = 0; n < NG; ++n) {
-      mma_16816<false>(d[n], a.x, b.x, a.y, b.y, B[n][0].x, B[n][0].y);
+      mma_16816<false, FRESH>(d[n], a.x, b.x, a.y, b.y, B[n][0].x, B[n][0].y);
       mma_16816<false>(d[n], a.z, b.z, a.w, b.w, B[n][0].z, B[n][0].w);
       if (LO) {
         mma_16816<false>(d[n], a.x, b.x, a.y, b.y, L[n][0].x, L[n][0].y);
@@ -409,7 +409,8 @@ __device__ __forceinline__ void half_mma(uint32_t entry, int hh, const uint4 (&B
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
         const uint4& v = B[n][i >> 1];
-        mma_16816<true>(d[n], a0, a1, a2, a3, i & 1 ? v.z : v.x, i & 1 ? v.w : v.y);
+        if (i == 0) mma_16816<true, FRESH>(d[n], a0, a1, a2, a3, v.x, v.y);
+        else mma_16816<true>(d[n], a0, a1, a2, a3, i & 1 ? v.z : v.x, i & 1 ? v.w : v.y);
       }
     }
   } else {
@@ -433,7 +434,8 @@ __device__ __forceinline__ void half_mma(uint32_t entry, int hh, const uint4 (&B
       }
 #pragma unroll
       for (int n = 0; n < NG; ++n) {
-        mma_16816<true>(d[n], oa[0], ob[0], oa[1], ob[1], B[n][i].x, B[n][i].y);
+        if (i == 0) mma_16816<true, FRESH>(d[n], oa[0], ob[0], oa[1], ob[1], B[n][i].x, B[n][i].y);
+        else mma_16816<true>(d[n], oa[0], ob[0], oa[1], ob[1], B[n][i].x, B[n][i].y);
         mma_16816<true>(d[n], oa[2], ob[2], oa[3], ob[3], B[n][i].z, B[n][i].w);
       }
     }
@@ -447,20 +449,29 @@ __device__ __forceinline__ int piece_k(int hh, int i) {
   return WF == OES_WFMT_BF16 ? 32 * hh + 8 * t : WF == OES_WFMT_FP8 ? 64 * hh + 16 * t + 8 * i : 32 * t + 16 * hh + 8 * i;
 }
 
-// The lane's copies of one step: 16 rows' kRowBytes from byte `at` of rows whose
-// first bytes for this lane are r0 (row g) and r1 (row g + 8); a row that is
-// absent (ok0, ok1) and bytes past `row` become zeros.
+// The lane's copies of one step: 16 rows' kRowBytes, at r0 (row g) and r1 (row g + 8) for
+// this lane; n0, n1: 16, or 0 for a row that is absent and becomes zeros.
 template <int WF>
-__device__ __forceinline__ void step_copy(uint32_t entry, const uint8_t* pool, const uint8_t* r0, const uint8_t* r1,
-                                          bool ok0, bool ok1, int at, int row) {
-  const int lane = threadIdx.x & 31, t = lane & 3;
+__device__ __forceinline__ void step_copy(uint32_t entry, const uint8_t* r0, const uint8_t* r1, int n0, int n1) {
+  const uint32_t mine = entry + (threadIdx.x & 31) * 16;
+#pragma unroll
+  for (int hh = 0; hh < Fmt<WF>::kChunks / 2; ++hh) {
+    cp_async16_part(mine + hh * 1024, r0 + hh * 64, n0);
+    cp_async16_part(mine + hh * 1024 + 512, r1 + hh * 64, n1);
+  }
+}
+// The same for a row's last step of `left` bytes: what is past them becomes zeros, and
+// nothing is read for it (any readable address stands in).
+template <int WF>
+__device__ __forceinline__ void step_copy_last(uint32_t entry, const uint8_t* r0, const uint8_t* r1, int n0, int n1,
+                                               int left, const uint8_t* any) {
+  const int lane = threadIdx.x & 31;
   const uint32_t mine = entry + lane * 16;
 #pragma unroll
   for (int hh = 0; hh < Fmt<WF>::kChunks / 2; ++hh) {
-    const int o = at + hh * 64;
-    const bool in = o + 16 * t < row;
-    cp_async16_take(mine + hh * 1024, in && ok0 ? r0 + o : pool, in && ok0);
-    cp_async16_take(mine + hh * 1024 + 512, in && ok1 ? r1 + o : pool, in && ok1);
+    const bool in = hh * 64 + 16 * (lane & 3) < left;
+    cp_async16_part(mine + hh * 1024, in ? r0 + hh * 64 : any, in ? n0 : 0);
+    cp_async16_part(mine + hh * 1024 + 512, in ? r1 + hh * 64 : any, in ? n1 : 0);
   }
 }
 
@@ -510,24 +521,42 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
   // x, with zeros up to a whole step
   const int xc = ns * (F::kStepK / 8);
   auto load_x = [&](int first, int n) {
-    for (int i0 = first & ~31; i0 < p.T * xc; i0 += n) {
-      const int i = i0 + lane, tok = i / xc, c = i - tok * xc;
-      const bool live = i < p.T * xc, in = live && c * 8 < p.H;
-      const uint16_t* src = p.x + (in ? (size_t)tok * p.H + c * 8 : 0);
-      uint8_t* dst = xs + tok * p.x_ld + c * 16;
-      if constexpr (F::kF16) {
-        float v[8];
+    constexpr int kAt = F::kF16 ? 4 : 1;  // pieces of 8 values loaded before the first is worked on
+    for (int i0 = first & ~31; i0 < p.T * xc; i0 += kAt * n) {
+      uint4 raw[kAt];
+      int tok[kAt], c[kAt];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[j] = 0.0f;
-        if (in) load_vals<8>(src, v);
-        uint4 o;
-        const float f = f16_group(v, o);
-        if (live) {
-          *reinterpret_cast<uint4*>(dst) = o;
-          if ((c & 15) == 0) xf[tok * ns + (c >> 4)] = f;
+      for (int j = 0; j < kAt; ++j) {
+        const int i = i0 + j * n + lane;
+        tok[j] = i / xc;
+        c[j] = i - tok[j] * xc;
+        const bool in = i < p.T * xc && c[j] * 8 < p.H;
+        const uint16_t* src = p.x + (in ? (size_t)tok[j] * p.H + c[j] * 8 : 0);
+        if constexpr (F::kF16) {
+          raw[j] = make_uint4(0u, 0u, 0u, 0u);
+          if (in) raw[j] = __ldcg(reinterpret_cast<const uint4*>(src));
+        } else if (i < p.T * xc) {
+          cp_async16_take(smem_u32(xs + tok[j] * p.x_ld + c[j] * 16), src, in);
         }
-      } else if (live) {
-        cp_async16_take(smem_u32(dst), src, in);
+      }
+      if constexpr (F::kF16) {
+#pragma unroll
+        for (int j = 0; j < kAt; ++j) {
+          if (i0 + j * n >= p.T * xc) break;
+          const uint32_t u[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+          float v[8];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            v[2 * e] = bf16_f32(u[e] & 0xFFFFu);
+            v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
+          }
+          uint4 o;
+          const float f = f16_group(v, o);
+          if (tok[j] < p.T) {
+            *reinterpret_cast<uint4*>(xs + tok[j] * p.x_ld + c[j] * 16) = o;
+            if ((c[j] & 15) == 0) xf[tok[j] * ns + (c[j] >> 4)] = f;
+          }
+        }
       }
     }
   };
@@ -554,33 +583,42 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
   q.b = q.j / per;
   q.r = q.j - q.b * per;
 
-  // the next step to copy: step cs of place c
+  // the next step to copy: step cs of place c, its weights for this lane at wp (gate) and
+  // wp + up, its scales at sp
   Place c = q;
   int cs = s0, at = 0;
-  const uint8_t* base = p.pool;
-  const uint8_t* w0 = p.pool;
+  const uint8_t *wp = p.pool, *sp = p.pool, *gsp = p.pool;
   const int64_t up = (int64_t)p.I * row;
+  const int last = row % F::kRowBytes;  // bytes of a short last step
   auto set_rows = [&]() {
     if (c.j >= hi || s0 >= ns) return;
-    base = p.pool + (int64_t)tb.slot[c.b] * p.row_bytes;
-    w0 = base + (int64_t)(c.r * 8 + g) * row + 16 * t;
+    const uint8_t* base = p.pool + (int64_t)tb.slot[c.b] * p.row_bytes;
+    wp = base + (int64_t)(c.r * 8 + g) * row + 16 * t + s0 * F::kRowBytes;
+    if constexpr (WF == OES_WFMT_FP8)
+      sp = base + p.s13 + ((int64_t)((lane & 1) * cdiv(p.I, 128) + ((c.r * 8) >> 7)) * ns + s0) * 4;
+    if constexpr (WF == OES_WFMT_NVFP4) {
+      const int r16 = lane & 15;
+      sp = base + p.s13 + ((int64_t)(2 * s0 + (lane >> 4)) * 2 * p.I + (r16 >> 3) * p.I + c.r * 8 + (r16 & 7)) * 4;
+      gsp = base + p.gs;
+    }
   };
   set_rows();
   auto copy_next = [&]() {
     if (c.j < hi && s0 < ns) {
       const uint32_t e = smem_u32(queue + at * kEntry);
-      step_copy<WF>(e, p.pool, w0, w0 + up, true, true, cs * F::kRowBytes, row);
+      const bool whole = last == 0 || cs + 1 < ns;
+      if (whole) step_copy<WF>(e, wp, wp + up, 16, 16);
+      else step_copy_last<WF>(e, wp, wp + up, 16, 16, last, p.pool);
+      wp += KS * F::kRowBytes;
       if constexpr (WF == OES_WFMT_FP8) {
-        const int ib = cdiv(p.I, 128);
-        if (lane < 2)
-          cp_async4_take(e + 2048 + 4 * lane, base + p.s13 + ((int64_t)(lane * ib + ((c.r * 8) >> 7)) * ns + cs) * 4, true);
+        if (lane < 2) cp_async4_take(e + 2048 + 4 * lane, sp, true);
+        sp += 4 * KS;
       }
       if constexpr (WF == OES_WFMT_NVFP4) {
-        const int r16 = lane & 15, k64 = 2 * cs + (lane >> 4);
-        const bool in = k64 * 64 < p.H;
-        cp_async4_take(e + 1024 + 4 * lane,
-                       base + p.s13 + ((int64_t)(in ? k64 : 0) * 2 * p.I + (r16 >> 3) * p.I + c.r * 8 + (r16 & 7)) * 4, in);
-        if (lane == 0) cp_async4_take(e + 1024 + 128, base + p.gs, true);
+        const bool in = whole || lane < 16;
+        cp_async4_take(e + 1024 + 4 * lane, in ? sp : p.pool, in);
+        sp += (int64_t)16 * KS * p.I;
+        if (lane == 0) cp_async4_take(e + 1024 + 128, gsp, true);
       }
       cs += KS;
       if (cs >= ns) {
@@ -621,28 +659,27 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
       cp_async_wait<S - 1>();
       if (F::kScale) __syncwarp();  // scales that other lanes copied
       const uint32_t e = smem_u32(queue + from * kEntry);
-      float d[NG][4], d1[NG][4];  // two chains of instructions
+      float d[NG][4], d1[NG][4];  // two chains of instructions with one group of tokens
 #pragma unroll
       for (int n = 0; n < NG; ++n)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          d[n][i] = F::kF16 ? 0.0f : acc[n][i];
-          d1[n][i] = 0.0f;
-        }
+        for (int i = 0; i < 4; ++i) d[n][i] = acc[n][i];
+      uint4 B[2][NG][F::kB];
 #pragma unroll
-      for (int hh = 0; hh < 2; ++hh) {
-        uint4 B[NG][F::kB];
+      for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
         for (int n = 0; n < NG; ++n)
 #pragma unroll
           for (int i = 0; i < F::kB; ++i)
-            B[n][i] = lds128(xb[n] + 2 * (s * F::kStepK + piece_k<WF>(hh, i) - piece_k<WF>(0, 0)));
-        half_mma<WF, NG, false>(e, hh, B, B, hh ? d1 : d);
+            B[hh][n][i] = lds128(xb[n] + 2 * (s * F::kStepK + piece_k<WF>(hh, i) - piece_k<WF>(0, 0)));
+      half_mma<WF, NG, false, F::kF16>(e, 0, B[0], B[0], d);
+      if constexpr (NG == 1) {
+        half_mma<WF, NG, false, true>(e, 1, B[1], B[1], d1);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) d[0][i] += d1[0][i];
+      } else {
+        half_mma<WF, NG, false, false>(e, 1, B[1], B[1], d);
       }
-#pragma unroll
-      for (int n = 0; n < NG; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[n][i] += d1[n][i];
       if constexpr (F::kF16) {
         float sg = 1.0f, su = 1.0f;
         if constexpr (WF == OES_WFMT_FP8) {
@@ -712,6 +749,10 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
 // experts ran at 1.9 TB/s; one step ahead, 4 tokens x 10 of 512 NVFP4 experts at 2.2.
 // Staged by the CTA for several blocks at a time, barriers and bookkeeping did.)
 constexpr int kRing = 2;  // rows of h of a step in the queue
+template <bool V>
+struct Bool {
+  static constexpr bool value = V;
+};
 
 // A row of h: kRow bytes, fp32 or in its form; kLine bytes of its form alone, in parts
 // kPart apart (bf16 rows have two), which spread over the banks.
@@ -763,73 +804,87 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
   const int ns = cdiv(p.I, F::kStepK);
   const int row_lo = blockIdx.x * p.rows_cta, row_hi = min(p.H, row_lo + p.rows_cta);
 
-  // A place in the warp's run of a tile: i of [.., i1), step s of block b
-  const int n_all = nb * ns, i0 = (int)((int64_t)warp * n_all / W), i1 = (int)((int64_t)(warp + 1) * n_all / W);
-  struct Place {
-    int i, b, s, row0;
-  };
-  Place start{i0, i0 / ns, 0, i0 < i1 ? row_lo : row_hi};
-  start.s = i0 - start.b * ns;
-  auto next = [&](Place& q) {
-    if (++q.s == ns) {
-      q.s = 0;
-      ++q.b;
-    }
-    if (++q.i == i1) {
-      const int r = q.row0 + kRowTile;
-      q = start;
-      q.row0 = r;
-    }
-  };
+  // The warp's run of a tile: `run` (block, step of K), from block b0, step s0 on
+  const int n_all = nb * ns, i0 = (int)((int64_t)warp * n_all / W);
+  const int run = (int)((int64_t)(warp + 1) * n_all / W) - i0, b0 = i0 / ns, s0 = i0 - b0 * ns;
 
-  // the next step to copy
-  Place c = start;
-  int at = 0;
-  const uint8_t* base = p.pool;
-  const uint8_t* w0 = p.pool;
-  bool ok0 = false, ok1 = false;
+  // The next step to copy: step cs of block cb, `left` of the tile at row crow; its
+  // weights for this lane at w0 and w1, its scales at sp, of its first rows of h at ho
+  int cb = b0, cs = s0, left = run, crow = run > 0 ? row_lo : row_hi, at = 0;
+  const uint8_t *w0 = p.pool, *w1 = p.pool, *sp = p.pool, *gsp = p.pool;
+  int n0 = 0, n1 = 0;
+  constexpr int kHLanes = F::kStepK / 4, kHAt = 32 / kHLanes;  // 16 bytes a lane: lanes a row of h, rows at a time
+  int ho[kRing / kHAt];
+  bool hin[kRing / kHAt];
+  const int last = row % F::kRowBytes;  // bytes of a short last step
+  bool sin = false;
   auto set_rows = [&]() {
-    if (c.row0 >= row_hi) return;
-    base = p.pool + (int64_t)tb.slot[c.b] * p.row_bytes;
-    w0 = base + p.w2 + (int64_t)(c.row0 + g) * row + 16 * t;
-    ok0 = c.row0 + g < row_hi;
-    ok1 = c.row0 + g + 8 < row_hi;
-  };
-  set_rows();
-  auto copy_w = [&]() {
-    const uint32_t e = smem_u32(queue + at * kEntry);
-    step_copy<WF>(e, p.pool, w0, w0 + 8 * row, ok0, ok1, c.s * F::kRowBytes, row);
+    if (crow >= row_hi) return;
+    const uint8_t* base = p.pool + (int64_t)tb.slot[cb] * p.row_bytes;
+    // absent rows read nothing; any address in the pool stands in
+    const bool ok0 = crow + g < row_hi, ok1 = crow + g + 8 < row_hi;
+    const uint8_t* w = base + p.w2 + (int64_t)(crow + g) * row + cs * F::kRowBytes + 16 * t;
+    w0 = ok0 ? w : p.pool;
+    w1 = ok1 ? w + 8 * row : p.pool;
+    n0 = ok0 ? 16 : 0;
+    n1 = ok1 ? 16 : 0;
     if constexpr (WF == OES_WFMT_FP8) {
-      const int r = c.row0 + lane;
-      if (lane < kRowTile)
-        cp_async4_take(e + 2048 + 4 * lane, base + p.s2 + ((int64_t)(r < row_hi ? r >> 7 : 0) * ns + c.s) * 4, r < row_hi);
+      const int r = crow + lane;
+      sin = lane < kRowTile && r < row_hi;
+      sp = sin ? base + p.s2 + ((int64_t)(r >> 7) * ns + cs) * 4 : p.pool;
     }
     if constexpr (WF == OES_WFMT_NVFP4) {
-      const int r = c.row0 + (lane & 15), k64 = 2 * c.s + (lane >> 4);
-      const bool in = r < row_hi && k64 * 64 < p.I;
-      cp_async4_take(e + 1024 + 4 * lane, base + p.s2 + (in ? (int64_t)k64 * p.H + r : 0) * 4, in);
-      if (lane == 0) cp_async4_take(e + 1024 + 128, base + p.gs + 4, true);
+      const int r = crow + (lane & 15);
+      sin = r < row_hi;
+      sp = sin ? base + p.s2 + ((int64_t)(2 * cs + (lane >> 4)) * p.H + r) * 4 : p.pool;
+      gsp = base + p.gs + 4;
     }
-  };
-  // the first kRing rows of h of place q, zeros past I and for rows that are not
-  auto copy_h = [&](const Place& q, int slot) {
-    const int first = tb.cum[q.b], n = __popc(tb.has[q.b]);
-    constexpr int kLanes = F::kStepK / 4;  // 16 bytes a lane
+    const int first = tb.cum[cb], n = __popc(tb.has[cb]);
 #pragma unroll
-    for (int j = 0; j < kRing; j += 32 / kLanes) {
-      const int rw = j + lane / kLanes, k = q.s * F::kStepK + lane % kLanes * 4;
-      const bool in = rw < n && k < p.I;
-      cp_async16_take(smem_u32(ring + (slot * kRing + rw) * kRow) + lane % kLanes * 16,
-                      p.h + (in ? (int64_t)tb.order[first + rw] * p.I + k : 0), in);
+    for (int j = 0; j < kRing / kHAt; ++j) {
+      const int rw = j * kHAt + lane / kHLanes;
+      hin[j] = rw < n;
+      ho[j] = (hin[j] ? tb.order[first + rw] : 0) * p.I + cs * F::kStepK + lane % kHLanes * 4;
     }
   };
+  set_rows();
   auto copy_next = [&]() {
-    if (c.row0 < row_hi) {
-      copy_w();
-      copy_h(c, at);
-      const int i = c.i;
-      next(c);
-      if (c.s == 0 || c.i != i + 1) set_rows();
+    if (crow < row_hi) {
+      const uint32_t e = smem_u32(queue + at * kEntry);
+      const bool whole = last == 0 || cs + 1 < ns;
+      if (whole) step_copy<WF>(e, w0, w1, n0, n1);
+      else step_copy_last<WF>(e, w0, w1, n0, n1, last, p.pool);
+      w0 += F::kRowBytes;
+      w1 += F::kRowBytes;
+      if constexpr (WF == OES_WFMT_FP8) {
+        if (lane < kRowTile) cp_async4_take(e + 2048 + 4 * lane, sp, sin);
+        sp += 4;
+      }
+      if constexpr (WF == OES_WFMT_NVFP4) {
+        const bool in = sin && (whole || lane < 16);
+        cp_async4_take(e + 1024 + 4 * lane, in ? sp : p.pool, in);
+        sp += sin ? (int64_t)8 * p.H : 0;
+        if (lane == 0) cp_async4_take(e + 1024 + 128, gsp, true);
+      }
+#pragma unroll
+      for (int j = 0; j < kRing / kHAt; ++j) {
+        const bool in = hin[j] && (whole || cs * F::kStepK + lane % kHLanes * 4 < p.I);
+        cp_async16_take(smem_u32(ring + (at * kRing + j * kHAt + lane / kHLanes) * kRow) + lane % kHLanes * 16,
+                        p.h + (in ? ho[j] : 0), in);
+        ho[j] += F::kStepK;
+      }
+      ++cs;
+      if (--left == 0) {
+        left = run;
+        cb = b0;
+        cs = s0;
+        crow += kRowTile;
+        set_rows();
+      } else if (cs == ns) {
+        cs = 0;
+        ++cb;
+        set_rows();
+      }
     }
     cp_async_commit();
     at = at + 1 == S ? 0 : at + 1;
@@ -860,9 +915,9 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
       o[kPart / 16] = make_uint4(b[0], b[1], b[2], b[3]);
     }
   };
-  // all rows of h of place q: those in the queue where they lie, the others here
-  auto form_rows = [&](const Place& q, int slot) {
-    const int first = tb.cum[q.b], n = __popc(tb.has[q.b]);
+  // all n rows of h of a step, `first` in the order: those in the queue where they lie, the
+  // others here
+  auto form_rows = [&](int first, int n, int step, int slot) {
     uint8_t* rows = ring + slot * kRing * kRow;
     float v[8];
     const float4* raw = reinterpret_cast<const float4*>(rows + min(hl, kRing - 1) * kRow + hp * 32);
@@ -873,7 +928,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
     form(v, rows + hl * kRow, hl, hl < kRing);
 #pragma unroll 1
     for (int j = kRing; j < n; j += kRowsAt) {
-      const int k = q.s * F::kStepK + hp * 8;
+      const int k = step * F::kStepK + hp * 8;
       const bool live = j + hl < n;
 #pragma unroll
       for (int i = 0; i < 8; ++i) v[i] = 0.0f;
@@ -887,7 +942,6 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
     }
   };
 
-  Place q = start;
   int from = 0;
   for (int row0 = row_lo; row0 < row_hi; row0 += kRowTile) {
     float acc[NG][4];
@@ -895,12 +949,12 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
     for (int n = 0; n < NG; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    while (q.row0 == row0) {
+    for (int b = b0, s1 = s0, rem = run; rem > 0; ++b) {
       // this lane's columns in the block: column g's row of h, and for columns 2t and
       // 2t + 1 whether they have a route, its weight and its row's factor; a column
       // without a route takes any row, its sums are not used
-      const int b = q.b;
       const uint32_t m = tb.has[b];
+      const int first = tb.cum[b], n_rows = __popc(m);
       uint32_t hrow[NG], hslot[NG], hfc[NG][2];
       float w[NG][2];
 #pragma unroll
@@ -922,22 +976,20 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
 #pragma unroll
         for (int i = 0; i < 4; ++i) blk[n][i] = 0.0f;
       float gs = 1.0f;
-      do {
+      const int end = min(ns, s1 + rem);
+      rem -= end - s1;
+      for (int st = s1; st < end; ++st) {
         cp_async_wait<S - 1>();
         __syncwarp();  // what other lanes brought
-        form_rows(q, from);
+        form_rows(first, n_rows, st, from);
         __syncwarp();
         const uint32_t e = smem_u32(queue + from * kEntry);
-        float d[NG][4], d1[NG][4];  // two chains of instructions
+        float d[NG][4], d1[NG][4];  // two chains of instructions with one group of tokens
 #pragma unroll
         for (int n = 0; n < NG; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            d[n][i] = F::kF16 ? 0.0f : blk[n][i];
-            d1[n][i] = 0.0f;
-          }
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh) {
+          for (int i = 0; i < 4; ++i) d[n][i] = blk[n][i];
+        auto half = [&](int hh, auto fresh, float(&to)[NG][4]) {
           uint4 B[NG][F::kB], L[NG][F::kB];
 #pragma unroll
           for (int n = 0; n < NG; ++n)
@@ -947,17 +999,21 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
               B[n][i] = lds128(a);
               L[n][i] = kParts == 2 ? lds128(a + kPart) : B[n][i];
             }
-          half_mma<WF, NG, kParts == 2>(e, hh, B, L, hh ? d1 : d);
+          half_mma<WF, NG, kParts == 2, decltype(fresh)::value>(e, hh, B, L, to);
+        };
+        half(0, Bool<F::kF16>{}, d);
+        if constexpr (NG == 1) {
+          half(1, Bool<true>{}, d1);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[0][i] += d1[0][i];
+        } else {
+          half(1, Bool<false>{}, d);
         }
-#pragma unroll
-        for (int n = 0; n < NG; ++n)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[n][i] += d1[n][i];
         if constexpr (F::kF16) {
-          float s0 = 1.0f, s1 = 1.0f;
+          float sc0 = 1.0f, sc1 = 1.0f;
           if constexpr (WF == OES_WFMT_FP8) {
-            s0 = __uint_as_float(lds32(e + 2048 + 4 * g));
-            s1 = __uint_as_float(lds32(e + 2048 + 32 + 4 * g));
+            sc0 = __uint_as_float(lds32(e + 2048 + 4 * g));
+            sc1 = __uint_as_float(lds32(e + 2048 + 32 + 4 * g));
           } else {
             gs = __uint_as_float(lds32(e + 1024 + 128));
           }
@@ -966,8 +1022,8 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float f = __uint_as_float(lds32(hfc[n][j]));
-              blk[n][j] = fmaf(s0 * f, d[n][j], blk[n][j]);
-              blk[n][2 + j] = fmaf(s1 * f, d[n][2 + j], blk[n][2 + j]);
+              blk[n][j] = fmaf(sc0 * f, d[n][j], blk[n][j]);
+              blk[n][2 + j] = fmaf(sc1 * f, d[n][2 + j], blk[n][2 + j]);
             }
         } else {
 #pragma unroll
@@ -978,8 +1034,8 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
         __syncwarp();  // read by all before the queue's entry is filled again
         from = from + 1 == S ? 0 : from + 1;
         copy_next();
-        next(q);
-      } while (q.b == b && q.row0 == row0 && q.s != 0);
+      }
+      s1 = 0;
       // a token without a route in this block takes nothing from it, not even a NaN of
       // its weights
 #pragma unroll
