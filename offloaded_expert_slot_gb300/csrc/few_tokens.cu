@@ -119,7 +119,8 @@ struct FewParams {
   uint16_t* out;
   int32_t* status;
   int64_t s13, w2, s2, gs;  // sections of an expert row
-  uint8_t* tables;          // from few_up to few_down: the number of blocks, and 16 bytes on the tables
+  uint8_t* tables;          // from few_up to few_down: the number of blocks, whether the tables are there,
+                            // and from byte 16 on the tables
   int x_ld;                 // bytes of a row of x in shared memory
   int rows_cta;             // few_down: rows of out a CTA owns
 };
@@ -517,7 +518,14 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
   const int ns = cdiv(p.H, F::kStepK);
   const Tables tb(reinterpret_cast<uint8_t*>(xf + (F::kF16 ? p.T * ns : 0)), p.T * p.k, NG);
   pdl_wait();
-  pdl_trigger();  // the down kernel; it reads what this kernel waited for, and h after this kernel's end
+  if (blockIdx.x == 0) {  // the tables are not there yet, before any CTA of the down kernel can look
+    if (tid == 0) {
+      *reinterpret_cast<volatile int32_t*>(p.tables + 4) = 0;
+      __threadfence();
+    }
+    __syncthreads();
+  }
+  pdl_trigger();
   // x, with zeros up to a whole step
   const int xc = ns * (F::kStepK / 8);
   auto load_x = [&](int first, int n) {
@@ -637,6 +645,11 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
     if (tid == 0) *reinterpret_cast<int32_t*>(p.tables) = nb;
     for (int i = tid; i < tables_bytes(p.T * p.k, NG) / 4; i += kThreads)
       reinterpret_cast<int32_t*>(p.tables + 16)[i] = tb.ids[i];
+    __syncthreads();
+    if (tid == 0) {
+      __threadfence();
+      asm volatile("st.release.gpu.global.s32 [%0], 1;" ::"l"(p.tables + 4) : "memory");
+    }
   }
 
   // columns past the tokens are not used: any row does
@@ -782,7 +795,20 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
   float* hf = reinterpret_cast<float*>(more + (8 * NG - kRing) * kLine);  // factors (kF16)
   float* part = reinterpret_cast<float*>(smem + W * down_warp_bytes<WF, NG, S>());  // [warp][lane][4 NG]
   const Tables tb(reinterpret_cast<uint8_t*>(part + kThreads * 4 * NG), p.T * p.k, NG);
-  pdl_wait();
+  // A CTA starts where one of few_up_kernel's has ended, some microseconds before all have
+  // and what they wrote is sure to be seen.  The tables were written early and say
+  // themselves that they are there; all else but h was complete before few_up_kernel passed its
+  // own wait.  So where the tables are there (nothing waits for them), the queues are filled with
+  // weights at once, and only h is waited for.
+  __shared__ int s_early;
+  if (tid == 0) {
+    int f;
+    asm volatile("ld.acquire.gpu.global.s32 %0, [%1];" : "=r"(f) : "l"(p.tables + 4) : "memory");
+    s_early = f;
+  }
+  __syncthreads();
+  const bool early = s_early == 1;
+  if (!early) pdl_wait();
   // The tables as few_up_kernel left them.  A workspace that another call writes at the
   // same time would be a mistake of the caller's, which no address may follow: whatever
   // stands here, indexes are kept within their ranges.
@@ -848,7 +874,11 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
     }
   };
   set_rows();
-  auto copy_next = [&]() {
+  auto copy_h = [&](int slot, int j, int o) {  // o < 0: zeros
+    cp_async16_take(smem_u32(ring + (slot * kRing + j * kHAt + lane / kHLanes) * kRow) + lane % kHLanes * 16,
+                    p.h + max(o, 0), o >= 0);
+  };
+  auto copy_next = [&](int* later) {  // later: takes what copy_h is to be given
     if (crow < row_hi) {
       const uint32_t e = smem_u32(queue + at * kEntry);
       const bool whole = last == 0 || cs + 1 < ns;
@@ -866,11 +896,13 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
         sp += sin ? (int64_t)8 * p.H : 0;
         if (lane == 0) cp_async4_take(e + 1024 + 128, gsp, true);
       }
+      const bool in_k = whole || cs * F::kStepK + lane % kHLanes * 4 < p.I;
 #pragma unroll
       for (int j = 0; j < kRing / kHAt; ++j) {
-        const bool in = hin[j] && (whole || cs * F::kStepK + lane % kHLanes * 4 < p.I);
-        cp_async16_take(smem_u32(ring + (at * kRing + j * kHAt + lane / kHLanes) * kRow) + lane % kHLanes * 16,
-                        p.h + (in ? ho[j] : 0), in);
+        const bool in = hin[j] && in_k;
+        const int o = in ? ho[j] : -1;
+        if (later) later[j] = o;
+        else copy_h(at, j, o);
         ho[j] += F::kStepK;
       }
       ++cs;
@@ -889,7 +921,22 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
     cp_async_commit();
     at = at + 1 == S ? 0 : at + 1;
   };
-  for (int i = 0; i < S; ++i) copy_next();
+  {
+    int later[S][kRing / kHAt];  // the first steps' rows of h
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+#pragma unroll
+      for (int j = 0; j < kRing / kHAt; ++j) later[i][j] = -1;
+      copy_next(later[i]);
+    }
+    if (early) pdl_wait();  // h
+#pragma unroll
+    for (int i = 0; i < S; ++i) {
+#pragma unroll
+      for (int j = 0; j < kRing / kHAt; ++j) copy_h(i, j, later[i][j]);
+      cp_async_commit();
+    }
+  }
 
   // 8 values of row j of the block to their form, at `to`
   const int hl = lane / kRowLanes, hp = lane % kRowLanes;
@@ -1033,7 +1080,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
         }
         __syncwarp();  // read by all before the queue's entry is filled again
         from = from + 1 == S ? 0 : from + 1;
-        copy_next();
+        copy_next(nullptr);
       }
       s1 = 0;
       // a token without a route in this block takes nothing from it, not even a NaN of
