@@ -446,15 +446,20 @@ size_t moe_layer_few_tokens_workspace_size(const oes_routed_experts *view, int T
  * Weights are decoded exactly, and the activations are not quantised, in the FP8
  * format neither (moe_grouped_gemm_slots quantises them there): sums are fp32, h
  * keeps 16 significant bits for bf16 weights and 11 for the others (with a common
- * exponent for each 128 values, so of any size), and out is rounded once.  The result does not depend on
- * timing; it is not bit for bit that of moe_grouped_gemm_slots, which rounds each
- * route's output row to bf16 before the weighted sum.
+ * exponent for each 128 values, so of any size), and out is rounded once.  The
+ * result does not depend on timing; it is not bit for bit that of
+ * moe_grouped_gemm_slots, which rounds each route's output row to bf16 before the
+ * weighted sum.
+ * The call makes no host synchronisation and can be captured into a CUDA graph
+ * (run it once before, since the first call of a size sets one-time kernel
+ * attributes).  The workspace holds what passes between the launches: calls that
+ * may overlap need their own.
  * x: device [T, H] bf16, pool, x and workspace 16-byte aligned; out: device
  * [T, H] bf16; status: device word or NULL.  H, I multiples of 64 in
  * [64, 16384], k <= OES_MAX_TOPK (and <= E with logits).  Layers of more than
  * 512 experts take one launch more for the routing, and rows of x that do not
- * fit in shared memory together (H above about 4700 for 16 tokens) take two
- * launches for each group of tokens that do. */
+ * fit in shared memory together (H above 4000 to 4700 for 16 tokens, by k) take
+ * two launches for each group of tokens that do. */
 int moe_layer_few_tokens(const oes_routed_experts *view, const uint16_t *x, int T, int k,
                          const void *logits, int dtype, int32_t *ids, float *weights,
                          void *workspace, size_t workspace_bytes, uint16_t *out, int32_t *status,
@@ -523,8 +528,9 @@ size_t moe_int8_gemm_workspace_size(int T, int K, int N);
  * OES_F32, row stride out_ld values.  xq and wq are 16-byte aligned and their row
  * strides multiples of 16 (bytes past K in a row are not read).  workspace: device
  * scratch of moe_int8_gemm_workspace_size(T, K, N) bytes, 256-byte aligned (NULL
- * where that is 0); calls that may overlap need their own.  T >= 0,
- * 1 <= K <= 65536, 1 <= N <= 2^24.  status: device word or NULL. */
+ * where that is 0); calls that may overlap need their own.  0 <= T <= 2^28,
+ * 1 <= K <= 65536, 1 <= N <= 2^24.  status: device word or NULL.  The first call
+ * of a size sets one-time kernel attributes: run it once before capturing it. */
 int moe_int8_gemm(const int8_t *xq, int64_t xq_ld, const float *xs, int T, int K, const int8_t *wq,
                   int64_t wq_ld, const float *ws, int N, void *out, int dtype, int64_t out_ld,
                   void *workspace, size_t workspace_bytes, int32_t *status, oes_stream_t stream);

@@ -5,33 +5,39 @@
 //
 // A few tokens reach a few experts each, so the layer is a stream of those
 // experts' weights (one token x 10 of 512 FP8 experts: 47 MB, 7 us at the copy
-// rate), and everything around that stream is latency.  Both kernels read the
-// logits and work out the routing, the experts' slots and the tables of the
-// chunk in every CTA, instead of waiting for a kernel that does (the same
-// device code as moe_route_topk, so the same ids and weights bit for bit).
+// rate), and everything around that stream is latency.
 //
-//   few_up_kernel    unit = (block, 8 rows of I): the 8 gate rows and the same
-//                    8 up rows are the 16 rows of one matrix instruction, so
-//                    that a lane has both factors of its h.  The CTA's eight
-//                    warps share K.
+//   few_up_kernel    routes the tokens and makes the chunk's tables in every CTA
+//                    (waiting for a kernel that does costs more), then h: a unit is
+//                    8 rows of I of one block, whose 8 gate rows and same 8 up rows
+//                    are the 16 rows of one matrix instruction, so that a lane has
+//                    both factors of its h.
 //   few_down_kernel  a CTA owns up to 16 rows of the output at a time and goes
-//                    through all blocks for them, its warps sharing
-//                    (block, K) steps; the weighted sum over a token's routes
-//                    is the accumulator.  It is launched while the first kernel
-//                    runs, repeats the routing and fills its queues with W2;
-//                    only the loads of h wait.
+//                    through all blocks for them, its warps sharing the (block, step
+//                    of K); the weighted sum over a token's routes is the
+//                    accumulator.  It takes the tables from the first kernel, and
+//                    its CTAs fill their queues with W2 while the last of that
+//                    kernel's still run.
 //
 // A block is one expert with at most one route of each token: column c of the
 // matrix instruction is token c, in both kernels.  An expert that a token lists
 // twice gets a second block for the second route.
 //
 // Weights go from memory into a queue of each lane's own (16-byte asynchronous
-// copies, read back by the same lane), so a warp has kept its next steps in
+// copies, read back by the same lane), so a warp keeps its next steps in
 // flight without registers and without a barrier.  The instructions are the
-// warp-wide m16n8k16: at 8 columns the tensor work is a hundredth of what the
-// stream takes, and tcgen05 tiles (128 weight rows, operands through shared
-// memory and TMEM) gave 9 to 31 % of the copy rate here, held up by their set-up
-// and hand-offs.
+// warp-wide m16n8k16, whose tensor work at 8 columns is a small part of what the
+// stream takes (13 % of the pipe); tcgen05 tiles (128 weight rows, operands through
+// shared memory and TMEM) gave 9 to 31 % of the copy rate for one token, held up by
+// their set-up and hand-offs.
+//
+// Measured (10 of 512 experts of 2048 x 768, replayed from a graph): 1 token FP8 17 us
+// (2.7 TB/s), bf16 22.7 us (4.2); 4 tokens NVFP4 40.7 us (2.5); 16 tokens bf16 220 us (5.9
+// TB/s, 88 % of the copy rate), FP8 136 us (4.8), NVFP4 143 us (2.6).  16 bf16 tokens are bound
+// by memory; the 8- and 4-bit formats by the instructions that decode and multiply (issue
+// slots 50 to 57 % busy, about 170 a 2 KB step of the first kernel and 240 of the second);
+// one token by latency: 4.6 us to the first weights (logits, top-k, tables, slots), 2 to 3
+// from one kernel to the next, 1.5 for the last sums.
 //
 // Weights are exact in 16 bits: bf16 as they are; e4m3 as f16, their block scales on
 // the fp32 sums of each 128 of K; e2m1 x e4m3 as f16, the global scale on the sums.
@@ -50,21 +56,6 @@
 #include "warp_mma.cuh"
 
 namespace oes {
-
-// Logits read through L2: the second kernel reads them while the first still
-// runs (see few_down_kernel).
-struct L2F32 { float v; };
-struct L2Bf16 { uint16_t v; };
-template <int V>
-__device__ __forceinline__ void load_logits(const L2F32* p, float* o) {
-  static_assert(V == 1, "one a load");
-  o[0] = __ldcg(reinterpret_cast<const float*>(p));
-}
-template <int V>
-__device__ __forceinline__ void load_logits(const L2Bf16* p, float* o) {
-  static_assert(V == 1, "one a load");
-  o[0] = bf16_f32(__ldcg(reinterpret_cast<const unsigned short*>(p)));
-}
 
 namespace {
 
@@ -163,7 +154,7 @@ __device__ __forceinline__ void topk_few(const LT* __restrict__ row, int E, int 
 #pragma unroll
   for (int j = 0; j < Q; ++j) {
     v[j] = __int_as_float(0x7fffffff);  // NaN: no expert
-    if (lane + 32 * j < E) load_logits<1>(row + lane + 32 * j, v + j);
+    if (lane + 32 * j < E) v[j] = load_logit(row + lane + 32 * j);
   }
   float m = -INFINITY;  // fmaxf skips NaN
 #pragma unroll
@@ -244,9 +235,9 @@ __device__ __forceinline__ int few_tables(const FewParams& p, const Tables& tb, 
       int32_t* ids = tb.ids + t * p.k;
       float* w = tb.w + t * p.k;
       if (p.logits_bf16)
-        topk_few(static_cast<const L2Bf16*>(p.logits) + (size_t)t * p.E, p.E, p.k, lane, ids, w, cand[warp]);
+        topk_few(static_cast<const uint16_t*>(p.logits) + (size_t)t * p.E, p.E, p.k, lane, ids, w, cand[warp]);
       else
-        topk_few(static_cast<const L2F32*>(p.logits) + (size_t)t * p.E, p.E, p.k, lane, ids, w, cand[warp]);
+        topk_few(static_cast<const float*>(p.logits) + (size_t)t * p.E, p.E, p.k, lane, ids, w, cand[warp]);
     }
   }
   if (routers == 0) init(tid, nt);
@@ -499,11 +490,17 @@ __device__ __forceinline__ float f16_group(const float (&v)[8], uint4& out) {
   return __uint_as_float((ex - 14u) << 23);
 }
 
+template <int V>
+struct Int {
+  static constexpr int value = V;
+};
+
 // ------------------------------------------------------------------ gate, up
 // A unit is 8 rows of I of a block.  The chunk's units are dealt out to the CTAs in
 // runs, and a CTA's to its teams of KS warps, which share the unit's K range.  KS 1: a
-// lane ends with both factors of its h, and no barrier follows the tables.  More where
-// there are few units (see launch_few): one warp has 16 KB in flight at most.
+// lane ends with both factors of its h, and no barrier follows the tables.  (With eight
+// warps a unit throughout, 16 tokens x 10 of 512 FP8 experts took 243 us, with one 166.)
+// More where there are few units (see launch_few): one warp keeps 8 KB in flight.
 template <int WF, int NG, int KS, int S>
 __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
   using F = Fmt<WF>;
@@ -638,6 +635,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
     cp_async_commit();
     at = at + 1 == S ? 0 : at + 1;
   };
+#pragma unroll 1  // 8 tokens' FP8 time is 1 to 2 % longer with the copies written out
   for (int i = 0; i < S; ++i) copy_next();
   if (blockIdx.x == 0) {
     // the tables, for the down kernel
@@ -661,10 +659,22 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
     for (int j = 0; j < 2; ++j) xfc[n][j] = smem_u32(xf + min(8 * n + 2 * t + j, p.T - 1) * ns);
   }
   int from = 0, buf = 0;
-  for (; q.j < hi; next(q), buf ^= 1) {
-    float acc[NG][4];
+  // A unit for GN groups of eight tokens from n0 on.  Of more than eight tokens most blocks
+  // have a route or two, in one group, and the other's instructions are left out, here
+  // and in the down kernel: 16 tokens x 10 of 512 experts in bf16 228 -> 220 us, NVFP4 152 -> 144,
+  // 12 tokens 181 -> 173 and 124 -> 116.
+  auto unit = [&](auto groups, int n0) {
+    constexpr int GN = decltype(groups)::value;
+    uint32_t ub[GN], uf[GN][2];
 #pragma unroll
-    for (int n = 0; n < NG; ++n)
+    for (int n = 0; n < GN; ++n) {
+      ub[n] = GN < NG && n0 > 0 ? xb[NG - 1] : xb[n];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) uf[n][j] = GN < NG && n0 > 0 ? xfc[NG - 1][j] : xfc[n][j];
+    }
+    float acc[GN][4];
+#pragma unroll
+    for (int n = 0; n < GN; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
     float gs = 1.0f;
@@ -672,26 +682,26 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
       cp_async_wait<S - 1>();
       if (F::kScale) __syncwarp();  // scales that other lanes copied
       const uint32_t e = smem_u32(queue + from * kEntry);
-      float d[NG][4], d1[NG][4];  // two chains of instructions with one group of tokens
+      float d[GN][4], d1[GN][4];  // two chains of instructions with one group of tokens
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+      for (int n = 0; n < GN; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[n][i] = acc[n][i];
-      uint4 B[2][NG][F::kB];
+      uint4 B[2][GN][F::kB];
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
+        for (int n = 0; n < GN; ++n)
 #pragma unroll
           for (int i = 0; i < F::kB; ++i)
-            B[hh][n][i] = lds128(xb[n] + 2 * (s * F::kStepK + piece_k<WF>(hh, i) - piece_k<WF>(0, 0)));
-      half_mma<WF, NG, false, F::kF16>(e, 0, B[0], B[0], d);
-      if constexpr (NG == 1) {
-        half_mma<WF, NG, false, true>(e, 1, B[1], B[1], d1);
+            B[hh][n][i] = lds128(ub[n] + 2 * (s * F::kStepK + piece_k<WF>(hh, i) - piece_k<WF>(0, 0)));
+      half_mma<WF, GN, false, F::kF16>(e, 0, B[0], B[0], d);
+      if constexpr (GN == 1) {
+        half_mma<WF, GN, false, true>(e, 1, B[1], B[1], d1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[0][i] += d1[0][i];
       } else {
-        half_mma<WF, NG, false, false>(e, 1, B[1], B[1], d);
+        half_mma<WF, GN, false, false>(e, 1, B[1], B[1], d);
       }
       if constexpr (F::kF16) {
         float sg = 1.0f, su = 1.0f;
@@ -703,16 +713,16 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
           gs = __uint_as_float(lds32(e + 1024 + 128));
         }
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
+        for (int n = 0; n < GN; ++n)
 #pragma unroll
           for (int j = 0; j < 2; ++j) {
-            const float f = __uint_as_float(lds32(xfc[n][j] + 4 * s));
+            const float f = __uint_as_float(lds32(uf[n][j] + 4 * s));
             acc[n][j] = fmaf(sg * f, d[n][j], acc[n][j]);
             acc[n][2 + j] = fmaf(su * f, d[n][2 + j], acc[n][2 + j]);
           }
       } else {
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
+        for (int n = 0; n < GN; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[n][i] = d[n][i];
       }
@@ -722,22 +732,22 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
     }
     if constexpr (KS == 1) {
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+      for (int n = 0; n < GN; ++n)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int r = tb.route[q.b * 8 * NG + 8 * n + 2 * t + j];
+          const int r = tb.route[q.b * 8 * NG + 8 * (n0 + n) + 2 * t + j];
           if (r >= 0) p.h[(int64_t)r * p.I + q.r * 8 + g] = silu_f32(gs * acc[n][j]) * (gs * acc[n][2 + j]);
         }
     } else {
       float* mine = part + ((buf * W + warp) * 32 + lane) * (4 * NG);
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+      for (int n = 0; n < GN; ++n)
         *reinterpret_cast<float4*>(mine + 4 * n) =
             make_float4(gs * acc[n][0], gs * acc[n][1], gs * acc[n][2], gs * acc[n][3]);
       asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(KS * 32) : "memory");
       const int tt = tid - team * KS * 32;
-      if (tt < 64 * NG) {
-        const int col = tt >> 3, r8 = tt & 7, r = tb.route[q.b * 8 * NG + col];
+      if (tt < 64 * GN) {
+        const int col = tt >> 3, r8 = tt & 7, r = tb.route[q.b * 8 * NG + 8 * n0 + col];
         if (r >= 0) {
           const float* v = part + ((buf * W + team * KS) * 32 + r8 * 4 + (col & 7) / 2) * (4 * NG) + (col >> 3) * 4 + (col & 1);
           float gate = 0.0f, upv = 0.0f;
@@ -749,6 +759,15 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
           p.h[(int64_t)r * p.I + q.r * 8 + r8] = silu_f32(gate) * upv;
         }
       }
+    }
+  };
+  for (; q.j < hi; next(q), buf ^= 1) {
+    if constexpr (NG == 1) {
+      unit(Int<1>{}, 0);
+    } else {
+      const uint32_t m = tb.has[q.b];
+      if ((m & 0xFFu) && m >> 8) unit(Int<2>{}, 0);
+      else unit(Int<1>{}, m >> 8 ? 1 : 0);
     }
   }
 }
@@ -762,10 +781,6 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
 // experts ran at 1.9 TB/s; one step ahead, 4 tokens x 10 of 512 NVFP4 experts at 2.2.
 // Staged by the CTA for several blocks at a time, barriers and bookkeeping did.)
 constexpr int kRing = 2;  // rows of h of a step in the queue
-template <bool V>
-struct Bool {
-  static constexpr bool value = V;
-};
 
 // A row of h: kRow bytes, fp32 or in its form; kLine bytes of its form alone, in parts
 // kPart apart (bf16 rows have two), which spread over the banks.
@@ -996,65 +1011,63 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
     for (int n = 0; n < NG; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    for (int b = b0, s1 = s0, rem = run; rem > 0; ++b) {
+    // block b's steps from s1 to end, for GN groups of tokens from n0 on
+    auto block = [&](auto groups, int n0, int b, uint32_t m, int s1, int end) {
+      constexpr int GN = decltype(groups)::value;
       // this lane's columns in the block: column g's row of h, and for columns 2t and
       // 2t + 1 whether they have a route, its weight and its row's factor; a column
       // without a route takes any row, its sums are not used
-      const uint32_t m = tb.has[b];
       const int first = tb.cum[b], n_rows = __popc(m);
-      uint32_t hrow[NG], hslot[NG], hfc[NG][2];
-      float w[NG][2];
+      uint32_t hrow[GN], hslot[GN], hfc[GN][2];
+      float w[GN][2];
 #pragma unroll
-      for (int n = 0; n < NG; ++n) {
+      for (int n = 0; n < GN; ++n) {
         auto row_of = [&](int col) { return (m >> col) & 1u ? __popc(m & ((1u << col) - 1)) : 0; };
-        const int r = row_of(8 * n + g);
+        const int r = row_of(8 * (n0 + n) + g);
         hslot[n] = r < kRing ? kRing * kRow : 0;
         hrow[n] = smem_u32(r < kRing ? ring + r * kRow : more + (r - kRing) * kLine) + 2 * piece_k<WF>(0, 0);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const int col = 8 * n + 2 * t + j;
+          const int col = 8 * (n0 + n) + 2 * t + j;
           w[n][j] = (m >> col) & 1u ? tb.w[max((int)tb.route[b * 8 * NG + col], 0)] : 0.0f;
           hfc[n][j] = smem_u32(hf + row_of(col));
         }
       }
-      float blk[NG][4];
+      float blk[GN][4];
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+      for (int n = 0; n < GN; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) blk[n][i] = 0.0f;
       float gs = 1.0f;
-      const int end = min(ns, s1 + rem);
-      rem -= end - s1;
       for (int st = s1; st < end; ++st) {
         cp_async_wait<S - 1>();
         __syncwarp();  // what other lanes brought
         form_rows(first, n_rows, st, from);
         __syncwarp();
         const uint32_t e = smem_u32(queue + from * kEntry);
-        float d[NG][4], d1[NG][4];  // two chains of instructions with one group of tokens
+        float d[GN][4], d1[GN][4];  // two chains of instructions with one group of tokens
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
+        for (int n = 0; n < GN; ++n)
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[n][i] = blk[n][i];
-        auto half = [&](int hh, auto fresh, float(&to)[NG][4]) {
-          uint4 B[NG][F::kB], L[NG][F::kB];
+        uint4 B[2][GN][F::kB], L[2][GN][F::kB];
 #pragma unroll
-          for (int n = 0; n < NG; ++n)
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+          for (int n = 0; n < GN; ++n)
 #pragma unroll
             for (int i = 0; i < F::kB; ++i) {
               const uint32_t a = hrow[n] + from * hslot[n] + 2 * (piece_k<WF>(hh, i) - piece_k<WF>(0, 0));
-              B[n][i] = lds128(a);
-              L[n][i] = kParts == 2 ? lds128(a + kPart) : B[n][i];
+              B[hh][n][i] = lds128(a);
+              L[hh][n][i] = kParts == 2 ? lds128(a + kPart) : B[hh][n][i];
             }
-          half_mma<WF, NG, kParts == 2, decltype(fresh)::value>(e, hh, B, L, to);
-        };
-        half(0, Bool<F::kF16>{}, d);
-        if constexpr (NG == 1) {
-          half(1, Bool<true>{}, d1);
+        half_mma<WF, GN, kParts == 2, F::kF16>(e, 0, B[0], L[0], d);
+        if constexpr (GN == 1) {
+          half_mma<WF, GN, kParts == 2, true>(e, 1, B[1], L[1], d1);
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[0][i] += d1[0][i];
         } else {
-          half(1, Bool<false>{}, d);
+          half_mma<WF, GN, kParts == 2, false>(e, 1, B[1], L[1], d);
         }
         if constexpr (F::kF16) {
           float sc0 = 1.0f, sc1 = 1.0f;
@@ -1065,7 +1078,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
             gs = __uint_as_float(lds32(e + 1024 + 128));
           }
 #pragma unroll
-          for (int n = 0; n < NG; ++n)
+          for (int n = 0; n < GN; ++n)
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
               const float f = __uint_as_float(lds32(hfc[n][j]));
@@ -1074,7 +1087,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
             }
         } else {
 #pragma unroll
-          for (int n = 0; n < NG; ++n)
+          for (int n = 0; n < GN; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) blk[n][i] = d[n][i];
         }
@@ -1082,14 +1095,29 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
         from = from + 1 == S ? 0 : from + 1;
         copy_next(nullptr);
       }
-      s1 = 0;
       // a token without a route in this block takes nothing from it, not even a NaN of
       // its weights
 #pragma unroll
-      for (int n = 0; n < NG; ++n)
+      for (int n = 0; n < GN; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-          if ((m >> (8 * n + 2 * t + (i & 1))) & 1u) acc[n][i] = fmaf(w[n][i & 1] * gs, blk[n][i], acc[n][i]);
+          if ((m >> (8 * (n0 + n) + 2 * t + (i & 1))) & 1u) {
+            const float f = w[n][i & 1] * gs;
+            if (GN == NG || n0 == 0) acc[n][i] = fmaf(f, blk[n][i], acc[n][i]);
+            else acc[NG - 1][i] = fmaf(f, blk[n][i], acc[NG - 1][i]);
+          }
+    };
+    for (int b = b0, s1 = s0, rem = run; rem > 0; ++b) {
+      const int end = min(ns, s1 + rem);
+      const uint32_t m = tb.has[b];
+      if constexpr (NG == 1) {
+        block(Int<1>{}, 0, b, m, s1, end);
+      } else {
+        if ((m & 0xFFu) && m >> 8) block(Int<2>{}, 0, b, m, s1, end);
+        else block(Int<1>{}, m >> 8 ? 1 : 0, b, m, s1, end);
+      }
+      rem -= end - s1;
+      s1 = 0;
     }
     if (row0 > row_lo) __syncthreads();  // the tile before has read its sums
     float* mine = part + (warp * 32 + lane) * (4 * NG);
@@ -1158,7 +1186,7 @@ template <int WF, int NG>
 int launch_few(FewParams p, cudaStream_t stream) {
   p.x_ld = x_stride<WF>(p.H);
   p.rows_cta = ceil_div(p.H, num_sms());
-  // Warps a unit: one of a CTA's sixteen keeps 16 KB in flight, so that few units on an
+  // Warps a unit: one of a CTA's sixteen keeps 8 KB in flight, so that few units on an
   // SM do not fill it.  Up to two units an SM: 1 token x 2 experts of 2048 x 128, bf16,
   // takes 8.7 us with 16 warps a unit and 11.8 with one, 1 x 1 of 4096 x 512 10.7 and
   // 17.1; up to eight: 1 x 10 of 2048 x 768 24.4 us with 4 and 25.1 with one (with 16,
@@ -1166,7 +1194,7 @@ int launch_few(FewParams p, cudaStream_t stream) {
   const int64_t units = (int64_t)p.T * p.k * (p.I / 8);  // at most
   const auto fits = [&](size_t smem) { return smem <= kSmemMost; };
   int rc;
-  if (units <= 2 * num_sms()) rc = launch_up<WF, NG, 16, 2>(p, stream);
+  if (units <= 2 * num_sms() && fits(up_smem<WF, NG, 16, 2>(p.T, p.k, p.H))) rc = launch_up<WF, NG, 16, 2>(p, stream);
   else if (units <= 8 * num_sms() && fits(up_smem<WF, NG, 4, 3>(p.T, p.k, p.H))) rc = launch_up<WF, NG, 4, 3>(p, stream);
   else if (fits(up_smem<WF, NG, 1, 4>(p.T, p.k, p.H))) rc = launch_up<WF, NG, 1, 4>(p, stream);
   else rc = launch_up<WF, NG, 1, 2>(p, stream);
@@ -1176,11 +1204,11 @@ int launch_few(FewParams p, cudaStream_t stream) {
   return launch_down<WF, NG, 3>(p, stream);
 }
 
-// Most tokens whose rows of x fit beside the queues.
+// Most tokens whose rows of x fit beside the shortest queues.
 template <int WF>
 int group_tokens(int T, int k, int H) {
   int n = T;
-  while (n > 1 && (n > 8 ? up_smem<WF, 2, 16, 2>(n, k, H) : up_smem<WF, 1, 16, 2>(n, k, H)) > kSmemMost) --n;
+  while (n > 1 && (n > 8 ? up_smem<WF, 2, 1, 2>(n, k, H) : up_smem<WF, 1, 1, 2>(n, k, H)) > kSmemMost) --n;
   return n;
 }
 

@@ -905,7 +905,9 @@ int run_stream(const StreamArgs& a, const Cut& c, cudaStream_t stream) {
                                                                     : launch_stream<4, OT>(a, c, stream);
 }
 
-bool sizes_ok(int T, int K, int N) { return T >= 0 && K >= 1 && K <= 65536 && N >= 1 && N <= (1 << 24); }
+bool sizes_ok(int T, int K, int N) {
+  return T >= 0 && T <= (1 << 28) && K >= 1 && K <= 65536 && N >= 1 && N <= (1 << 24);
+}
 
 }  // namespace
 }  // namespace oes

@@ -59,7 +59,7 @@ class Layer:
         """out against 64 bits, with the routing the call wrote or read.  Bound
         of each element: every fp32 sum of n products, in any order, is off by at
         most (n / 16 + 18) units of 2^-23 of the sum of the products' sizes (an
-        instruction adds 16 of them at a time to the sum before, and eight warps'
+        instruction adds 16 of them at a time to the sum before, and sixteen warps'
         sums are added); silu is off by 17 x 2^-24 of itself and its slope is
         below 1.1; h rounds by half a step (of the second of two bf16 numbers; of f16,
         whose smallest steps are 2^-39 of the largest value nearby), and out."""
@@ -185,6 +185,24 @@ def test_wide_rows(fmt, T, H):
     m.set_routes(ids, rng(6).random((T, 2)))
     m.call()
     m.check()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "fp8", "nvfp4"])
+@pytest.mark.parametrize("T,H,I", [(16, 128, 64), (9, 192, 1024), (16, 64, 4096)])
+def test_experts_of_early_late_and_all_tokens(fmt, T, H, I):
+    """Experts that only tokens before the ninth chose, only tokens from there on, both, and one token alone; a NaN
+    of one token's row stays in its own result."""
+    m = Layer(fmt, T, 3, 6, H, I)
+    ids = np.array([[0 if t < 8 else 1, 2, 3 if t == 2 else 4 if t == 8 else 5 if t % 5 == 0 else -1] for t in range(T)])
+    m.set_routes(ids, rng(12).random((T, 3)) + 0.1)
+    m.call()
+    m.check()
+    clean = m.out.clone()
+    m.x[T - 1, 5] = float("nan")
+    m.call()
+    torch.cuda.synchronize()
+    assert torch.isnan(m.out[T - 1].float()).all()
+    assert torch.equal(m.out[: T - 1], clean[: T - 1])
 
 
 def test_wide_rows_from_logits_in_groups():

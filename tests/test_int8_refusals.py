@@ -30,7 +30,8 @@ def test_quantize_refuses(kw):
     refused(oes.moe_int8_quantize, *a.values(), dtype=dtype)
 
 
-@pytest.mark.parametrize("kw", [dict(T=-1), dict(K=0), dict(N=0), dict(K=65537), dict(N=(1 << 24) + 1), dict(xq=0),
+@pytest.mark.parametrize("kw", [dict(T=-1), dict(T=(1 << 28) + 1), dict(K=0), dict(N=0), dict(K=65537),
+                                dict(N=(1 << 24) + 1), dict(xq=0),
                                 dict(xs=0), dict(wq=0), dict(ws=0), dict(out=0), dict(xq=P + 8), dict(wq=P + 4),
                                 dict(xq_ld=136), dict(wq_ld=200), dict(xq_ld=112), dict(wq_ld=0), dict(out_ld=63),
                                 dict(xs=P + 1), dict(ws=P + 2), dict(out=P + 1), dict(dtype=5), dict(status=P + 2),
