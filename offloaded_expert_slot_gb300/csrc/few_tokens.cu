@@ -31,9 +31,9 @@
 // shared memory and TMEM) gave 9 to 31 % of the copy rate for one token, held up by
 // their set-up and hand-offs.
 //
-// Measured (10 of 512 experts of 2048 x 768, replayed from a graph): 1 token FP8 17 us
-// (2.7 TB/s), bf16 22.7 us (4.2); 4 tokens NVFP4 40.7 us (2.5); 16 tokens bf16 220 us (5.9
-// TB/s, 88 % of the copy rate), FP8 136 us (4.8), NVFP4 143 us (2.6).  16 bf16 tokens are bound
+// Measured (10 of 512 experts of 2048 x 768, replayed from a graph): 1 token FP8 16.9 us
+// (2.8 TB/s), bf16 21.6 us (4.4); 4 tokens NVFP4 39.9 us (2.6); 16 tokens bf16 205 to 213 us (6.1 to
+// 6.4 TB/s, 90 to 94 % of the copy rate, by GPU), FP8 137 us (4.8), NVFP4 144 us (2.5).  16 bf16 tokens are bound
 // by memory; the 8- and 4-bit formats by the instructions that decode and multiply (issue
 // slots 50 to 57 % busy, about 170 a 2 KB step of the first kernel and 240 of the second);
 // one token by latency: 4.6 us to the first weights (logits, top-k, tables, slots), 2 to 3
@@ -106,7 +106,7 @@ struct FewParams {
   int logits_bf16;
   int32_t* ids;
   float* weights;
-  float* h;  // [T k, I]
+  void* h;  // [T k, I] fp32, or for bf16 weights two bf16 a word: the value and what its rounding left
   uint16_t* out;
   int32_t* status;
   int64_t s13, w2, s2, gs;  // sections of an expert row
@@ -490,6 +490,21 @@ __device__ __forceinline__ float f16_group(const float (&v)[8], uint4& out) {
   return __uint_as_float((ex - 14u) << 23);
 }
 
+// One value of a route's h, for the down kernel: fp32, or two bf16 in a word, the second what
+// the first's rounding left (16 significant bits).
+template <int WF>
+__device__ __forceinline__ void store_h(const FewParams& p, int r, int i, float v) {
+  if constexpr (Fmt<WF>::kF16) {
+    static_cast<float*>(p.h)[(int64_t)r * p.I + i] = v;
+  } else {
+    const uint32_t hi = f32_bf16(v);
+    const float f = bf16_f32(hi);
+    // an infinity leaves nothing (and not the NaN of its difference)
+    const uint32_t lo = f32_bf16(fabsf(f) < INFINITY ? v - f : 0.0f);
+    static_cast<uint32_t*>(p.h)[(int64_t)r * p.I + i] = hi | lo << 16;
+  }
+}
+
 template <int V>
 struct Int {
   static constexpr int value = V;
@@ -736,7 +751,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int r = tb.route[q.b * 8 * NG + 8 * (n0 + n) + 2 * t + j];
-          if (r >= 0) p.h[(int64_t)r * p.I + q.r * 8 + g] = silu_f32(gs * acc[n][j]) * (gs * acc[n][2 + j]);
+          if (r >= 0) store_h<WF>(p, r, q.r * 8 + g, silu_f32(gs * acc[n][j]) * (gs * acc[n][2 + j]));
         }
     } else {
       float* mine = part + ((buf * W + warp) * 32 + lane) * (4 * NG);
@@ -756,7 +771,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
             gate += v[w * 32 * 4 * NG];
             upv += v[w * 32 * 4 * NG + 2];
           }
-          p.h[(int64_t)r * p.I + q.r * 8 + r8] = silu_f32(gate) * upv;
+          store_h<WF>(p, r, q.r * 8 + r8, silu_f32(gate) * upv);
         }
       }
     }
@@ -774,21 +789,22 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
 
 // ---------------------------------------------------------------------- down
 // The (block, step of K) of a tile of rows are dealt out to the CTA's warps in runs.
-// The rows of h of a step's tokens come through the warp's queue too, in fp32, the
-// first kRing of them (few blocks have more; those are loaded when they are needed),
-// and are put into the form that the instructions take where they lie.  (Loaded by
-// each lane as it needs them, their latency set the pace: 16 tokens x 10 of 200 bf16
-// experts ran at 1.9 TB/s; one step ahead, 4 tokens x 10 of 512 NVFP4 experts at 2.2.
-// Staged by the CTA for several blocks at a time, barriers and bookkeeping did.)
+// The rows of h of a step's tokens come through the warp's queue too, the first kRing of them
+// (few blocks have more; those are loaded when they are needed).  For 8- and 4-bit weights they
+// are fp32, and become f16 where they lie; for bf16 weights the first kernel left each value as two
+// bf16 in a word, and lanes part them on their way to the instruction (splitting fp32 rows here, in every
+// CTA, took 22.5 us for one token and 209 for sixteen, not 21.6 and 205; two planes in memory,
+// 21.9 and 206).  (Loaded by each lane as it needs them, their latency set the pace: 16 tokens
+// x 10 of 200 bf16 experts ran at 1.9 TB/s.  Staged by the CTA for several blocks at a
+// time, barriers and bookkeeping did.)
 constexpr int kRing = 2;  // rows of h of a step in the queue
 
-// A row of h: kRow bytes, fp32 or in its form; kLine bytes of its form alone, in parts
-// kPart apart (bf16 rows have two), which spread over the banks.
+// A row of h: kRow bytes as it comes, kLine in the form that the instructions take, kBytes a value:
+// f16, or for bf16 weights the two bf16 as they come.  16 bytes more spread rows over the banks.
 template <int WF>
 struct HRow {
-  static constexpr int kParts = Fmt<WF>::kF16 ? 1 : 2;
-  static constexpr int kPart = Fmt<WF>::kStepK * 2 + 16, kLine = kParts * kPart;
-  static constexpr int kRow = Fmt<WF>::kF16 ? Fmt<WF>::kStepK * 4 + 16 : kLine;
+  static constexpr int kBytes = Fmt<WF>::kF16 ? 2 : 4;
+  static constexpr int kLine = Fmt<WF>::kStepK * kBytes + 16, kRow = Fmt<WF>::kStepK * 4 + 16;
 };
 template <int WF, int NG, int S>
 __host__ __device__ constexpr int down_warp_bytes() {  // queue, rows of h in it, further rows, factors
@@ -800,7 +816,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
   using F = Fmt<WF>;
   constexpr int kThreads = W * 32;
   constexpr int kEntry = entry_bytes<WF>();
-  constexpr int kParts = HRow<WF>::kParts, kPart = HRow<WF>::kPart, kLine = HRow<WF>::kLine, kRow = HRow<WF>::kRow;
+  constexpr int kHB = HRow<WF>::kBytes, kLine = HRow<WF>::kLine, kRow = HRow<WF>::kRow;
   constexpr int kRowLanes = F::kStepK / 8, kRowsAt = 32 / kRowLanes;  // 8 values a lane: lanes a row, rows at a time
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
@@ -858,6 +874,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
   const uint8_t *w0 = p.pool, *w1 = p.pool, *sp = p.pool, *gsp = p.pool;
   int n0 = 0, n1 = 0;
   constexpr int kHLanes = F::kStepK / 4, kHAt = 32 / kHLanes;  // 16 bytes a lane: lanes a row of h, rows at a time
+  const int hk = lane % kHLanes * 4;
   int ho[kRing / kHAt];
   bool hin[kRing / kHAt];
   const int last = row % F::kRowBytes;  // bytes of a short last step
@@ -888,13 +905,13 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
     for (int j = 0; j < kRing / kHAt; ++j) {
       const int rw = j * kHAt + lane / kHLanes;
       hin[j] = rw < n;
-      ho[j] = (hin[j] ? tb.order[first + rw] : 0) * p.I + cs * F::kStepK + lane % kHLanes * 4;
+      ho[j] = (hin[j] ? tb.order[first + rw] : 0) * p.I + cs * F::kStepK + hk;
     }
   };
   set_rows();
   auto copy_h = [&](int slot, int j, int o) {  // o < 0: zeros
-    cp_async16_take(smem_u32(ring + (slot * kRing + j * kHAt + lane / kHLanes) * kRow) + lane % kHLanes * 16,
-                    p.h + max(o, 0), o >= 0);
+    cp_async16_take(smem_u32(ring + (slot * kRing + j * kHAt + lane / kHLanes) * kRow + hk * 4),
+                    static_cast<const float*>(p.h) + max(o, 0), o >= 0);
   };
   auto copy_next = [&](int* later) {  // later: takes what copy_h is to be given
     if (crow < row_hi) {
@@ -914,7 +931,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
         sp += sin ? (int64_t)8 * p.H : 0;
         if (lane == 0) cp_async4_take(e + 1024 + 128, gsp, true);
       }
-      const bool in_k = whole || cs * F::kStepK + lane % kHLanes * 4 < p.I;
+      const bool in_k = whole || cs * F::kStepK + hk < p.I;
 #pragma unroll
       for (int j = 0; j < kRing / kHAt; ++j) {
         const bool in = hin[j] && in_k;
@@ -956,54 +973,62 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
     }
   }
 
-  // 8 values of row j of the block to their form, at `to`
+  // The rows of h of a step of the block, n of them, `first` in the order.  For f16: 8 values of
+  // row j to their form at `to`, those in the queue where they lie.
   const int hl = lane / kRowLanes, hp = lane % kRowLanes;
   auto form = [&](const float (&v)[8], uint8_t* to, int j, bool live) {
-    uint4* o = reinterpret_cast<uint4*>(to + hp * 16);
-    if constexpr (F::kF16) {
-      uint4 x;
-      const float f = f16_group(v, x);
-      if (live) {
-        *o = x;
-        if (hp == 0) hf[j] = f;
-      }
-    } else if (live) {
-      uint32_t a[4], b[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        a[i] = f32x2_bf16x2(v[2 * i], v[2 * i + 1]);
-        const float x0 = bf16_f32(a[i] & 0xFFFFu), x1 = __uint_as_float(a[i] & 0xFFFF0000u);
-        // an infinity leaves nothing (and not the NaN of its difference)
-        b[i] = f32x2_bf16x2(fabsf(x0) < INFINITY ? v[2 * i] - x0 : 0.0f, fabsf(x1) < INFINITY ? v[2 * i + 1] - x1 : 0.0f);
-      }
-      o[0] = make_uint4(a[0], a[1], a[2], a[3]);
-      o[kPart / 16] = make_uint4(b[0], b[1], b[2], b[3]);
+    uint4 x;
+    const float f = f16_group(v, x);
+    if (live) {
+      *reinterpret_cast<uint4*>(to + hp * 16) = x;
+      if (hp == 0) hf[j] = f;
     }
   };
-  // all n rows of h of a step, `first` in the order: those in the queue where they lie, the
-  // others here
   auto form_rows = [&](int first, int n, int step, int slot) {
-    uint8_t* rows = ring + slot * kRing * kRow;
-    float v[8];
-    const float4* raw = reinterpret_cast<const float4*>(rows + min(hl, kRing - 1) * kRow + hp * 32);
-    const float4 x = raw[0], y = raw[1];
-    v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
-    v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
-    __syncwarp();  // read by all before it is written over
-    form(v, rows + hl * kRow, hl, hl < kRing);
+    if constexpr (F::kF16) {
+      uint8_t* rows = ring + slot * kRing * kRow;
+      float v[8];
+      const float4* raw = reinterpret_cast<const float4*>(rows + min(hl, kRing - 1) * kRow + hp * 32);
+      const float4 x = raw[0], y = raw[1];
+      v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
+      v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+      __syncwarp();  // read by all before it is written over
+      form(v, rows + hl * kRow, hl, hl < kRing);
 #pragma unroll 1
-    for (int j = kRing; j < n; j += kRowsAt) {
-      const int k = step * F::kStepK + hp * 8;
-      const bool live = j + hl < n;
+      for (int j = kRing; j < n; j += kRowsAt) {
+        const int k = step * F::kStepK + hp * 8;
+        const bool live = j + hl < n;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-      if (live && k < p.I) {
-        const float4* h = reinterpret_cast<const float4*>(p.h + (int64_t)tb.order[first + j + hl] * p.I + k);
-        const float4 a = __ldcg(h), b = __ldcg(h + 1);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        for (int i = 0; i < 8; ++i) v[i] = 0.0f;
+        if (live && k < p.I) {
+          const float4* h = reinterpret_cast<const float4*>(static_cast<const float*>(p.h) + (int64_t)tb.order[first + j + hl] * p.I + k);
+          const float4 a = __ldcg(h), b = __ldcg(h + 1);
+          v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+          v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        }
+        form(v, more + (j + hl - kRing) * kLine, j + hl, live);
       }
-      form(v, more + (j + hl - kRing) * kLine, j + hl, live);
+      __syncwarp();
+    } else if (n > kRing) {
+      const int k = step * F::kStepK + hk;
+      const uint32_t* h = static_cast<const uint32_t*>(p.h) + k;
+#pragma unroll 1
+      for (int j0 = kRing + lane / kHLanes; j0 < n; j0 += 3 * kHAt) {
+        uint4 v[3];
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int j = j0 + i * kHAt;
+          v[i] = make_uint4(0u, 0u, 0u, 0u);
+          if (j < n && k < p.I)
+            v[i] = __ldcg(reinterpret_cast<const uint4*>(h + (int64_t)tb.order[first + j] * p.I));
+        }
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          const int j = j0 + i * kHAt;
+          if (j < n) *reinterpret_cast<uint4*>(more + (j - kRing) * kLine + hk * 4) = v[i];
+        }
+      }
+      __syncwarp();
     }
   };
 
@@ -1028,7 +1053,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
         auto row_of = [&](int col) { return (m >> col) & 1u ? __popc(m & ((1u << col) - 1)) : 0; };
         const int r = row_of(8 * (n0 + n) + g);
         hslot[n] = r < kRing ? kRing * kRow : 0;
-        hrow[n] = smem_u32(r < kRing ? ring + r * kRow : more + (r - kRing) * kLine) + 2 * piece_k<WF>(0, 0);
+        hrow[n] = smem_u32(r < kRing ? ring + r * kRow : more + (r - kRing) * kLine) + kHB * piece_k<WF>(0, 0);
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int col = 8 * (n0 + n) + 2 * t + j;
@@ -1046,7 +1071,6 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
         cp_async_wait<S - 1>();
         __syncwarp();  // what other lanes brought
         form_rows(first, n_rows, st, from);
-        __syncwarp();
         const uint32_t e = smem_u32(queue + from * kEntry);
         float d[GN][4], d1[GN][4];  // two chains of instructions with one group of tokens
 #pragma unroll
@@ -1060,17 +1084,24 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
           for (int n = 0; n < GN; ++n)
 #pragma unroll
             for (int i = 0; i < F::kB; ++i) {
-              const uint32_t a = hrow[n] + from * hslot[n] + 2 * (piece_k<WF>(hh, i) - piece_k<WF>(0, 0));
-              B[hh][n][i] = lds128(a);
-              L[hh][n][i] = kParts == 2 ? lds128(a + kPart) : B[hh][n][i];
+              const uint32_t a = hrow[n] + from * hslot[n] + kHB * (piece_k<WF>(hh, i) - piece_k<WF>(0, 0));
+              const uint4 v = lds128(a);
+              B[hh][n][i] = L[hh][n][i] = v;
+              if constexpr (!F::kF16) {
+                const uint4 u = lds128(a + 16);
+                B[hh][n][i] = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410),
+                                         __byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410));
+                L[hh][n][i] = make_uint4(__byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x7632),
+                                         __byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632));
+              }
             }
-        half_mma<WF, GN, kParts == 2, F::kF16>(e, 0, B[0], L[0], d);
+        half_mma<WF, GN, !F::kF16, F::kF16>(e, 0, B[0], L[0], d);
         if constexpr (GN == 1) {
-          half_mma<WF, GN, kParts == 2, true>(e, 1, B[1], L[1], d1);
+          half_mma<WF, GN, !F::kF16, true>(e, 1, B[1], L[1], d1);
 #pragma unroll
           for (int i = 0; i < 4; ++i) d[0][i] += d1[0][i];
         } else {
-          half_mma<WF, GN, kParts == 2, false>(e, 1, B[1], L[1], d);
+          half_mma<WF, GN, !F::kF16, false>(e, 1, B[1], L[1], d);
         }
         if constexpr (F::kF16) {
           float sc0 = 1.0f, sc1 = 1.0f;
@@ -1317,8 +1348,8 @@ extern "C" int moe_layer_few_tokens(const oes_routed_experts* v, const uint16_t*
   p.logits_bf16 = dtype == OES_LOGITS_BF16;
   p.ids = ids;
   p.weights = weights;
-  p.h = static_cast<float*>(workspace);
-  p.tables = reinterpret_cast<uint8_t*>(p.h + (size_t)T * k * v->I);
+  p.h = workspace;
+  p.tables = static_cast<uint8_t*>(workspace) + (size_t)T * k * v->I * 4;
   p.out = out;
   p.status = status;
   if (logits && v->E > kFusedExperts) {
