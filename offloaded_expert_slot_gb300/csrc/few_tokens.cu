@@ -934,10 +934,9 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
       const bool in_k = whole || cs * F::kStepK + hk < p.I;
 #pragma unroll
       for (int j = 0; j < kRing / kHAt; ++j) {
-        const bool in = hin[j] && in_k;
-        const int o = in ? ho[j] : -1;
-        if (later) later[j] = o;
-        else copy_h(at, j, o);
+        const int o = in_k ? ho[j] : -1;
+        if (later) later[j] = hin[j] ? o : -1;
+        else if (hin[j]) copy_h(at, j, o);  // a row that the block has not is not read
         ho[j] += F::kStepK;
       }
       ++cs;

@@ -127,6 +127,34 @@ def test_routed_from_logits(fmt, T, k, E, dtype):
     assert torch.equal(ids, m.ids) and torch.equal(w, m.w)      # the router's, bit for bit
 
 
+@pytest.mark.parametrize("E,k", [(512, 32), (512, 10), (40, 5), (33, 32), (5, 5)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_odd_logits_are_routed_as_the_router_does(E, k, dtype):
+    """Equal rows, rows with nothing, one or a few numbers above -inf, NaN rows, infinities, zeros of both signs,
+    masks of the type's lowest value."""
+    T = 12
+    z = rng(21).standard_normal((T, E)).astype(np.float32)
+    z[0] = 1.5
+    z[1] = -np.inf
+    z[2] = np.nan
+    z[3] = -np.inf
+    z[3, E - 1] = -3.0
+    z[4, 2:] = -np.inf
+    z[5, ::2] = np.inf
+    z[6] = np.where(np.arange(E) % 3, 0.0, -0.0)
+    z[7, 3:] = torch.finfo(dtype).min
+    z[8, ::2] = np.nan
+    z[9] = torch.finfo(dtype).min
+    z[10] = np.arange(E) % 2
+    logits = torch.from_numpy(z).to(dtype).cuda()
+    m = Layer("fp8", T, k, E, 64, 64)
+    m.call(logits=logits)
+    ids, w = torch.empty_like(m.ids), torch.empty_like(m.w)
+    oes.moe_route_topk(logits, T, E, k, ids, w)
+    torch.cuda.synchronize()
+    assert torch.equal(ids, m.ids) and torch.equal(w.view(torch.int32), m.w.view(torch.int32))
+
+
 def test_routing_matches_the_oracle():
     m = Layer("fp8", 6, 8, 128, 64, 64)
     logits = rng(3).standard_normal((6, 128)).astype(np.float32)
@@ -353,6 +381,38 @@ def test_graph_replay_on_new_tokens():
         gb.replay()
         m.check()
         n.check()
+
+
+@pytest.mark.parametrize("T", [1, 16])
+def test_layers_in_a_row(T):
+    """Each call's result is the next one's input, through one workspace, without a wait in between and from a
+    graph, as with one."""
+    k, E, H = 2, 8, 512
+    a, b = Layer("bf16", T, k, E, H, 256), Layer("nvfp4", T, k, E, H, 128, seed=2)
+    first, x, y = a.x.clone(), a.x.clone(), torch.empty_like(a.x)
+    z = torch.from_numpy(rng(31).standard_normal((T, E)).astype(np.float32)).cuda()
+
+    def run(wait):
+        x.copy_(first)
+        for _ in range(6):
+            for m, i, o in ((a, x, y), (b, y, x)):
+                oes.moe_layer_few_tokens(m.view, i, T, k, m.ids, m.w, a.ws, a.bytes, o, m.status, logits=z)
+                if wait:
+                    torch.cuda.synchronize()
+
+    run(True)
+    want = x.clone()
+    run(False)
+    torch.cuda.synchronize()
+    assert torch.equal(x.view(torch.int16), want.view(torch.int16))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=torch.cuda.Stream()):
+        run(False)
+    for _ in range(3):
+        x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(x.view(torch.int16), want.view(torch.int16))
 
 
 def test_two_calls_at_once():
