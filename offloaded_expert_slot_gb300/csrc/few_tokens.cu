@@ -88,7 +88,7 @@ struct Fmt<OES_WFMT_FP8> {
 template <>
 struct Fmt<OES_WFMT_NVFP4> {
   static constexpr int kStepK = 128, kRowBytes = 64, kChunks = 2, kB = 2, kXPad = 16;
-  static constexpr int kScale = 128 + 16;  // [2 x 64 of K][16 rows][4] e4m3, then the global scale
+  static constexpr int kScale = 128;  // [2 x 64 of K][16 rows][4] e4m3
   static constexpr bool kF16 = true;
 };
 template <int WF>
@@ -607,7 +607,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
   // wp + up, its scales at sp
   Place c = q;
   int cs = s0, at = 0;
-  const uint8_t *wp = p.pool, *sp = p.pool, *gsp = p.pool;
+  const uint8_t *wp = p.pool, *sp = p.pool;
   const int64_t up = (int64_t)p.I * row;
   const int last = row % F::kRowBytes;  // bytes of a short last step
   auto set_rows = [&]() {
@@ -619,7 +619,6 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
     if constexpr (WF == OES_WFMT_NVFP4) {
       const int r16 = lane & 15;
       sp = base + p.s13 + ((int64_t)(2 * s0 + (lane >> 4)) * 2 * p.I + (r16 >> 3) * p.I + c.r * 8 + (r16 & 7)) * 4;
-      gsp = base + p.gs;
     }
   };
   set_rows();
@@ -638,7 +637,6 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
         const bool in = whole || lane < 16;
         cp_async4_take(e + 1024 + 4 * lane, in ? sp : p.pool, in);
         sp += (int64_t)16 * KS * p.I;
-        if (lane == 0) cp_async4_take(e + 1024 + 128, gsp, true);
       }
       cs += KS;
       if (cs >= ns) {
@@ -692,7 +690,9 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
     for (int n = 0; n < GN; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    float gs = 1.0f;
+    float gs = 1.0f;  // needed at the end
+    if constexpr (WF == OES_WFMT_NVFP4)
+      gs = __ldcg(reinterpret_cast<const float*>(p.pool + (int64_t)tb.slot[q.b] * p.row_bytes + p.gs));
     for (int s = s0; s < ns; s += KS) {
       cp_async_wait<S - 1>();
       if (F::kScale) __syncwarp();  // scales that other lanes copied
@@ -724,8 +724,6 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
           const uint2 sc = lds64(e + 2048);
           sg = __uint_as_float(sc.x);
           su = __uint_as_float(sc.y);
-        } else {
-          gs = __uint_as_float(lds32(e + 1024 + 128));
         }
 #pragma unroll
         for (int n = 0; n < GN; ++n)
@@ -871,7 +869,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
   // The next step to copy: step cs of block cb, `left` of the tile at row crow; its
   // weights for this lane at w0 and w1, its scales at sp, of its first rows of h at ho
   int cb = b0, cs = s0, left = run, crow = run > 0 ? row_lo : row_hi, at = 0;
-  const uint8_t *w0 = p.pool, *w1 = p.pool, *sp = p.pool, *gsp = p.pool;
+  const uint8_t *w0 = p.pool, *w1 = p.pool, *sp = p.pool;
   int n0 = 0, n1 = 0;
   constexpr int kHLanes = F::kStepK / 4, kHAt = 32 / kHLanes;  // 16 bytes a lane: lanes a row of h, rows at a time
   const int hk = lane % kHLanes * 4;
@@ -898,7 +896,6 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
       const int r = crow + (lane & 15);
       sin = r < row_hi;
       sp = sin ? base + p.s2 + ((int64_t)(2 * cs + (lane >> 4)) * p.H + r) * 4 : p.pool;
-      gsp = base + p.gs + 4;
     }
     const int first = tb.cum[cb], n = __popc(tb.has[cb]);
 #pragma unroll
@@ -929,7 +926,6 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
         const bool in = sin && (whole || lane < 16);
         cp_async4_take(e + 1024 + 4 * lane, in ? sp : p.pool, in);
         sp += sin ? (int64_t)8 * p.H : 0;
-        if (lane == 0) cp_async4_take(e + 1024 + 128, gsp, true);
       }
       const bool in_k = whole || cs * F::kStepK + hk < p.I;
 #pragma unroll
@@ -1065,7 +1061,9 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
       for (int n = 0; n < GN; ++n)
 #pragma unroll
         for (int i = 0; i < 4; ++i) blk[n][i] = 0.0f;
-      float gs = 1.0f;
+      float gs = 1.0f;  // needed at the end
+      if constexpr (WF == OES_WFMT_NVFP4)
+        gs = __ldcg(reinterpret_cast<const float*>(p.pool + (int64_t)tb.slot[b] * p.row_bytes + p.gs) + 1);
       for (int st = s1; st < end; ++st) {
         cp_async_wait<S - 1>();
         __syncwarp();  // what other lanes brought
@@ -1107,8 +1105,6 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
           if constexpr (WF == OES_WFMT_FP8) {
             sc0 = __uint_as_float(lds32(e + 2048 + 4 * g));
             sc1 = __uint_as_float(lds32(e + 2048 + 32 + 4 * g));
-          } else {
-            gs = __uint_as_float(lds32(e + 1024 + 128));
           }
 #pragma unroll
           for (int n = 0; n < GN; ++n)
