@@ -32,12 +32,11 @@
 // their set-up and hand-offs.
 //
 // Measured (10 of 512 experts of 2048 x 768, replayed from a graph): 1 token FP8 16.9 us
-// (2.8 TB/s), bf16 21.6 us (4.4); 4 tokens NVFP4 39.9 us (2.6); 16 tokens bf16 205 to 213 us (6.1 to
-// 6.4 TB/s, 90 to 94 % of the copy rate, by GPU), FP8 137 us (4.8), NVFP4 144 us (2.5).  16 bf16 tokens are bound
-// by memory; the 8- and 4-bit formats by the instructions that decode and multiply (issue
-// slots 50 to 57 % busy, about 170 a 2 KB step of the first kernel and 240 of the second);
-// one token by latency: 4.6 us to the first weights (logits, top-k, tables, slots), 2 to 3
-// from one kernel to the next, 1.5 for the last sums.
+// (2.8 TB/s), bf16 21.5 us (4.4); 4 tokens NVFP4 38.5 us (2.7); 16 tokens bf16 206 to 217 us (6.0 to
+// 6.3 TB/s, 89 to 93 % of the copy rate, by GPU), FP8 132 us (5.0), NVFP4 142 us (2.6).  16 bf16 tokens
+// are bound by memory; the 8- and 4-bit formats by the instructions that decode and multiply (issue
+// slots 44 to 54 % busy); one token by latency: 4.6 us to the first weights (logits, top-k, tables,
+// slots), 2 to 3 from one kernel to the next, 1.5 for the last sums.
 //
 // Weights are exact in 16 bits: bf16 as they are; e4m3 as f16, their block scales on
 // the fp32 sums of each 128 of K; e2m1 x e4m3 as f16, the global scale on the sums.
