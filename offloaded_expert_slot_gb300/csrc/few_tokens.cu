@@ -27,9 +27,9 @@
 // copies, read back by the same lane), so a warp keeps its next steps in
 // flight without registers and without a barrier.  The instructions are the
 // warp-wide m16n8k16, whose tensor work at 8 columns is a small part of what the
-// stream takes (13 % of the pipe); tcgen05 tiles (128 weight rows, operands through
-// shared memory and TMEM) gave 9 to 31 % of the copy rate for one token, held up by
-// their set-up and hand-offs.
+// stream takes (10 to 18 % of the pipe); the grouped GEMM's tcgen05 tiles (128 weight rows,
+// operands through shared memory and TMEM) reach 9 to 30 % of the copy rate for 1 to 64
+// tokens of NVFP4 experts, held up by their set-up and hand-offs.
 //
 // Measured (10 of 512 experts of 2048 x 768, replayed from a graph): 1 token FP8 16.9 us
 // (2.8 TB/s), bf16 21.5 us (4.4); 4 tokens NVFP4 38.5 us (2.7); 16 tokens bf16 206 to 217 us (6.0 to
@@ -43,7 +43,7 @@
 // For bf16 weights x is taken as it is and h as two bf16 numbers, the second what
 // rounding to the first left (a bf16 h alone would add as much error as out's own
 // rounding does).  For the others x and h are f16 numbers with a power of two for
-// each 128 (f16_group).  h passes between the kernels in fp32, the sums over a
+// each 128 (f16_group), and h passes between the kernels in fp32.  The sums over a
 // token's routes stay in fp32, and out is rounded once.
 #include <algorithm>
 
