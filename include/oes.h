@@ -445,7 +445,7 @@ size_t moe_layer_few_tokens_workspace_size(const oes_routed_experts *view, int T
  * view->wfmt: OES_WFMT_BF16, OES_WFMT_FP8 or OES_WFMT_NVFP4, rows as above.
  * Weights are decoded exactly, and the activations are not quantised, in the FP8
  * format neither (moe_grouped_gemm_slots quantises them there): sums are fp32, h
- * keeps 16 significant bits for bf16 weights and 11 for the others (with a common
+ * keeps 24 significant bits for bf16 weights and 22 for the others (with a common
  * exponent for each 128 values, so of any size), and out is rounded once.  The
  * result does not depend on timing; it is not bit for bit that of
  * moe_grouped_gemm_slots, which rounds each route's output row to bf16 before the

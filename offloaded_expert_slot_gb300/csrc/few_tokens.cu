@@ -19,9 +19,10 @@
 //                    its CTAs fill their queues with W2 while the last of that
 //                    kernel's still run.
 //
-// A block is one expert with at most one route of each token: column c of the
-// matrix instruction is token c, in both kernels.  An expert that a token lists
-// twice gets a second block for the second route.
+// A block is one expert with at most one route of each token.  In the first kernel
+// column c of the matrix instruction is token c, in the second the columns are the parts
+// of the block's rows of h.  An expert that a token lists twice gets a second block for
+// the second route.
 //
 // Weights go from memory into a queue of each lane's own (16-byte asynchronous
 // copies, read back by the same lane), so a warp keeps its next steps in
@@ -40,11 +41,14 @@
 //
 // Weights are exact in 16 bits: bf16 as they are; e4m3 as f16, their block scales on
 // the fp32 sums of each 128 of K; e2m1 x e4m3 as f16, the global scale on the sums.
-// For bf16 weights x is taken as it is and h as two bf16 numbers, the second what
-// rounding to the first left (a bf16 h alone would add as much error as out's own
-// rounding does).  For the others x and h are f16 numbers with a power of two for
-// each 128 (f16_group), and h passes between the kernels in fp32.  The sums over a
-// token's routes stay in fp32, and out is rounded once.
+// h is fp32.  For bf16 weights x is taken as it is, and h as three bf16 numbers, which hold
+// all of it; for the others x is f16 numbers with a power of two for each 128, exact
+// unless 2^31 smaller than the largest of them, and h two such (f16_group), of 22 bits.
+// (h of 16 and of 11 bits, as it was: of the 16-token case's results 383 of 131072 were not
+// the 64-bit sums' roundings, now 35, of one token's in FP8 856 of 8192, now 1; fp32 matrix
+// products of torch miss 113 and 5.)  An instruction's sum is what the tensor core keeps of
+// it, so no chain of them goes past a step: steps are added up in fp32, as are a token's
+// routes, and out is rounded once.
 #include <algorithm>
 
 #include "common.cuh"
@@ -95,6 +99,9 @@ __host__ __device__ constexpr int entry_bytes() {
   return Fmt<WF>::kChunks * 512 + Fmt<WF>::kScale;
 }
 
+// Bytes of a value of h.
+__host__ __device__ constexpr int h_value_bytes(int wfmt) { return wfmt == OES_WFMT_BF16 ? 6 : 4; }
+
 struct FewParams {
   const uint8_t* pool;
   int64_t row_bytes;
@@ -105,7 +112,7 @@ struct FewParams {
   int logits_bf16;
   int32_t* ids;
   float* weights;
-  void* h;  // [T k, I] fp32, or for bf16 weights two bf16 a word: the value and what its rounding left
+  void* h;  // [T k, I] (store_h)
   uint16_t* out;
   int32_t* status;
   int64_t s13, w2, s2, gs;  // sections of an expert row
@@ -115,30 +122,32 @@ struct FewParams {
   int rows_cta;             // few_down: rows of out a CTA owns
 };
 
-// The chunk's tables, in shared memory.  A block's first route leads it.
+// The chunk's tables, in shared memory.  A block's first route leads it.  few_down takes
+// the first down_tables_bytes() of them.
 struct Tables {
-  int32_t* ids;    // [R]
   float* w;        // [R]
-  int32_t* lead;   // [R] first route of the route's block, -1 for one that does not count
-  int32_t* blk;    // [R] block of a leading route
   int32_t* slot;   // [blocks]
   uint32_t* has;   // [blocks] which tokens have a route in the block
+  int16_t* order;  // [R] the routes that count, block after block, each by its tokens
+  int16_t* cum;    // [blocks] a block's first place there
+  int32_t* ids;    // [R], few_up alone from here on
+  int32_t* lead;   // [R] first route of the route's block, -1 for one that does not count
+  int32_t* blk;    // [R] block of a leading route
   int16_t* route;  // [blocks][8 NG] route of each token in the block, or -1
-  int16_t* order;  // [R] few_down: the routes that count, block after block
-  int16_t* cum;    // [blocks] few_down: a block's first place there
-  __device__ __forceinline__ Tables(uint8_t* base, int R, int ng) {
-    ids = reinterpret_cast<int32_t*>(base);
-    w = reinterpret_cast<float*>(ids + R);
-    lead = reinterpret_cast<int32_t*>(w + R);
-    blk = lead + R;
-    slot = blk + R;
+  __device__ __forceinline__ Tables(uint8_t* base, int R) {
+    w = reinterpret_cast<float*>(base);
+    slot = reinterpret_cast<int32_t*>(w + R);
     has = reinterpret_cast<uint32_t*>(slot + R);
-    route = reinterpret_cast<int16_t*>(has + R);
-    order = route + R * 8 * ng;
+    order = reinterpret_cast<int16_t*>(has + R);
     cum = order + R;
+    ids = reinterpret_cast<int32_t*>(base + R * 16);
+    lead = ids + R;
+    blk = lead + R;
+    route = reinterpret_cast<int16_t*>(blk + R);
   }
 };
-__host__ __device__ constexpr int tables_bytes(int R, int ng) { return (R * (28 + 16 * ng) + 15) / 16 * 16; }
+__host__ __device__ constexpr int down_tables_bytes(int R) { return R * 16; }
+__host__ __device__ constexpr int tables_bytes(int R, int ng) { return R * (28 + 16 * ng); }
 
 // One token's top-k by one warp, the ids and weights of topk_row_filtered bit for bit
 // (the same threshold, the same order of the candidates, topk_write), made for a single
@@ -371,11 +380,10 @@ __device__ void few_order(const FewParams& p, const Tables& tb, int nb) {
 }
 
 // The matrix instructions of half a step: the lane's weights from its queue entry,
-// added onto d (row g and g + 8, columns 2t and 2t + 1, of each 8 tokens), or FRESH from
-// zero.  B are the lane's values of the columns, L what their rounding to bf16 left (LO).
-template <int WF, int NG, bool LO, bool FRESH>
-__device__ __forceinline__ void half_mma(uint32_t entry, int hh, const uint4 (&B)[NG][Fmt<WF>::kB],
-                                         const uint4 (&L)[NG][Fmt<WF>::kB], float (&d)[NG][4]) {
+// added onto d (row g and g + 8, columns 2t and 2t + 1, of each 8 columns), or FRESH from
+// zero.  B are the lane's values of the columns.
+template <int WF, int NG, bool FRESH>
+__device__ __forceinline__ void half_mma(uint32_t entry, int hh, const uint4 (&B)[NG][Fmt<WF>::kB], float (&d)[NG][4]) {
   const int lane = threadIdx.x & 31;
   const uint32_t mine = entry + lane * 16;
   if constexpr (WF == OES_WFMT_BF16) {
@@ -384,10 +392,6 @@ __device__ __forceinline__ void half_mma(uint32_t entry, int hh, const uint4 (&B
     for (int n = 0; n < NG; ++n) {
       mma_16816<false, FRESH>(d[n], a.x, b.x, a.y, b.y, B[n][0].x, B[n][0].y);
       mma_16816<false>(d[n], a.z, b.z, a.w, b.w, B[n][0].z, B[n][0].w);
-      if (LO) {
-        mma_16816<false>(d[n], a.x, b.x, a.y, b.y, L[n][0].x, L[n][0].y);
-        mma_16816<false>(d[n], a.z, b.z, a.w, b.w, L[n][0].z, L[n][0].w);
-      }
     }
   } else if constexpr (WF == OES_WFMT_FP8) {
     const uint4 a = lds128(mine + hh * 1024), b = lds128(mine + hh * 1024 + 512);
@@ -469,11 +473,14 @@ __device__ __forceinline__ void step_copy_last(uint32_t entry, const uint8_t* r0
 // Activations for 8- and 4-bit weights: f16 numbers with one power of two for each
 // 128 along K, chosen so that the largest is in [2^14, 2^15).  The sums of a step
 // span just such 128, so the factor goes to the sums.  A number keeps 11
-// significant bits down to 2^-29 of its group's largest, and nothing leaves f16's
-// range, whatever the activations' own.  The group is 16 neighbouring lanes' 8
-// values each; returns the factor that undoes it.  A NaN stays one and counts for
+// significant bits down to 2^-29 of its group's largest (a bf16 number all of its 8 down to
+// 2^-31), and nothing leaves f16's range, whatever the activations' own.  TWO: a second
+// number holds what the first one's 11 bits left, together 22 bits, down to 2^-17 of the
+// largest (2^-39 of the largest is the least difference).  The group is 16 neighbouring
+// lanes' 8 values each; returns the factor that undoes it.  A NaN stays one and counts for
 // nothing else, an infinity stays one.
-__device__ __forceinline__ float f16_group(const float (&v)[8], uint4& out) {
+template <bool TWO>
+__device__ __forceinline__ float f16_group(const float (&v)[8], uint4& first, uint4& second) {
   float m = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
@@ -481,26 +488,41 @@ __device__ __forceinline__ float f16_group(const float (&v)[8], uint4& out) {
   for (int o = 8; o >= 1; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const uint32_t ex = min(max(__float_as_uint(m) >> 23, 27u), 254u);  // 2^-100 at least
   const float f = __uint_as_float((268u - ex) << 23);
-  uint32_t o[4];
+  uint32_t a[4], b[4];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(o[i]) : "f"(v[2 * i + 1] * f), "f"(v[2 * i] * f));
-  out = make_uint4(o[0], o[1], o[2], o[3]);
+  for (int i = 0; i < 4; ++i) {
+    float lo = v[2 * i] * f, hi = v[2 * i + 1] * f;
+    if (TWO) {
+      const float l = __uint_as_float(__float_as_uint(lo) & 0xFFFFE000u), h = __uint_as_float(__float_as_uint(hi) & 0xFFFFE000u);
+      asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(b[i]) : "f"(hi - h), "f"(lo - l));
+      if (m == INFINITY) b[i] = 0u;  // what an infinity leaves is none of its difference's NaN
+      lo = l;
+      hi = h;
+    }
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(a[i]) : "f"(hi), "f"(lo));
+  }
+  first = make_uint4(a[0], a[1], a[2], a[3]);
+  if (TWO) second = make_uint4(b[0], b[1], b[2], b[3]);
   return __uint_as_float((ex - 14u) << 23);
 }
 
-// One value of a route's h, for the down kernel: fp32, or two bf16 in a word, the second what
-// the first's rounding left (16 significant bits).
+// One value of a route's h, for the down kernel: fp32, or for bf16 weights as three bf16 numbers, each what
+// rounding to those before left (24 significant bits, all that fp32 has), the first ones of 64 values
+// before their second and third ones.
 template <int WF>
 __device__ __forceinline__ void store_h(const FewParams& p, int r, int i, float v) {
   if constexpr (Fmt<WF>::kF16) {
     static_cast<float*>(p.h)[(int64_t)r * p.I + i] = v;
   } else {
-    const uint32_t hi = f32_bf16(v);
-    const float f = bf16_f32(hi);
+    constexpr int K = Fmt<WF>::kStepK;
+    const uint32_t one = f32_bf16(v);
     // an infinity leaves nothing (and not the NaN of its difference)
-    const uint32_t lo = f32_bf16(fabsf(f) < INFINITY ? v - f : 0.0f);
-    static_cast<uint32_t*>(p.h)[(int64_t)r * p.I + i] = hi | lo << 16;
+    const float left = fabsf(bf16_f32(one)) < INFINITY ? v - bf16_f32(one) : 0.0f;
+    const uint32_t two = f32_bf16(left);
+    uint16_t* to = static_cast<uint16_t*>(p.h) + ((int64_t)r * p.I + i / K * K) * 3 + i % K;
+    to[0] = (uint16_t)one;
+    to[K] = (uint16_t)two;
+    to[2 * K] = (uint16_t)f32_bf16(left - bf16_f32(two));
   }
 }
 
@@ -527,7 +549,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
   uint8_t* xs = reinterpret_cast<uint8_t*>(part + (KS > 1 ? 2 * kThreads * 4 * NG : 0));
   float* xf = reinterpret_cast<float*>(xs + p.T * p.x_ld);  // [T][ns] factors of x (kF16)
   const int ns = cdiv(p.H, F::kStepK);
-  const Tables tb(reinterpret_cast<uint8_t*>(xf + (F::kF16 ? p.T * ns : 0)), p.T * p.k, NG);
+  const Tables tb(reinterpret_cast<uint8_t*>(xf + (F::kF16 ? p.T * ns : 0)), p.T * p.k);
   pdl_wait();
   if (blockIdx.x == 0) {  // the tables are not there yet, before any CTA of the down kernel can look
     if (tid == 0) {
@@ -570,7 +592,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
             v[2 * e + 1] = __uint_as_float(u[e] & 0xFFFF0000u);
           }
           uint4 o;
-          const float f = f16_group(v, o);
+          const float f = f16_group<false>(v, o, o);
           if (tok[j] < p.T) {
             *reinterpret_cast<uint4*>(xs + tok[j] * p.x_ld + c[j] * 16) = o;
             if ((c[j] & 15) == 0) xf[tok[j] * ns + (c[j] >> 4)] = f;
@@ -653,8 +675,8 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
     // the tables, for the down kernel
     few_order<NG>(p, tb, nb);
     if (tid == 0) *reinterpret_cast<int32_t*>(p.tables) = nb;
-    for (int i = tid; i < tables_bytes(p.T * p.k, NG) / 4; i += kThreads)
-      reinterpret_cast<int32_t*>(p.tables + 16)[i] = tb.ids[i];
+    for (int i = tid; i < down_tables_bytes(p.T * p.k) / 4; i += kThreads)
+      reinterpret_cast<int32_t*>(p.tables + 16)[i] = reinterpret_cast<const int32_t*>(tb.w)[i];
     __syncthreads();
     if (tid == 0) {
       __threadfence();
@@ -697,10 +719,6 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
       if (F::kScale) __syncwarp();  // scales that other lanes copied
       const uint32_t e = smem_u32(queue + from * kEntry);
       float d[GN][4], d1[GN][4];  // two chains of instructions with one group of tokens
-#pragma unroll
-      for (int n = 0; n < GN; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) d[n][i] = acc[n][i];
       uint4 B[2][GN][F::kB];
 #pragma unroll
       for (int hh = 0; hh < 2; ++hh)
@@ -709,13 +727,13 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
 #pragma unroll
           for (int i = 0; i < F::kB; ++i)
             B[hh][n][i] = lds128(ub[n] + 2 * (s * F::kStepK + piece_k<WF>(hh, i) - piece_k<WF>(0, 0)));
-      half_mma<WF, GN, false, F::kF16>(e, 0, B[0], B[0], d);
+      half_mma<WF, GN, true>(e, 0, B[0], d);
       if constexpr (GN == 1) {
-        half_mma<WF, GN, false, true>(e, 1, B[1], B[1], d1);
+        half_mma<WF, GN, true>(e, 1, B[1], d1);
 #pragma unroll
         for (int i = 0; i < 4; ++i) d[0][i] += d1[0][i];
       } else {
-        half_mma<WF, GN, false, false>(e, 1, B[1], B[1], d);
+        half_mma<WF, GN, false>(e, 1, B[1], d);
       }
       if constexpr (F::kF16) {
         float sg = 1.0f, su = 1.0f;
@@ -736,7 +754,7 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
 #pragma unroll
         for (int n = 0; n < GN; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) acc[n][i] = d[n][i];
+          for (int i = 0; i < 4; ++i) acc[n][i] += d[n][i];
       }
       if (F::kScale) __syncwarp();
       from = from + 1 == S ? 0 : from + 1;
@@ -788,41 +806,59 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
 // The (block, step of K) of a tile of rows are dealt out to the CTA's warps in runs.
 // The rows of h of a step's tokens come through the warp's queue too, the first kRing of them
 // (few blocks have more; those are loaded when they are needed).  For 8- and 4-bit weights they
-// are fp32, and become f16 where they lie; for bf16 weights the first kernel left each value as two
-// bf16 in a word, and lanes part them on their way to the instruction (splitting fp32 rows here, in every
-// CTA, took 22.5 us for one token and 209 for sixteen, not 21.6 and 205; two planes in memory,
-// 21.9 and 206).  (Loaded by each lane as it needs them, their latency set the pace: 16 tokens
+// are fp32, and become pairs of f16 where they lie; for bf16 weights the first kernel left the three bf16
+// numbers of each value (parted here, in every CTA, 16 tokens took 232 us where this takes 219).
+// (Loaded by each lane as it needs them, their latency set the pace: 16 tokens
 // x 10 of 200 bf16 experts ran at 1.9 TB/s.  Staged by the CTA for several blocks at a
-// time, barriers and bookkeeping did.)
+// time, barriers and bookkeeping did.  With powers of two and pairs of f16 for each 8 values from the
+// first kernel, one token of FP8 experts took 19 us, not 16.8.)
 constexpr int kRing = 2;  // rows of h of a step in the queue
 
-// A row of h: kRow bytes as it comes, kLine in the form that the instructions take, kBytes a value:
-// f16, or for bf16 weights the two bf16 as they come.  16 bytes more spread rows over the banks.
+// A step of a row of h in shared memory, in kParts planes of 16-bit numbers: the three bf16 numbers of
+// its values, or the two f16 numbers that the fp32 values become where they lie.  Pieces of 16 bytes
+// have their places permuted (plane_at), so that the lanes that read a piece of neighbouring columns
+// meet no bank twice.
 template <int WF>
 struct HRow {
-  static constexpr int kBytes = Fmt<WF>::kF16 ? 2 : 4;
-  static constexpr int kLine = Fmt<WF>::kStepK * kBytes + 16, kRow = Fmt<WF>::kStepK * 4 + 16;
+  static constexpr int kParts = Fmt<WF>::kF16 ? 2 : 3, kPlane = Fmt<WF>::kStepK * 2;
+  static constexpr int kRow = Fmt<WF>::kStepK * h_value_bytes(WF), kPieces = kRow / 16;  // also in memory
+  static_assert(kRow == kParts * kPlane, "planes of a row");
 };
+// Piece c of plane `part` of a block's row r.
+template <int WF>
+__device__ __forceinline__ int plane_at(int r, int part, int c) {
+  const int to = WF == OES_WFMT_BF16 ? c ^ 4 * ((r + part) & 1) : WF == OES_WFMT_FP8 ? c ^ part : c ^ c >> 3 ^ 2 * part;
+  return part * HRow<WF>::kPlane + to * 16;
+}
+template <int WF, int S>
+__host__ __device__ constexpr int down_queue_bytes() {  // and the rows of h in it
+  return S * (entry_bytes<WF>() + kRing * HRow<WF>::kRow);
+}
 template <int WF, int NG, int S>
-__host__ __device__ constexpr int down_warp_bytes() {  // queue, rows of h in it, further rows, factors
-  return S * (entry_bytes<WF>() + kRing * HRow<WF>::kRow) + (8 * NG - kRing) * HRow<WF>::kLine + 32 * NG;
+__host__ __device__ constexpr int down_warp_bytes() {  // queue, further rows (at a tile's end the sums), factors
+  static_assert((8 * NG - kRing) * HRow<WF>::kRow >= 32 * 16 * NG, "a warp's sums");
+  return down_queue_bytes<WF, S>() + (8 * NG - kRing) * HRow<WF>::kRow + (Fmt<WF>::kF16 ? 64 : 0);
 }
 
+// The columns of the instructions are the parts of a block's rows of h, row after row: a block of two
+// routes in bf16, or of four in the other formats, fills one instruction's eight.  (With columns that belong to
+// tokens and instructions of their own for the second parts, four tokens of NVFP4 experts took 42.4 us.)
 template <int WF, int NG, int S>
 __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) {
   using F = Fmt<WF>;
-  constexpr int kThreads = W * 32;
-  constexpr int kEntry = entry_bytes<WF>();
-  constexpr int kHB = HRow<WF>::kBytes, kLine = HRow<WF>::kLine, kRow = HRow<WF>::kRow;
+  using HR = HRow<WF>;
+  constexpr int kThreads = W * 32, kParts = HR::kParts;
+  constexpr int kEntry = entry_bytes<WF>(), kRow = HR::kRow;
+  constexpr int kWarp = down_warp_bytes<WF, NG, S>();
+  static_assert(kEntry % 64 == 0 && kWarp % 64 == 0 && (F::kF16 || (kEntry % 128 == 0 && kWarp % 128 == 0)), "permuted pieces");
   constexpr int kRowLanes = F::kStepK / 8, kRowsAt = 32 / kRowLanes;  // 8 values a lane: lanes a row, rows at a time
   extern __shared__ __align__(128) uint8_t smem[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
-  uint8_t* queue = smem + warp * down_warp_bytes<WF, NG, S>();
+  uint8_t* queue = smem + warp * kWarp;
   uint8_t* ring = queue + S * kEntry;                    // [S][kRing] rows of h
-  uint8_t* more = ring + S * kRing * kRow;               // rows past those
-  float* hf = reinterpret_cast<float*>(more + (8 * NG - kRing) * kLine);  // factors (kF16)
-  float* part = reinterpret_cast<float*>(smem + W * down_warp_bytes<WF, NG, S>());  // [warp][lane][4 NG]
-  const Tables tb(reinterpret_cast<uint8_t*>(part + kThreads * 4 * NG), p.T * p.k, NG);
+  uint8_t* more = ring + S * kRing * kRow;               // rows past those; at a tile's end [lane][4 NG] sums
+  float* hf = reinterpret_cast<float*>(more + (8 * NG - kRing) * kRow);  // factors (kF16)
+  const Tables tb(smem + W * kWarp, p.T * p.k);
   // The next kernel's CTAs take the SMs as this one's leave them (these fill an SM each) and wait
   // there for the last; left to the kernel's end, a call in a row takes 0.15 to 0.6 us more.
   pdl_trigger();
@@ -844,8 +880,8 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
   // same time would be a mistake of the caller's, which no address may follow: whatever
   // stands here, indexes are kept within their ranges.
   const int R = p.T * p.k, nb = min(max(__ldcg(reinterpret_cast<const int32_t*>(p.tables)), 0), R);
-  for (int i = tid; i < tables_bytes(R, NG) / 16; i += kThreads)
-    reinterpret_cast<int4*>(tb.ids)[i] = __ldcg(reinterpret_cast<const int4*>(p.tables + 16) + i);
+  for (int i = tid; i < down_tables_bytes(R) / 16; i += kThreads)
+    reinterpret_cast<int4*>(tb.w)[i] = __ldcg(reinterpret_cast<const int4*>(p.tables + 16) + i);
   __syncthreads();
   for (int i = tid; i < nb; i += kThreads) {
     if ((uint32_t)tb.slot[i] >= (uint32_t)p.S) tb.slot[i] = 0;
@@ -854,8 +890,6 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
   }
   for (int i = tid; i < R; i += kThreads)
     if ((uint32_t)tb.order[i] >= (uint32_t)R) tb.order[i] = 0;
-  for (int i = tid; i < nb * 8 * NG; i += kThreads)
-    if (tb.route[i] >= R) tb.route[i] = 0;
   __syncthreads();
   const int row = p.I * F::kRowBytes / F::kStepK;
   const int ns = cdiv(p.I, F::kStepK);
@@ -870,10 +904,9 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
   int cb = b0, cs = s0, left = run, crow = run > 0 ? row_lo : row_hi, at = 0;
   const uint8_t *w0 = p.pool, *w1 = p.pool, *sp = p.pool;
   int n0 = 0, n1 = 0;
-  constexpr int kHLanes = F::kStepK / 4, kHAt = 32 / kHLanes;  // 16 bytes a lane: lanes a row of h, rows at a time
-  const int hk = lane % kHLanes * 4;
-  int ho[kRing / kHAt];
-  bool hin[kRing / kHAt];
+  constexpr int kCopies = cdiv(kRing * HR::kPieces, 32);  // of 16 bytes a lane, for a step's rows of h
+  int ho[kCopies];
+  bool hin[kCopies];
   const int last = row % F::kRowBytes;  // bytes of a short last step
   bool sin = false;
   auto set_rows = [&]() {
@@ -898,16 +931,21 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
     }
     const int first = tb.cum[cb], n = __popc(tb.has[cb]);
 #pragma unroll
-    for (int j = 0; j < kRing / kHAt; ++j) {
-      const int rw = j * kHAt + lane / kHLanes;
-      hin[j] = rw < n;
-      ho[j] = (hin[j] ? tb.order[first + rw] : 0) * p.I + cs * F::kStepK + hk;
+    for (int j = 0; j < kCopies; ++j) {
+      const int pc = lane + 32 * j, rw = pc / HR::kPieces;
+      hin[j] = rw < min(n, kRing);
+      ho[j] = (hin[j] ? tb.order[first + rw] : 0) * p.I * h_value_bytes(WF) + cs * kRow + pc % HR::kPieces * 16;
     }
   };
   set_rows();
+  auto piece_at = [&](int rw, int pc) {  // where a row's piece lies: fp32 as it comes, else in its plane
+    return F::kF16 ? pc * 16 : plane_at<WF>(rw, pc / (HR::kPlane / 16), pc % (HR::kPlane / 16));
+  };
   auto copy_h = [&](int slot, int j, int o) {  // o < 0: zeros
-    cp_async16_take(smem_u32(ring + (slot * kRing + j * kHAt + lane / kHLanes) * kRow + hk * 4),
-                    static_cast<const float*>(p.h) + max(o, 0), o >= 0);
+    const int pc = lane + 32 * j, rw = pc / HR::kPieces;
+    if (pc < kRing * HR::kPieces)
+      cp_async16_take(smem_u32(ring + (slot * kRing + rw) * kRow + piece_at(rw, pc % HR::kPieces)),
+                      static_cast<const uint8_t*>(p.h) + max(o, 0), o >= 0);
   };
   auto copy_next = [&](int* later) {  // later: takes what copy_h is to be given
     if (crow < row_hi) {
@@ -926,24 +964,21 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
         cp_async4_take(e + 1024 + 4 * lane, in ? sp : p.pool, in);
         sp += sin ? (int64_t)8 * p.H : 0;
       }
-      const bool in_k = whole || cs * F::kStepK + hk < p.I;
 #pragma unroll
-      for (int j = 0; j < kRing / kHAt; ++j) {
-        const int o = in_k ? ho[j] : -1;
+      for (int j = 0; j < kCopies; ++j) {
+        const int o = whole || cs * F::kStepK + lane * 4 < p.I ? ho[j] : -1;  // bf16's steps are whole
         if (later) later[j] = hin[j] ? o : -1;
         else if (hin[j]) copy_h(at, j, o);  // a row that the block has not is not read
-        ho[j] += F::kStepK;
+        ho[j] += kRow;
       }
-      ++cs;
-      if (--left == 0) {
-        left = run;
-        cb = b0;
-        cs = s0;
-        crow += kRowTile;
-        set_rows();
-      } else if (cs == ns) {
-        cs = 0;
-        ++cb;
+      const bool tile_done = --left == 0;
+      if (++cs == ns || tile_done) {
+        cs = tile_done ? s0 : 0;
+        cb = tile_done ? b0 : cb + 1;
+        if (tile_done) {
+          left = run;
+          crow += kRowTile;
+        }
         set_rows();
       }
     }
@@ -951,34 +986,37 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
     at = at + 1 == S ? 0 : at + 1;
   };
   {
-    int later[S][kRing / kHAt];  // the first steps' rows of h
+    int later[S][kCopies];  // the first steps' rows of h
 #pragma unroll
     for (int i = 0; i < S; ++i) {
 #pragma unroll
-      for (int j = 0; j < kRing / kHAt; ++j) later[i][j] = -1;
+      for (int j = 0; j < kCopies; ++j) later[i][j] = -1;
       copy_next(later[i]);
     }
     if (early) pdl_wait();  // h
 #pragma unroll
     for (int i = 0; i < S; ++i) {
 #pragma unroll
-      for (int j = 0; j < kRing / kHAt; ++j) copy_h(i, j, later[i][j]);
+      for (int j = 0; j < kCopies; ++j) copy_h(i, j, later[i][j]);
       cp_async_commit();
     }
   }
 
   // The rows of h of a step of the block, n of them, `first` in the order.  For f16: 8 values of
-  // row j to their form at `to`, those in the queue where they lie.
+  // row j to their parts in the row at `to`, those in the queue where they lie.
   const int hl = lane / kRowLanes, hp = lane % kRowLanes;
   auto form = [&](const float (&v)[8], uint8_t* to, int j, bool live) {
-    uint4 x;
-    const float f = f16_group(v, x);
+    uint4 x, y;
+    const float f = f16_group<true>(v, x, y);
     if (live) {
-      *reinterpret_cast<uint4*>(to + hp * 16) = x;
+      *reinterpret_cast<uint4*>(to + plane_at<WF>(j, 0, hp)) = x;
+      *reinterpret_cast<uint4*>(to + plane_at<WF>(j, 1, hp)) = y;
       if (hp == 0) hf[j] = f;
     }
   };
   auto form_rows = [&](int first, int n, int step, int slot) {
+    const uint8_t* h = static_cast<const uint8_t*>(p.h) + (int64_t)step * kRow;
+    const int64_t ld = (int64_t)p.I * h_value_bytes(WF);
     if constexpr (F::kF16) {
       uint8_t* rows = ring + slot * kRing * kRow;
       float v[8];
@@ -990,165 +1028,163 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
       form(v, rows + hl * kRow, hl, hl < kRing);
 #pragma unroll 1
       for (int j = kRing; j < n; j += kRowsAt) {
-        const int k = step * F::kStepK + hp * 8;
         const bool live = j + hl < n;
 #pragma unroll
         for (int i = 0; i < 8; ++i) v[i] = 0.0f;
-        if (live && k < p.I) {
-          const float4* h = reinterpret_cast<const float4*>(static_cast<const float*>(p.h) + (int64_t)tb.order[first + j + hl] * p.I + k);
-          const float4 a = __ldcg(h), b = __ldcg(h + 1);
+        if (live && step * F::kStepK + hp * 8 < p.I) {
+          const float4* at = reinterpret_cast<const float4*>(h + tb.order[first + j + hl] * ld + hp * 32);
+          const float4 a = __ldcg(at), b = __ldcg(at + 1);
           v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
           v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
         }
-        form(v, more + (j + hl - kRing) * kLine, j + hl, live);
+        form(v, more + (j + hl - kRing) * kRow, j + hl, live);
       }
       __syncwarp();
     } else if (n > kRing) {
-      const int k = step * F::kStepK + hk;
-      const uint32_t* h = static_cast<const uint32_t*>(p.h) + k;
+      // a piece of a row each for 24 lanes, four rows loaded together
+      static_assert(F::kF16 || HR::kPieces <= 32, "bf16 rows of h");
+      const bool on = lane < HR::kPieces;
+      const uint32_t to = smem_u32(more) + piece_at(0, lane);
 #pragma unroll 1
-      for (int j0 = kRing + lane / kHLanes; j0 < n; j0 += 3 * kHAt) {
-        uint4 v[3];
+      for (int j0 = kRing; j0 < n; j0 += 4) {
+        uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const int j = j0 + i * kHAt;
+        for (int i = 0; i < 4; ++i) {
           v[i] = make_uint4(0u, 0u, 0u, 0u);
-          if (j < n && k < p.I)
-            v[i] = __ldcg(reinterpret_cast<const uint4*>(h + (int64_t)tb.order[first + j] * p.I));
+          if (on && j0 + i < n) v[i] = __ldcg(reinterpret_cast<const uint4*>(h + tb.order[first + j0 + i] * ld + lane * 16));
         }
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          const int j = j0 + i * kHAt;
-          if (j < n) *reinterpret_cast<uint4*>(more + (j - kRing) * kLine + hk * 4) = v[i];
-        }
+        for (int i = 0; i < 4; ++i)  // of row 1 the other half first, and so on
+          if (on && j0 + i < n) sts128((to + (j0 + i - kRing) * kRow) ^ (i & 1 ? 64 : 0), v[i]);
       }
       __syncwarp();
     }
   };
 
+  // The lane's operands of column v = 8 n + g: a block's parts lie plane after plane, the first
+  // rows' in the queue and the others' behind it.  What lies there past the block's rows goes into
+  // sums that are not used.
+  constexpr int kPlane = HR::kPlane, kMost = cdiv(8 * NG * kParts, 8);  // instructions' columns
+  const bool queued = g < kRing * kParts;
+  const uint32_t swz = plane_at<WF>(g / kParts, g % kParts, piece_k<WF>(0, 0) / 8) - g % kParts * kPlane;
+  const uint32_t hm = smem_u32(more) + (g - kRing * kParts) * kPlane + swz;
+  const uint32_t h0 = queued ? smem_u32(ring) + g * kPlane + swz : hm, h0slot = queued ? kRing * kRow : 0;
+  const uint32_t hfc = smem_u32(hf) + 4 * t;
+
   int from = 0;
   for (int row0 = row_lo; row0 < row_hi; row0 += kRowTile) {
-    float acc[NG][4];
+    float acc[NG][4];  // of tokens 8 n + 2t and + 1, rows g and g + 8
 #pragma unroll
     for (int n = 0; n < NG; ++n)
 #pragma unroll
       for (int i = 0; i < 4; ++i) acc[n][i] = 0.0f;
-    // block b's steps from s1 to end, for GN groups of tokens from n0 on
-    auto block = [&](auto groups, int n0, int b, uint32_t m, int s1, int end) {
-      constexpr int GN = decltype(groups)::value;
-      // this lane's columns in the block: column g's row of h, and for columns 2t and
-      // 2t + 1 whether they have a route, its weight and its row's factor; a column
-      // without a route takes any row, its sums are not used
-      const int first = tb.cum[b], n_rows = __popc(m);
-      uint32_t hrow[GN], hslot[GN], hfc[GN][2];
-      float w[GN][2];
+#pragma unroll 1
+    for (int b = b0, s1 = s0, rem = run; rem > 0; ++b) {
+      const int end = min(ns, s1 + rem);
+      rem -= end - s1;
+      const uint32_t m = tb.has[b];
+      const int first = tb.cum[b], n_rows = __popc(m), n8 = (n_rows * kParts + 7) / 8;
+      constexpr int kSums = F::kF16 ? 2 : 4;  // f16: this lane's two columns are both parts of row 4 n + t, added at once
+      float blk[kMost][kSums];
 #pragma unroll
-      for (int n = 0; n < GN; ++n) {
-        auto row_of = [&](int col) { return (m >> col) & 1u ? __popc(m & ((1u << col) - 1)) : 0; };
-        const int r = row_of(8 * (n0 + n) + g);
-        hslot[n] = r < kRing ? kRing * kRow : 0;
-        hrow[n] = smem_u32(r < kRing ? ring + r * kRow : more + (r - kRing) * kLine) + kHB * piece_k<WF>(0, 0);
+      for (int n = 0; n < kMost; ++n)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const int col = 8 * (n0 + n) + 2 * t + j;
-          w[n][j] = (m >> col) & 1u ? tb.w[max((int)tb.route[b * 8 * NG + col], 0)] : 0.0f;
-          hfc[n][j] = smem_u32(hf + row_of(col));
-        }
-      }
-      float blk[GN][4];
-#pragma unroll
-      for (int n = 0; n < GN; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) blk[n][i] = 0.0f;
+        for (int i = 0; i < kSums; ++i) blk[n][i] = 0.0f;
       float gs = 1.0f;  // needed at the end
       if constexpr (WF == OES_WFMT_NVFP4)
         gs = __ldcg(reinterpret_cast<const float*>(p.pool + (int64_t)tb.slot[b] * p.row_bytes + p.gs) + 1);
+#pragma unroll 1
       for (int st = s1; st < end; ++st) {
         cp_async_wait<S - 1>();
         __syncwarp();  // what other lanes brought
         form_rows(first, n_rows, st, from);
         const uint32_t e = smem_u32(queue + from * kEntry);
-        float d[GN][4], d1[GN][4];  // two chains of instructions with one group of tokens
+        auto step = [&](auto groups) {  // GN instructions' columns
+          constexpr int GN = decltype(groups)::value;
+          float d[GN][4], d1[GN][4];  // two chains of instructions with one's columns
+          uint4 B[2][GN][F::kB];
+          auto load = [&](int hh) {
 #pragma unroll
-        for (int n = 0; n < GN; ++n)
+            for (int n = 0; n < GN; ++n)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[n][i] = blk[n][i];
-        uint4 B[2][GN][F::kB], L[2][GN][F::kB];
-#pragma unroll
-        for (int hh = 0; hh < 2; ++hh)
-#pragma unroll
-          for (int n = 0; n < GN; ++n)
-#pragma unroll
-            for (int i = 0; i < F::kB; ++i) {
-              const uint32_t a = hrow[n] + from * hslot[n] + kHB * (piece_k<WF>(hh, i) - piece_k<WF>(0, 0));
-              const uint4 v = lds128(a);
-              B[hh][n][i] = L[hh][n][i] = v;
-              if constexpr (!F::kF16) {
-                const uint4 u = lds128(a + 16);
-                B[hh][n][i] = make_uint4(__byte_perm(v.x, v.y, 0x5410), __byte_perm(v.z, v.w, 0x5410),
-                                         __byte_perm(u.x, u.y, 0x5410), __byte_perm(u.z, u.w, 0x5410));
-                L[hh][n][i] = make_uint4(__byte_perm(v.x, v.y, 0x7632), __byte_perm(v.z, v.w, 0x7632),
-                                         __byte_perm(u.x, u.y, 0x7632), __byte_perm(u.z, u.w, 0x7632));
+              for (int i = 0; i < F::kB; ++i) {
+                // the lane's pieces differ in these bits of their numbers, permuted or not
+                constexpr int kHalf = WF == OES_WFMT_FP8 ? 0 : WF == OES_WFMT_BF16 ? 64 : 32;
+                const uint32_t at = n == 0 ? h0 + from * h0slot : hm + n * (8 * kPlane);
+                B[hh][n][i] = lds128((at ^ (kHalf * hh + 16 * i)) + (WF == OES_WFMT_FP8 ? 128 * hh : 0));
               }
-            }
-        half_mma<WF, GN, !F::kF16, F::kF16>(e, 0, B[0], L[0], d);
-        if constexpr (GN == 1) {
-          half_mma<WF, GN, !F::kF16, true>(e, 1, B[1], L[1], d1);
+          };
+          load(0);
+          if (GN <= 2) load(1);
+          half_mma<WF, GN, true>(e, 0, B[0], d);
+          if (GN > 2) load(1);
+          if constexpr (GN == 1) {
+            half_mma<WF, GN, true>(e, 1, B[1], d1);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[0][i] += d1[0][i];
-        } else {
-          half_mma<WF, GN, !F::kF16, false>(e, 1, B[1], L[1], d);
-        }
-        if constexpr (F::kF16) {
-          float sc0 = 1.0f, sc1 = 1.0f;
-          if constexpr (WF == OES_WFMT_FP8) {
-            sc0 = __uint_as_float(lds32(e + 2048 + 4 * g));
-            sc1 = __uint_as_float(lds32(e + 2048 + 32 + 4 * g));
+            for (int i = 0; i < 4; ++i) d[0][i] += d1[0][i];
+          } else {
+            half_mma<WF, GN, false>(e, 1, B[1], d);
           }
-#pragma unroll
-          for (int n = 0; n < GN; ++n)
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-              const float f = __uint_as_float(lds32(hfc[n][j]));
-              blk[n][j] = fmaf(sc0 * f, d[n][j], blk[n][j]);
-              blk[n][2 + j] = fmaf(sc1 * f, d[n][2 + j], blk[n][2 + j]);
+          if constexpr (F::kF16) {
+            float sc0 = 1.0f, sc1 = 1.0f;
+            if constexpr (WF == OES_WFMT_FP8) {
+              sc0 = __uint_as_float(lds32(e + 2048 + 4 * g));
+              sc1 = __uint_as_float(lds32(e + 2048 + 32 + 4 * g));
             }
-        } else {
 #pragma unroll
-          for (int n = 0; n < GN; ++n)
+            for (int n = 0; n < GN; ++n) {
+              const float f = __uint_as_float(lds32(hfc + 16 * n));
+              blk[n][0] = fmaf(sc0 * f, d[n][0] + d[n][1], blk[n][0]);
+              blk[n][1] = fmaf(sc1 * f, d[n][2] + d[n][3], blk[n][1]);
+            }
+          } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) blk[n][i] = d[n][i];
-        }
+            for (int n = 0; n < GN; ++n)
+#pragma unroll
+              for (int i = 0; i < kSums; ++i) blk[n][i] += d[n][i];
+          }
+        };
+        if (n8 <= 1) step(Int<1>{});
+        else if (n8 == 2) step(Int<2>{});
+        else if (NG == 2 && (F::kF16 || n8 > 3)) step(Int<kMost>{});
+        else if constexpr (!F::kF16) step(Int<3>{});
         __syncwarp();  // read by all before the queue's entry is filled again
         from = from + 1 == S ? 0 : from + 1;
         copy_next(nullptr);
       }
-      // a token without a route in this block takes nothing from it, not even a NaN of
-      // its weights
-#pragma unroll
-      for (int n = 0; n < GN; ++n)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if ((m >> (8 * (n0 + n) + 2 * t + (i & 1))) & 1u) {
-            const float f = w[n][i & 1] * gs;
-            if (GN == NG || n0 == 0) acc[n][i] = fmaf(f, blk[n][i], acc[n][i]);
-            else acc[NG - 1][i] = fmaf(f, blk[n][i], acc[NG - 1][i]);
-          }
-    };
-    for (int b = b0, s1 = s0, rem = run; rem > 0; ++b) {
-      const int end = min(ns, s1 + rem);
-      const uint32_t m = tb.has[b];
-      if constexpr (NG == 1) {
-        block(Int<1>{}, 0, b, m, s1, end);
-      } else {
-        if ((m & 0xFFu) && m >> 8) block(Int<2>{}, 0, b, m, s1, end);
-        else block(Int<1>{}, m >> 8 ? 1 : 0, b, m, s1, end);
-      }
-      rem -= end - s1;
       s1 = 0;
+      // Each row's sums, its parts' columns together, to the lanes of its token.  A token without a route
+      // in this block takes nothing from it, not even a NaN of its weights.
+      uint32_t left = m;
+#pragma unroll
+      for (int r = 0; r < 8 * NG; ++r) {
+        if (r >= n_rows) break;
+        const int col = __ffs(left) - 1;
+        left &= left - 1;
+        const float f = tb.w[tb.order[first + r]] * gs;
+        float sum0 = 0.0f, sum1 = 0.0f;
+        if constexpr (F::kF16) {
+          sum0 = __shfl_sync(0xffffffffu, blk[r / 4][0], (lane & ~3) | (r & 3));
+          sum1 = __shfl_sync(0xffffffffu, blk[r / 4][1], (lane & ~3) | (r & 3));
+        } else {
+#pragma unroll
+          for (int part = 0; part < kParts; ++part) {
+            const int v = r * kParts + part, from_lane = (lane & ~3) | ((v & 7) >> 1);
+            sum0 += __shfl_sync(0xffffffffu, blk[v / 8][v & 1], from_lane);
+            sum1 += __shfl_sync(0xffffffffu, blk[v / 8][2 + (v & 1)], from_lane);
+          }
+        }
+#pragma unroll
+        for (int n = 0; n < NG; ++n)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (col == 8 * n + 2 * t + j) {
+              acc[n][j] = fmaf(f, sum0, acc[n][j]);
+              acc[n][2 + j] = fmaf(f, sum1, acc[n][2 + j]);
+            }
+      }
     }
-    if (row0 > row_lo) __syncthreads();  // the tile before has read its sums
-    float* mine = part + (warp * 32 + lane) * (4 * NG);
+    float* mine = reinterpret_cast<float*>(more) + lane * (4 * NG);
 #pragma unroll
     for (int n = 0; n < NG; ++n)
       *reinterpret_cast<float4*>(mine + 4 * n) = make_float4(acc[n][0], acc[n][1], acc[n][2], acc[n][3]);
@@ -1156,12 +1192,14 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
     for (int i = tid; i < kRowTile * p.T; i += kThreads) {
       const int r16 = i & 15, tok = i >> 4;
       if (row0 + r16 >= row_hi) continue;
-      const float* v = part + ((r16 & 7) * 4 + (tok & 7) / 2) * (4 * NG) + (tok >> 3) * 4 + (r16 >> 3) * 2 + (tok & 1);
+      const float* v = reinterpret_cast<const float*>(smem + down_queue_bytes<WF, S>()) +
+                       ((r16 & 7) * 4 + (tok & 7) / 2) * (4 * NG) + (tok >> 3) * 4 + (r16 >> 3) * 2 + (tok & 1);
       float s = 0.0f;
 #pragma unroll
-      for (int w = 0; w < W; ++w) s += v[w * 32 * 4 * NG];
+      for (int w = 0; w < W; ++w) s += v[w * (kWarp / 4)];
       p.out[(int64_t)tok * p.H + row0 + r16] = (uint16_t)f32_bf16(s);
     }
+    if (row0 + kRowTile < row_hi) __syncthreads();  // read before the next tile's rows of h come there
   }
 }
 
@@ -1194,12 +1232,14 @@ int launch_up(const FewParams& p, cudaStream_t stream) {
   return OES_OK;
 }
 
+constexpr size_t kDownSmemMost = 227 * 1024 - 128;  // few_down's own, beside its static shared memory
 template <int WF, int NG, int S>
-size_t down_smem(int T, int k) {
-  return (size_t)W * down_warp_bytes<WF, NG, S>() + W * 32 * 16 * NG + tables_bytes(T * k, NG);
+constexpr size_t down_smem(int T, int k) {
+  return (size_t)W * down_warp_bytes<WF, NG, S>() + down_tables_bytes(T * k);
 }
 template <int WF, int NG, int S>
 int launch_down(const FewParams& p, cudaStream_t stream) {
+  static_assert(down_smem<WF, NG, S>(8 * NG, OES_MAX_TOPK) <= kDownSmemMost, "few_down's shared memory");
   const size_t smem = down_smem<WF, NG, S>(p.T, p.k);
   int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(few_down_kernel<WF, NG, S>), smem,
                                       "few_down_kernel: shared memory limit");
@@ -1227,9 +1267,9 @@ int launch_few(FewParams p, cudaStream_t stream) {
   else if (fits(up_smem<WF, NG, 1, 4>(p.T, p.k, p.H))) rc = launch_up<WF, NG, 1, 4>(p, stream);
   else rc = launch_up<WF, NG, 1, 2>(p, stream);
   if (rc) return rc;
-  if constexpr (NG == 2)  // with eight tokens three steps always fit
-    if (!fits(down_smem<WF, NG, 3>(p.T, p.k))) return launch_down<WF, NG, 2>(p, stream);
-  return launch_down<WF, NG, 3>(p, stream);
+  // Three steps in the second kernel's queues; those of FP8 experts do not fit for more than
+  // eight tokens.
+  return launch_down<WF, NG, WF == OES_WFMT_FP8 && NG == 2 ? 2 : 3>(p, stream);
 }
 
 // Most tokens whose rows of x fit beside the shortest queues.
@@ -1287,7 +1327,7 @@ static_assert(OES_FEW_TOKENS_MAX == kMaxTokens, "tokens a call");
 extern "C" size_t moe_layer_few_tokens_workspace_size(const oes_routed_experts* v, int T, int k) {
   if (check_view(v, T, k, "moe_layer_few_tokens_workspace_size") || T == 0) return 0;
   // h, then the tables of a group of tokens
-  return ((size_t)T * k * v->I * 4 + 16 + tables_bytes(T * k, 2) + 255) / 256 * 256;
+  return ((size_t)T * k * v->I * h_value_bytes(v->wfmt) + 16 + down_tables_bytes(T * k) + 255) / 256 * 256;
 }
 
 extern "C" int moe_layer_few_tokens(const oes_routed_experts* v, const uint16_t* x, int T, int k, const void* logits,
@@ -1343,7 +1383,7 @@ extern "C" int moe_layer_few_tokens(const oes_routed_experts* v, const uint16_t*
   p.ids = ids;
   p.weights = weights;
   p.h = workspace;
-  p.tables = static_cast<uint8_t*>(workspace) + (size_t)T * k * v->I * 4;
+  p.tables = static_cast<uint8_t*>(workspace) + (size_t)T * k * v->I * h_value_bytes(v->wfmt);
   p.out = out;
   p.status = status;
   if (logits && v->E > kFusedExperts) {
