@@ -443,10 +443,13 @@ size_t moe_layer_few_tokens_workspace_size(const oes_routed_experts *view, int T
  * without a route gets zeros.  A routed expert with e2s outside [0, S) sets
  * OES_DEV_BAD_ID and its routes give 0.
  * view->wfmt: OES_WFMT_BF16, OES_WFMT_FP8 or OES_WFMT_NVFP4, rows as above.
- * Weights are decoded exactly, and the activations are not quantised, in the FP8
- * format neither (moe_grouped_gemm_slots quantises them there): sums are fp32, h
- * keeps 24 significant bits for bf16 weights and 22 for the others (with a common
- * exponent for each 128 values, so of any size), and out is rounded once.  The
+ * Weights are decoded exactly, and the activations are not quantised to 8 bits, in
+ * the FP8 format neither (moe_grouped_gemm_slots quantises them there).  For bf16
+ * weights x is taken as it is, and h keeps 24 significant bits.  For the others both
+ * have a common exponent for each 128 values, so that they may be of any size: x is
+ * exact down to 2^-31 of the largest of its 128, and what is below 2^-39 of it counts
+ * as 0; h keeps 22 significant bits, with differences below 2^-39 of its largest lost.
+ * Sums are fp32 and out is rounded once.  The
  * result does not depend on timing; it is not bit for bit that of
  * moe_grouped_gemm_slots, which rounds each route's output row to bf16 before the
  * weighted sum.
@@ -457,9 +460,19 @@ size_t moe_layer_few_tokens_workspace_size(const oes_routed_experts *view, int T
  * x: device [T, H] bf16, pool, x and workspace 16-byte aligned; out: device
  * [T, H] bf16; status: device word or NULL.  H, I multiples of 64 in
  * [64, 16384], k <= OES_MAX_TOPK (and <= E with logits).  Layers of more than
- * 512 experts take one launch more for the routing, and rows of x that do not
- * fit in shared memory together (H above 4000 to 4700 for 16 tokens, by k) take
- * two launches for each group of tokens that do. */
+ * 512 experts take one launch more for the routing.  Rows of x that do not fit in
+ * shared memory together take two launches for each group of tokens that do, and
+ * each group reads its experts' weights anew: for 16 tokens from H = 4096 (k = 32)
+ * to 5056 (k = 1) on with bf16 weights, 3904 to 4928 with FP8, 4928 to 5824 with NVFP4.
+ * Which call for a decode step: measured on one GB300, from the logits, beside
+ * moe_route_topk, moe_align_block_size and moe_grouped_gemm_slots, this one is the faster
+ * for NVFP4 weights; for bf16 ones while the tokens are one group; for FP8 ones up to 8
+ * tokens.  10 of 512 experts of 2048 x 768, us here and there:
+ *   tokens       1            4            8            16
+ *   bf16     22    46     65    83    118   136    217   220
+ *   FP8      17    29     43    49     77    78    139   120
+ *   NVFP4    16    46     38    77     65   117    145   195
+ * In two groups, 16 tokens x 8 of 64 experts of 7168 x 1024 in bf16: 686 against 406. */
 int moe_layer_few_tokens(const oes_routed_experts *view, const uint16_t *x, int T, int k,
                          const void *logits, int dtype, int32_t *ids, float *weights,
                          void *workspace, size_t workspace_bytes, uint16_t *out, int32_t *status,

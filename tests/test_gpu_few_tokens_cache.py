@@ -5,8 +5,7 @@ import pytest
 import torch
 
 from offloaded_expert_slot_gb300 import oes
-from offloaded_expert_slot_gb300.configs import C2, scaled
-from offloaded_expert_slot_gb300.inputs import expert_layer_rows, rng
+from offloaded_expert_slot_gb300.inputs import rng
 from test_gpu_few_tokens import WFMT, Layer
 
 pytestmark = pytest.mark.gpu
