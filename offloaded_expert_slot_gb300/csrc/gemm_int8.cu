@@ -4,11 +4,11 @@
 //   out[t, n] = xs[t] ws[n] sum_k x[t, k] w[n, k]
 //
 // GB300's tensor cores have no fast integer products, and need none here: f16
-// holds every 8-bit integer exactly, its products are below 2^14 and exact in the
-// tensor core, and fp32 sums of up to 1024 of them stay below 2^24, where
-// integers are exact.  So the sums of at most 1024 of K come from f16 matrix
-// instructions and are added up as 32-bit integers: the sum is the integer, whatever
-// the order, at the f16 rate.
+// holds every 8-bit integer exactly, its products are at most 2^14 ((-128)^2) and exact
+// in the tensor core, and fp32 sums of up to 1024 of them are at most 2^24, up to which
+// fp32 holds every integer.  So the sums of at most 1024 of K (kDrainK, and no more:
+// 1024 (-128)^2 is 2^24) come from f16 matrix instructions and are added up as 32-bit
+// integers: the sum is the integer, whatever the order, at the f16 rate.
 //
 //   int8_stream_kernel  few rows: warps stream the weights through queues of their
 //                       own (as in few_tokens.cu) into warp-wide instructions, x
@@ -37,7 +37,10 @@ namespace {
 // and become f16 on their way to the instruction.  The tokens stand in shared memory as f16, in
 // two chunks of K; where K has more, each group has one tile of rows, and chunk after
 // chunk is loaded into registers under the products of the chunk two before it.
+constexpr int kDrainK = 1024;  // of K in one fp32 sum
+static_assert(kDrainK * 128 * 128 <= 1 << 24, "integers that fp32 holds");
 constexpr int kStepK = 128;
+static_assert(kDrainK % kStepK == 0, "whole steps in a sum");
 constexpr int kEntry = 2048;    // 16 rows of a step
 constexpr int kTokensMost = 32;  // of a CTA
 
@@ -190,7 +193,7 @@ __global__ void __launch_bounds__(W * 32, 1) int8_stream_kernel(const StreamArgs
   int32_t acc[NG][4];
   // the sums of the tile at row0; all warps come here together where chunks are reloaded
   auto tile = [&](int row0) {
-    float d[NG][4];  // sums of up to 8 steps (1024 of K), integers below 2^24
+    float d[NG][4];  // sums of up to 8 steps (kDrainK), integers of at most 2^24
     int steps_in = 0;
 #pragma unroll
     for (int n = 0; n < NG; ++n)
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(W * 32, 1) int8_stream_kernel(const StreamArgs
             mma_16816<true>(d[n], m[3][0], m[3][1], m[3][2], m[3][3], v.z, v.w);
           }
         }
-        if (++steps_in == 1024 / kStepK) {
+        if (++steps_in == kDrainK / kStepK) {
           drain();
           steps_in = 0;
         }
@@ -354,7 +357,7 @@ __global__ void __launch_bounds__(256) int8_to_f16_kernel(const CvtArgs a) {
 
 constexpr int kTileM = 128;
 constexpr int kBlkBytes = 128;        // 64 f16 of K, a pipeline stage's row
-constexpr int kDrain = 16;            // stages (1024 of K) a TMEM buffer sums
+constexpr int kDrain = kDrainK / 64;  // stages a TMEM buffer sums
 constexpr int kEpiW0 = 4, kEpi = 8;   // epilogue warps: two a TMEM lane quarter
 constexpr int kTmThreads = (kEpiW0 + kEpi) * 32;
 
