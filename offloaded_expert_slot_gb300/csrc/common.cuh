@@ -47,9 +47,9 @@ inline int64_t ceil_div64(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Every kernel of the library is launched as a programmatic dependent of the
 // kernel before it on the stream: the launch may begin while that kernel is
-// still running, and the kernel's first statement, pdl_wait(), waits until
-// it has completed and its memory is visible.  So no kernel touches global
-// memory before its predecessor is done, and the launch latency between
+// still running, and pdl_wait() waits until it has completed and its memory is
+// visible.  No kernel touches before its wait what another one on the stream
+// may still read or write, so the stream's order holds, and the launch latency between
 // dependent kernels (route -> distinct -> ensure -> ... -> combine) overlaps
 // the predecessor's tail.  Inside a captured graph the same order holds.
 // A PlainLaunches scope on the calling thread launches without the
@@ -93,16 +93,26 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));
 }
 
-// First statement of every kernel: pdl_wait() waits for the previous kernel
-// on the stream to complete (a no-op for a launch that is not programmatic).
-// The short kernels of the chain (routing, distinct, ensure, flags, align,
-// table copies) then call pdl_trigger() at once, so that the next kernel is
-// launched while they run; its CTAs are released only once every CTA of this
-// grid has started, and they wait the same way.  The long, wide kernels (the
-// GEMMs, the x preparation, the combine, the row copies) leave the trigger
-// to their completion: their successors' CTAs would otherwise sit resident
-// and waiting beside them, which measured slower where copies and GEMMs run
-// side by side (the staged layer sequence).
+// pdl_wait() waits for the previous kernel on the stream to complete (a no-op for
+// a launch that is not programmatic).  It comes before a kernel's first access to
+// global memory, but in the second kernels of a pair: the down products of
+// the experts (gemm.cu, gemm_fp8.cu) and few_down_kernel (few_tokens.cu) read tables and
+// weights before it.  Those were complete before the first kernel of the pair
+// passed its own wait, and the second is launched only once every CTA of the
+// first has called pdl_trigger() after that wait, or ended.  Only h is waited for.
+//
+// pdl_trigger() lets the next kernel be launched: its CTAs are released once every
+// CTA of this grid has called it or ended, and they wait the same way, for this
+// grid's completion, wherever the call stands.  The short kernels (routing, distinct,
+// ensure, flags, align, table copies, quantisers, norms, products of few rows) call
+// it right after their wait (pdl_begin).  So does few_up_kernel, once the word that
+// few_down_kernel looks at is cleared; few_down_kernel calls it at its start, since
+// its CTAs fill an SM and its successor's take their places one by one; and
+// the experts' first products call it after their set-up, where few units follow.  The
+// other long, wide kernels (the x preparation, the combine, the row copies, the
+// products on tensor memory) leave it to their completion: their successors' CTAs would
+// otherwise sit resident and waiting beside them, which measured slower where
+// copies and GEMMs run side by side (the staged layer sequence).
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
