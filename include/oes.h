@@ -520,7 +520,8 @@ int moe_fp8_gemm(const uint8_t *xq, int64_t xq_ld, const float *xs, int T, int K
  * q[t, i] = the integer nearest to the real number 127 v / amax, ties to even.
  * A row with a NaN or an infinity gets a NaN scale and codes of 0 (the row reads as
  * NaN).  act, x, dtype, x_ld as in moe_fp8_quantize (for OES_ACT_SWIGLU, v is
- * fp32); q: device, row stride q_ld >= K; scale: device [T] fp32.  T >= 0,
+ * fp32, silu as there, so that a quotient that close to a tie may get the other
+ * integer); q: device, row stride q_ld >= K; scale: device [T] fp32.  T >= 0,
  * 1 <= K <= 2^28.  Rows are read and written 8 values at a time when K, strides and
  * addresses allow it (K a multiple of 8; x and its rows 16-byte, q and its rows
  * 8-byte aligned). */
