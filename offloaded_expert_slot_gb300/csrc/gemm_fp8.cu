@@ -163,12 +163,6 @@ __device__ __forceinline__ void bulk_store(void* dst, const void* src, int bytes
 }
 __device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
 __device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
-// ----- clusters: a shared address of another CTA, and its barriers
-__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
 // Into another CTA's shared memory, the bytes counted by a barrier there: whoever
 // waits for that barrier sees them.  With plain stores, a fence and a releasing
 // arrival 1 x 1536 x 2048 took 5.4 us, like this 3.9.
@@ -176,10 +170,6 @@ __device__ __forceinline__ void st_async(uint32_t addr, float v, uint32_t bar) {
   asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr),
                "r"(__float_as_uint(v)), "r"(bar)
                : "memory");
-}
-__device__ __forceinline__ void cluster_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 
 // Once every role of a CTA in which a wait gave up has ended, by one thread: no

@@ -596,17 +596,8 @@ __device__ __forceinline__ uint32_t cluster_rank() {
   asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
   return r;
 }
-__device__ __forceinline__ uint32_t addr_in_rank(uint32_t saddr, uint32_t rank) {
-  uint32_t r;
-  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
-  return r;
-}
 __device__ __forceinline__ void arrive_remote(uint32_t cluster_addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_addr) : "memory");
-}
-__device__ __forceinline__ void pair_barrier() {
-  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
-  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 __device__ __forceinline__ void pair_mma_f16(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc,
                                              uint32_t accumulate) {
@@ -670,7 +661,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTmThreads, 1)
     tc_fence_before();
   }
   __syncthreads();
-  pair_barrier();  // the other CTA's barriers and tensor memory are there
+  cluster_barrier();  // the other CTA's barriers and tensor memory are there
   tc_fence_after();
   const uint32_t tmem_base = s_tmem;
   pdl_wait();  // the f16 copies
@@ -690,7 +681,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTmThreads, 1)
           // Rank 0 expects both CTAs' bytes.  Rank 1's may come first: its stage was released
           // with rank 0's, and the phase does not end before rank 0's arrival.
           uint8_t* X = stages + s * kStage;
-          const uint32_t bar = addr_in_rank(smem_u32(&full[s]), 0);
+          const uint32_t bar = map_rank(smem_u32(&full[s]), 0);
           if (rank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStage);
           pair_load_2d(X, &maps.x, bar, kb * 64, m);
           pair_load_2d(X + kTileM * kBlkBytes, &maps.w, bar, kb * 64, n);
@@ -764,7 +755,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTmThreads, 1)
         __syncwarp();
         if (lane == 0) {
           if (rank == 0) mbar_arrive(&tempty[a]);
-          else arrive_remote(addr_in_rank(smem_u32(&tempty[a]), 0));
+          else arrive_remote(map_rank(smem_u32(&tempty[a]), 0));
         }
       }
       if (on) store_tile<OT, kCols>(p, acc, stg, q, m0, n0, nvalid);
@@ -777,11 +768,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTmThreads, 1)
   // it reads, no arrival the CTA it goes to.
   if (warp == 2 && lane == 0) mbar_wait(&s_mma_done, 0, p.status);
   __syncwarp();
-  pair_barrier();
+  cluster_barrier();
   if (rank == 0 && threadIdx.x == 0) {
     int theirs, their_dead;
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(theirs) : "r"(addr_in_rank(smem_u32(&s_fills), 1)));
-    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(their_dead) : "r"(addr_in_rank(smem_u32(&s_dead), 1)));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(theirs) : "r"(map_rank(smem_u32(&s_fills), 1)));
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(their_dead) : "r"(map_rank(smem_u32(&s_dead), 1)));
     if (s_dead || their_dead) {
       // A wait gave up, and one producer may have stopped before the other: what a phase
       // of the last ns is short of is made up, then its bytes are waited for.
@@ -797,7 +788,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kTmThreads, 1)
     }
   }
   __syncthreads();
-  pair_barrier();
+  cluster_barrier();
   if (warp == 2) {
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, 512;" ::"r"(tmem_base) : "memory");

@@ -1,5 +1,6 @@
 // Device helpers of the warp-specialised tcgen05 kernels: bounded waits that leave a
-// CTA able to end, the uniform warp index, and moves of registers between warps.
+// CTA able to end, the uniform warp index, moves of registers between warps, and
+// addresses and barriers of a cluster.
 #pragma once
 
 #include "common.cuh"
@@ -96,6 +97,16 @@ __device__ __forceinline__ bool elect_one() {
 }
 __device__ __forceinline__ void named_bar(int id, int threads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(threads) : "memory");
+}
+// ----- clusters: a shared address of another CTA, and the barrier of all
+__device__ __forceinline__ uint32_t map_rank(uint32_t saddr, uint32_t rank) {
+  uint32_t r;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(saddr), "r"(rank));
+  return r;
+}
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 template <int N>
 __device__ __forceinline__ void regs_inc() {
