@@ -28,16 +28,16 @@
 // copies, read back by the same lane), so a warp keeps its next steps in
 // flight without registers and without a barrier.  The instructions are the
 // warp-wide m16n8k16, whose tensor work at 8 columns is a small part of what the
-// stream takes (10 to 18 % of the pipe); the grouped GEMM's tcgen05 tiles (128 weight rows,
+// stream takes (9 to 19 % of the pipe); the grouped GEMM's tcgen05 tiles (128 weight rows,
 // operands through shared memory and TMEM) reach 9 to 30 % of the copy rate for 1 to 64
 // tokens of NVFP4 experts, held up by their set-up and hand-offs.
 //
-// Measured (10 of 512 experts of 2048 x 768, replayed from a graph): 1 token FP8 16.9 us
-// (2.8 TB/s), bf16 21.5 us (4.4); 4 tokens NVFP4 38.5 us (2.7); 16 tokens bf16 206 to 217 us (6.0 to
-// 6.3 TB/s, 89 to 93 % of the copy rate, by GPU), FP8 132 us (5.0), NVFP4 142 us (2.6).  16 bf16 tokens
+// Measured (10 of 512 experts of 2048 x 768, replayed from a graph): 1 token FP8 16.8 us
+// (2.8 TB/s), bf16 21.9 us (4.3); 4 tokens NVFP4 38.9 us (2.6); 16 tokens bf16 207 to 219 us (6.0 to
+// 6.3 TB/s, 88 to 93 % of the copy rate, by GPU), FP8 138 us (4.8), NVFP4 143 us (2.6).  16 bf16 tokens
 // are bound by memory; the 8- and 4-bit formats by the instructions that decode and multiply (issue
-// slots 44 to 54 % busy); one token by latency: 4.6 us to the first weights (logits, top-k, tables,
-// slots), 2 to 3 from one kernel to the next, 1.5 for the last sums.
+// slots 37 to 52 % busy); one token by latency: 4.4 us to the first weights (logits, top-k, tables,
+// slots), 2 to 3 from one kernel to the next, 1.3 for the last sums.
 //
 // Weights are exact in 16 bits: bf16 as they are; e4m3 as f16, their block scales on
 // the fp32 sums of each 128 of K; e2m1 x e4m3 as f16, the global scale on the sums.
@@ -694,9 +694,9 @@ __global__ void __launch_bounds__(W * 32, 1) few_up_kernel(const FewParams p) {
   }
   int from = 0, buf = 0;
   // A unit for GN groups of eight tokens from n0 on.  Of more than eight tokens most blocks
-  // have a route or two, in one group, and the other's instructions are left out, here
-  // and in the down kernel: 16 tokens x 10 of 512 experts in bf16 228 -> 220 us, NVFP4 152 -> 144,
-  // 12 tokens 181 -> 173 and 124 -> 116.
+  // have a route or two, in one group, and the other's instructions are left out.  (Here and
+  // in a down kernel whose columns were tokens too: 16 tokens x 10 of 512 experts in bf16 228 -> 220
+  // us, NVFP4 152 -> 144, 12 tokens 181 -> 173 and 124 -> 116.)
   auto unit = [&](auto groups, int n0) {
     constexpr int GN = decltype(groups)::value;
     uint32_t ub[GN], uf[GN][2];
