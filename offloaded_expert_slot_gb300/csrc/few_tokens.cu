@@ -1153,36 +1153,46 @@ __global__ void __launch_bounds__(W * 32, 1) few_down_kernel(const FewParams p) 
         copy_next(nullptr);
       }
       s1 = 0;
-      // Each row's sums, its parts' columns together, to the lanes of its token.  A token without a route
-      // in this block takes nothing from it, not even a NaN of its weights.
-      uint32_t left = m;
+      // Each row's sums, its parts' columns together, to the lanes of its token, through the further
+      // rows' place (by shuffles, row after row, whose code is fetched anew each time, 16 tokens x 10 of 32
+      // bf16 experts took 82 us, so 79).  A token without a route in this block takes nothing from it, not
+      // even a NaN of its weights.
+      constexpr int kCols = F::kF16 ? 4 * kMost : 8 * kMost, kLd = kCols + 4;  // a row's sums; of each of 16 rows of out
+      static_assert((8 * NG - kRing) * kRow >= 16 * kLd * 4, "a block's sums");
+      float* sums = reinterpret_cast<float*>(more);
 #pragma unroll
-      for (int r = 0; r < 8 * NG; ++r) {
-        if (r >= n_rows) break;
-        const int col = __ffs(left) - 1;
-        left &= left - 1;
-        const float f = tb.w[tb.order[first + r]] * gs;
-        float sum0 = 0.0f, sum1 = 0.0f;
-        if constexpr (F::kF16) {
-          sum0 = __shfl_sync(0xffffffffu, blk[r / 4][0], (lane & ~3) | (r & 3));
-          sum1 = __shfl_sync(0xffffffffu, blk[r / 4][1], (lane & ~3) | (r & 3));
-        } else {
-#pragma unroll
-          for (int part = 0; part < kParts; ++part) {
-            const int v = r * kParts + part, from_lane = (lane & ~3) | ((v & 7) >> 1);
-            sum0 += __shfl_sync(0xffffffffu, blk[v / 8][v & 1], from_lane);
-            sum1 += __shfl_sync(0xffffffffu, blk[v / 8][2 + (v & 1)], from_lane);
+      for (int n = 0; n < kMost; ++n)
+        if (n < n8) {
+          if constexpr (F::kF16) {
+            sums[g * kLd + 4 * n + t] = blk[n][0];
+            sums[(g + 8) * kLd + 4 * n + t] = blk[n][1];
+          } else {
+            *reinterpret_cast<float2*>(sums + g * kLd + 8 * n + 2 * t) = make_float2(blk[n][0], blk[n][1]);
+            *reinterpret_cast<float2*>(sums + (g + 8) * kLd + 8 * n + 2 * t) = make_float2(blk[n][2], blk[n][3]);
           }
         }
+      __syncwarp();
 #pragma unroll
-        for (int n = 0; n < NG; ++n)
+      for (int n = 0; n < NG; ++n)
 #pragma unroll
-          for (int j = 0; j < 2; ++j)
-            if (col == 8 * n + 2 * t + j) {
-              acc[n][j] = fmaf(f, sum0, acc[n][j]);
-              acc[n][2 + j] = fmaf(f, sum1, acc[n][2 + j]);
+        for (int j = 0; j < 2; ++j) {
+          const int col = 8 * n + 2 * t + j;
+          if ((m >> col) & 1u) {
+            const int r = __popc(m & ((1u << col) - 1));
+            const float f = tb.w[tb.order[first + r]] * gs;
+            constexpr int kEach = F::kF16 ? 1 : kParts;
+            const float* v = sums + g * kLd + r * kEach;
+            float sum0 = v[0], sum1 = v[8 * kLd];
+#pragma unroll
+            for (int part = 1; part < kEach; ++part) {
+              sum0 += v[part];
+              sum1 += v[8 * kLd + part];
             }
-      }
+            acc[n][j] = fmaf(f, sum0, acc[n][j]);
+            acc[n][2 + j] = fmaf(f, sum1, acc[n][2 + j]);
+          }
+        }
+      __syncwarp();  // read before others' sums or rows come there
     }
     float* mine = reinterpret_cast<float*>(more) + lane * (4 * NG);
 #pragma unroll
